@@ -327,6 +327,138 @@ upf_status upf_select_noalloc(const upf_batch* batch, const upf_params* params, 
  * tested.  Errors: INVALID_ARG (ctx NULL, cycles < 0). */
 upf_status upf_set_wait_limit(upf_ctx* ctx, int64_t cycles);
 
+/* ------------------------------------------------------------------------
+ * 4-bit KV cache of the kept tokens
+ * ------------------------------------------------------------------------
+ * What follows the selection of a prefill layer (section 三: KV slots of the
+ * kept tokens, and the per-layer number of KV entries that decode reads):
+ * writing the kept tokens' keys and values into one layer's cache at their
+ * slot ids, reading entries back, and attending to them.  The article leaves
+ * the cache to the serving engine; these calls are this library's own.
+ *
+ * A group of 16 dims of one token and kv head is held as 16 e2m1 codes (the
+ * 4-bit floats 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one e4m3
+ * scale s:
+ *   s    = e4m3(min(max|x| * 2^-exp / 6, 448)),  code = e2m1(x * 2^-exp / s),
+ * both to nearest, ties to even, the code saturating at 6; a zero scale holds
+ * zeros, and a group with a NaN or an infinity in it reads back as 16 NaNs.
+ * A code stands for e2m1 * s * 2^exp, which is exact in bf16.  Keys have the
+ * exponent k_exp, values v_exp.
+ *
+ * data:      device, upf_kv_cache_bytes() bytes, 128-byte aligned, contents as
+ *            written by upf_kv_write (codes of slots never written may be
+ *            anything).  16 consecutive slots of one kv head are one record of
+ *            18*head_dim bytes, record (slot / 16, head) at index
+ *            (slot / 16) * num_kv_heads + head; with P = max(1, d / 128),
+ *            D = d / P, C = D / 16 and row = slot % 16 = 8 half + 2 pair + bit
+ *            a record is: K codes [P][16 rows][D/2] (low nibble: even dim), V
+ *            codes [P][half 2][chunk 8][pair 4][bit 2][C], K scales
+ *            [16 rows][d/16], V scales [P][half 2][D/16][pair 4][bit 2].
+ * num_slots: slots of the cache, a multiple of 16.
+ * num_kv_heads: 1 to 256.  head_dim: 64, 128 or 256.  k_exp, v_exp: -32 to 32. */
+typedef struct upf_kv_cache {
+  void* data;
+  int64_t num_slots;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t k_exp;
+  int32_t v_exp;
+} upf_kv_cache;
+
+/* Element type of keys, values, queries and outputs. */
+typedef enum upf_dtype { UPF_BF16 = 0, UPF_F16 = 1 } upf_dtype;
+
+/* Bytes of `data` (only the sizes of `cache` are read); 0 and the last error
+ * if they are invalid. */
+size_t upf_kv_cache_bytes(const upf_kv_cache* cache);
+
+/* Bytes of workspace upf_kv_write needs for num_tokens tokens (scratch, 256-byte
+ * aligned, any contents); 0 and the last error if the arguments are invalid. */
+size_t upf_kv_write_workspace_bytes(const upf_kv_cache* cache, int32_t num_tokens);
+
+/* Quantise tokens' keys and values and write them at their slots.
+ * k, v: device, token t kv head h at k + t*k_row_stride + h*head_dim; row strides
+ *    in elements, >= num_kv_heads*head_dim and multiples of 8; 16-byte aligned.
+ * slots: device int64 [num_tokens] slot ids (e.g. slot_out of upf_compact).  A
+ *    negative id skips its token; an id >= num_slots skips it and sets
+ *    UPF_ERR_INVALID_ARG in the status word; of tokens with the same slot the
+ *    last one is written, as if they were written in order.
+ * num_tokens_dev: device int32 [1] (nullable): only the first
+ *    min(num_tokens, *num_tokens_dev) tokens are written (e.g. total_kept).
+ * Slots not named keep their bytes.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+upf_status upf_kv_write(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, const void* k, int64_t k_row_stride,
+                        const void* v, int64_t v_row_stride, const int64_t* slots, int32_t num_tokens,
+                        const int32_t* num_tokens_dev, void* ws, size_t ws_bytes, void* stream);
+
+/* Read the values held at slots: row t of k and v (either may be NULL) receives
+ * slot slots[t], rounded once to `dtype` (exact in bf16).  Rows of skipped tokens
+ * (negative or too large id, or at and past *num_tokens_dev) are left as they
+ * are; a slot may be named any number of times.  Layouts, strides, slots and
+ * num_tokens_dev as for upf_kv_write.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+upf_status upf_kv_read(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, const int64_t* slots,
+                       int32_t num_tokens, const int32_t* num_tokens_dev, void* k, int64_t k_row_stride, void* v,
+                       int64_t v_row_stride, void* stream);
+
+/* New tokens that attend to the cache.
+ * num_reqs:     R requests.  Request r has kv_len[r] entries in the cache, its
+ *               new tokens' own entries (already written) the last of them.
+ * num_q_heads, kv_of_q: as in upf_batch; at most 256 heads.
+ * num_q_tokens: rows of q, out and lse.
+ * max_q_len:    most new tokens of any request (1 for decoding), at most 1024.
+ * cu_q:         device int32 [R+1]: request r's new tokens are rows
+ *               [cu_q[r], cu_q[r+1]); NULL: one each (num_q_tokens = R).  Rows
+ *               outside every request are left as they are.
+ * kv_len:       device int32 [R] (e.g. from upf_history_kv_len), 0 allowed.
+ * page_table:   device int32, entry e of request r is in slot
+ *               page * page_size + e % page_size with
+ *               page = page_table[r * page_stride + e / page_size].  Only the
+ *               pages of entries that some row of r sees are looked up, so those
+ *               of entries behind the window may be gone.
+ * max_pages:    pages in a table row: kv_len[r] <= max_pages * page_size.
+ * page_size:    power of two from 16 to 65536.
+ * window, sinks: query i of request r, at p = kv_len[r] - q_len + i, sees the
+ *               entries e <= p with p - e < window or e < sinks; window 0: all
+ *               e <= p.  Entries are counted as they lie in the cache.
+ * softmax_scale <= 0 selects 1/sqrt(head_dim). */
+typedef struct upf_kv_query {
+  int32_t num_reqs;
+  int32_t num_q_heads;
+  const int32_t* kv_of_q;
+  int32_t num_q_tokens;
+  int32_t max_q_len;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t page_stride;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t window;
+  int32_t sinks;
+  float softmax_scale;
+} upf_kv_query;
+
+/* Bytes of workspace upf_kv_attend needs (scratch, 256-byte aligned, any
+ * contents; depends on the sizes alone, not on the lengths in device memory);
+ * 0 and the last error if the arguments are invalid. */
+size_t upf_kv_attend_workspace_bytes(const upf_kv_cache* cache, const upf_kv_query* query);
+
+/* Attention of the new tokens over the cache:
+ *   out = sum_e softmax_e(scale * q . k_e) v_e,   lse = ln sum_e exp(scale * q . k_e)
+ * over the entries e that the row sees; a row that sees none gets out = 0 and
+ * lse = -inf.
+ * q, out: device, row t head h at q + t*q_row_stride + h*head_dim (`dtype`), row
+ *         strides >= H_q*head_dim and multiples of 8, 16-byte aligned; out must
+ *         not overlap q or the cache.
+ * lse:    device float32 [num_q_tokens, H_q] (nullable), natural logarithm.
+ * Lengths or pages out of range set UPF_ERR_INVALID_ARG in the status word:
+ * a request whose cu_q entries are not ascending within [0, num_q_tokens], or
+ * with more than max_q_len rows, is skipped; one with a bad kv_len gets empty
+ * rows; entries of a bad page are not seen.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
+                         const void* q, int64_t q_row_stride, void* out, int64_t out_row_stride, float* lse, void* ws,
+                         size_t ws_bytes, void* stream);
+
 /* Tracing (per-stage device timing).  Stages, in launch order:
  * 0 describe (batch descriptor; upf_select_tokens launches none for batches
  * whose descriptor travels in the kernel parameters), 1 score pass 1, 2 score

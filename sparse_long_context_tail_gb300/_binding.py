@@ -47,6 +47,20 @@ class UpfCompactIO(ctypes.Structure):
                 ("layer_id", c_int32), ("history_cap", c_int32), ("history", c_void_p), ("history_len", c_void_p)]
 
 
+class UpfKvCache(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("num_slots", c_int64), ("num_kv_heads", c_int32), ("head_dim", c_int32),
+                ("k_exp", c_int32), ("v_exp", c_int32)]
+
+
+class UpfKvQuery(ctypes.Structure):
+    _fields_ = [("num_reqs", c_int32), ("num_q_heads", c_int32), ("kv_of_q", POINTER(c_int32)),
+                ("num_q_tokens", c_int32), ("max_q_len", c_int32), ("cu_q", c_void_p), ("kv_len", c_void_p),
+                ("page_table", c_void_p), ("page_stride", c_int64), ("max_pages", c_int32), ("page_size", c_int32),
+                ("window", c_int32), ("sinks", c_int32), ("softmax_scale", c_float)]
+
+
+UPF_BF16, UPF_F16 = 0, 1
+
 _SIGNATURES = {
     "upf_version": ([], c_int),
     "upf_default_params": ([POINTER(UpfParams)], None),
@@ -72,6 +86,15 @@ _SIGNATURES = {
     "upf_revive": ([c_void_p, POINTER(UpfBatch), c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p], c_int),
     "upf_history_kv_len": ([c_void_p, POINTER(UpfBatch), c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p],
                            c_int),
+    "upf_kv_cache_bytes": ([POINTER(UpfKvCache)], c_size_t),
+    "upf_kv_write_workspace_bytes": ([POINTER(UpfKvCache), c_int32], c_size_t),
+    "upf_kv_write": ([c_void_p, POINTER(UpfKvCache), c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
+                      c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "upf_kv_read": ([c_void_p, POINTER(UpfKvCache), c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_void_p,
+                     c_int64, c_void_p], c_int),
+    "upf_kv_attend_workspace_bytes": ([POINTER(UpfKvCache), POINTER(UpfKvQuery)], c_size_t),
+    "upf_kv_attend": ([c_void_p, POINTER(UpfKvCache), POINTER(UpfKvQuery), c_int32, c_void_p, c_int64, c_void_p,
+                       c_int64, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
     "upf_stage_name": ([c_int32], c_char_p),
     "upf_profile_enable": ([c_void_p, c_int32], c_int),
     "upf_profile_read": ([c_void_p, c_void_p, c_void_p, c_int32], c_int),
@@ -131,6 +154,22 @@ def make_compact_io(row_bytes=0, hidden_in=0, hidden_out=0, pos_in=0, pos_out=0,
     return UpfCompactIO(row_bytes, hidden_in or None, hidden_out or None, pos_in or None, pos_out or None,
                         slot_in or None, slot_out or None, kept_index or None, cu_seqlens_out or None,
                         total_kept or None, layer_id, history_cap, history or None, history_len or None)
+
+
+def make_kv_cache(data: int, num_slots: int, num_kv_heads: int, head_dim: int, k_exp: int = 0,
+                  v_exp: int = 0) -> UpfKvCache:
+    return UpfKvCache(data or None, num_slots, num_kv_heads, head_dim, k_exp, v_exp)
+
+
+def make_kv_query(num_reqs: int, num_q_heads: int, num_q_tokens: int, kv_len: int, page_table: int, page_stride: int,
+                  max_pages: int, page_size: int, cu_q: int = 0, max_q_len: int = 1, window: int = 0, sinks: int = 0,
+                  softmax_scale: float = 0.0, kv_of_q: Optional[Sequence[int]] = None):
+    """Build a upf_kv_query; returns (struct, keepalive) -- keep both alive during the call."""
+    kv = None if kv_of_q is None else np.ascontiguousarray(kv_of_q, dtype=np.int32)
+    x = UpfKvQuery(num_reqs, num_q_heads, kv.ctypes.data_as(POINTER(c_int32)) if kv is not None else None,
+                   num_q_tokens, max_q_len, cu_q or None, kv_len or None, page_table or None, page_stride, max_pages,
+                   page_size, window, sinks, softmax_scale)
+    return x, kv
 
 
 # ------------------------------------------------------- entry points (C ABI) --
@@ -221,6 +260,43 @@ def upf_revive(ctx, batch, kept_index, total_kept, rows, row_bytes, full, stream
 def upf_history_kv_len(ctx, batch, history, history_len, history_cap, layer_id, kv_len, stream=0):
     _check(load().upf_history_kv_len(ctx, ctypes.byref(batch), history, history_len, history_cap, layer_id, kv_len,
                                      stream or None))
+
+
+def upf_kv_cache_bytes(cache: UpfKvCache) -> int:
+    n = load().upf_kv_cache_bytes(ctypes.byref(cache))
+    if n == 0:
+        raise UpfError(1, upf_last_error())
+    return n
+
+
+def upf_kv_write_workspace_bytes(cache: UpfKvCache, num_tokens: int) -> int:
+    n = load().upf_kv_write_workspace_bytes(ctypes.byref(cache), num_tokens)
+    if n == 0:
+        raise UpfError(1, upf_last_error())
+    return n
+
+
+def upf_kv_write(ctx, cache, dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens, num_tokens_dev, ws, ws_bytes,
+                 stream=0):
+    _check(load().upf_kv_write(ctx, ctypes.byref(cache), dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens,
+                               num_tokens_dev or None, ws, ws_bytes, stream or None))
+
+
+def upf_kv_read(ctx, cache, dtype, slots, num_tokens, num_tokens_dev, k, k_row_stride, v, v_row_stride, stream=0):
+    _check(load().upf_kv_read(ctx, ctypes.byref(cache), dtype, slots, num_tokens, num_tokens_dev or None, k or None,
+                              k_row_stride, v or None, v_row_stride, stream or None))
+
+
+def upf_kv_attend_workspace_bytes(cache: UpfKvCache, query: UpfKvQuery) -> int:
+    n = load().upf_kv_attend_workspace_bytes(ctypes.byref(cache), ctypes.byref(query))
+    if n == 0:
+        raise UpfError(1, upf_last_error())
+    return n
+
+
+def upf_kv_attend(ctx, cache, query, dtype, q, q_row_stride, out, out_row_stride, lse, ws, ws_bytes, stream=0):
+    _check(load().upf_kv_attend(ctx, ctypes.byref(cache), ctypes.byref(query), dtype, q, q_row_stride, out,
+                                out_row_stride, lse or None, ws, ws_bytes, stream or None))
 
 
 NUM_STAGES = 8

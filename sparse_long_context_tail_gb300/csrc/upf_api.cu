@@ -706,6 +706,94 @@ upf_status launch_compact_all(upf_ctx* ctx, const upf::CompactArgs& ca, cudaStre
   return UPF_OK;
 }
 
+// ------------------------------------------------------------ 4-bit KV cache --
+
+upf_status check_cache(const upf_kv_cache* c, bool need_data) {
+  if (!c) return fail(UPF_ERR_INVALID_ARG, "cache is NULL");
+  if (c->num_slots < 16 || c->num_slots % 16)
+    return fail(UPF_ERR_INVALID_ARG, "num_slots must be a positive multiple of 16 (got %lld)", (long long)c->num_slots);
+  if (c->num_slots > (1LL << 36)) return fail(UPF_ERR_UNSUPPORTED, "num_slots above 2^36");
+  if (c->num_kv_heads < 1 || c->num_kv_heads > upf::kMaxHeads)
+    return fail(UPF_ERR_INVALID_ARG, "num_kv_heads must be in [1, %d] (got %d)", upf::kMaxHeads, c->num_kv_heads);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(UPF_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", c->head_dim);
+  if (c->k_exp < -32 || c->k_exp > 32 || c->v_exp < -32 || c->v_exp > 32)
+    return fail(UPF_ERR_INVALID_ARG, "k_exp and v_exp must be in [-32, 32]");
+  if (need_data && (!c->data || reinterpret_cast<uintptr_t>(c->data) % 128))
+    return fail(UPF_ERR_INVALID_ARG, "cache data must be set and 128-byte aligned");
+  return UPF_OK;
+}
+
+upf_status check_dtype(int32_t dtype) {
+  if (dtype != UPF_BF16 && dtype != UPF_F16) return fail(UPF_ERR_INVALID_ARG, "dtype must be UPF_BF16 or UPF_F16 (got %d)", dtype);
+  return UPF_OK;
+}
+
+// Rows of `heads` heads of head_dim elements.
+upf_status check_rows(const char* name, const void* p, int64_t stride, int heads, int d) {
+  if (!p || !aligned16(p)) return fail(UPF_ERR_INVALID_ARG, "%s must be set and 16-byte aligned", name);
+  if (stride < (int64_t)heads * d || stride % 8)
+    return fail(UPF_ERR_INVALID_ARG, "%s's row stride must be >= heads * head_dim and a multiple of 8 (got %lld)", name,
+                (long long)stride);
+  return UPF_OK;
+}
+
+upf_status check_ws_bytes(const void* ws, size_t have, size_t need) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return fail(UPF_ERR_INVALID_ARG, "workspace must be set and 256-byte aligned");
+  if (have < need) return fail(UPF_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", have, need);
+  return UPF_OK;
+}
+
+upf_status check_tokens(const upf_kv_cache* c, int32_t num_tokens) {
+  if (num_tokens < 0 || num_tokens > (1 << 30)) return fail(UPF_ERR_INVALID_ARG, "num_tokens must be in [0, 2^30]");
+  if ((int64_t)num_tokens * c->num_kv_heads * (c->head_dim / 16) > (1LL << 38))
+    return fail(UPF_ERR_UNSUPPORTED, "too many tokens for one call");
+  return UPF_OK;
+}
+
+upf_status check_query(const upf_kv_cache* c, const upf_kv_query* x, bool need_data) {
+  if (!x) return fail(UPF_ERR_INVALID_ARG, "query is NULL");
+  if (x->num_reqs < 1) return fail(UPF_ERR_INVALID_ARG, "num_reqs must be >= 1 (got %d)", x->num_reqs);
+  if (x->num_reqs > (1 << 20)) return fail(UPF_ERR_UNSUPPORTED, "num_reqs above 2^20");
+  if (x->num_q_heads < 1 || x->num_q_heads % c->num_kv_heads)
+    return fail(UPF_ERR_INVALID_ARG, "need H_q %% H_kv == 0 and both >= 1 (got %d, %d)", x->num_q_heads, c->num_kv_heads);
+  if (x->num_q_heads > upf::kMaxHeads)
+    return fail(UPF_ERR_UNSUPPORTED, "num_q_heads %d above %d", x->num_q_heads, upf::kMaxHeads);
+  if (x->kv_of_q) {
+    int cnt[upf::kMaxHeads] = {};
+    for (int h = 0; h < x->num_q_heads; ++h) {
+      const int g = x->kv_of_q[h];
+      if (g < 0 || g >= c->num_kv_heads) return fail(UPF_ERR_INVALID_ARG, "kv_of_q[%d]=%d out of range", h, g);
+      cnt[g]++;
+    }
+    for (int g = 0; g < c->num_kv_heads; ++g)
+      if (cnt[g] != x->num_q_heads / c->num_kv_heads)
+        return fail(UPF_ERR_INVALID_ARG, "kv_of_q maps %d q heads to kv head %d, need %d", cnt[g], g,
+                    x->num_q_heads / c->num_kv_heads);
+  }
+  if (x->num_q_tokens < 0 || x->num_q_tokens > (1 << 30))
+    return fail(UPF_ERR_INVALID_ARG, "num_q_tokens must be in [0, 2^30]");
+  if (x->max_q_len < 1) return fail(UPF_ERR_INVALID_ARG, "max_q_len must be >= 1 (got %d)", x->max_q_len);
+  if (x->max_q_len > 1024) return fail(UPF_ERR_UNSUPPORTED, "max_q_len %d above 1024", x->max_q_len);
+  if (x->page_size < 16 || x->page_size > 65536 || (x->page_size & (x->page_size - 1)))
+    return fail(UPF_ERR_INVALID_ARG, "page_size must be a power of two from 16 to 65536 (got %d)", x->page_size);
+  if (x->max_pages < 1 || (int64_t)x->max_pages * x->page_size > (1LL << 30))
+    return fail(UPF_ERR_INVALID_ARG, "max_pages must be >= 1 and max_pages * page_size at most 2^30");
+  if (x->window < 0 || x->sinks < 0) return fail(UPF_ERR_INVALID_ARG, "window and sinks must be >= 0");
+  if (!std::isfinite(x->softmax_scale)) return fail(UPF_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (!need_data) return UPF_OK;
+  if (!x->kv_len || !x->page_table) return fail(UPF_ERR_INVALID_ARG, "kv_len and page_table are required");
+  if (x->page_stride < x->max_pages) return fail(UPF_ERR_INVALID_ARG, "page_stride must be >= max_pages");
+  if (!x->cu_q && x->num_q_tokens != x->num_reqs)
+    return fail(UPF_ERR_INVALID_ARG, "without cu_q there is one new token per request (num_q_tokens %d, num_reqs %d)",
+                x->num_q_tokens, x->num_reqs);
+  return UPF_OK;
+}
+
+size_t write_ws_bytes(const upf_kv_cache* c, int32_t num_tokens) {
+  return num_tokens <= upf::kKvFewTokens ? 256 : align256(size_t(c->num_slots) * sizeof(int32_t));
+}
+
 }  // namespace
 
 void upf::set_last_error(const char* msg) { g_last_error = msg ? msg : ""; }
@@ -1046,6 +1134,145 @@ upf_status upf_select_tokens(upf_ctx* ctx, const upf_batch* batch, const upf_par
   UPF_LAUNCH(staged(ctx, kFinalize, s, [&] { return upf::launch_block_means(se, s, true); }), "finalize scores");
   UPF_LAUNCH(staged(ctx, kSelect, s, [&] { return upf::launch_select(se, s, true); }), "select");
   return launch_compact_all(ctx, compact_args(ctx, batch, pl, keep_bits, io, ws), s, true);
+}
+
+size_t upf_kv_cache_bytes(const upf_kv_cache* cache) {
+  if (check_cache(cache, false) != UPF_OK) return 0;
+  return size_t(cache->num_slots / 16) * cache->num_kv_heads * 18 * cache->head_dim;
+}
+
+size_t upf_kv_write_workspace_bytes(const upf_kv_cache* cache, int32_t num_tokens) {
+  if (check_cache(cache, false) != UPF_OK || check_tokens(cache, num_tokens) != UPF_OK) return 0;
+  return write_ws_bytes(cache, num_tokens);
+}
+
+upf_status upf_kv_write(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, const void* k, int64_t k_row_stride,
+                        const void* v, int64_t v_row_stride, const int64_t* slots, int32_t num_tokens,
+                        const int32_t* num_tokens_dev, void* ws, size_t ws_bytes, void* stream) {
+  upf_status st;
+  if ((st = check_cache(cache, true)) != UPF_OK) return st;
+  if ((st = check_dtype(dtype)) != UPF_OK) return st;
+  if ((st = check_tokens(cache, num_tokens)) != UPF_OK) return st;
+  if (num_tokens == 0) return check_ctx(ctx);
+  if ((st = check_rows("k", k, k_row_stride, cache->num_kv_heads, cache->head_dim)) != UPF_OK) return st;
+  if ((st = check_rows("v", v, v_row_stride, cache->num_kv_heads, cache->head_dim)) != UPF_OK) return st;
+  if (!slots) return fail(UPF_ERR_INVALID_ARG, "slots is NULL");
+  if ((st = check_ws_bytes(ws, ws_bytes, write_ws_bytes(cache, num_tokens))) != UPF_OK) return st;
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  DeviceGuard guard(ctx->device);
+  upf::KvWriteArgs a;
+  a.data = static_cast<uint8_t*>(cache->data);
+  a.num_slots = cache->num_slots;
+  a.H = cache->num_kv_heads;
+  a.d = cache->head_dim;
+  a.T = num_tokens;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.slots = slots;
+  a.count = num_tokens_dev;
+  a.k_mul = std::ldexp(1.f, -cache->k_exp);
+  a.v_mul = std::ldexp(1.f, -cache->v_exp);
+  a.owner = num_tokens <= upf::kKvFewTokens ? nullptr : static_cast<int32_t*>(ws);
+  a.status = ctx->status_dev;
+  UPF_LAUNCH(upf::launch_kv_write(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv write");
+  return UPF_OK;
+}
+
+upf_status upf_kv_read(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, const int64_t* slots,
+                       int32_t num_tokens, const int32_t* num_tokens_dev, void* k, int64_t k_row_stride, void* v,
+                       int64_t v_row_stride, void* stream) {
+  upf_status st;
+  if ((st = check_cache(cache, true)) != UPF_OK) return st;
+  if ((st = check_dtype(dtype)) != UPF_OK) return st;
+  if ((st = check_tokens(cache, num_tokens)) != UPF_OK) return st;
+  if (num_tokens == 0) return check_ctx(ctx);
+  if (!k && !v) return fail(UPF_ERR_INVALID_ARG, "k and v are both NULL");
+  if (k && (st = check_rows("k", k, k_row_stride, cache->num_kv_heads, cache->head_dim)) != UPF_OK) return st;
+  if (v && (st = check_rows("v", v, v_row_stride, cache->num_kv_heads, cache->head_dim)) != UPF_OK) return st;
+  if (!slots) return fail(UPF_ERR_INVALID_ARG, "slots is NULL");
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  DeviceGuard guard(ctx->device);
+  upf::KvReadArgs a;
+  a.data = static_cast<const uint8_t*>(cache->data);
+  a.num_slots = cache->num_slots;
+  a.H = cache->num_kv_heads;
+  a.d = cache->head_dim;
+  a.T = num_tokens;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.slots = slots;
+  a.count = num_tokens_dev;
+  a.k_mul = std::ldexp(1.f, cache->k_exp);
+  a.v_mul = std::ldexp(1.f, cache->v_exp);
+  a.status = ctx->status_dev;
+  UPF_LAUNCH(upf::launch_kv_read(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv read");
+  return UPF_OK;
+}
+
+size_t upf_kv_attend_workspace_bytes(const upf_kv_cache* cache, const upf_kv_query* query) {
+  if (check_cache(cache, false) != UPF_OK || check_query(cache, query, false) != UPF_OK) return 0;
+  return upf::kv_attend_workspace_bytes(query->num_reqs, cache->num_kv_heads, query->num_q_heads / cache->num_kv_heads,
+                                        query->max_q_len, cache->head_dim);
+}
+
+upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
+                         const void* q, int64_t q_row_stride, void* out, int64_t out_row_stride, float* lse, void* ws,
+                         size_t ws_bytes, void* stream) {
+  upf_status st;
+  if ((st = check_cache(cache, true)) != UPF_OK) return st;
+  if ((st = check_dtype(dtype)) != UPF_OK) return st;
+  if ((st = check_query(cache, query, true)) != UPF_OK) return st;
+  if (query->num_q_tokens == 0) return check_ctx(ctx);
+  if ((st = check_rows("q", q, q_row_stride, query->num_q_heads, cache->head_dim)) != UPF_OK) return st;
+  if ((st = check_rows("out", out, out_row_stride, query->num_q_heads, cache->head_dim)) != UPF_OK) return st;
+  const int gamma = query->num_q_heads / cache->num_kv_heads;
+  const size_t need = upf::kv_attend_workspace_bytes(query->num_reqs, cache->num_kv_heads, gamma, query->max_q_len,
+                                                     cache->head_dim);
+  if ((st = check_ws_bytes(ws, ws_bytes, need)) != UPF_OK) return st;
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  DeviceGuard guard(ctx->device);
+  upf::KvAttendArgs a;
+  a.data = static_cast<const uint8_t*>(cache->data);
+  a.num_slots = cache->num_slots;
+  a.H = cache->num_kv_heads;
+  a.d = cache->head_dim;
+  a.R = query->num_reqs;
+  a.Hq = query->num_q_heads;
+  a.gamma = gamma;
+  a.num_q = query->num_q_tokens;
+  a.max_q = query->max_q_len;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.q_stride = q_row_stride;
+  a.out_stride = out_row_stride;
+  a.cu_q = query->cu_q;
+  a.kv_len = query->kv_len;
+  a.page_table = query->page_table;
+  a.page_stride = query->page_stride;
+  a.max_pages = query->max_pages;
+  a.page_shift = 0;
+  while ((1 << a.page_shift) < query->page_size) a.page_shift++;
+  a.window = query->window;
+  a.sinks = query->sinks;
+  const float scale = query->softmax_scale > 0.f ? query->softmax_scale : 1.0f / std::sqrt(float(cache->head_dim));
+  a.scale_log2 = std::ldexp(scale * 1.4426950408889634f, cache->k_exp);
+  a.v_mul = std::ldexp(1.f, cache->v_exp);
+  a.status = ctx->status_dev;
+  a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
+  a.ws = ws;
+  int fill[upf::kMaxHeads] = {};
+  for (int h = 0; h < a.Hq; ++h) {
+    const int g = query->kv_of_q ? query->kv_of_q[h] : h / gamma;
+    a.kv_of_q[h] = uint8_t(g);
+    a.qhead[g * gamma + fill[g]++] = uint8_t(h);
+  }
+  UPF_LAUNCH(upf::launch_kv_attend(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv attend");
+  return UPF_OK;
 }
 
 }  // extern "C"

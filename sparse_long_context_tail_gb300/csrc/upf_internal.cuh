@@ -174,6 +174,60 @@ struct HistoryArgs {
   int32_t* kv_len;
 };
 
+// The 4-bit KV cache (layout: kv_layout.cuh).
+constexpr int kKvFewTokens = 1024;   // calls of at most this many tokens write without claiming their slots
+
+struct KvWriteArgs {
+  uint8_t* data;
+  int64_t num_slots;
+  int32_t H, d, T;
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;   // elements between tokens
+  const int64_t* slots;         // [T]
+  const int32_t* count;         // nullable: tokens to write, read on the device
+  float k_mul, v_mul;           // 2^-exp
+  int32_t* owner;               // [num_slots] (nullable: at most kKvFewTokens tokens)
+  int32_t* status;
+};
+
+struct KvReadArgs {
+  const uint8_t* data;
+  int64_t num_slots;
+  int32_t H, d, T;
+  void* k;                      // nullable
+  void* v;                      // nullable
+  int64_t k_stride, v_stride;
+  const int64_t* slots;
+  const int32_t* count;
+  float k_mul, v_mul;           // 2^exp
+  int32_t* status;
+};
+
+struct KvAttendArgs {
+  const uint8_t* data;
+  int64_t num_slots;
+  int32_t H, d, R, Hq, gamma;
+  int32_t num_q, max_q;         // rows of q; most new tokens of a request
+  const void* q;
+  void* out;
+  float* lse;                   // nullable
+  int64_t q_stride, out_stride;
+  const int32_t* cu_q;          // nullable: one new token per request
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t page_stride;
+  int32_t max_pages, page_shift;
+  int32_t window, sinks;        // window 0: none
+  float scale_log2;             // softmax scale * 2^k_exp * log2 e
+  float v_mul;                  // 2^v_exp
+  int32_t* status;
+  long long wait_limit;
+  void* ws;
+  uint8_t kv_of_q[kMaxHeads];   // kv head of each q head
+  uint8_t qhead[kMaxHeads];     // q heads of kv head g at [g*gamma, (g+1)*gamma)
+};
+
 // Programmatic dependent launch.  Kernels launched after the first one of an
 // API call may start while their predecessor is finishing; each kernel lets its
 // own dependent start early and waits for its predecessor (full completion and
@@ -241,5 +295,9 @@ struct GatherListArgs {
 cudaError_t launch_gather_list(const GatherListArgs& a, cudaStream_t s, bool pdl = false);
 cudaError_t launch_revive(const ReviveArgs& a, cudaStream_t s, bool pdl = false);
 cudaError_t launch_history_kv_len(const HistoryArgs& a, cudaStream_t s, bool pdl = false);
+cudaError_t launch_kv_write(const KvWriteArgs& a, bool f16, cudaStream_t s);
+cudaError_t launch_kv_read(const KvReadArgs& a, bool f16, cudaStream_t s);
+cudaError_t launch_kv_attend(const KvAttendArgs& a, bool f16, cudaStream_t s);
+size_t kv_attend_workspace_bytes(int R, int H, int gamma, int max_q, int d);
 
 }  // namespace upf

@@ -1,0 +1,523 @@
+"""The 4-bit KV cache on the GPU against the float64 oracle.
+
+Writing and reading back are exact: every code and scale is the definition's, so
+what is read in bf16 equals the oracle's values bit for bit, and in fp16 its
+rounding.  Attention is compared with a tolerance derived from the arithmetic (`_bound`).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_oracle as K
+from sparse_long_context_tail_gb300 import _binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def make(num_slots, H, d, fill=0xA5, **kw):
+    from sparse_long_context_tail_gb300.kvcache import QuantKVCache
+    c = QuantKVCache(num_slots, H, d, **kw)
+    c.storage.fill_(fill)          # unwritten slots hold rubbish: 0xFF is a NaN scale
+    return c
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g) * scale
+    x *= torch.exp2(torch.randint(-3, 4, shape[:-1] + (1,), generator=g).float())
+    return x.to(dtype).to(DEV)
+
+
+def f64(t):
+    return t.cpu().double().numpy()
+
+
+# ------------------------------------------------------------ write and read --
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,d", [(1, 64), (2, 64), (3, 128), (8, 128), (2, 256)])
+@pytest.mark.parametrize("T", [1, 2, 17, 131])
+def test_what_is_written_is_read_back(T, H, d, dtype):
+    c = make(16 * 20, H, d, k_exp=1, v_exp=-2)
+    before = c.storage.clone()
+    k, v = rand((T, H, d), dtype, 1), rand((T, H, d), dtype, 2)
+    slots = torch.randperm(c.num_slots, generator=torch.Generator().manual_seed(3))[:T]
+    c.write(k, v, slots.to(DEV))
+    want = [K.cache_values(f64(k), 1), K.cache_values(f64(v), -2)]
+    got = [f64(x) for x in c.read(slots.to(DEV))]
+    packed = c.storage.cpu().numpy()
+    for of in range(2):
+        np.testing.assert_array_equal(got[of], want[of])
+        np.testing.assert_array_equal(K.unpack(packed, slots.tolist(), H, d, (1, -2)[of], bool(of)), want[of])
+    for x, w in zip(c.read(slots.to(DEV), dtype=F16), want):
+        np.testing.assert_array_equal(x.cpu().numpy(), w.astype(np.float16))
+    others = torch.ones(c.num_slots, dtype=torch.bool)
+    others[slots] = False
+    rest = others.nonzero().flatten().to(DEV)
+    now = c.storage.clone()
+    c.storage.copy_(before)
+    was = c.read(rest)
+    c.storage.copy_(now)
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(was, c.read(rest)))
+    assert c.status() == 0
+
+
+def test_every_tie_and_border_is_the_definitions():
+    """All 7-bit values against every 4-bit scale: x = m 2^e around each tie and each e4m3 border."""
+    rows = []
+    for top in list(range(64, 128)):                      # amax = top / 16 * 2^e
+        for e in (-9, -6, -1, 0, 3, 7):
+            g = torch.arange(0, 128, 8) * top / 128.0 / 16.0
+            g[0] = top / 16.0
+            rows.append(g * 2.0 ** e * torch.where(torch.arange(16) % 3 == 0, -1.0, 1.0))
+    for sb in range(1, 0x7F):                              # amax = 6 s: the ties themselves
+        s = K.E4M3[sb]
+        rows.append(torch.tensor([6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -.75, -1.25, -1.75, -2.5, -3.5, -5, 0]) * s)
+        if sb > 1:                                         # amax / 6 midway between two scales
+            rows.append(torch.cat([torch.tensor([3 * (s + K.E4M3[sb - 1])]), torch.linspace(-1, 1, 15) * s]))
+    x = torch.stack(rows)
+    x = torch.cat([x, torch.zeros(-len(x) % 8, 16)]).view(-1, 1, 128)
+    for dtype in (BF16, F16):
+        y = x.to(dtype).to(DEV)
+        y = torch.where(torch.isfinite(y), y, torch.zeros_like(y))
+        c = make((len(y) + 15) // 16 * 16, 1, 128)
+        slots = torch.arange(len(y), device=DEV)
+        c.write(y, -y, slots)
+        k, v = c.read(slots)
+        np.testing.assert_array_equal(f64(k), K.cache_values(f64(y), 0))
+        np.testing.assert_array_equal(f64(v), -K.cache_values(f64(y), 0))
+
+
+def test_non_finite_extreme_and_tiny_groups():
+    x = torch.ones(6, 1, 64)
+    x[0, 0, 3], x[1, 0, 17], x[2, 0, 63] = float("nan"), float("inf"), float("-inf")
+    x[3] *= 3e38
+    x[4] *= 1e-39
+    x[5] = 0
+    for exp in (-32, 0, 32):
+        c = make(16, 1, 64, k_exp=exp, v_exp=exp)
+        slots = torch.arange(6, device=DEV)
+        y = x.to(BF16).to(DEV)
+        c.write(y, y, slots)
+        want = K.cache_values(f64(y), exp)
+        assert np.isnan(want).sum() == 48
+        for got in c.read(slots):
+            np.testing.assert_array_equal(f64(got), want)
+        # in fp16 values past its range become infinite, as any rounding to it does
+        with np.errstate(over="ignore"):
+            np.testing.assert_array_equal(c.read(slots, dtype=F16)[0].cpu().numpy(), want.astype(np.float16))
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_a_slot_given_twice_holds_the_last_token(T):
+    H, d = 2, 128
+    c = make(16 * 64, H, d)
+    k, v = rand((T, H, d), BF16, 5), rand((T, H, d), BF16, 6)
+    slots = torch.randint(0, 30 if T == 40 else 1000, (T,), generator=torch.Generator().manual_seed(7))
+    for _ in range(3):
+        c.write(k, v, slots.to(DEV))
+        last = {int(s): t for t, s in enumerate(slots)}
+        at, own = list(last), list(last.values())
+        got = c.read(torch.tensor(at, device=DEV))
+        np.testing.assert_array_equal(f64(got[0]), K.cache_values(f64(k[own]), 0))
+        np.testing.assert_array_equal(f64(got[1]), K.cache_values(f64(v[own]), 0))
+        slots = slots.flip(0)
+    # a slot may be read any number of times
+    many = torch.tensor([at[0]] * 5 + [at[1]], device=DEV)
+    r = c.read(many)[0]
+    assert torch.equal(r[0], r[4]) and c.status() == 0
+
+
+@pytest.mark.parametrize("T", [33, 2000])
+def test_skipped_tokens_and_device_counts(T):
+    H, d, n = 2, 64, T - 7
+    c = make(16 * 200, H, d, fill=0)
+    k, v = rand((T, H, d), F16, 8), rand((T, H, d), F16, 9)
+    slots = torch.randperm(c.num_slots, generator=torch.Generator().manual_seed(1))[:T]
+    used = slots.clone()
+    used[3] = -1
+    used[5] = -(1 << 40)
+    c.write(k, v, used.to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV))
+    want = K.cache_values(f64(k), 0)
+    want[[3, 5]] = 0
+    want[n:] = 0
+    np.testing.assert_array_equal(f64(c.read(slots.to(DEV))[0]), want)
+    out = (torch.full_like(k, 7.0), torch.full_like(v, 7.0))
+    c.read(used.to(DEV), out=out, num_tokens=torch.tensor([n], dtype=torch.int32, device=DEV))
+    want[[3, 5]] = 7
+    want[n:] = 7
+    np.testing.assert_array_equal(f64(out[0]), want)
+    for count in (0, -4):
+        c.write(-k, -v, slots.to(DEV), torch.tensor([count], dtype=torch.int32, device=DEV))
+    c.write(k[:0], v[:0], slots[:0].to(DEV))
+    assert c.read(slots[:0].to(DEV))[0].shape == (0, H, d)
+    want[[3, 5]] = 0
+    want[n:] = 0
+    np.testing.assert_array_equal(f64(c.read(slots.to(DEV))[0]), want)
+    # a count above the tokens given is cut down to them
+    c.write(k, v, slots.to(DEV), torch.tensor([T + 100], dtype=torch.int32, device=DEV))
+    np.testing.assert_array_equal(f64(c.read(slots.to(DEV))[0]), K.cache_values(f64(k), 0))
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("T", [4, 1500])
+def test_slots_past_the_cache_are_reported_and_skipped(T):
+    c = make(1600, 1, 64, fill=0)
+    k = rand((T, 1, 64), BF16, 1)
+    slots = torch.arange(T, device=DEV)
+    slots[2] = 1600
+    c.write(k, k, slots)
+    assert c.status() == 1 and c.status() == 0
+    out = (torch.zeros_like(k), torch.zeros_like(k))
+    c.read(slots, out=out)
+    assert c.status() == 1 and not out[0][2].any()
+    want = K.cache_values(f64(k), 0)
+    want[2] = 0
+    np.testing.assert_array_equal(f64(out[0]), want)
+
+
+def test_strided_rows_and_outputs():
+    T, H, d = 50, 2, 128
+    rows = rand((T, 3 * H, d), BF16, 4)          # one projection's rows: [q | k | v]
+    k, v = rows[:, H:2 * H], rows[:, 2 * H:]
+    c = make(64, H, d)
+    slots = torch.arange(T, device=DEV)
+    c.write(k, v, slots)
+    wide = torch.zeros(T, 3 * H, d, dtype=BF16, device=DEV)
+    c.read(slots, out=(wide[:, :H], wide[:, 2 * H:]))
+    np.testing.assert_array_equal(f64(wide[:, :H]), K.cache_values(f64(k), 0))
+    np.testing.assert_array_equal(f64(wide[:, 2 * H:]), K.cache_values(f64(v), 0))
+    assert not wide[:, H:2 * H].any()
+    with pytest.raises(B.UpfError):              # rows that do not start on 16 bytes
+        off = torch.zeros(T * H * d + 1, dtype=BF16, device=DEV)[1:].view(T, H, d)
+        c.write(off, off, slots)
+
+
+# ------------------------------------------------------------------ attention --
+
+class Batch:
+    """Requests of given lengths in shuffled pages, written through the operator itself."""
+
+    def __init__(self, lens, Hq, H, d, page=16, dtype=BF16, seed=0, k_exp=0, v_exp=0, spare=2, scale=1.0):
+        self.lens, self.page, self.H = list(lens), page, H
+        need = [-(-n // page) for n in lens]
+        total = sum(need) + spare
+        self.cache = make(total * page, H, d, fill=0xFF, k_exp=k_exp, v_exp=v_exp)
+        order = torch.randperm(total, generator=torch.Generator().manual_seed(seed))
+        width = max(max(need), 1)
+        self.table = torch.full((len(lens), width + 1), -1, dtype=torch.int32)
+        at = 0
+        for r, m in enumerate(need):
+            self.table[r, :m] = order[at:at + m].int()
+            at += m
+        slots = [[int(self.table[r, e // page]) * page + e % page for e in range(n)] for r, n in enumerate(lens)]
+        self.slots = torch.tensor(sum(slots, []), dtype=torch.int64)
+        T = len(self.slots)
+        k, v = rand((T, H, d), dtype, seed + 1, 0.5 * scale), rand((T, H, d), dtype, seed + 2)
+        if T:
+            self.cache.write(k, v, self.slots.to(DEV))
+        cut = np.cumsum([0] + self.lens)
+        kk, vv = K.cache_values(f64(k), k_exp), K.cache_values(f64(v), v_exp)
+        self.k = [kk[cut[r]:cut[r + 1]] for r in range(len(lens))]
+        self.v = [vv[cut[r]:cut[r + 1]] for r in range(len(lens))]
+        self.table, self.kv_len = self.table.to(DEV), torch.tensor(self.lens, dtype=torch.int32, device=DEV)
+        self.Hq, self.d, self.dtype = Hq, d, dtype
+
+    def queries(self, news, seed=9, scale=1.0):
+        cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        return rand((int(cu[-1]), self.Hq, self.d), self.dtype, seed, scale), cu
+
+
+def _bound(dtype, ref):
+    """Tolerances (out, lse) per element, from the arithmetic:
+
+    * one rounding to the output type: eps / 2 of the value;
+    * each softmax weight is rounded to f16 once: 2^-11 of it (weights under 2^-26 of the
+      row's reference lose more: at most 2^-39 each, 2^-19 over 2^20 entries);
+    * a logit sums d products in at most 16 matrix steps, each of which may drop 2^-22 of
+      the sum of magnitudes; a query element under 2^-14 of its row's largest may lose
+      2^-25 of that largest; the factor and the exponential add 2^-21 of the logit and of
+      the weight.  delta bounds the logit's error, and weights are off by 2 delta;
+    * the weighted sum takes seen / 16 matrix steps and up to 64 joins of parts, 2^-22 each.
+    """
+    out, lse, spread, reach, flat, seen = ref
+    delta = reach * 2.0 ** -18 + flat * 2.0 ** -24 + reach * 2.0 ** -21 + 2.0 ** -21
+    rel = 2.0 ** -11 + 2.0 ** -19 + 2 * delta + (seen[:, None] / 16 + 64) * 2.0 ** -22
+    finite = np.where(np.isfinite(lse), lse, 0)
+    return (np.abs(out) * (torch.finfo(dtype).eps / 2) * (1 + rel[..., None]) + rel[..., None] * spread
+            + float(torch.finfo(dtype).smallest_normal) * float(torch.finfo(dtype).eps),
+            delta + 2.0 ** -20 + (seen[:, None] / 16 + 64) * 2.0 ** -22 + np.abs(finite) * 2.0 ** -22)
+
+
+def compare(got, ref, dtype):
+    out, lse = f64(got[0]), f64(got[1])
+    b_out, b_lse = _bound(dtype, ref)
+    np.testing.assert_array_equal(np.isneginf(lse), np.isneginf(ref[1]))
+    bad = np.abs(out - ref[0]) > b_out
+    assert np.isfinite(out).all() and not bad.any(), (np.argwhere(bad)[:5], (np.abs(out - ref[0]) / b_out).max())
+    see = np.isfinite(ref[1])
+    assert (np.abs(lse[see] - ref[1][see]) <= b_lse[see]).all(), np.abs(lse[see] - ref[1][see]).max()
+
+
+def check(batch, news, window=0, sinks=0, scale=None, kv_of_q=None, q_scale=1.0, cu=True):
+    q, cu_q = batch.queries(news, scale=q_scale)
+    ref = K.attend(f64(q), batch.k, batch.v, cu_q, window, sinks, scale, kv_of_q)
+    got = batch.cache.attend(q, batch.table, batch.kv_len, batch.page,
+                             cu_q=torch.from_numpy(cu_q).to(DEV) if cu else None, max_q_len=max(max(news), 1),
+                             window=window, sinks=sinks, softmax_scale=scale, kv_of_q=kv_of_q)
+    assert batch.cache.status() == 0
+    compare(got, ref, batch.dtype)
+    return q, got, ref
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,H,d", [(8, 2, 64), (5, 1, 64), (4, 4, 128), (8, 2, 128), (12, 1, 128), (20, 1, 128),
+                                    (16, 2, 256), (4, 2, 256)])
+def test_one_new_token_each(Hq, H, d, dtype):
+    b = Batch([1, 2, 15, 16, 17, 31, 32, 33, 0, 100, 257, 700], Hq, H, d, dtype=dtype, k_exp=1, v_exp=-1)
+    check(b, [1] * 12, cu=False)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_page_sizes(page, d):
+    check(Batch([1, page - 1, page, page + 1, 3 * page + 5], 4, 2, d, page=page), [1] * 5)
+
+
+@pytest.mark.parametrize("Hq,H,d", [(8, 2, 64), (8, 2, 128), (3, 3, 128), (16, 2, 256)])
+@pytest.mark.parametrize("news", [[1, 3, 0, 7, 2], [2, 2, 2, 2, 2], [33, 1, 5, 40, 9]])
+def test_several_new_tokens(news, Hq, H, d):
+    b = Batch([40, 3, 9, 130, 2], Hq, H, d)      # request 4: more new tokens than entries leave rows empty
+    check(b, news)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (33, 4), (64, 16), (100, 300), (5000, 3), (0, 7)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_windows_and_sinks(window, sinks, d):
+    check(Batch([1, 20, 64, 333, 600], 4, 2, d), [1, 1, 2, 3, 1], window=window, sinks=sinks)
+
+
+def test_pages_behind_the_window_may_be_gone():
+    b = Batch([500, 300], 8, 2, 128)
+    news, window, sinks = [2, 1], 40, 3
+    lost = b.table.clone()
+    for r, n in enumerate(b.lens):
+        first = (n - news[r] - window + 1) // 16
+        lost[r, 1:first] = -7
+    b.table = lost
+    check(b, news, window=window, sinks=sinks)
+
+
+def test_scales_head_maps_and_large_and_small_queries():
+    b = Batch([77, 200], 6, 3, 128)
+    check(b, [1, 1], scale=0.5, kv_of_q=[0, 1, 2, 0, 1, 2])
+    check(b, [1, 2], kv_of_q=[2, 2, 1, 1, 0, 0])
+    check(b, [1, 2], q_scale=2.0 ** -60)         # logits of nothing: the mean of the values
+    check(b, [1, 2], q_scale=64.0)               # a few entries take all the weight
+
+
+def test_one_entry_is_given_back_exactly():
+    b = Batch([1, 1], 4, 2, 128)
+    q, got, ref = check(b, [1, 1])
+    np.testing.assert_array_equal(f64(got[0]), ref[0])
+
+
+def test_a_long_request_and_many_requests():
+    check(Batch([30000], 8, 2, 64, page=64), [1])
+    rng = np.random.default_rng(5)
+    check(Batch(rng.integers(0, 60, 300).tolist(), 2, 1, 64), [1] * 300)
+
+
+def test_rows_of_no_request_are_left_alone():
+    b = Batch([40, 50], 4, 2, 128)
+    q, cu = b.queries([1, 2])
+    q = torch.cat([q, rand((3, 4, 128), BF16, 1)])
+    out, lse = torch.full_like(q, 5.0), torch.full((6, 4), 5.0, device=DEV)
+    b.cache.attend(q, b.table, b.kv_len, 16, cu_q=torch.from_numpy(cu).to(DEV), max_q_len=2, out=out, lse=lse)
+    assert (out[3:] == 5).all() and (lse[3:] == 5).all()
+    compare((out[:3], lse[:3]), K.attend(f64(q[:3]), b.k, b.v, cu), BF16)
+
+
+def test_padded_tables_and_strided_rows():
+    b = Batch([40, 50, 9], 4, 2, 64)
+    q, cu = b.queries([1, 1, 1])
+    wide = torch.zeros(3, 12, 64, dtype=BF16, device=DEV)
+    wide[:, 4:8] = q
+    table = torch.full((3, 40), -1, dtype=torch.int32, device=DEV)
+    table[:, :b.table.shape[1]] = b.table
+    o = torch.zeros(3, 12, 64, dtype=BF16, device=DEV)
+    got = b.cache.attend(wide[:, 4:8], table[:, :b.table.shape[1]], b.kv_len, 16, out=o[:, 8:])
+    compare(got, K.attend(f64(q), b.k, b.v, cu), BF16)
+    assert not o[:, :8].any()
+
+
+def test_non_finite_entries_show_only_where_they_are_seen():
+    b = Batch([60, 60], 4, 2, 128)
+    bad = rand((1, 2, 128), BF16, 3)
+    bad[0, 0, 5] = float("nan")
+    b.cache.write(bad, bad, b.slots[20:21].to(DEV))       # entry 20 of request 0, kv head 0
+    q, cu = b.queries([1, 1])
+    got = b.cache.attend(q, b.table, b.kv_len, 16)
+    assert torch.isnan(got.out[0, :2]).all() and torch.isnan(got.lse[0, :2]).all()
+    got2 = b.cache.attend(q, b.table, b.kv_len, 16, window=39, sinks=20)
+    b.k[0][20] = b.v[0][20] = 0
+    compare(got2, K.attend(f64(q), b.k, b.v, cu, 39, 20), BF16)
+    inf = q.clone()
+    inf[1, 0, 0] = float("inf")
+    got3 = b.cache.attend(inf, b.table, b.kv_len, 16, window=39, sinks=20)
+    assert torch.isnan(got3.out[1, 0]).all() and torch.equal(got3.out[1, 1:], got2.out[1, 1:])
+
+
+def test_bad_tables_are_reported_and_touch_nothing_else():
+    b = Batch([40, 50, 60], 4, 2, 128)
+    q, cu = b.queries([1, 1, 1])
+    good = K.attend(f64(q), b.k, b.v, cu)
+    for page in (-1, 10 ** 6, 2 ** 31 - 1):
+        t = b.table.clone()
+        t[1, 1] = page                           # entries 16..31 of request 1 are not seen
+        got = b.cache.attend(q, t, b.kv_len, 16)
+        assert b.cache.status() == 1 and b.cache.status() == 0
+        cut = [b.k[0], np.delete(b.k[1], range(16, 32), 0), b.k[2]], [b.v[0], np.delete(b.v[1], range(16, 32), 0), b.v[2]]
+        compare(got, K.attend(f64(q), *cut, cu), BF16)
+    for n in (-1, 16 * b.table.shape[1] + 1, 2 ** 31 - 1):
+        kv = b.kv_len.clone()
+        kv[1] = n                                # an empty row
+        got = b.cache.attend(q, b.table, kv, 16)
+        assert b.cache.status() == 1
+        ref = [x.copy() for x in good]
+        ref[0][1], ref[1][1] = 0, -np.inf
+        compare(got, ref, BF16)
+    for wrong in ([0, 2, 1, 3], [0, -1, 2, 3], [0, 1, 2, 9], [0, 0, 3, 3]):
+        out, lse = torch.full_like(q, 5.0), torch.full((3, 4), 5.0, device=DEV)
+        b.cache.attend(q, b.table, b.kv_len, 16, cu_q=torch.tensor(wrong, dtype=torch.int32, device=DEV), max_q_len=2,
+                       out=out, lse=lse)
+        assert b.cache.status() == 1
+
+
+def test_results_repeat_bit_for_bit():
+    b = Batch([3000, 17, 900], 8, 2, 128)
+    q, cu = b.queries([2, 1, 2])
+    cu = torch.from_numpy(cu).to(DEV)
+    first = b.cache.attend(q, b.table, b.kv_len, 16, cu_q=cu, max_q_len=2)
+    for _ in range(5):
+        again = b.cache.attend(q, b.table, b.kv_len, 16, cu_q=cu, max_q_len=2)
+        assert torch.equal(first.out, again.out) and torch.equal(first.lse, again.lse)
+
+
+def test_two_captured_steps_and_an_eager_one():
+    """Write and attend captured twice on one cache's stream; lengths change between replays."""
+    b = Batch([300, 40], 8, 2, 128)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    q, cu = b.queries([1, 1])
+    k, v = rand((2, 2, 128), BF16, 31), rand((2, 2, 128), BF16, 32)
+    slots = torch.full((2,), -1, dtype=torch.int64, device=DEV)
+    graphs, outs = [], []
+    with torch.cuda.stream(stream):
+        for _ in range(2):
+            b.cache.write(k, v, slots)
+            b.cache.attend(q, b.table, b.kv_len, 16)
+        for window in (0, 33):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                b.cache.write(k, v, slots)
+                outs.append(b.cache.attend(q, b.table, b.kv_len, 16, window=window))
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for step in range(3):
+        # replace the last entry of each request, then look at fewer entries every step
+        lens = [300 - 7 * step, 40 - step]
+        b.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        k.copy_(rand((2, 2, 128), BF16, 40 + step))
+        cut = [0, 300]
+        at = [cut[r] + lens[r] - 1 for r in range(2)]
+        slots.copy_(b.slots[at])
+        for r in range(2):
+            b.k[r][lens[r] - 1] = K.cache_values(f64(k[r]), 0)
+            b.v[r][lens[r] - 1] = K.cache_values(f64(v[r]), 0)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        kk, vv = [b.k[r][:lens[r]] for r in range(2)], [b.v[r][:lens[r]] for r in range(2)]
+        for out, window in zip(outs, (0, 33)):
+            compare(out, K.attend(f64(q), kk, vv, cu, window), BF16)
+        compare(b.cache.attend(q, b.table, b.kv_len, 16), K.attend(f64(q), kk, vv, cu), BF16)
+
+
+def test_entries_far_into_a_large_cache():
+    """Byte offsets past 2^32: 4.8 GB of slots, the pages at its end."""
+    from sparse_long_context_tail_gb300.kvcache import QuantKVCache
+    H, d = 8, 256
+    c = QuantKVCache(2 ** 21, H, d)
+    T = 40
+    slots = c.num_slots - 64 + torch.arange(T, device=DEV)
+    k, v = rand((T, H, d), BF16, 1), rand((T, H, d), BF16, 2)
+    c.write(k, v, slots)
+    np.testing.assert_array_equal(f64(c.read(slots)[0]), K.cache_values(f64(k), 0))
+    q = rand((1, 16, d), BF16, 3)
+    table = torch.arange(c.num_slots // 16 - 4, c.num_slots // 16, device=DEV, dtype=torch.int32)[None]
+    got = c.attend(q, table, torch.tensor([T], dtype=torch.int32, device=DEV), 16)
+    compare(got, K.attend(f64(q), [K.cache_values(f64(k), 0)], [K.cache_values(f64(v), 0)], [0, 1]), BF16)
+
+
+# ---------------------------------------------------- after the selection path --
+
+def test_selected_tokens_are_written_at_their_slots_and_attended():
+    """select_tokens -> the kept rows' K and V into the cache at slot_out -> the history's KV lengths -> attention."""
+    from sparse_long_context_tail_gb300 import workload as wl
+    from sparse_long_context_tail_gb300.selector import TokenSelector
+    spec = wl.WorkloadSpec("kv", [900, 0, 1500], 8, 2, 128, 256, planted=[2, 0, 3], seed=31)
+    w = wl.generate(spec)
+    cu = w.cu_seqlens
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    k_full = up(w.k_bits.view(np.int16)).view(BF16)
+    hidden = rand((w.total_tokens, 2 * 128), BF16, 3)          # stands for the rows the next layer projects V from
+    R, cap = 3, 2
+    hist, hlen = torch.zeros((R, cap, 2), dtype=torch.int32, device=DEV), torch.zeros(R, dtype=torch.int32, device=DEV)
+    # every request has its own run of pages; a kept token's slot is where its page and offset are
+    page = 32
+    start = np.cumsum([0] + [-(-int(n) // page) for n in np.diff(cu)])
+    table = torch.full((R, int(np.diff(start).max())), -1, dtype=torch.int32)
+    perm = torch.randperm(int(start[-1]), generator=torch.Generator().manual_seed(2))
+    for r in range(R):
+        table[r, :start[r + 1] - start[r]] = perm[start[r]:start[r + 1]].int()
+    sel = TokenSelector(0)
+    out = sel.select_tokens(up(w.q_full_bits().view(np.int16)).view(BF16), k_full, cu, up(cu), 8, 2, 128, hidden,
+                            layer_id=4, history=hist, history_len=hlen,
+                            params=B.make_params(128, 64, 128, 128, 0.9))
+    cu2 = out.cu_seqlens_out.cpu().numpy()
+    total = int(out.total_kept)
+    kept = out.kept_index.long()
+    kept[total:] = 0
+    slots = torch.full((w.total_tokens,), 1, dtype=torch.int64)      # rows past total_kept: a slot that must not change
+    for r in range(R):
+        e = torch.arange(int(cu2[r + 1] - cu2[r]))
+        slots[cu2[r]:cu2[r + 1]] = table[r, e // page].long() * page + e % page
+    c = make(int(start[-1]) * page, 2, 128)
+    k, v = k_full[kept], out.hidden_out.view(-1, 2, 128)
+    c.write(k, v, slots.to(DEV), out.total_kept)                    # no host read of the count
+    kv = torch.empty(R, dtype=torch.int32, device=DEV)
+    cu_dev = up(cu)
+    batch, keep = B.make_batch(cu_dev.data_ptr(), cu, 8, 2, 128)
+    B.upf_history_kv_len(sel.ctx, batch, hist.data_ptr(), hlen.data_ptr(), cap, 4, kv.data_ptr(),
+                         torch.cuda.current_stream().cuda_stream)
+    q = rand((R, 8, 128), BF16, 8)
+    got = c.attend(q, table.to(DEV), kv, page, window=256, sinks=128)
+    assert sel.status() == 0 and c.status() == 0
+    assert kv.tolist() == np.diff(cu2).tolist() and total < w.total_tokens
+    kk, vv = K.cache_values(f64(k[:total]), 0), K.cache_values(f64(v[:total]), 0)
+    ref = K.attend(f64(q), [kk[cu2[r]:cu2[r + 1]] for r in range(R)], [vv[cu2[r]:cu2[r + 1]] for r in range(R)],
+                   [0, 1, 2, 3], 256, 128)
+    compare(got, ref, BF16)
+    back = c.read(slots[:total].to(DEV))
+    np.testing.assert_array_equal(f64(back[0]), kk)
+    sel.close()
