@@ -100,12 +100,12 @@ def attend(q: np.ndarray, k: Sequence[np.ndarray], v: Sequence[np.ndarray], cu_q
            sinks: int = 0, scale: Optional[float] = None, kv_of_q: Optional[Sequence[int]] = None):
     """out, lse and the row's bounds of the tolerances: q [N, H_q, d]; k[r], v[r]: [n_r, H_kv, d].
 
-    ``spread`` [N, H_q, d] = sum_e p_e |v_e|; ``reach`` [N, H_q] = scale * max_e sum |q| |k_e|;
+    ``spread`` [N, H_q, d] = sum_e p_e |v_e|; ``total`` [N, H_q, d] = sum_e |v_e|; ``reach`` [N, H_q] = scale * max_e sum |q| |k_e|;
     ``flat`` [N, H_q] = scale * max|q| * max_e sum |k_e|; ``seen`` [N]: entries."""
     q = np.asarray(q, dtype=np.float64)
     N, Hq, d = q.shape
     scale = d ** -0.5 if scale is None else scale
-    out, spread = np.zeros((N, Hq, d)), np.zeros((N, Hq, d))
+    out, spread, total = (np.zeros((N, Hq, d)) for _ in range(3))
     lse, reach, flat = np.full((N, Hq), -np.inf), np.zeros((N, Hq)), np.zeros((N, Hq))
     seen = np.zeros(N, dtype=np.int64)
     for r in range(len(cu_q) - 1):
@@ -125,6 +125,7 @@ def attend(q: np.ndarray, k: Sequence[np.ndarray], v: Sequence[np.ndarray], cu_q
                 w /= w.sum()
                 out[a + i, h] = w @ ve
                 spread[a + i, h] = w @ np.abs(ve)
+                total[a + i, h] = np.abs(ve).sum(0)
                 reach[a + i, h] = scale * (np.abs(ke) @ np.abs(row)).max()
                 flat[a + i, h] = scale * np.abs(row).max() * np.abs(ke).sum(1).max()
-    return out, lse, spread, reach, flat, seen
+    return out, lse, spread, total, reach, flat, seen

@@ -99,6 +99,17 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, lo
   return true;
 }
 
+// mbar_wait_idle whose first look does not suspend either, so that a short limit
+// is kept to about `ns`.
+__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, long long limit, uint32_t ns) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_hint(bar, parity, ns)) {
+    if (clock64() - t0 > limit) return false;
+  }
+  return true;
+}
+
 // ----------------------------------------------------------------- TMA ----
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
@@ -113,6 +124,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Untiled copy global -> shared: both addresses 16-byte aligned, size a multiple of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
       : "memory");
 }
 

@@ -712,7 +712,7 @@ upf_status check_cache(const upf_kv_cache* c, bool need_data) {
   if (!c) return fail(UPF_ERR_INVALID_ARG, "cache is NULL");
   if (c->num_slots < 16 || c->num_slots % 16)
     return fail(UPF_ERR_INVALID_ARG, "num_slots must be a positive multiple of 16 (got %lld)", (long long)c->num_slots);
-  if (c->num_slots > (1LL << 36)) return fail(UPF_ERR_UNSUPPORTED, "num_slots above 2^36");
+  if (c->num_slots > (1LL << 35)) return fail(UPF_ERR_UNSUPPORTED, "num_slots above 2^35");
   if (c->num_kv_heads < 1 || c->num_kv_heads > upf::kMaxHeads)
     return fail(UPF_ERR_INVALID_ARG, "num_kv_heads must be in [1, %d] (got %d)", upf::kMaxHeads, c->num_kv_heads);
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
@@ -1215,8 +1215,7 @@ upf_status upf_kv_read(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, c
 
 size_t upf_kv_attend_workspace_bytes(const upf_kv_cache* cache, const upf_kv_query* query) {
   if (check_cache(cache, false) != UPF_OK || check_query(cache, query, false) != UPF_OK) return 0;
-  return upf::kv_attend_workspace_bytes(query->num_reqs, cache->num_kv_heads, query->num_q_heads / cache->num_kv_heads,
-                                        query->max_q_len, cache->head_dim);
+  return upf::kv_attend_workspace_bytes(query->num_q_heads / cache->num_kv_heads, query->max_q_len, cache->head_dim);
 }
 
 upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
@@ -1230,8 +1229,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   if ((st = check_rows("q", q, q_row_stride, query->num_q_heads, cache->head_dim)) != UPF_OK) return st;
   if ((st = check_rows("out", out, out_row_stride, query->num_q_heads, cache->head_dim)) != UPF_OK) return st;
   const int gamma = query->num_q_heads / cache->num_kv_heads;
-  const size_t need = upf::kv_attend_workspace_bytes(query->num_reqs, cache->num_kv_heads, gamma, query->max_q_len,
-                                                     cache->head_dim);
+  const size_t need = upf::kv_attend_workspace_bytes(gamma, query->max_q_len, cache->head_dim);
   if ((st = check_ws_bytes(ws, ws_bytes, need)) != UPF_OK) return st;
   if ((st = check_ctx(ctx)) != UPF_OK) return st;
   DeviceGuard guard(ctx->device);
@@ -1257,7 +1255,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   a.max_pages = query->max_pages;
   a.page_shift = 0;
   while ((1 << a.page_shift) < query->page_size) a.page_shift++;
-  a.window = query->window;
+  a.window = query->window < (1 << 30) ? query->window : 0;   // no request has 2^30 entries behind a query
   a.sinks = query->sinks;
   const float scale = query->softmax_scale > 0.f ? query->softmax_scale : 1.0f / std::sqrt(float(cache->head_dim));
   a.scale_log2 = std::ldexp(scale * 1.4426950408889634f, cache->k_exp);
@@ -1268,7 +1266,6 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   int fill[upf::kMaxHeads] = {};
   for (int h = 0; h < a.Hq; ++h) {
     const int g = query->kv_of_q ? query->kv_of_q[h] : h / gamma;
-    a.kv_of_q[h] = uint8_t(g);
     a.qhead[g * gamma + fill[g]++] = uint8_t(h);
   }
   UPF_LAUNCH(upf::launch_kv_attend(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv attend");

@@ -224,7 +224,6 @@ struct KvAttendArgs {
   int32_t* status;
   long long wait_limit;
   void* ws;
-  uint8_t kv_of_q[kMaxHeads];   // kv head of each q head
   uint8_t qhead[kMaxHeads];     // q heads of kv head g at [g*gamma, (g+1)*gamma)
 };
 
@@ -298,6 +297,6 @@ cudaError_t launch_history_kv_len(const HistoryArgs& a, cudaStream_t s, bool pdl
 cudaError_t launch_kv_write(const KvWriteArgs& a, bool f16, cudaStream_t s);
 cudaError_t launch_kv_read(const KvReadArgs& a, bool f16, cudaStream_t s);
 cudaError_t launch_kv_attend(const KvAttendArgs& a, bool f16, cudaStream_t s);
-size_t kv_attend_workspace_bytes(int R, int H, int gamma, int max_q, int d);
+size_t kv_attend_workspace_bytes(int gamma, int max_q, int d);
 
 }  // namespace upf

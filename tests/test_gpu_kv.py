@@ -240,19 +240,22 @@ def _bound(dtype, ref):
     """Tolerances (out, lse) per element, from the arithmetic:
 
     * one rounding to the output type: eps / 2 of the value;
-    * each softmax weight is rounded to f16 once: 2^-11 of it (weights under 2^-26 of the
-      row's reference lose more: at most 2^-39 each, 2^-19 over 2^20 entries);
+    * each softmax weight is rounded to f16 once, as 2^12 times its ratio to a reference that
+      is at most the row's largest weight: half a step is 2^-11 of it, or, under the smallest
+      normal number 2^-14, half of the fixed step 2^-24, which is 2^-25 / 2^12 = 2^-37 of the
+      reference.  A normalised weight is thus off by 2^-11 of itself and 2^-37, and the sum by
+      2^-11 sum p |v| + 2^-37 sum |v| (the second shows where the heavy entries hold zeros);
     * a logit sums d products in at most 16 matrix steps, each of which may drop 2^-22 of
       the sum of magnitudes; a query element under 2^-14 of its row's largest may lose
       2^-25 of that largest; the factor and the exponential add 2^-21 of the logit and of
       the weight.  delta bounds the logit's error, and weights are off by 2 delta;
     * the weighted sum takes seen / 16 matrix steps and up to 64 joins of parts, 2^-22 each.
     """
-    out, lse, spread, reach, flat, seen = ref
+    out, lse, spread, total, reach, flat, seen = ref
     delta = reach * 2.0 ** -18 + flat * 2.0 ** -24 + reach * 2.0 ** -21 + 2.0 ** -21
-    rel = 2.0 ** -11 + 2.0 ** -19 + 2 * delta + (seen[:, None] / 16 + 64) * 2.0 ** -22
+    rel = 2.0 ** -11 + 2 * delta + (seen[:, None] / 16 + 64) * 2.0 ** -22
     finite = np.where(np.isfinite(lse), lse, 0)
-    return (np.abs(out) * (torch.finfo(dtype).eps / 2) * (1 + rel[..., None]) + rel[..., None] * spread
+    return (np.abs(out) * (torch.finfo(dtype).eps / 2) * (1 + rel[..., None]) + rel[..., None] * spread + 2.0 ** -37 * total
             + float(torch.finfo(dtype).smallest_normal) * float(torch.finfo(dtype).eps),
             delta + 2.0 ** -20 + (seen[:, None] / 16 + 64) * 2.0 ** -22 + np.abs(finite) * 2.0 ** -22)
 
@@ -261,10 +264,12 @@ def compare(got, ref, dtype):
     out, lse = f64(got[0]), f64(got[1])
     b_out, b_lse = _bound(dtype, ref)
     np.testing.assert_array_equal(np.isneginf(lse), np.isneginf(ref[1]))
-    bad = np.abs(out - ref[0]) > b_out
-    assert np.isfinite(out).all() and not bad.any(), (np.argwhere(bad)[:5], (np.abs(out - ref[0]) / b_out).max())
+    over = np.abs(out - ref[0]) / b_out
+    bad = np.argwhere(~(over <= 1))
+    assert len(bad) == 0, f"{len(bad)} of {over.size} outputs, first {bad[:4].tolist()}, up to {np.nanmax(over):.3g} of the bound"
     see = np.isfinite(ref[1])
-    assert (np.abs(lse[see] - ref[1][see]) <= b_lse[see]).all(), np.abs(lse[see] - ref[1][see]).max()
+    over = np.abs(lse[see] - ref[1][see]) / b_lse[see]
+    assert (over <= 1).all(), f"lse: {np.nanmax(over):.3g} of the bound"
 
 
 def check(batch, news, window=0, sinks=0, scale=None, kv_of_q=None, q_scale=1.0, cu=True):
@@ -521,3 +526,21 @@ def test_selected_tokens_are_written_at_their_slots_and_attended():
     back = c.read(slots[:total].to(DEV))
     np.testing.assert_array_equal(f64(back[0]), kk)
     sel.close()
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_cache_recovers():
+    """The copies' waits limited to one SM cycle.  Every warp streams more tiles than its ring holds (the many
+    entries lie in the same few pages), so some record is not there that soon: the kernel reports it, waits for its
+    own copies and returns, and the next call is right."""
+    b = Batch([500, 300], 8, 4, 128)
+    q, cu = b.queries([1, 1])
+    n = 1 << 20
+    table = b.table[:1, :16].repeat(2, n // 256)
+    kv = torch.full((2,), n, dtype=torch.int32, device=DEV)
+    B.upf_set_wait_limit(b.cache.ctx, 1)
+    b.cache.attend(q, table, kv, 16)
+    assert b.cache.status() == 6
+    B.upf_set_wait_limit(b.cache.ctx, 0)
+    check(b, [1, 1])
+    b.cache.attend(q, table, kv, 16)
+    assert b.cache.status() == 0
