@@ -17,14 +17,15 @@
 //
 // Work.  A unit is (request, kv head, chunk of kRows rows); its tiles are the
 // 32-entry runs that some row sees.  All units' tiles, in order, are dealt out to
-// the CTAs in equal shares, from the lengths in device memory: ragged batches
+// the workers in equal shares, from the lengths in device memory: ragged batches
 // balance themselves and a captured call stays valid when the lengths change.  A
-// CTA's warps take its tiles in turn, each with its own ring of records filled by
-// bulk copies (two records of 18 d bytes a tile), its own running reference and
-// sums; at the end of a unit the CTA joins its warps through shared memory.  A
-// unit that lies in one CTA's share is written out at once; others leave a part
-// (reference, sum, weighted sum, all fp32) per CTA in the workspace, which
-// kv_attend_join_kernel adds up in a fixed order, so results repeat bit for bit.
+// worker is a CTA, whose warps take its tiles in turn and are joined through shared
+// memory, or, where units are short, a single warp that shares nothing.  Every
+// warp has its own ring of records filled by bulk copies (two records of 18 d
+// bytes a tile), its own reference and sums.  A unit that lies in one worker's
+// share is written out at once; others leave a part (reference, sum, weighted sum,
+// all fp32) per worker in the workspace, which kv_attend_join_kernel adds up in a
+// fixed order, so results repeat bit for bit.
 //
 // Arithmetic.  A code times its scale has at most six significant bits and is
 // exact in f16, and so is a query after division by the power of two of its
@@ -35,6 +36,7 @@
 // running maximum by 2^3, so that weights down to 2^-26 of the reference keep all
 // their bits.
 #include <cfloat>
+#include <climits>
 
 #include "kv_layout.cuh"
 #include "sm100_ptx.cuh"
@@ -44,7 +46,7 @@ namespace upf {
 
 namespace {
 
-constexpr int kWarps = 4;        // of a CTA
+constexpr int kWarps = 8;        // of a CTA
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;        // entries per tile (two records)
 constexpr float kWeightExp = 12.f;   // weights are 2^(x - m + 12)
@@ -94,57 +96,82 @@ __device__ __forceinline__ int chunks_of(const KvAttendArgs& a, const Request& x
   return (x.q_len * a.gamma + rows - 1) / rows;
 }
 
-// Tiles of all requests up to the first that a thread looks at, and the total.
-// Thread i looks at requests [i * per, (i + 1) * per).
-template <int kCount>
-__device__ long long scan_tiles(const KvAttendArgs& a, int rows, int per, long long (&warp_sums)[kCount / 32],
-                                long long& total) {
-  long long mine = 0;
+// Cost of a unit in the dealing, in tiles, beside its tiles: the rows' load, the
+// first copies' latency and the writing out.
+constexpr int kUnitCostCta = 16, kUnitCostWarp = 4;
+// Workers are warps where units have fewer tiles than this on average.
+constexpr int kShortUnit = 24;
+
+// How the tiles are dealt out.  Along the dealing a unit takes cost + tiles places.
+struct Deal {
+  bool warps;          // a worker is a warp
+  int cost;            // of a unit
+  long long total;     // places of all units
+  long long share;     // places of a worker
+};
+
+// Each thread looks at requests [i * per, (i + 1) * per); `before` are the places
+// of the requests before them.
+__device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&warp_sums)[kWarps], long long& before) {
+  long long tiles = 0, units = 0;
   for (int j = 0; j < per; ++j) {
     const int r = threadIdx.x * per + j;
     if (r >= a.R) break;
     const Request x = load_request(a, r);
-    mine += (long long)x.tiles * a.H * chunks_of(a, x, rows);
+    if (x.tiles == 0) continue;
+    const long long u = (long long)a.H * chunks_of(a, x, rows);
+    units += u;
+    tiles += u * x.tiles;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = mine;
+  long long t = tiles, u = units;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, s);
-    if (lane >= s) incl += y;
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, t, s), z = __shfl_up_sync(0xFFFFFFFFu, u, s);
+    if (lane >= s) {
+      t += y;
+      u += z;
+    }
   }
-  if (lane == 31) warp_sums[warp] = incl;
+  if (lane == 31) warp_sums[warp] = make_longlong2(t, u);
   __syncthreads();
-  long long before = incl - mine;
-  total = 0;
+  t -= tiles;
+  u -= units;
+  long long all_t = 0, all_u = 0;
 #pragma unroll
-  for (int w = 0; w < kCount / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      t += warp_sums[w].x;
+      u += warp_sums[w].y;
+    }
+    all_t += warp_sums[w].x;
+    all_u += warp_sums[w].y;
   }
-  return before;
+  Deal d;
+  d.warps = all_t < all_u * kShortUnit;
+  d.cost = d.warps ? kUnitCostWarp : kUnitCostCta;
+  d.total = all_t + all_u * d.cost;
+  before = t + u * d.cost;
+  const long long workers = d.warps ? (long long)gridDim.x * kWarps : gridDim.x;
+  d.share = max((d.total + workers - 1) / workers, (long long)(d.warps ? 1 : kWarps));
+  return d;
 }
 
-// Tiles per CTA: an equal share, and at least one for every warp.
-__device__ __forceinline__ long long share_of(long long total, int ctas) {
-  const long long s = (total + ctas - 1) / ctas;
-  return s < kWarps ? kWarps : s;
-}
-
-// The workspace.  A CTA works on at most two units that others work on too: the
-// one its share begins in the middle of, and the one that goes on after its
-// share.  The part of the latter (or of a unit that does both) is at 2 c + 1, that
-// of the former at 2 c, and the CTAs c0 .. c1 - 1 of a shared unit, for which it is
-// the latter, note it for the join.
+// The workspace.  A worker has at most two units that others work on too: the one
+// its share begins in the middle of, and the one that goes on after its share.
+// The part of the latter (or of a unit that does both) is at 2 w + 1, that of the
+// former at 2 w.  The workers first .. last - 1 of a shared unit, for which it is the
+// latter, note it for the join, each warp of theirs its portion.
 struct Shared {
-  int c0, c1;             // CTAs of the unit (c0 < 0: no unit goes on after this CTA's share)
+  int first, last;        // workers of the unit (first < 0: nothing to join)
   int h, row0, rows, q0;  // kv head, first row of the chunk, rows of the request, its first row in q
+  int portion, portions;
 };
 
 struct Parts {
-  float* o;         // [2 ctas][rows][d]
-  float2* ml;       // [2 ctas][rows]: reference, sum
-  Shared* shared;   // [ctas]
+  float* o;         // [2 * workers][rows][d]
+  float2* ml;       // [2 * workers][rows]: reference, sum
+  Shared* shared;   // [warps of the grid]
 };
 
 // ------------------------------------------------------------ main kernel --
@@ -157,13 +184,14 @@ struct Shape {
   static constexpr int kSteps = kPart / 16;            // mma steps over the dims of a part, and dim tiles of it
   static constexpr int kRecord = kv::record_bytes(kDim);
   static constexpr int kStage = 2 * kRecord;
-  static constexpr int kStages = kDim == 64 ? 4 : 2;
+  static constexpr int kCtasPerSm = kDim * NT <= 128 ? 2 : 1;
+  static constexpr int kStages = kDim == 64 ? 4 : kDim == 128 ? 2 * NT : 2;
   static constexpr bool kQueryInSmem = kDim * NT > 256;
-  static constexpr int kCtasPerSm = kDim == 64 ? 4 : kDim == 128 ? (NT == 1 ? 4 : 3) : 2;
   static constexpr int kJoinRow = kPart + 4;           // floats; the pad spreads the rows over the banks
   static constexpr int kJoinBytes = kWarps * kRows * kJoinRow * 4;
-  static constexpr int kQueryBytes = kQueryInSmem ? kRows * kDim * 2 : 0;
-  static constexpr int kSmem = kWarps * kStages * kStage + kJoinBytes + kQueryBytes;
+  // queries that do not fit the registers lie in the warp's own part of the join buffer
+  static_assert(!kQueryInSmem || kRows * kDim * 2 <= kRows * kJoinRow * 4, "queries fit a warp's join rows");
+  static constexpr int kSmem = kWarps * kStages * kStage + kJoinBytes;
   static constexpr int kCtas = kCtasPerSm * kPlanSMs;
 };
 
@@ -180,8 +208,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+__device__ __forceinline__ __half2 as_half2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(as_half2(a), b);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -193,36 +223,30 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // (x & m) | (y & ~m)
 __device__ __forceinline__ uint32_t merge_bits(uint32_t x, uint32_t y, uint32_t m) { return (x & m) | (y & ~m); }
 
-// Where in the tiles of all units a CTA or warp stands.
-struct Cursor {
+// A unit in the dealing.
+struct Unit {
   int r, h, c;        // request, kv head, chunk
-  int t, end;         // tile of the unit, and the end of this CTA's tiles of it
-  long long left;     // tiles of the CTA's share from t on
+  long long place;    // its first place
   Request x;
 };
 
-// Enter the unit at (r, h, c) from tile t; units without tiles are passed over.
-__device__ __forceinline__ void enter(const KvAttendArgs& a, Cursor& k, int rows) {
-  while (k.left > 0 && k.r < a.R) {
-    if (k.c == 0 && k.h == 0) k.x = load_request(a, k.r);
-    if (k.x.tiles > 0 && k.c < chunks_of(a, k.x, rows)) {
-      k.end = int(min((long long)k.x.tiles, k.t + k.left));
+__device__ __forceinline__ void next_unit(const KvAttendArgs& a, Unit& u, int cost, int rows) {
+  u.place += u.x.tiles + cost;
+  if (++u.c < chunks_of(a, u.x, rows)) return;
+  u.c = 0;
+  if (++u.h < a.H) return;
+  u.h = 0;
+  do {
+    if (++u.r >= a.R) {
+      u.place = LLONG_MAX;
       return;
     }
-    k.c = 0;
-    if (++k.h == a.H || k.x.tiles == 0 || k.x.q_len == 0) {
-      k.h = 0;
-      ++k.r;
-    }
-  }
-  k.left = 0;
+    u.x = load_request(a, u.r);
+  } while (u.x.tiles == 0);
 }
 
-__device__ __forceinline__ void next_unit(const KvAttendArgs& a, Cursor& k, int from, int rows) {
-  k.left -= k.end - from;
-  k.t = 0;
-  ++k.c;
-  enter(a, k, rows);
+__device__ __forceinline__ float lse_of(float top, float all) {
+  return all == 0.f ? -INFINITY : (top - kWeightExp + log2f(all)) * kLn2;
 }
 
 template <typename T, int kDim, int NT>
@@ -230,19 +254,40 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   using S = Shape<kDim, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][S::kStages];
-  __shared__ long long warp_sums[kWarps];
-  __shared__ Cursor start;
-  __shared__ float sh_m[kWarps][S::kRows], sh_l[kWarps][S::kRows];
+  __shared__ longlong2 warp_sums[kWarps];
+  __shared__ Unit starts[kWarps];
+  __shared__ float sh_m[kWarps][S::kRows], sh_l[kWarps][S::kRows], sh_top[S::kRows], sh_all[S::kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   pdl_trigger();
 
-  // ---- this CTA's share
+  // ---- this worker's share
   const int per = (a.R + kThreads - 1) / kThreads;
-  long long total;
-  const long long before = scan_tiles<kThreads>(a, S::kRows, per, warp_sums, total);
-  const long long share = share_of(total, gridDim.x);
-  const long long first = blockIdx.x * share;
+  long long before;
+  const Deal deal = deal_out(a, S::kRows, per, warp_sums, before);
+  const int group = deal.warps ? 1 : kWarps, rank = deal.warps ? 0 : warp;   // warps of a worker, and which this is
+  const int worker = deal.warps ? blockIdx.x * kWarps + warp : blockIdx.x;
+  for (int j = 0; j < per; ++j) {
+    // the thread whose requests hold a worker's first place finds its unit
+    const int r = threadIdx.x * per + j;
+    if (r >= a.R) break;
+    Unit u;
+    u.x = load_request(a, r);
+    if (u.x.tiles == 0) continue;
+    const int chunks = chunks_of(a, u.x, S::kRows), places = u.x.tiles + deal.cost;
+    const long long end = before + (long long)places * a.H * chunks;
+    for (int w = 0; w < kWarps / group; ++w) {
+      const long long first = (long long)(blockIdx.x * (kWarps / group) + w) * deal.share;
+      if (first < before || first >= end) continue;
+      const int unit = int((first - before) / places);
+      u.r = r;
+      u.h = unit / chunks;
+      u.c = unit % chunks;
+      u.place = before + (long long)unit * places;
+      starts[w] = u;
+    }
+    before = end;
+  }
   // rows that see nothing because their request has no entries
   for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
     const Request x = load_request(a, r);
@@ -254,111 +299,79 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       if (a.lse && i % (kDim / 2) == 0) a.lse[at * a.Hq + h] = -INFINITY;
     }
   }
-  if (first >= total) {
-    if (threadIdx.x == 0) parts.shared[blockIdx.x].c0 = -1;
-    return;
-  }
-  {
-    // the thread whose requests hold tile `first` finds its place
-    long long at = before;
-    for (int j = 0; j < per; ++j) {
-      const int r = threadIdx.x * per + j;
-      if (r >= a.R) break;
-      Cursor k;
-      k.x = load_request(a, r);
-      const int chunks = chunks_of(a, k.x, S::kRows);
-      const long long n = (long long)k.x.tiles * a.H * chunks;
-      if (first >= at && first < at + n) {
-        const long long in = first - at;
-        const int unit = int(in / k.x.tiles);
-        k.r = r;
-        k.h = unit / chunks;
-        k.c = unit % chunks;
-        k.t = int(in % k.x.tiles);
-        k.left = min(share, total - first);
-        k.end = int(min((long long)k.x.tiles, k.t + k.left));
-        start = k;
-      }
-      at += n;
-    }
-  }
-  if (lane == 0)
+  if (lane == 0) {
+    parts.shared[blockIdx.x * kWarps + warp].first = -1;
     for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp][s]), 1);
+  }
   ptx::fence_barrier_init();
   __syncthreads();
+  const long long my_first = worker * deal.share, my_end = min(my_first + deal.share, deal.total);
+  if (my_first >= deal.total) return;   // a whole CTA, or a warp that meets no other again
 
   uint8_t* const ring = smem + warp * (S::kStages * S::kStage);
   float* const join = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kStage);
-  __half* const sq = reinterpret_cast<__half*>(smem + kWarps * S::kStages * S::kStage + S::kJoinBytes);
+  uint32_t* const sq = reinterpret_cast<uint32_t*>(join + warp * S::kRows * S::kJoinRow);
   const uint32_t bar0 = ptx::smem_u32(&bars[warp][0]), ring0 = ptx::smem_u32(ring);
-
-  // ---- the copies: a second cursor ahead of the one that is being worked on
-  Cursor ic = start;
-  int it = ic.t + warp;          // the warp's next tile to fetch
-  int held = -1;                 // first of the 16 tiles whose records the lanes know
-  uint32_t block = 0;            // lane: record of tile held + kWarps * (lane / 2), half lane % 2
-  uint32_t usable = 0, usable_ring = 0;   // bit per lane; two bits per stage
-  int issued = 0, taken = 0, fill = 0;
+  int fill = 0, stage = 0;       // next stage to fill, to take
+  int in_flight = 0;             // stages filled and not taken
+  uint32_t phase = 0, usable_ring = 0;   // two bits per stage: which of its records may be looked at
   bool dead = false;
 
-  auto issue = [&]() {
-    if (dead) return;
-    while (ic.left > 0 && it >= ic.end) {
-      next_unit(a, ic, ic.t, S::kRows);
-      it = warp;
-      held = -1;
-    }
-    if (ic.left <= 0) return;
-    if (held < 0 || it >= held + 16 * kWarps) {
-      held = it;
-      const int tile = it + kWarps * (lane >> 1);
-      bool ok = false;
-      if (tile < ic.end) {
-        const int e0 = (tile < ic.x.sink_t ? tile : tile - ic.x.sink_t + ic.x.lo_t) * kTile + (lane & 1) * 16;
-        if (e0 < ic.x.n && (e0 + 15 >= ic.x.lo || e0 < ic.x.sinks)) {
-          const int page = a.page_table[(int64_t)ic.r * a.page_stride + (e0 >> a.page_shift)];
-          const int64_t b = ((int64_t)page << (a.page_shift - 4)) + ((e0 & ((1 << a.page_shift) - 1)) >> 4);
-          ok = page >= 0 && b < (a.num_slots >> 4);
-          if (!ok) set_status(a.status, UPF_ERR_INVALID_ARG);
-          block = uint32_t(b);
-        }
-      }
-      usable = __ballot_sync(0xFFFFFFFFu, ok);
-    }
-    const int src = (it - held) / kWarps * 2;
-    const uint32_t two = (usable >> src) & 3u;
-    const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, block, src), b1 = __shfl_sync(0xFFFFFFFFu, block, src + 1);
-    usable_ring = (usable_ring & ~(3u << (2 * fill))) | (two << (2 * fill));
-    if (lane == 0) {
-      const uint32_t bar = bar0 + 8 * fill, dst = ring0 + fill * S::kStage;
-      ptx::mbar_arrive_expect_tx(bar, S::kRecord * __popc(two));
-      if (two & 1u) ptx::bulk_load(dst, a.data + ((int64_t)b0 * a.H + ic.h) * S::kRecord, S::kRecord, bar);
-      if (two & 2u) ptx::bulk_load(dst + S::kRecord, a.data + ((int64_t)b1 * a.H + ic.h) * S::kRecord, S::kRecord, bar);
-    }
-    __syncwarp();
-    it += kWarps;
-    ++issued;
-    if (++fill == S::kStages) fill = 0;
-  };
-  for (int s = 0; s < S::kStages; ++s) issue();
+  for (Unit u = starts[deal.warps ? warp : 0]; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
+    const int begin = int(max(0LL, my_first - u.place - deal.cost));
+    const int end = int(min((long long)u.x.tiles, my_end - u.place - deal.cost));
+    if (end <= begin) continue;
 
-  int stage = 0;
-  uint32_t phase = 0;
-  Cursor k = start;
-  while (k.left > 0) {
+    // ---- the copies.  The lanes know the records of the warp's next 16 tiles: lane 2 i + b the
+    // b-th record of the i-th.
+    int it = begin + rank, held = -1;
+    uint32_t block = 0, usable = 0;
+    auto issue = [&]() {
+      if (it >= end || dead) return;
+      if (held < 0 || it >= held + 16 * group) {
+        held = it;
+        const int tile = it + group * (lane >> 1);
+        bool ok = false;
+        if (tile < end) {
+          const int e0 = (tile < u.x.sink_t ? tile : tile - u.x.sink_t + u.x.lo_t) * kTile + (lane & 1) * 16;
+          if (e0 < u.x.n && (e0 + 15 >= u.x.lo || e0 < u.x.sinks)) {
+            const int page = a.page_table[(int64_t)u.r * a.page_stride + (e0 >> a.page_shift)];
+            const int64_t b = ((int64_t)page << (a.page_shift - 4)) + ((e0 & ((1 << a.page_shift) - 1)) >> 4);
+            ok = page >= 0 && b < (a.num_slots >> 4);
+            if (!ok) set_status(a.status, UPF_ERR_INVALID_ARG);
+            block = uint32_t(b);
+          }
+        }
+        usable = __ballot_sync(0xFFFFFFFFu, ok);
+      }
+      const int src = (it - held) / group;
+      const uint32_t two = (usable >> (2 * src)) & 3u;
+      usable_ring = (usable_ring & ~(3u << (2 * fill))) | (two << (2 * fill));
+      if ((lane >> 1) == src) {
+        const uint32_t bar = bar0 + 8 * fill;
+        if ((lane & 1) == 0) ptx::mbar_arrive_expect_tx(bar, S::kRecord * __popc(two));
+        if ((two >> (lane & 1)) & 1u)
+          ptx::bulk_load(ring0 + fill * S::kStage + (lane & 1) * S::kRecord,
+                         a.data + ((int64_t)block * a.H + u.h) * S::kRecord, S::kRecord, bar);
+      }
+      __syncwarp();
+      it += group;
+      ++in_flight;
+      if (++fill == S::kStages) fill = 0;
+    };
+    for (int s = 0; s < S::kStages; ++s) issue();
+
     // ---- the unit's rows
-    const int row0 = k.c * S::kRows, rows = k.x.q_len * a.gamma;   // rows of the request
-    const int base = k.x.n - k.x.q_len;                            // position of query 0
+    const int row0 = u.c * S::kRows, rows = u.x.q_len * a.gamma;   // rows of the request
+    const int base = u.x.n - u.x.q_len;                            // position of query 0
     uint32_t qf[S::kQueryInSmem ? 1 : S::kParts * S::kSteps][NT][2];
     float f[NT][2];          // logit factor of rows 2 t4, 2 t4 + 1 of each eight
-    int pos[NT][2];          // their positions (-1: no such row)
-    if constexpr (S::kQueryInSmem) __syncthreads();   // the last unit's reads are done
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int rho = row0 + nt * 8 + g;
       const bool real = rho < rows;
       const int i = real ? rho / a.gamma : 0, j = real ? rho - i * a.gamma : 0;
-      const T* src = static_cast<const T*>(a.q) + (int64_t)(k.x.q0 + i) * a.q_stride + (int)a.qhead[k.h * a.gamma + j] * kDim;
+      const T* src = static_cast<const T*>(a.q) + (int64_t)(u.x.q0 + i) * a.q_stride + (int)a.qhead[u.h * a.gamma + j] * kDim;
       constexpr int kWords = S::kPart / 8;   // 32-bit words of this lane's quarter of a part
       uint32_t w[S::kParts][kWords];
       float amax = 0.f;
@@ -366,19 +379,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       for (int p = 0; p < S::kParts; ++p) {
         const uint4* v = reinterpret_cast<const uint4*>(src + p * 128 + t4 * (S::kPart / 4));
 #pragma unroll
-        for (int u = 0; u < kWords / 4; ++u) {
-          const uint4 y = real ? v[u] : make_uint4(0, 0, 0, 0);
-          w[p][4 * u] = y.x;
-          w[p][4 * u + 1] = y.y;
-          w[p][4 * u + 2] = y.z;
-          w[p][4 * u + 3] = y.w;
-        }
-#pragma unroll
-        for (int u = 0; u < kWords; ++u) {
-          const float2 y = kv::pair_to_float2(w[p][u], static_cast<const T*>(nullptr));
-          amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+        for (int x = 0; x < kWords / 4; ++x) {
+          const uint4 y = real ? v[x] : make_uint4(0, 0, 0, 0);
+          w[p][4 * x] = y.x;
+          w[p][4 * x + 1] = y.y;
+          w[p][4 * x + 2] = y.z;
+          w[p][4 * x + 3] = y.w;
         }
       }
+#pragma unroll
+      for (int p = 0; p < S::kParts; ++p)
+#pragma unroll
+        for (int x = 0; x < kWords; ++x) {
+          const float2 y = kv::pair_to_float2(w[p][x], static_cast<const T*>(nullptr));
+          amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+        }
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       // 2^-e and 2^e with e the exponent of the largest element (0 for a row of zeros)
@@ -388,252 +403,254 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
 #pragma unroll
       for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
-        for (int u = 0; u < kWords; ++u) {
-          const float2 y = kv::pair_to_float2(w[p][u], static_cast<const T*>(nullptr));
+        for (int x = 0; x < kWords; ++x) {
+          const float2 y = kv::pair_to_float2(w[p][x], static_cast<const T*>(nullptr));
           const uint32_t v = pack_f16(y.x * down, y.y * down);
           if constexpr (S::kQueryInSmem) {
-            // every warp writes the same values; read back as [step][nt][lane] pairs
-            reinterpret_cast<uint32_t*>(sq)[(((p * S::kSteps + u / 2) * NT + nt) * 32 + lane) * 2 + (u & 1)] = v;
+            sq[(((p * S::kSteps + x / 2) * NT + nt) * 32 + lane) * 2 + (x & 1)] = v;   // read back by this lane
           } else {
-            qf[p * S::kSteps + u / 2][nt][u & 1] = v;
+            qf[p * S::kSteps + x / 2][nt][x & 1] = v;
           }
         }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)   // never 0: it multiplies the -inf of unseen entries
+        f[nt][b] = fmaxf(a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4), FLT_MIN);
+    }
+    const int p_min = base + row0 / a.gamma, p_max = base + (min(rows, row0 + S::kRows) - 1) / a.gamma;
+    // does row y of this lane's columns (nt, b) see entry e?
+    auto sees = [&](int nt, int b, int e) {
+      const int y = row0 + nt * 8 + 2 * t4 + b, p = base + y / a.gamma;
+      return y < rows && e <= p && (a.window == 0 || p - e < a.window || e < a.sinks);
+    };
+
+    // weights are 2^(f s + c) with c = 12 - m; the reference m moves when s passes `limit`
+    float o[S::kParts * S::kSteps][NT][4];
+    float c[NT][2], limit[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        f[nt][b] = a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4);
-        const int rr = row0 + nt * 8 + 2 * t4 + b;
-        pos[nt][b] = rr < rows ? base + rr / a.gamma : -1;
+        c[nt][b] = FLT_MAX;
+        limit[nt][b] = -FLT_MAX;
+        l[nt][b] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < S::kParts * S::kSteps; ++mt) o[mt][nt][b] = o[mt][nt][b + 2] = 0.f;
       }
-    }
-    if constexpr (S::kQueryInSmem) __syncthreads();
-    const int last_row = min(rows, row0 + S::kRows) - 1;
-    const int p_min = base + row0 / a.gamma, p_max = base + last_row / a.gamma;
 
-    float o[S::kParts * S::kSteps][NT][4];
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -FLT_MAX;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < S::kParts * S::kSteps; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
-    }
-
-    for (int t = k.t + warp; t < k.end; t += kWarps) {
-      if (dead) {   // a copy did not come in time: no more work, only its own copies are waited for
-        if (taken < issued) ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
-      } else if (!ptx::mbar_wait_poll(bar0 + 8 * stage, phase, a.wait_limit, 64)) {
-        dead = true;
-        if (lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
-        ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
+    for (int t = begin + rank; t < end; t += group) {
+      if (in_flight > 0) {
+        if (!ptx::mbar_wait_poll(bar0 + 8 * stage, phase, dead ? kDefaultWaitCycles : a.wait_limit, 64)) {
+          // a copy did not come in time: no more work, the warp's own copies are waited for
+          dead = true;
+          if (lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
+          ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
+        }
+        dead = __any_sync(0xFFFFFFFFu, dead);
       }
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
-      const uint8_t* const rec = ring + stage * S::kStage;
-      if (!dead) {
-        const int e0 = (t < k.x.sink_t ? t : t - k.x.sink_t + k.x.lo_t) * kTile;
-        const bool whole = two == 3u && e0 + kTile - 1 <= p_min &&
-                           (a.window == 0 || p_max - e0 < a.window || e0 + kTile <= a.sinks);
-        // ---- logits: S^T[entry][row]
-        float s[2][NT][4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint8_t* const rb = rec + b * S::kRecord;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][nt][i] = 0.f;
-#pragma unroll
-          for (int p = 0; p < S::kParts; ++p) {
-            constexpr int kW = S::kPart / 32;   // words of a lane's quarter row: 2 or 4
-            uint32_t w[2][kW], sc[2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint8_t* const src = rb + p * (8 * S::kPart) + (g + 8 * half) * (S::kPart / 2) + t4 * (S::kPart / 8);
-              if constexpr (kW == 4) {
-                const uint4 y = *reinterpret_cast<const uint4*>(src);
-                w[half][0] = y.x;
-                w[half][1] = y.y;
-                w[half][2] = y.z;
-                w[half][3] = y.w;
-                sc[half] = kv::e4m3x2_to_f16x2(
-                    *reinterpret_cast<const uint16_t*>(rb + kv::k_scale(kDim, g + 8 * half, p * 8 + 2 * t4)));
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(src);
-                w[half][0] = y.x;
-                w[half][1] = y.y;
-                sc[half] = kv::e4m3x2_to_f16x2(rb[kv::k_scale(kDim, g + 8 * half, t4)]);
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < kW; ++u) {   // eight dims of the lane: two steps
-              uint32_t x0[4], x1[4];
-              kv::e2m1x8_to_f16(w[0][u], x0);
-              kv::e2m1x8_to_f16(w[1][u], x1);
-              // at d >= 128 the second half of the quarter is the second group
-              const uint32_t sel = (kW == 4 && u >= 2) ? 0x3232u : 0x1010u;
-              const uint32_t s0 = __byte_perm(sc[0], 0, sel), s1 = __byte_perm(sc[1], 0, sel);
-#pragma unroll
-              for (int st = 0; st < 2; ++st) {
-                const uint32_t af[4] = {hmul2(x0[2 * st], s0), hmul2(x1[2 * st], s1), hmul2(x0[2 * st + 1], s0),
-                                        hmul2(x1[2 * st + 1], s1)};
-                const int step = p * S::kSteps + 2 * u + st;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if constexpr (S::kQueryInSmem) {
-                    const uint2 y = reinterpret_cast<const uint2*>(sq)[(step * NT + nt) * 32 + lane];
-                    const uint32_t bf[2] = {y.x, y.y};
-                    mma_f16(s[b][nt], af, bf);
-                  } else {
-                    mma_f16(s[b][nt], af, qf[step][nt]);
-                  }
-                }
-              }
-            }
+      if (dead) {
+        if (in_flight > 0) {
+          --in_flight;
+          if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1;
           }
         }
-        // ---- weights: 2^(x - m + 12), in f16 as operand B of the second product
+        continue;
+      }
+      const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
+      const uint8_t* const rec = ring + stage * S::kStage;
+      const int e0 = (t < u.x.sink_t ? t : t - u.x.sink_t + u.x.lo_t) * kTile;
+      const bool whole = two == 3u && e0 + kTile - 1 <= p_min &&
+                         (a.window == 0 || p_max - e0 < a.window || e0 + kTile <= a.sinks);
+      // ---- logits: S^T[entry][row]
+      float s[2][NT][4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][nt][i] *= f[nt][i & 1];
-        if (!whole) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int e = e0 + 16 * b + g + 8 * (i >> 1), p = pos[nt][i & 1];
-                const bool see = ((two >> b) & 1u) && e <= p && (a.window == 0 || p - e < a.window || e < a.sinks);
-                if (!see) s[b][nt][i] = -INFINITY;
-              }
-        }
-        bool over = false;
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* const rb = rec + b * S::kRecord;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) over |= fmaxf(s[0][nt][i], s[1][nt][i]) > m[nt][i & 1] + kLag;
-        if (__any_sync(0xFFFFFFFFu, over)) {
+          for (int i = 0; i < 4; ++i) s[b][nt][i] = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int p = 0; p < S::kParts; ++p) {
+          constexpr int kW = S::kPart / 32;   // words of a lane's quarter row: 2 or 4
+          uint32_t w[2][kW];
+          __half2 sc[2];                      // scales of the quarter's first and second group
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float x = fmaxf(fmaxf(s[0][nt][b], s[0][nt][b + 2]), fmaxf(s[1][nt][b], s[1][nt][b + 2]));
+          for (int half = 0; half < 2; ++half) {
+            const uint8_t* const src = rb + p * (8 * S::kPart) + (g + 8 * half) * (S::kPart / 2) + t4 * (S::kPart / 8);
+            if constexpr (kW == 4) {
+              const uint4 y = *reinterpret_cast<const uint4*>(src);
+              w[half][0] = y.x;
+              w[half][1] = y.y;
+              w[half][2] = y.z;
+              w[half][3] = y.w;
+              sc[half] = as_half2(kv::e4m3x2_to_f16x2(
+                  *reinterpret_cast<const uint16_t*>(rb + kv::k_scale(kDim, g + 8 * half, p * 8 + 2 * t4))));
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(src);
+              w[half][0] = y.x;
+              w[half][1] = y.y;
+              sc[half] = as_half2(kv::e4m3x2_to_f16x2(rb[kv::k_scale(kDim, g + 8 * half, t4)]));
+            }
+          }
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-              const float m2 = fmaxf(m[nt][b], x), c = ptx::ex2_approx(m[nt][b] - m2);
-              m[nt][b] = m2;
-              l[nt][b] *= c;
+          for (int x = 0; x < kW; ++x) {   // eight dims of the lane: two steps
+            uint32_t x0[4], x1[4];
+            kv::e2m1x8_to_f16(w[0][x], x0);
+            kv::e2m1x8_to_f16(w[1][x], x1);
+            const bool second = kW == 4 && x >= 2;
+            const __half2 s0 = second ? __high2half2(sc[0]) : __low2half2(sc[0]);
+            const __half2 s1 = second ? __high2half2(sc[1]) : __low2half2(sc[1]);
 #pragma unroll
-              for (int mt = 0; mt < S::kParts * S::kSteps; ++mt) {
-                o[mt][nt][b] *= c;
-                o[mt][nt][b + 2] *= c;
+            for (int st = 0; st < 2; ++st) {
+              const uint32_t af[4] = {hmul2(x0[2 * st], s0), hmul2(x1[2 * st], s1), hmul2(x0[2 * st + 1], s0),
+                                      hmul2(x1[2 * st + 1], s1)};
+              const int step = p * S::kSteps + 2 * x + st;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (S::kQueryInSmem) {
+                  const uint2 y = reinterpret_cast<const uint2*>(sq)[(step * NT + nt) * 32 + lane];
+                  const uint32_t bf[2] = {y.x, y.y};
+                  mma_f16(s[b][nt], af, bf);
+                } else {
+                  mma_f16(s[b][nt], af, qf[step][nt]);
+                }
               }
             }
+          }
         }
-        uint32_t pf[2][NT][2];
+      }
+      // ---- weights, in f16 as operand B of the second product
+      if (!whole) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              w[i] = ptx::ex2_approx(s[b][nt][i] + (kWeightExp - m[nt][i & 1]));
-              l[nt][i & 1] += w[i];
+            for (int i = 0; i < 4; ++i)
+              if (!((two >> b) & 1u) || !sees(nt, i & 1, e0 + 16 * b + g + 8 * (i >> 1))) s[b][nt][i] = -INFINITY;
+      }
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          over |= fmaxf(fmaxf(s[0][nt][i], s[1][nt][i]), fmaxf(s[0][nt][i + 2], s[1][nt][i + 2])) > limit[nt][i];
+      if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float x = fmaxf(fmaxf(s[0][nt][b], s[0][nt][b + 2]), fmaxf(s[1][nt][b], s[1][nt][b + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+            if (x > limit[nt][b]) {
+              const float c2 = kWeightExp - x * f[nt][b], k = ptx::ex2_approx(c2 - c[nt][b]);
+              c[nt][b] = c2;
+              limit[nt][b] = x + kLag / f[nt][b];
+              l[nt][b] *= k;
+#pragma unroll
+              for (int mt = 0; mt < S::kParts * S::kSteps; ++mt) {
+                o[mt][nt][b] *= k;
+                o[mt][nt][b + 2] *= k;
+              }
             }
-            pf[b][nt][0] = transpose8x8(pack_f16(w[0], w[1]));
-            pf[b][nt][1] = transpose8x8(pack_f16(w[2], w[3]));
           }
-        // ---- weighted sum: O^T[dim][row]
-        uint32_t bad = 0;   // a NaN scale among the values of a tile with unseen entries
+      }
+      uint32_t pf[2][NT][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint8_t* const rb = rec + b * S::kRecord;
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int p = 0; p < S::kParts; ++p) {
-            constexpr int kW = S::kPart / 64;   // words of a chunk: 1 or 2
-            uint32_t w[2][2][kW], sc[2];        // [entries 2 t4.. or 2 t4 + 8..][entry of the two]
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = ptx::ex2_approx(__fmaf_rn(s[b][nt][i], f[nt][i & 1], c[nt][i & 1]));
+            l[nt][i & 1] += w[i];
+          }
+          pf[b][nt][0] = transpose8x8(pack_f16(w[0], w[1]));
+          pf[b][nt][1] = transpose8x8(pack_f16(w[2], w[3]));
+        }
+      // ---- weighted sum: O^T[dim][row]
+      uint32_t bad = 0;   // a NaN scale among the values of a tile with unseen entries
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* const rb = rec + b * S::kRecord;
+#pragma unroll
+        for (int p = 0; p < S::kParts; ++p) {
+          constexpr int kW = S::kPart / 64;   // words of a chunk: 1 or 2
+          uint32_t w[2][2][kW];               // [entries 2 t4.. or 2 t4 + 8..][entry of the two]
+          __half2 sc[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint8_t* const src = rb + 8 * kDim + p * (8 * S::kPart) + half * (4 * S::kPart) + lane * (8 * kW);
+            if constexpr (kW == 2) {
+              const uint4 y = *reinterpret_cast<const uint4*>(src);
+              w[half][0][0] = y.x;
+              w[half][0][1] = y.y;
+              w[half][1][0] = y.z;
+              w[half][1][1] = y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(src);
+              w[half][0][0] = y.x;
+              w[half][1][0] = y.y;
+            }
+            uint32_t raw = *reinterpret_cast<const uint16_t*>(rb + 17 * kDim + p * S::kPart + half * (S::kPart / 2) +
+                                                              (kW == 2 ? g : g >> 1) * 8 + 2 * t4);
+            if (!whole) {
+              // 0 * NaN would reach the rows that do not see the entry: take the scale as 0 and
+              // give the NaN to the rows that do see it below
+              if ((raw & 0x7Fu) == 0x7Fu) {
+                raw &= 0xFF00u;
+                bad = 1;
+              }
+              if ((raw & 0x7F00u) == 0x7F00u) {
+                raw &= 0x00FFu;
+                bad = 1;
+              }
+            }
+            sc[half] = as_half2(kv::e4m3x2_to_f16x2(uint16_t(raw)));
+          }
+#pragma unroll
+          for (int x = 0; x < kW; ++x) {
+            // low nibbles of both entries side by side (even dims), then the high ones
+            uint32_t lo[2][4], hi[2][4];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const uint8_t* const src = rb + 8 * kDim + p * (8 * S::kPart) + half * (4 * S::kPart) + lane * (8 * kW);
-              if constexpr (kW == 2) {
-                const uint4 y = *reinterpret_cast<const uint4*>(src);
-                w[half][0][0] = y.x;
-                w[half][0][1] = y.y;
-                w[half][1][0] = y.z;
-                w[half][1][1] = y.w;
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(src);
-                w[half][0][0] = y.x;
-                w[half][1][0] = y.y;
-              }
-              uint32_t raw = *reinterpret_cast<const uint16_t*>(rb + 17 * kDim + p * S::kPart + half * (S::kPart / 2) +
-                                                                (kW == 2 ? g : g >> 1) * 8 + 2 * t4);
-              if (!whole) {
-                // 0 * NaN would reach the rows that do not see the entry: take the scale as 0 and
-                // give the NaN to the rows that do see it below
-                if ((raw & 0x7Fu) == 0x7Fu) {
-                  raw &= 0xFF00u;
-                  bad = 1;
-                }
-                if ((raw & 0x7F00u) == 0x7F00u) {
-                  raw &= 0x00FFu;
-                  bad = 1;
-                }
-              }
-              sc[half] = kv::e4m3x2_to_f16x2(uint16_t(raw));
+              kv::e2m1x8_to_f16(merge_bits(w[half][0][x], w[half][1][x] << 4, 0x0F0F0F0Fu), lo[half]);
+              kv::e2m1x8_to_f16(merge_bits(w[half][0][x] >> 4, w[half][1][x], 0x0F0F0F0Fu), hi[half]);
             }
 #pragma unroll
-            for (int u = 0; u < kW; ++u) {
-              // low nibbles of both entries side by side (even dims), then the high ones
-              uint32_t lo[2][4], hi[2][4];
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t af[4] = {hmul2(lo[0][j], sc[0]), hmul2(hi[0][j], sc[0]), hmul2(lo[1][j], sc[1]),
+                                      hmul2(hi[1][j], sc[1])};
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                kv::e2m1x8_to_f16(merge_bits(w[half][0][u], w[half][1][u] << 4, 0x0F0F0F0Fu), lo[half]);
-                kv::e2m1x8_to_f16(merge_bits(w[half][0][u] >> 4, w[half][1][u], 0x0F0F0F0Fu), hi[half]);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t af[4] = {hmul2(lo[0][j], sc[0]), hmul2(hi[0][j], sc[0]), hmul2(lo[1][j], sc[1]),
-                                        hmul2(hi[1][j], sc[1])};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(o[p * S::kSteps + 4 * u + j][nt], af, pf[b][nt]);
-              }
+              for (int nt = 0; nt < NT; ++nt) mma_f16(o[p * S::kSteps + 4 * x + j][nt], af, pf[b][nt]);
             }
           }
         }
-        if (!whole && __any_sync(0xFFFFFFFFu, bad)) {
-          for (int b = 0; b < 2; ++b)
-            for (int row = 0; row < 16; ++row) {
-              const int e = e0 + 16 * b + row;
-#pragma unroll
-              for (int p = 0; p < S::kParts; ++p) {
-                const int grp = p * (S::kPart / 16) + (S::kPart == 128 ? g : g >> 1);
-                const bool nan = (rec[b * S::kRecord + kv::v_scale(kDim, row, grp)] & 0x7F) == 0x7F;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    const int q = pos[nt][c];
-                    const bool see = ((two >> b) & 1u) && e <= q && (a.window == 0 || q - e < a.window || e < a.sinks);
-                    if (nan && see)
-#pragma unroll
-                      for (int mt = 0; mt < S::kSteps; ++mt) {
-                        o[p * S::kSteps + mt][nt][c] = __int_as_float(0x7FFFFFFF);
-                        o[p * S::kSteps + mt][nt][c + 2] = __int_as_float(0x7FFFFFFF);
-                      }
-                  }
-              }
-            }
-        }
       }
-      ++taken;
+      if (!whole && __any_sync(0xFFFFFFFFu, bad)) {
+        for (int b = 0; b < 2; ++b)
+          for (int row = 0; row < 16; ++row) {
+            const int e = e0 + 16 * b + row;
+#pragma unroll
+            for (int p = 0; p < S::kParts; ++p) {
+              const int grp = p * (S::kPart / 16) + (S::kPart == 128 ? g : g >> 1);
+              const bool nan = (rec[b * S::kRecord + kv::v_scale(kDim, row, grp)] & 0x7F) == 0x7F;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                  if (nan && ((two >> b) & 1u) && sees(nt, d, e))
+#pragma unroll
+                    for (int mt = 0; mt < S::kSteps; ++mt)
+                      o[p * S::kSteps + mt][nt][d] = o[p * S::kSteps + mt][nt][d + 2] = __int_as_float(0x7FFFFFFF);
+            }
+          }
+      }
+      --in_flight;
       if (++stage == S::kStages) {
         stage = 0;
         phase ^= 1;
@@ -642,33 +659,78 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       issue();
     }
 
-    // ---- join the warps
+    // ---- write the unit, or this worker's part of it
+    const bool goes_on = end < u.x.tiles, alone = !goes_on && begin == 0;
+    const size_t part = (size_t)2 * worker + (goes_on ? 1 : 0);
+    if (goes_on && lane == 0) {
+      Shared note;
+      note.first = int((u.place + deal.cost) / deal.share);
+      note.last = int((u.place + deal.cost + u.x.tiles - 1) / deal.share);
+      note.h = u.h;
+      note.row0 = row0;
+      note.rows = rows;
+      note.q0 = u.x.q0;
+      note.portion = (worker - note.first) * group + rank;
+      note.portions = (note.last - note.first) * group;
+      parts.shared[blockIdx.x * kWarps + warp] = note;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][b] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][b], d);
+    if (deal.warps) {
+      // straight from the registers: a lane holds the dims of chunk g of its two columns
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int row = nt * 8 + 2 * t4 + b, rho = row0 + row;
+          if (rho >= rows) continue;
+          const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
+          const int64_t at = u.x.q0 + qi;
+          const float all = l[nt][b], inv = all == 0.f ? 0.f : a.v_mul / all, m = kWeightExp - c[nt][b];
+#pragma unroll
+          for (int p = 0; p < S::kParts; ++p) {
+            const int dim = p * 128 + g * (S::kPart / 8);
+            if (alone) {
+              uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim);
+#pragma unroll
+              for (int mt = 0; mt < S::kSteps; mt += 4) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  w[i] = kv::float2_to_pair(o[p * S::kSteps + mt + i][nt][b] * inv, o[p * S::kSteps + mt + i][nt][b + 2] * inv,
+                                            static_cast<const T*>(nullptr));
+                *reinterpret_cast<uint4*>(dst + mt) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              float* const dst = parts.o + (part * S::kRows + row) * kDim + dim;
+#pragma unroll
+              for (int mt = 0; mt < S::kSteps; mt += 2)
+                *reinterpret_cast<float4*>(dst + 2 * mt) =
+                    make_float4(o[p * S::kSteps + mt][nt][b], o[p * S::kSteps + mt][nt][b + 2],
+                                o[p * S::kSteps + mt + 1][nt][b], o[p * S::kSteps + mt + 1][nt][b + 2]);
+            }
+          }
+          if (g == 0) {
+            if (!alone) parts.ml[part * S::kRows + row] = make_float2(m, all);
+            else if (a.lse) a.lse[at * a.Hq + head] = lse_of(m, all);
+          }
+        }
+      __syncwarp();   // sq is free again
+      continue;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
         if (g == 0) {
-          sh_m[warp][nt * 8 + 2 * t4 + b] = m[nt][b];
+          sh_m[warp][nt * 8 + 2 * t4 + b] = kWeightExp - c[nt][b];
           sh_l[warp][nt * 8 + 2 * t4 + b] = l[nt][b];
         }
-      }
     __syncthreads();
-    const bool alone = k.t == 0 && k.end == k.x.tiles;
-    const bool goes_on = k.end < k.x.tiles;
-    const size_t part = 2 * blockIdx.x + (goes_on ? 1 : 0);
-    if (threadIdx.x == 0 && k.left == k.end - k.t) {   // the share's last unit
-      Shared u;
-      const long long t0 = min(first + share, total) - k.end;   // the unit's first tile
-      u.c0 = goes_on ? int(t0 / share) : -1;
-      u.c1 = int((t0 + k.x.tiles - 1) / share);
-      u.h = k.h;
-      u.row0 = row0;
-      u.rows = rows;
-      u.q0 = k.x.q0;
-      parts.shared[blockIdx.x] = u;
-    }
     float scale[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -677,8 +739,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         float top = -FLT_MAX;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][nt * 8 + 2 * t4 + b]);
-        scale[nt][b] = ptx::ex2_approx(m[nt][b] - top);
+        scale[nt][b] = ptx::ex2_approx(kWeightExp - c[nt][b] - top);
       }
+    if (threadIdx.x < S::kRows) {
+      float top = -FLT_MAX, all = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][threadIdx.x]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx(sh_m[w][threadIdx.x] - top);
+      sh_top[threadIdx.x] = top;
+      sh_all[threadIdx.x] = all;
+    }
     for (int p = 0; p < S::kParts; ++p) {
       if (p) __syncthreads();
 #pragma unroll
@@ -710,30 +781,24 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
           sum.x += v.x;
           sum.y += v.y;
         }
-        float top = -FLT_MAX, all = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][row]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) all += sh_l[w][row] * ptx::ex2_approx(sh_m[w][row] - top);
+        const float all = sh_all[row];
         if (alone) {
-          const int qi = rho / a.gamma, head = a.qhead[k.h * a.gamma + rho - qi * a.gamma];
-          const int64_t at = k.x.q0 + qi;
+          const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
+          const int64_t at = u.x.q0 + qi;
           const float inv = all == 0.f ? 0.f : a.v_mul / all;
           *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim) =
               kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
-          if (a.lse && p == 0 && y == 0) a.lse[at * a.Hq + head] = all == 0.f ? -INFINITY : (top - kWeightExp + log2f(all)) * kLn2;
+          if (a.lse && p == 0 && y == 0) a.lse[at * a.Hq + head] = lse_of(sh_top[row], all);
         } else {
           *reinterpret_cast<float2*>(parts.o + (part * S::kRows + row) * kDim + dim) = sum;
-          if (p == 0 && y == 0) parts.ml[part * S::kRows + row] = make_float2(top, all);
+          if (p == 0 && y == 0) parts.ml[part * S::kRows + row] = make_float2(sh_top[row], all);
         }
       }
     }
-    __syncthreads();   // the join buffer and sh_m, sh_l are free again
-    next_unit(a, k, k.t, S::kRows);
+    __syncthreads();   // the join buffer, sh_m, sh_l, sh_top and sh_all are free again
   }
-  while (taken < issued) {   // only after a wait that ran out
+  for (; in_flight > 0; --in_flight) {   // only after a wait that ran out
     ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
-    ++taken;
     if (++stage == S::kStages) {
       stage = 0;
       phase ^= 1;
@@ -743,55 +808,95 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
 
 // ------------------------------------------------------------------- join --
 
-constexpr int kJoinThreads = 256;
-
-// Adds up the parts of shared units.  CTA c takes its portion of the outputs of
-// the unit that goes on after share c, so that the CTAs c0 .. c1 - 1 of a unit
-// with many parts all work on it.  2^k lanes add up one pair of dims.
+// Adds up the parts of shared units.  Each warp of the workers that a unit goes on
+// after takes its portion of the outputs (four dims each), so that all of them
+// work on a unit with many parts.  2^k lanes add up one output, each every 2^k-th
+// part; what they load does not hang on what they loaded before.
 template <typename T, int kDim, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_attend_join_kernel(const KvAttendArgs a, const Parts parts) {
+__global__ void __launch_bounds__(kThreads) kv_attend_join_kernel(const KvAttendArgs a, const Parts parts) {
   using S = Shape<kDim, NT>;
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
   pdl_wait();
-  const Shared u = parts.shared[blockIdx.x];
-  if (u.c0 < 0) return;
-  const int rows = min(S::kRows, u.rows - u.row0), outputs = rows * (kDim / 2);
-  const int workers = u.c1 - u.c0, each = (outputs + workers - 1) / workers;
-  int lanes = 1;
-  while (lanes < 32 && 2 * lanes * each <= kJoinThreads) lanes *= 2;
-  const int sub = threadIdx.x & (lanes - 1);
-  const int from = (blockIdx.x - u.c0) * each, to = min(outputs, from + each);
+  const Shared u = parts.shared[blockIdx.x * kWarps + (threadIdx.x >> 5)];
+  if (u.first < 0) return;
+  const int rows = min(S::kRows, u.rows - u.row0), outputs = rows * (kDim / 4);
+  const int each = (outputs + u.portions - 1) / u.portions;
+  int lanes = 32;
+  while (lanes > 1 && (lanes * each > 32 || lanes > u.last - u.first + 1)) lanes >>= 1;
+  const int sub = lane & (lanes - 1);
+  const int from = u.portion * each, to = min(outputs, from + each);
   // every lane makes every round: the shuffles need all of them
-  for (int base = from; base < to; base += kJoinThreads / lanes) {
-    const int i = base + threadIdx.x / lanes;
+  for (int at0 = from; at0 < to; at0 += 32 / lanes) {
+    const int i = at0 + lane / lanes;
     const bool mine = i < to;
-    const int row = mine ? i / (kDim / 2) : 0, j = mine ? i % (kDim / 2) : 0;
-    float top = -FLT_MAX;
-    for (int c = u.c0 + sub; c <= u.c1; c += lanes)
-      top = fmaxf(top, parts.ml[(size_t)(2 * c + (c < u.c1)) * S::kRows + row].x);
-    for (int d = 1; d < lanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    float all = 0.f;
-    float2 sum = make_float2(0.f, 0.f);
-    for (int c = u.c0 + sub; c <= u.c1; c += lanes) {
-      const size_t at = (size_t)(2 * c + (c < u.c1)) * S::kRows + row;
-      const float2 ml = parts.ml[at], v = reinterpret_cast<const float2*>(parts.o + at * kDim)[j];
-      const float w = ptx::ex2_approx(ml.x - top);
-      sum.x += v.x * w;
-      sum.y += v.y * w;
-      all += ml.y * w;
+    const int row = mine ? i / (kDim / 4) : 0, j = mine ? i % (kDim / 4) : 0;
+    float m = -FLT_MAX, all = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w0 = u.first + sub; w0 <= u.last; w0 += kBatch * lanes) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int w = w0 + x * lanes;
+        ml[x] = make_float2(-FLT_MAX, 0.f);
+        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w <= u.last) {
+          const size_t at = (size_t)(2 * w + (w < u.last)) * S::kRows + row;
+          ml[x] = parts.ml[at];
+          v[x] = reinterpret_cast<const float4*>(parts.o + at * kDim)[j];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
+      const float k = ptx::ex2_approx(m - top);
+      m = top;
+      all *= k;
+      sum.x *= k;
+      sum.y *= k;
+      sum.z *= k;
+      sum.w *= k;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const float y = ptx::ex2_approx(ml[x].x - top);
+        all += ml[x].y * y;
+        sum.x += v[x].x * y;
+        sum.y += v[x].y * y;
+        sum.z += v[x].z * y;
+        sum.w += v[x].w * y;
+      }
     }
     for (int d = 1; d < lanes; d <<= 1) {
+      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), top = fmaxf(m, m2);
+      const float k = ptx::ex2_approx(m - top);
+      m = top;
+      all *= k;
+      sum.x *= k;
+      sum.y *= k;
+      sum.z *= k;
+      sum.w *= k;
+      all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
       sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, d);
       sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, d);
-      all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+      sum.z += __shfl_xor_sync(0xFFFFFFFFu, sum.z, d);
+      sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, d);
     }
     if (!mine || sub) continue;
     const int rho = u.row0 + row, q = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - q * a.gamma];
     const int64_t at = u.q0 + q;
     const float inv = all == 0.f ? 0.f : a.v_mul / all;
-    reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim)[j] =
-        kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
-    if (a.lse && j == 0) a.lse[at * a.Hq + head] = all == 0.f ? -INFINITY : (top - kWeightExp + log2f(all)) * kLn2;
+    uint2 w;
+    w.x = kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
+    w.y = kv::float2_to_pair(sum.z * inv, sum.w * inv, static_cast<const T*>(nullptr));
+    reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim)[j] = w;
+    if (a.lse && j == 0) a.lse[at * a.Hq + head] = lse_of(m, all);
   }
+}
+
+template <int kDim, int NT>
+constexpr size_t part_rows() {
+  return (size_t)2 * Shape<kDim, NT>::kCtas * kWarps * Shape<kDim, NT>::kRows;
 }
 
 template <typename T, int kDim, int NT>
@@ -799,13 +904,13 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t s) {
   using S = Shape<kDim, NT>;
   Parts parts;
   parts.o = static_cast<float*>(a.ws);
-  parts.ml = reinterpret_cast<float2*>(parts.o + (size_t)2 * S::kCtas * S::kRows * kDim);
-  parts.shared = reinterpret_cast<Shared*>(parts.ml + (size_t)2 * S::kCtas * S::kRows);
+  parts.ml = reinterpret_cast<float2*>(parts.o + part_rows<kDim, NT>() * kDim);
+  parts.shared = reinterpret_cast<Shared*>(parts.ml + part_rows<kDim, NT>());
   cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, kDim, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_kernel(kv_attend_kernel<T, kDim, NT>, S::kCtas, kThreads, S::kSmem, s, false, a, parts);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kv_attend_join_kernel<T, kDim, NT>, S::kCtas, kJoinThreads, 0, s, true, a, parts);
+  return launch_kernel(kv_attend_join_kernel<T, kDim, NT>, S::kCtas, kThreads, 0, s, true, a, parts);
 }
 
 template <int kDim>
@@ -816,8 +921,8 @@ cudaError_t launch_dim(const KvAttendArgs& a, bool f16, cudaStream_t s) {
 
 template <int kDim, int NT>
 constexpr size_t ws_bytes() {
-  using S = Shape<kDim, NT>;
-  return (size_t)2 * S::kCtas * S::kRows * (kDim * sizeof(float) + sizeof(float2)) + S::kCtas * sizeof(Shared);
+  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2)) +
+         (size_t)Shape<kDim, NT>::kCtas * kWarps * sizeof(Shared);
 }
 
 template <int kDim>

@@ -99,14 +99,16 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, lo
   return true;
 }
 
-// mbar_wait_idle whose first look does not suspend either, so that a short limit
-// is kept to about `ns`.
+// As mbar_wait_idle, but a wait that took longer than `limit` has run out even if
+// the phase is complete by then (a poll may suspend for longer than `ns`).
 __device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, long long limit, uint32_t ns) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait_hint(bar, parity, ns)) {
+  bool done;
+  do {
+    done = mbar_try_wait_hint(bar, parity, ns);
     if (clock64() - t0 > limit) return false;
-  }
+  } while (!done);
   return true;
 }
 
