@@ -37,6 +37,7 @@
 // their bits.
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "kv_layout.cuh"
 #include "sm100_ptx.cuh"
@@ -46,7 +47,7 @@ namespace upf {
 
 namespace {
 
-constexpr int kWarps = 8;        // of a CTA
+constexpr int kLogWarps = 3, kWarps = 1 << kLogWarps;   // of a CTA
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;        // entries per tile (two records)
 constexpr float kWeightExp = 12.f;   // weights are 2^(x - m + 12)
@@ -96,11 +97,16 @@ __device__ __forceinline__ int chunks_of(const KvAttendArgs& a, const Request& x
   return (x.q_len * a.gamma + rows - 1) / rows;
 }
 
+// a / b, both >= 0, by the short division where it will do.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // Cost of a unit in the dealing, in tiles, beside its tiles: the rows' load, the
 // first copies' latency and the writing out.
 constexpr int kUnitCostCta = 16, kUnitCostWarp = 4;
 // Workers are warps where units have fewer tiles than this on average.
-constexpr int kShortUnit = 24;
+constexpr int kShortUnit = 64;
 
 // How the tiles are dealt out.  Along the dealing a unit takes cost + tiles places.
 struct Deal {
@@ -153,7 +159,7 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&w
   d.total = all_t + all_u * d.cost;
   before = t + u * d.cost;
   const long long workers = d.warps ? (long long)gridDim.x * kWarps : gridDim.x;
-  d.share = max((d.total + workers - 1) / workers, (long long)(d.warps ? 1 : kWarps));
+  d.share = max(quotient(d.total + workers - 1, workers), (long long)(d.warps ? 1 : kWarps));
   return d;
 }
 
@@ -185,13 +191,13 @@ struct Shape {
   static constexpr int kRecord = kv::record_bytes(kDim);
   static constexpr int kStage = 2 * kRecord;
   static constexpr int kCtasPerSm = kDim * NT <= 128 ? 2 : 1;
-  static constexpr int kStages = kDim == 64 ? 4 : kDim == 128 ? 2 * NT : 2;
+  static constexpr int kStages = kDim == 64 ? 6 : kDim == 128 ? 3 * NT : NT == 1 ? 3 : 2;
   static constexpr bool kQueryInSmem = kDim * NT > 256;
   static constexpr int kJoinRow = kPart + 4;           // floats; the pad spreads the rows over the banks
-  static constexpr int kJoinBytes = kWarps * kRows * kJoinRow * 4;
-  // queries that do not fit the registers lie in the warp's own part of the join buffer
-  static_assert(!kQueryInSmem || kRows * kDim * 2 <= kRows * kJoinRow * 4, "queries fit a warp's join rows");
-  static constexpr int kSmem = kWarps * kStages * kStage + kJoinBytes;
+  // At the end of a unit a warp's ring is empty and holds its rows for the join.
+  static_assert(kRows * kJoinRow * 4 <= kStages * kStage, "a warp's join rows fit its ring");
+  static constexpr int kQueryBytes = kQueryInSmem ? kRows * kDim * 2 : 0;   // of a warp
+  static constexpr int kSmem = kWarps * (kStages * kStage + kQueryBytes);
   static constexpr int kCtas = kCtasPerSm * kPlanSMs;
 };
 
@@ -200,6 +206,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], c
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// As mma_f16, from zero.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   const int per = (a.R + kThreads - 1) / kThreads;
   long long before;
   const Deal deal = deal_out(a, S::kRows, per, warp_sums, before);
-  const int group = deal.warps ? 1 : kWarps, rank = deal.warps ? 0 : warp;   // warps of a worker, and which this is
+  const int lg = deal.warps ? 0 : kLogWarps, group = 1 << lg, rank = deal.warps ? 0 : warp;   // warps of a worker; which this is
   const int worker = deal.warps ? blockIdx.x * kWarps + warp : blockIdx.x;
   for (int j = 0; j < per; ++j) {
     // the thread whose requests hold a worker's first place finds its unit
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     for (int w = 0; w < kWarps / group; ++w) {
       const long long first = (long long)(blockIdx.x * (kWarps / group) + w) * deal.share;
       if (first < before || first >= end) continue;
-      const int unit = int((first - before) / places);
+      const int unit = int(quotient(first - before, places));
       u.r = r;
       u.h = unit / chunks;
       u.c = unit % chunks;
@@ -309,12 +323,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   if (my_first >= deal.total) return;   // a whole CTA, or a warp that meets no other again
 
   uint8_t* const ring = smem + warp * (S::kStages * S::kStage);
-  float* const join = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kStage);
-  uint32_t* const sq = reinterpret_cast<uint32_t*>(join + warp * S::kRows * S::kJoinRow);
+  uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + kWarps * S::kStages * S::kStage + warp * S::kQueryBytes);
   const uint32_t bar0 = ptx::smem_u32(&bars[warp][0]), ring0 = ptx::smem_u32(ring);
-  int fill = 0, stage = 0;       // next stage to fill, to take
-  int in_flight = 0;             // stages filled and not taken
-  uint32_t phase = 0, usable_ring = 0;   // two bits per stage: which of its records may be looked at
+  int stage = 0, in_flight = 0;          // next stage to take; stages filled and not taken
+  uint32_t phases = 0, usable_ring = 0;  // a bit per stage; two bits per stage: which of its records may be looked at
   bool dead = false;
 
   for (Unit u = starts[deal.warps ? warp : 0]; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
@@ -322,76 +334,83 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     const int end = int(min((long long)u.x.tiles, my_end - u.place - deal.cost));
     if (end <= begin) continue;
 
-    // ---- the copies.  The lanes know the records of the warp's next 16 tiles: lane 2 i + b the
-    // b-th record of the i-th.
-    int it = begin + rank, held = -1;
-    uint32_t block = 0, usable = 0;
-    auto issue = [&]() {
-      if (it >= end || dead) return;
-      if (held < 0 || it >= held + 16 * group) {
-        held = it;
-        const int tile = it + group * (lane >> 1);
-        bool ok = false;
-        if (tile < end) {
-          const int e0 = (tile < u.x.sink_t ? tile : tile - u.x.sink_t + u.x.lo_t) * kTile + (lane & 1) * 16;
-          if (e0 < u.x.n && (e0 + 15 >= u.x.lo || e0 < u.x.sinks)) {
-            const int page = a.page_table[(int64_t)u.r * a.page_stride + (e0 >> a.page_shift)];
-            const int64_t b = ((int64_t)page << (a.page_shift - 4)) + ((e0 & ((1 << a.page_shift) - 1)) >> 4);
-            ok = page >= 0 && b < (a.num_slots >> 4);
-            if (!ok) set_status(a.status, UPF_ERR_INVALID_ARG);
-            block = uint32_t(b);
-          }
-        }
-        usable = __ballot_sync(0xFFFFFFFFu, ok);
-      }
-      const int src = (it - held) / group;
-      const uint32_t two = (usable >> (2 * src)) & 3u;
-      usable_ring = (usable_ring & ~(3u << (2 * fill))) | (two << (2 * fill));
-      if ((lane >> 1) == src) {
-        const uint32_t bar = bar0 + 8 * fill;
-        if ((lane & 1) == 0) ptx::mbar_arrive_expect_tx(bar, S::kRecord * __popc(two));
-        if ((two >> (lane & 1)) & 1u)
-          ptx::bulk_load(ring0 + fill * S::kStage + (lane & 1) * S::kRecord,
-                         a.data + ((int64_t)block * a.H + u.h) * S::kRecord, S::kRecord, bar);
-      }
-      __syncwarp();
-      it += group;
-      ++in_flight;
-      if (++fill == S::kStages) fill = 0;
-    };
-    for (int s = 0; s < S::kStages; ++s) issue();
-
-    // ---- the unit's rows
+    // ---- the unit's rows, asked for before the copies so that they do not queue behind them
     const int row0 = u.c * S::kRows, rows = u.x.q_len * a.gamma;   // rows of the request
     const int base = u.x.n - u.x.q_len;                            // position of query 0
-    uint32_t qf[S::kQueryInSmem ? 1 : S::kParts * S::kSteps][NT][2];
-    float f[NT][2];          // logit factor of rows 2 t4, 2 t4 + 1 of each eight
+    constexpr int kWords = S::kPart / 8;   // 32-bit words of a lane's quarter of a part
+    uint32_t raw[NT][S::kParts][kWords];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int rho = row0 + nt * 8 + g;
       const bool real = rho < rows;
       const int i = real ? rho / a.gamma : 0, j = real ? rho - i * a.gamma : 0;
       const T* src = static_cast<const T*>(a.q) + (int64_t)(u.x.q0 + i) * a.q_stride + (int)a.qhead[u.h * a.gamma + j] * kDim;
-      constexpr int kWords = S::kPart / 8;   // 32-bit words of this lane's quarter of a part
-      uint32_t w[S::kParts][kWords];
-      float amax = 0.f;
 #pragma unroll
       for (int p = 0; p < S::kParts; ++p) {
         const uint4* v = reinterpret_cast<const uint4*>(src + p * 128 + t4 * (S::kPart / 4));
 #pragma unroll
         for (int x = 0; x < kWords / 4; ++x) {
           const uint4 y = real ? v[x] : make_uint4(0, 0, 0, 0);
-          w[p][4 * x] = y.x;
-          w[p][4 * x + 1] = y.y;
-          w[p][4 * x + 2] = y.z;
-          w[p][4 * x + 3] = y.w;
+          raw[nt][p][4 * x] = y.x;
+          raw[nt][p][4 * x + 1] = y.y;
+          raw[nt][p][4 * x + 2] = y.z;
+          raw[nt][p][4 * x + 3] = y.w;
         }
       }
+    }
+
+    // ---- the copies.  The lanes know the records of the warp's next 16 tiles: lane 2 i + b the
+    // b-th record of the i-th.
+    int it = begin + rank, held = INT_MIN / 2;
+    const uint8_t* record = nullptr;
+    uint32_t usable = 0;
+    auto entry_of = [&](int t) { return (t < u.x.sink_t ? t : t - u.x.sink_t + u.x.lo_t) * kTile; };
+    auto issue = [&](int s) {   // the next tile into stage s
+      if (it >= end || dead) return;
+      int src = (it - held) >> lg;
+      if (src >= 16) {
+        held = it;
+        src = 0;
+        const int tile = it + ((lane >> 1) << lg);
+        bool ok = false;
+        if (tile < end) {
+          const int e0 = entry_of(tile) + (lane & 1) * 16;
+          if (e0 < u.x.n && (e0 + 15 >= u.x.lo || e0 < u.x.sinks)) {
+            const int page = a.page_table[(int64_t)u.r * a.page_stride + (e0 >> a.page_shift)];
+            const int64_t b = ((int64_t)page << (a.page_shift - 4)) + ((e0 & ((1 << a.page_shift) - 1)) >> 4);
+            ok = page >= 0 && b < (a.num_slots >> 4);
+            if (!ok) set_status(a.status, UPF_ERR_INVALID_ARG);
+            record = a.data + (b * a.H + u.h) * S::kRecord;
+          }
+        }
+        usable = __ballot_sync(0xFFFFFFFFu, ok);
+      }
+      const uint32_t two = (usable >> (2 * src)) & 3u;
+      usable_ring = (usable_ring & ~(3u << (2 * s))) | (two << (2 * s));
+      if ((lane >> 1) == src) {
+        const uint32_t bar = bar0 + 8 * s;
+        if ((lane & 1) == 0) ptx::mbar_arrive_expect_tx(bar, two == 3u ? 2 * S::kRecord : two ? S::kRecord : 0);
+        if ((two >> (lane & 1)) & 1u)
+          ptx::bulk_load(ring0 + s * S::kStage + (lane & 1) * S::kRecord, record, S::kRecord, bar);
+      }
+      it += group;
+      ++in_flight;
+    };
+    for (int s = 0; s < S::kStages; ++s) issue(s);
+    stage = 0;
+    __syncwarp();
+
+    // ---- the rows as operand B, divided by the power of two of their largest element
+    uint32_t qf[S::kQueryInSmem ? 1 : S::kParts * S::kSteps][NT][2];
+    float f[NT][2];          // logit factor of rows 2 t4, 2 t4 + 1 of each eight
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float amax = 0.f;
 #pragma unroll
       for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
         for (int x = 0; x < kWords; ++x) {
-          const float2 y = kv::pair_to_float2(w[p][x], static_cast<const T*>(nullptr));
+          const float2 y = kv::pair_to_float2(raw[nt][p][x], static_cast<const T*>(nullptr));
           amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
         }
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
         for (int x = 0; x < kWords; ++x) {
-          const float2 y = kv::pair_to_float2(w[p][x], static_cast<const T*>(nullptr));
+          const float2 y = kv::pair_to_float2(raw[nt][p][x], static_cast<const T*>(nullptr));
           const uint32_t v = pack_f16(y.x * down, y.y * down);
           if constexpr (S::kQueryInSmem) {
             sq[(((p * S::kSteps + x / 2) * NT + nt) * 32 + lane) * 2 + (x & 1)] = v;   // read back by this lane
@@ -437,40 +456,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         for (int mt = 0; mt < S::kParts * S::kSteps; ++mt) o[mt][nt][b] = o[mt][nt][b + 2] = 0.f;
       }
 
-    for (int t = begin + rank; t < end; t += group) {
-      if (in_flight > 0) {
-        if (!ptx::mbar_wait_poll(bar0 + 8 * stage, phase, dead ? kDefaultWaitCycles : a.wait_limit, 64)) {
-          // a copy did not come in time: no more work, the warp's own copies are waited for
-          dead = true;
-          if (lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
-          ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
-        }
-        dead = __any_sync(0xFFFFFFFFu, dead);
-      }
-      if (dead) {
-        if (in_flight > 0) {
-          --in_flight;
-          if (++stage == S::kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-        continue;
-      }
-      const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
-      const uint8_t* const rec = ring + stage * S::kStage;
-      const int e0 = (t < u.x.sink_t ? t : t - u.x.sink_t + u.x.lo_t) * kTile;
-      const bool whole = two == 3u && e0 + kTile - 1 <= p_min &&
-                         (a.window == 0 || p_max - e0 < a.window || e0 + kTile <= a.sinks);
+    // One tile from the records at `rec`; masked: some row does not see some entry of it, or a record of
+    // it may not be looked at (bits of `two`).
+    auto work = [&](auto masked, const uint8_t* rec, int e0, uint32_t two) {
+      constexpr bool kMasked = decltype(masked)::value;
       // ---- logits: S^T[entry][row]
       float s[2][NT][4];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint8_t* const rb = rec + b * S::kRecord;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[b][nt][i] = 0.f;
 #pragma unroll
         for (int p = 0; p < S::kParts; ++p) {
           constexpr int kW = S::kPart / 32;   // words of a lane's quarter row: 2 or 4
@@ -509,20 +503,24 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
               const int step = p * S::kSteps + 2 * x + st;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
+                uint32_t bf[2];
                 if constexpr (S::kQueryInSmem) {
                   const uint2 y = reinterpret_cast<const uint2*>(sq)[(step * NT + nt) * 32 + lane];
-                  const uint32_t bf[2] = {y.x, y.y};
-                  mma_f16(s[b][nt], af, bf);
+                  bf[0] = y.x;
+                  bf[1] = y.y;
                 } else {
-                  mma_f16(s[b][nt], af, qf[step][nt]);
+                  bf[0] = qf[step][nt][0];
+                  bf[1] = qf[step][nt][1];
                 }
+                if (step == 0) mma_f16_zero(s[b][nt], af, bf);
+                else mma_f16(s[b][nt], af, bf);
               }
             }
           }
         }
       }
       // ---- weights, in f16 as operand B of the second product
-      if (!whole) {
+      if constexpr (kMasked) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -598,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
             }
             uint32_t raw = *reinterpret_cast<const uint16_t*>(rb + 17 * kDim + p * S::kPart + half * (S::kPart / 2) +
                                                               (kW == 2 ? g : g >> 1) * 8 + 2 * t4);
-            if (!whole) {
+            if constexpr (kMasked) {
               // 0 * NaN would reach the rows that do not see the entry: take the scale as 0 and
               // give the NaN to the rows that do see it below
               if ((raw & 0x7Fu) == 0x7Fu) {
@@ -631,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
           }
         }
       }
-      if (!whole && __any_sync(0xFFFFFFFFu, bad)) {
+      if (kMasked && __any_sync(0xFFFFFFFFu, bad)) {
         for (int b = 0; b < 2; ++b)
           for (int row = 0; row < 16; ++row) {
             const int e = e0 + 16 * b + row;
@@ -650,13 +648,30 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
             }
           }
       }
-      --in_flight;
-      if (++stage == S::kStages) {
-        stage = 0;
-        phase ^= 1;
+    };
+
+    // tiles [whole0, whole1) lie inside every row's window and before every row's position
+    const int whole1 = u.x.sink_t - u.x.lo_t + (p_min + 1) / kTile;
+    const int whole0 = u.x.sink_t - u.x.lo_t + (a.window ? (max(0, p_max - a.window + 1) + kTile - 1) / kTile : 0);
+    for (int t = begin + rank; t < end; t += group) {
+      const bool late = dead || !ptx::mbar_wait_poll(bar0 + 8 * stage, (phases >> stage) & 1u, a.wait_limit, 64);
+      if (__any_sync(0xFFFFFFFFu, late)) {
+        // a copy did not come in time: no more work, the warp's own copies are waited for
+        if (!dead && lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
+        dead = true;
+        if (in_flight == 0) break;
+        ptx::mbar_wait(bar0 + 8 * stage, (phases >> stage) & 1u, kDefaultWaitCycles);
+      } else {
+        const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
+        const uint8_t* const rec = ring + stage * S::kStage;
+        if (two == 3u && t >= whole0 && t < whole1) work(std::false_type(), rec, 0, two);
+        else work(std::true_type(), rec, entry_of(t), two);
       }
+      --in_flight;
+      phases ^= 1u << stage;
       __syncwarp();
-      issue();
+      issue(stage);
+      if (++stage == S::kStages) stage = 0;
     }
 
     // ---- write the unit, or this worker's part of it
@@ -664,8 +679,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     const size_t part = (size_t)2 * worker + (goes_on ? 1 : 0);
     if (goes_on && lane == 0) {
       Shared note;
-      note.first = int((u.place + deal.cost) / deal.share);
-      note.last = int((u.place + deal.cost + u.x.tiles - 1) / deal.share);
+      note.first = int(quotient(u.place + deal.cost, deal.share));
+      note.last = int(quotient(u.place + deal.cost + u.x.tiles - 1, deal.share));
       note.h = u.h;
       note.row0 = row0;
       note.rows = rows;
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
               if (p) x[i] = o[S::kSteps + mt][nt][i];
             x[i] *= scale[nt][i & 1];
           }
-          float* const dst = join + (warp * S::kRows + nt * 8 + 2 * t4) * S::kJoinRow + mt * 16 + g * 2;
+          float* const dst = reinterpret_cast<float*>(ring) + (nt * 8 + 2 * t4) * S::kJoinRow + mt * 16 + g * 2;
           *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[2]);
           *reinterpret_cast<float2*>(dst + S::kJoinRow) = make_float2(x[1], x[3]);
         }
@@ -777,7 +792,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(join + (w * S::kRows + row) * S::kJoinRow + 2 * y);
+          const float2 v = *reinterpret_cast<const float2*>(smem + w * (S::kStages * S::kStage) +
+                                                            (row * S::kJoinRow + 2 * y) * 4);
           sum.x += v.x;
           sum.y += v.y;
         }
@@ -795,14 +811,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         }
       }
     }
-    __syncthreads();   // the join buffer, sh_m, sh_l, sh_top and sh_all are free again
-  }
-  for (; in_flight > 0; --in_flight) {   // only after a wait that ran out
-    ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
-    if (++stage == S::kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
+    // the rings take copies again, sh_m, sh_l, sh_top and sh_all new values
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
   }
 }
 
