@@ -153,8 +153,8 @@ const char* upf_status_name(upf_status s);
 /* Thread-local message describing the last failed call on this thread ("" if none). */
 const char* upf_last_error(void);
 
-/* Create a context on `device` (allocates a few bytes of device memory for the
- * status word).  *out receives the context.  Errors: INVALID_ARG (out NULL or
+/* Create a context on `device` (allocates some 32 KiB of device memory for the
+ * status word and counters).  *out receives the context.  Errors: INVALID_ARG (out NULL or
  * bad device), CUDA. */
 upf_status upf_create(upf_ctx** out, int device);
 

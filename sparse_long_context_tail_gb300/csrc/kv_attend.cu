@@ -23,9 +23,9 @@
 // memory, or, where units are short, a single warp that shares nothing.  Every
 // warp has its own ring of records filled by bulk copies (two records of 18 d
 // bytes a tile), its own reference and sums.  A unit that lies in one worker's
-// share is written out at once; others leave a part (reference, sum, weighted sum,
-// all fp32) per worker in the workspace, which kv_attend_join_kernel adds up in a
-// fixed order, so results repeat bit for bit.
+// share is written out at once; of others every worker leaves its part (reference,
+// sum, weighted sum, all fp32) in the workspace, and the last one to do so adds the
+// parts up, in worker order whoever it is, so results repeat bit for bit.
 //
 // Arithmetic.  A code times its scale has at most six significant bits and is
 // exact in f16, and so is a query after division by the power of two of its
@@ -118,13 +118,20 @@ struct Deal {
 
 // Each thread looks at requests [i * per, (i + 1) * per); `before` are the places
 // of the requests before them.
-__device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&warp_sums)[kWarps], long long& before) {
+// `mine`: the first of the thread's requests; `empty`: some request has no tiles.
+__device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&warp_sums)[kWarps], long long& before,
+                         Request& mine, bool& empty) {
   long long tiles = 0, units = 0;
+  bool none = false;
   for (int j = 0; j < per; ++j) {
     const int r = threadIdx.x * per + j;
     if (r >= a.R) break;
     const Request x = load_request(a, r);
-    if (x.tiles == 0) continue;
+    if (j == 0) mine = x;
+    if (x.tiles == 0) {
+      none = true;
+      continue;
+    }
     const long long u = (long long)a.H * chunks_of(a, x, rows);
     units += u;
     tiles += u * x.tiles;
@@ -140,7 +147,7 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&w
     }
   }
   if (lane == 31) warp_sums[warp] = make_longlong2(t, u);
-  __syncthreads();
+  empty = __syncthreads_or(none);
   t -= tiles;
   u -= units;
   long long all_t = 0, all_u = 0;
@@ -166,21 +173,20 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&w
 // The workspace.  A worker has at most two units that others work on too: the one
 // its share begins in the middle of, and the one that goes on after its share.
 // The part of the latter (or of a unit that does both) is at 2 w + 1, that of the
-// former at 2 w.  The workers first .. last - 1 of a shared unit, for which it is the
-// latter, note it for the join, each warp of theirs its portion.
-struct Shared {
-  int first, last;        // workers of the unit (first < 0: nothing to join)
-  int h, row0, rows, q0;  // kv head, first row of the chunk, rows of the request, its first row in q
-  int portion, portions;
-};
-
+// former at 2 w.
 struct Parts {
   float* o;         // [2 * workers][rows][d]
   float2* ml;       // [2 * workers][rows]: reference, sum
-  Shared* shared;   // [warps of the grid]
 };
 
-// ------------------------------------------------------------ main kernel --
+// Parts are counted in by at most kFan workers at a time, so that no worker has to
+// add up more than kFan of them: workers first + kFan i .. of a unit count at the
+// first of them, whose part then stands for them all, and these count at `first`
+// in the second half of the counters.  The unit that goes on after a worker is the
+// only one that counts at it.  Counters are zero between calls.
+constexpr int kFan = 16;
+
+// ---------------------------------------------------------------- kernel --
 
 template <int kDim, int NT>
 struct Shape {
@@ -199,6 +205,13 @@ struct Shape {
   static constexpr int kQueryBytes = kQueryInSmem ? kRows * kDim * 2 : 0;   // of a warp
   static constexpr int kSmem = kWarps * (kStages * kStage + kQueryBytes);
   static constexpr int kCtas = kCtasPerSm * kPlanSMs;
+  static constexpr int kMaxWorkers = kCtas * kWarps;
+  static_assert(2 * kMaxWorkers <= kKvCounters, "counters of the context");
+  // The part that stands for the kFan workers from w on of a unit that begins at worker `first`
+  // and has more.  Of such units, at most one has a later worker and one its first in a
+  // run of kFan workers.
+  static constexpr int kPartSlots = 2 * kMaxWorkers + 2 * (kMaxWorkers / kFan + 1);
+  __device__ static int group_part(int w, int first) { return 2 * kMaxWorkers + 2 * (w / kFan) + (w == first); }
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -263,6 +276,131 @@ __device__ __forceinline__ float lse_of(float top, float all) {
   return all == 0.f ? -INFINITY : (top - kWeightExp + log2f(all)) * kLn2;
 }
 
+// Adds up n parts of a unit's workers first .. last in order, by `count` threads: those of
+// workers w0, w0 + 1, ... or, if `groups`, those that stand for kFan workers each.
+// The sum goes to out and lse or, if `to` >= 0, to that part.  2^k lanes add up
+// four dims of a row, each every 2^k-th part; what they load does not hang on what
+// they loaded before.
+template <typename T, int kDim, int NT>
+__device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Unit& u, int first, int last, int w0, int n,
+                          bool groups, int to, int thread, int count) {
+  using S = Shape<kDim, NT>;
+  constexpr int kBatch = 4;
+  const int row0 = u.c * S::kRows, rows = min(S::kRows, u.x.q_len * a.gamma - row0), outputs = rows * (kDim / 4);
+  int lanes = 1;
+  while (lanes < 32 && 2 * lanes * outputs <= count && lanes < n) lanes *= 2;
+  const int sub = thread & (lanes - 1);
+  // every lane makes every round: the shuffles need all of them
+  for (int at0 = 0; at0 < outputs; at0 += count / lanes) {
+    const int i = at0 + thread / lanes;
+    const bool mine = i < outputs;
+    const int row = mine ? i / (kDim / 4) : 0, j = mine ? i % (kDim / 4) : 0;
+    float m = -FLT_MAX, all = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = sub; k0 < n; k0 += kBatch * lanes) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int k = k0 + x * lanes, w = groups ? w0 + k * kFan : w0 + k;
+        ml[x] = make_float2(-FLT_MAX, 0.f);
+        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < n) {   // from L2: other SMs wrote them
+          const size_t at = (size_t)(groups && w < last ? S::group_part(w, first) : 2 * w + (w < last)) * S::kRows + row;
+          ml[x] = __ldcg(parts.ml + at);
+          v[x] = __ldcg(reinterpret_cast<const float4*>(parts.o + at * kDim) + j);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
+      const float c = ptx::ex2_approx(m - top);
+      m = top;
+      all *= c;
+      sum.x *= c;
+      sum.y *= c;
+      sum.z *= c;
+      sum.w *= c;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const float y = ptx::ex2_approx(ml[x].x - top);
+        all += ml[x].y * y;
+        sum.x += v[x].x * y;
+        sum.y += v[x].y * y;
+        sum.z += v[x].z * y;
+        sum.w += v[x].w * y;
+      }
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), top = fmaxf(m, m2);
+      const float c = ptx::ex2_approx(m - top);
+      m = top;
+      all *= c;
+      sum.x *= c;
+      sum.y *= c;
+      sum.z *= c;
+      sum.w *= c;
+      all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+      sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, d);
+      sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, d);
+      sum.z += __shfl_xor_sync(0xFFFFFFFFu, sum.z, d);
+      sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, d);
+    }
+    if (!mine || sub) continue;
+    if (to >= 0) {
+      const size_t at = (size_t)to * S::kRows + row;
+      reinterpret_cast<float4*>(parts.o + at * kDim)[j] = sum;
+      if (j == 0) parts.ml[at] = make_float2(m, all);
+      continue;
+    }
+    const int rho = row0 + row, q = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - q * a.gamma];
+    const int64_t at = u.x.q0 + q;
+    const float inv = all == 0.f ? 0.f : a.v_mul / all;
+    uint2 w;
+    w.x = kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
+    w.y = kv::float2_to_pair(sum.z * inv, sum.w * inv, static_cast<const T*>(nullptr));
+    reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim)[j] = w;
+    if (a.lse && j == 0) a.lse[at * a.Hq + head] = lse_of(m, all);
+  }
+}
+
+// One more at the counter: what this CTA's threads wrote before the barrier before
+// this is seen by whoever reads the counter after.
+__device__ __forceinline__ int count_in(int32_t* counter) {
+  int n;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+  return n;
+}
+
+// Counts this worker's part of a unit in; the worker that completes the count adds
+// the parts up.  arrive(counter): everything that the worker's threads wrote is out,
+// and how many came before.
+template <typename T, int kDim, int NT, typename Arrive>
+__device__ void finish_unit(const KvAttendArgs& a, const Parts& parts, const Unit& u, const Deal& deal, int worker, int thread,
+                            int count, Arrive&& arrive) {
+  using S = Shape<kDim, NT>;
+  const long long place = u.place + deal.cost;
+  const int first = int(quotient(place, deal.share)), last = int(quotient(place + u.x.tiles - 1, deal.share));
+  const int n = last - first + 1;
+  int32_t* counter = a.counters + first;
+  int w0 = first, members = n;
+  if (n > kFan) {
+    w0 = first + (worker - first) / kFan * kFan;
+    members = min(kFan, last - w0 + 1);
+    if (members > 1) {
+      if (arrive(a.counters + w0) != members - 1) return;
+      if (thread == 0) a.counters[w0] = 0;
+      add_parts<T, kDim, NT>(a, parts, u, first, last, w0, members, false, S::group_part(w0, first), thread, count);
+    }
+    counter = a.counters + S::kMaxWorkers + first;
+    w0 = first;
+    members = (n + kFan - 1) / kFan;
+  }
+  if (arrive(counter) != members - 1) return;
+  if (thread == 0) *counter = 0;
+  add_parts<T, kDim, NT>(a, parts, u, first, last, w0, members, n > kFan, -1, thread, count);
+}
+
 template <typename T, int kDim, int NT>
 __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_attend_kernel(const KvAttendArgs a, const Parts parts) {
   using S = Shape<kDim, NT>;
@@ -273,12 +411,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   __shared__ float sh_m[kWarps][S::kRows], sh_l[kWarps][S::kRows], sh_top[S::kRows], sh_all[S::kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  pdl_trigger();
+  __shared__ int sh_count;
+  if (lane == 0)
+    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp][s]), 1);
+  ptx::fence_barrier_init();
+  pdl_wait();
 
   // ---- this worker's share
   const int per = (a.R + kThreads - 1) / kThreads;
   long long before;
-  const Deal deal = deal_out(a, S::kRows, per, warp_sums, before);
+  Request mine;
+  bool empty;
+  const Deal deal = deal_out(a, S::kRows, per, warp_sums, before, mine, empty);
   const int lg = deal.warps ? 0 : kLogWarps, group = 1 << lg, rank = deal.warps ? 0 : warp;   // warps of a worker; which this is
   const int worker = deal.warps ? blockIdx.x * kWarps + warp : blockIdx.x;
   for (int j = 0; j < per; ++j) {
@@ -286,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     const int r = threadIdx.x * per + j;
     if (r >= a.R) break;
     Unit u;
-    u.x = load_request(a, r);
+    u.x = j ? load_request(a, r) : mine;
     if (u.x.tiles == 0) continue;
     const int chunks = chunks_of(a, u.x, S::kRows), places = u.x.tiles + deal.cost;
     const long long end = before + (long long)places * a.H * chunks;
@@ -303,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     before = end;
   }
   // rows that see nothing because their request has no entries
-  for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
+  for (int r = blockIdx.x; empty && r < a.R; r += gridDim.x) {
     const Request x = load_request(a, r);
     if (x.tiles) continue;
     for (int i = threadIdx.x; i < x.q_len * a.Hq * (kDim / 2); i += kThreads) {
@@ -313,11 +457,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       if (a.lse && i % (kDim / 2) == 0) a.lse[at * a.Hq + h] = -INFINITY;
     }
   }
-  if (lane == 0) {
-    parts.shared[blockIdx.x * kWarps + warp].first = -1;
-    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp][s]), 1);
-  }
-  ptx::fence_barrier_init();
   __syncthreads();
   const long long my_first = worker * deal.share, my_end = min(my_first + deal.share, deal.total);
   if (my_first >= deal.total) return;   // a whole CTA, or a warp that meets no other again
@@ -677,18 +816,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     // ---- write the unit, or this worker's part of it
     const bool goes_on = end < u.x.tiles, alone = !goes_on && begin == 0;
     const size_t part = (size_t)2 * worker + (goes_on ? 1 : 0);
-    if (goes_on && lane == 0) {
-      Shared note;
-      note.first = int(quotient(u.place + deal.cost, deal.share));
-      note.last = int(quotient(u.place + deal.cost + u.x.tiles - 1, deal.share));
-      note.h = u.h;
-      note.row0 = row0;
-      note.rows = rows;
-      note.q0 = u.x.q0;
-      note.portion = (worker - note.first) * group + rank;
-      note.portions = (note.last - note.first) * group;
-      parts.shared[blockIdx.x * kWarps + warp] = note;
-    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -734,7 +861,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
             else if (a.lse) a.lse[at * a.Hq + head] = lse_of(m, all);
           }
         }
-      __syncwarp();   // sq is free again
+      __syncwarp();   // sq is free again, the part is written
+      if (!alone)
+        finish_unit<T, kDim, NT>(a, parts, u, deal, worker, lane, 32, [&](int32_t* counter) {
+          int n = 0;
+          __syncwarp();
+          if (lane == 0) n = count_in(counter);
+          return __shfl_sync(0xFFFFFFFFu, n, 0);
+        });
       continue;
     }
 #pragma unroll
@@ -814,100 +948,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     // the rings take copies again, sh_m, sh_l, sh_top and sh_all new values
     ptx::fence_proxy_async_smem();
     __syncthreads();
-  }
-}
-
-// ------------------------------------------------------------------- join --
-
-// Adds up the parts of shared units.  Each warp of the workers that a unit goes on
-// after takes its portion of the outputs (four dims each), so that all of them
-// work on a unit with many parts.  2^k lanes add up one output, each every 2^k-th
-// part; what they load does not hang on what they loaded before.
-template <typename T, int kDim, int NT>
-__global__ void __launch_bounds__(kThreads) kv_attend_join_kernel(const KvAttendArgs a, const Parts parts) {
-  using S = Shape<kDim, NT>;
-  constexpr int kBatch = 4;
-  const int lane = threadIdx.x & 31;
-  pdl_wait();
-  const Shared u = parts.shared[blockIdx.x * kWarps + (threadIdx.x >> 5)];
-  if (u.first < 0) return;
-  const int rows = min(S::kRows, u.rows - u.row0), outputs = rows * (kDim / 4);
-  const int each = (outputs + u.portions - 1) / u.portions;
-  int lanes = 32;
-  while (lanes > 1 && (lanes * each > 32 || lanes > u.last - u.first + 1)) lanes >>= 1;
-  const int sub = lane & (lanes - 1);
-  const int from = u.portion * each, to = min(outputs, from + each);
-  // every lane makes every round: the shuffles need all of them
-  for (int at0 = from; at0 < to; at0 += 32 / lanes) {
-    const int i = at0 + lane / lanes;
-    const bool mine = i < to;
-    const int row = mine ? i / (kDim / 4) : 0, j = mine ? i % (kDim / 4) : 0;
-    float m = -FLT_MAX, all = 0.f;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w0 = u.first + sub; w0 <= u.last; w0 += kBatch * lanes) {
-      float2 ml[kBatch];
-      float4 v[kBatch];
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const int w = w0 + x * lanes;
-        ml[x] = make_float2(-FLT_MAX, 0.f);
-        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w <= u.last) {
-          const size_t at = (size_t)(2 * w + (w < u.last)) * S::kRows + row;
-          ml[x] = parts.ml[at];
-          v[x] = reinterpret_cast<const float4*>(parts.o + at * kDim)[j];
-        }
-      }
-      float top = m;
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
-      const float k = ptx::ex2_approx(m - top);
-      m = top;
-      all *= k;
-      sum.x *= k;
-      sum.y *= k;
-      sum.z *= k;
-      sum.w *= k;
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const float y = ptx::ex2_approx(ml[x].x - top);
-        all += ml[x].y * y;
-        sum.x += v[x].x * y;
-        sum.y += v[x].y * y;
-        sum.z += v[x].z * y;
-        sum.w += v[x].w * y;
-      }
-    }
-    for (int d = 1; d < lanes; d <<= 1) {
-      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), top = fmaxf(m, m2);
-      const float k = ptx::ex2_approx(m - top);
-      m = top;
-      all *= k;
-      sum.x *= k;
-      sum.y *= k;
-      sum.z *= k;
-      sum.w *= k;
-      all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-      sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, d);
-      sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, d);
-      sum.z += __shfl_xor_sync(0xFFFFFFFFu, sum.z, d);
-      sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, d);
-    }
-    if (!mine || sub) continue;
-    const int rho = u.row0 + row, q = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - q * a.gamma];
-    const int64_t at = u.q0 + q;
-    const float inv = all == 0.f ? 0.f : a.v_mul / all;
-    uint2 w;
-    w.x = kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
-    w.y = kv::float2_to_pair(sum.z * inv, sum.w * inv, static_cast<const T*>(nullptr));
-    reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim)[j] = w;
-    if (a.lse && j == 0) a.lse[at * a.Hq + head] = lse_of(m, all);
+    if (!alone)
+      finish_unit<T, kDim, NT>(a, parts, u, deal, worker, threadIdx.x, kThreads, [&](int32_t* counter) {
+        __syncthreads();
+        if (threadIdx.x == 0) sh_count = count_in(counter);
+        __syncthreads();
+        return sh_count;
+      });
   }
 }
 
 template <int kDim, int NT>
 constexpr size_t part_rows() {
-  return (size_t)2 * Shape<kDim, NT>::kCtas * kWarps * Shape<kDim, NT>::kRows;
+  return (size_t)Shape<kDim, NT>::kPartSlots * Shape<kDim, NT>::kRows;
 }
 
 template <typename T, int kDim, int NT>
@@ -916,12 +969,9 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t s) {
   Parts parts;
   parts.o = static_cast<float*>(a.ws);
   parts.ml = reinterpret_cast<float2*>(parts.o + part_rows<kDim, NT>() * kDim);
-  parts.shared = reinterpret_cast<Shared*>(parts.ml + part_rows<kDim, NT>());
   cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, kDim, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kv_attend_kernel<T, kDim, NT>, S::kCtas, kThreads, S::kSmem, s, false, a, parts);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kv_attend_join_kernel<T, kDim, NT>, S::kCtas, kThreads, 0, s, true, a, parts);
+  return launch_kernel(kv_attend_kernel<T, kDim, NT>, S::kCtas, kThreads, S::kSmem, s, true, a, parts);
 }
 
 template <int kDim>
@@ -932,8 +982,7 @@ cudaError_t launch_dim(const KvAttendArgs& a, bool f16, cudaStream_t s) {
 
 template <int kDim, int NT>
 constexpr size_t ws_bytes() {
-  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2)) +
-         (size_t)Shape<kDim, NT>::kCtas * kWarps * sizeof(Shared);
+  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2));
 }
 
 template <int kDim>

@@ -18,7 +18,7 @@
 struct upf_ctx {
   int device;
   int num_sms;
-  int32_t* status_dev;  // [64] device words; [0] = status
+  int32_t* status_dev;  // [64 + kKvCounters] device words; [0] = status, from [64] on the cache attention's counters
   long long wait_limit = 0;  // pipeline waits of the scoring kernels, cycles (0: default)
   // tracing
   bool profiling = false;
@@ -849,11 +849,12 @@ upf_status upf_create(upf_ctx** out, int device) {
     delete c;
     return fail(UPF_ERR_UNSUPPORTED, "libupf is built for sm_103a; device %d is sm_%d%d", device, major, minor);
   }
-  if ((e = cudaMalloc(&c->status_dev, 64 * sizeof(int32_t))) != cudaSuccess) {
+  const size_t words = 64 + upf::kKvCounters;
+  if ((e = cudaMalloc(&c->status_dev, words * sizeof(int32_t))) != cudaSuccess) {
     delete c;
     return cuda_fail(e, "cudaMalloc(status)");
   }
-  if ((e = cudaMemset(c->status_dev, 0, 64 * sizeof(int32_t))) != cudaSuccess) {
+  if ((e = cudaMemset(c->status_dev, 0, words * sizeof(int32_t))) != cudaSuccess) {
     cudaFree(c->status_dev);
     delete c;
     return cuda_fail(e, "cudaMemset(status)");
@@ -1262,6 +1263,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   a.v_mul = std::ldexp(1.f, cache->v_exp);
   a.status = ctx->status_dev;
   a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
+  a.counters = ctx->status_dev + 64;
   a.ws = ws;
   int fill[upf::kMaxHeads] = {};
   for (int h = 0; h < a.Hq; ++h) {

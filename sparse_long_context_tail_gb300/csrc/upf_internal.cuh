@@ -175,6 +175,7 @@ struct HistoryArgs {
 };
 
 // The 4-bit KV cache (layout: kv_layout.cuh).
+constexpr int kKvCounters = 8192;    // words of the context that the cache attention counts in
 constexpr int kKvFewTokens = 1024;   // calls of at most this many tokens write without claiming their slots
 
 struct KvWriteArgs {
@@ -222,6 +223,7 @@ struct KvAttendArgs {
   float scale_log2;             // softmax scale * 2^k_exp * log2 e
   float v_mul;                  // 2^v_exp
   int32_t* status;
+  int32_t* counters;            // [kKvCounters] of the context, zero between calls
   long long wait_limit;
   void* ws;
   uint8_t qhead[kMaxHeads];     // q heads of kv head g at [g*gamma, (g+1)*gamma)
