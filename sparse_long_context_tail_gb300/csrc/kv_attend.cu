@@ -19,10 +19,14 @@
 // 32-entry runs that some row sees.  All units' tiles, in order, are dealt out to
 // the workers in equal shares, from the lengths in device memory: ragged batches
 // balance themselves and a captured call stays valid when the lengths change.  A
-// worker is a CTA, whose warps take its tiles in turn and are joined through shared
-// memory, or, where units are short, a single warp that shares nothing.  Every
-// warp has its own ring of records filled by bulk copies (two records of 18 d
-// bytes a tile), its own reference and sums.  A unit that lies in one worker's
+// worker is a CTA, whose teams take its tiles in turn and are joined through shared
+// memory, or, where units are short, a single team that shares nothing.  A team is
+// one warp, or as many as it takes for each to hold the weighted sums of its dims
+// in 32 registers a lane (128 dims of eight rows, 64 of sixteen), so that sixteen
+// warps fit an SM at every head size: each multiplies its dims of the queries and
+// keys, the team adds the logits up through shared memory, and each weighs its dims
+// of the values.  Every team has its own ring of records filled by bulk copies (two
+// records of 18 d bytes a tile).  A unit that lies in one worker's
 // share is written out at once; of others every worker leaves its part (reference,
 // sum, weighted sum, all fp32) in the workspace, and the last one to do so adds the
 // parts up, in worker order whoever it is, so results repeat bit for bit.
@@ -104,13 +108,13 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 
 // Cost of a unit in the dealing, in tiles, beside its tiles: the rows' load, the
 // first copies' latency and the writing out.
-constexpr int kUnitCostCta = 16, kUnitCostWarp = 4;
-// Workers are warps where units have fewer tiles than this on average.
+constexpr int kUnitCostCta = 16, kUnitCostTeam = 4;
+// Workers are teams where units have fewer tiles than this on average.
 constexpr int kShortUnit = 64;
 
 // How the tiles are dealt out.  Along the dealing a unit takes cost + tiles places.
 struct Deal {
-  bool warps;          // a worker is a warp
+  bool teams;          // a worker is a team
   int cost;            // of a unit
   long long total;     // places of all units
   long long share;     // places of a worker
@@ -119,7 +123,7 @@ struct Deal {
 // Each thread looks at requests [i * per, (i + 1) * per); `before` are the places
 // of the requests before them.
 // `mine`: the first of the thread's requests; `empty`: some request has no tiles.
-__device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&warp_sums)[kWarps], long long& before,
+__device__ Deal deal_out(const KvAttendArgs& a, int rows, int teams, int per, longlong2 (&warp_sums)[kWarps], long long& before,
                          Request& mine, bool& empty) {
   long long tiles = 0, units = 0;
   bool none = false;
@@ -161,12 +165,12 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int per, longlong2 (&w
     all_u += warp_sums[w].y;
   }
   Deal d;
-  d.warps = all_t < all_u * kShortUnit;
-  d.cost = d.warps ? kUnitCostWarp : kUnitCostCta;
+  d.teams = all_t < all_u * kShortUnit;
+  d.cost = d.teams ? kUnitCostTeam : kUnitCostCta;
   d.total = all_t + all_u * d.cost;
   before = t + u * d.cost;
-  const long long workers = d.warps ? (long long)gridDim.x * kWarps : gridDim.x;
-  d.share = max(quotient(d.total + workers - 1, workers), (long long)(d.warps ? 1 : kWarps));
+  const long long workers = d.teams ? (long long)gridDim.x * teams : gridDim.x;
+  d.share = max(quotient(d.total + workers - 1, workers), (long long)(d.teams ? 1 : teams));
   return d;
 }
 
@@ -191,21 +195,25 @@ constexpr int kFan = 16;
 template <int kDim, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kParts = kDim >= 128 ? kDim / 128 : 1;
-  static constexpr int kPart = kDim / kParts;          // dims per part: 64 or 128
-  static constexpr int kSteps = kPart / 16;            // mma steps over the dims of a part, and dim tiles of it
+  static constexpr int kPart = kDim >= 128 ? 128 : kDim;      // dims per part of a record
+  static constexpr int kSlice = NT == 1 ? kPart : 64;         // dims of a warp
+  static constexpr int kHalves = kPart / kSlice;              // slices of a part
+  static constexpr int kMembers = kDim / kSlice;              // warps of a team
+  static constexpr int kLogTeams = kLogWarps - (kMembers == 4 ? 2 : kMembers == 2 ? 1 : 0), kTeams = 1 << kLogTeams;
+  static constexpr int kSteps = kSlice / 16;                  // mma steps over a slice, and dim tiles of it
   static constexpr int kRecord = kv::record_bytes(kDim);
   static constexpr int kStage = 2 * kRecord;
-  static constexpr int kCtasPerSm = kDim * NT <= 128 ? 2 : 1;
-  static constexpr int kStages = kDim == 64 ? 6 : kDim == 128 ? 3 * NT : NT == 1 ? 3 : 2;
-  static constexpr bool kQueryInSmem = kDim * NT > 256;
-  static constexpr int kJoinRow = kPart + 4;           // floats; the pad spreads the rows over the banks
-  // At the end of a unit a warp's ring is empty and holds its rows for the join.
-  static_assert(kRows * kJoinRow * 4 <= kStages * kStage, "a warp's join rows fit its ring");
-  static constexpr int kQueryBytes = kQueryInSmem ? kRows * kDim * 2 : 0;   // of a warp
-  static constexpr int kSmem = kWarps * (kStages * kStage + kQueryBytes);
+  // two CTAs an SM: about 110 KB each
+  static constexpr int kCtasPerSm = 2;
+  static constexpr int kStages = kDim == 64 ? 6 : kMembers == 1 ? 3 : NT == 2 ? 5 : 2;
+  static constexpr int kRing = kStages * kStage;              // of a team
+  static constexpr int kExchange = kMembers > 1 ? 32 * 8 * NT * 4 : 0;   // a warp's logits of a tile
+  static constexpr int kJoinRow = kSlice + 4;                 // floats; the pad spreads the rows over the banks
+  // At the end of a unit a team's ring is empty and holds its warps' rows for the join.
+  static_assert(kRows * kJoinRow * 4 <= kRing / kMembers && kRing / kMembers % 16 == 0, "a warp's join rows fit its share of the ring");
+  static constexpr int kSmem = kTeams * kRing + kWarps * kExchange;
   static constexpr int kCtas = kCtasPerSm * kPlanSMs;
-  static constexpr int kMaxWorkers = kCtas * kWarps;
+  static constexpr int kMaxWorkers = kCtas * kTeams;
   static_assert(2 * kMaxWorkers <= kKvCounters, "counters of the context");
   // The part that stands for the kFan workers from w on of a unit that begins at worker `first`
   // and has more.  Of such units, at most one has a later worker and one its first in a
@@ -401,19 +409,47 @@ __device__ void finish_unit(const KvAttendArgs& a, const Parts& parts, const Uni
   add_parts<T, kDim, NT>(a, parts, u, first, last, w0, members, n > kFan, -1, thread, count);
 }
 
+// A team's barriers: one warp, or kMembers warps on the named barrier 1 + team.
+template <int kMembers>
+__device__ __forceinline__ void team_sync(int team) {
+  if constexpr (kMembers == 1) __syncwarp();
+  else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + team), "n"(32 * kMembers) : "memory");
+}
+
+// The same, and whether x holds in any thread of the team.
+template <int kMembers>
+__device__ __forceinline__ bool team_any(int team, bool x) {
+  if constexpr (kMembers == 1) {
+    return __any_sync(0xFFFFFFFFu, x);
+  } else {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(x)), "r"(1 + team), "n"(32 * kMembers)
+        : "memory");
+    return r != 0;
+  }
+}
+
 template <typename T, int kDim, int NT>
 __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_attend_kernel(const KvAttendArgs a, const Parts parts) {
   using S = Shape<kDim, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[kWarps][S::kStages];
+  __shared__ __align__(8) uint64_t bars[S::kTeams][S::kStages];
   __shared__ longlong2 warp_sums[kWarps];
-  __shared__ Unit starts[kWarps];
-  __shared__ float sh_m[kWarps][S::kRows], sh_l[kWarps][S::kRows], sh_top[S::kRows], sh_all[S::kRows];
+  __shared__ Unit starts[S::kTeams];
+  __shared__ float sh_m[S::kTeams][S::kRows], sh_l[S::kTeams][S::kRows], sh_top[S::kRows], sh_all[S::kRows];
+  __shared__ int sh_count[S::kTeams];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / S::kMembers, member = warp % S::kMembers;
+  const int part = member / S::kHalves, half = member % S::kHalves;   // this warp's slice
   const int g = lane >> 2, t4 = lane & 3;
-  __shared__ int sh_count;
-  if (lane == 0)
-    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[warp][s]), 1);
+  if (member == 0 && lane == 0)
+    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[team][s]), 1);
   ptx::fence_barrier_init();
   pdl_wait();
 
@@ -422,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   long long before;
   Request mine;
   bool empty;
-  const Deal deal = deal_out(a, S::kRows, per, warp_sums, before, mine, empty);
-  const int lg = deal.warps ? 0 : kLogWarps, group = 1 << lg, rank = deal.warps ? 0 : warp;   // warps of a worker; which this is
-  const int worker = deal.warps ? blockIdx.x * kWarps + warp : blockIdx.x;
+  const Deal deal = deal_out(a, S::kRows, S::kTeams, per, warp_sums, before, mine, empty);
+  const int lg = deal.teams ? 0 : S::kLogTeams, group = 1 << lg, rank = deal.teams ? 0 : team;   // teams of a worker; which this is
+  const int worker = deal.teams ? blockIdx.x * S::kTeams + team : blockIdx.x;
   for (int j = 0; j < per; ++j) {
     // the thread whose requests hold a worker's first place finds its unit
     const int r = threadIdx.x * per + j;
@@ -434,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     if (u.x.tiles == 0) continue;
     const int chunks = chunks_of(a, u.x, S::kRows), places = u.x.tiles + deal.cost;
     const long long end = before + (long long)places * a.H * chunks;
-    for (int w = 0; w < kWarps / group; ++w) {
-      const long long first = (long long)(blockIdx.x * (kWarps / group) + w) * deal.share;
+    for (int w = 0; w < S::kTeams / group; ++w) {
+      const long long first = (long long)(blockIdx.x * (S::kTeams / group) + w) * deal.share;
       if (first < before || first >= end) continue;
       const int unit = int(quotient(first - before, places));
       u.r = r;
@@ -459,16 +495,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   }
   __syncthreads();
   const long long my_first = worker * deal.share, my_end = min(my_first + deal.share, deal.total);
-  if (my_first >= deal.total) return;   // a whole CTA, or a warp that meets no other again
+  if (my_first >= deal.total) return;   // a whole CTA, or a team that meets no other again
 
-  uint8_t* const ring = smem + warp * (S::kStages * S::kStage);
-  uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + kWarps * S::kStages * S::kStage + warp * S::kQueryBytes);
-  const uint32_t bar0 = ptx::smem_u32(&bars[warp][0]), ring0 = ptx::smem_u32(ring);
+  uint8_t* const ring = smem + team * S::kRing;
+  uint8_t* const join = ring + member * (S::kRing / S::kMembers);
+  float4* const exchange = reinterpret_cast<float4*>(smem + S::kTeams * S::kRing + team * S::kMembers * S::kExchange) + lane;
+  const uint32_t bar0 = ptx::smem_u32(&bars[team][0]), ring0 = ptx::smem_u32(ring);
+  // where in a record this lane's keys, values and their scales are
+  const int k_at = part * (8 * S::kPart) + g * (S::kPart / 2) + t4 * (S::kPart / 8) + half * 8;
+  const int ks_at = 16 * kDim + g * (kDim / 16) + part * 8 + (S::kPart == 128 ? 2 * t4 + half : t4);
+  const int v_at = 8 * kDim + part * (8 * S::kPart) + lane * (S::kPart / 8) + half * 4;
+  const int vs_at = 17 * kDim + part * S::kPart + (S::kPart == 128 ? g : g >> 1) * 8 + 2 * t4;
+  const int dim0 = part * 128 + g * (S::kPart / 8) + half * 8;   // first of the lane's 2 kSteps dims of the output
   int stage = 0, in_flight = 0;          // next stage to take; stages filled and not taken
   uint32_t phases = 0, usable_ring = 0;  // a bit per stage; two bits per stage: which of its records may be looked at
   bool dead = false;
 
-  for (Unit u = starts[deal.warps ? warp : 0]; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
+  for (Unit u = starts[deal.teams ? team : 0]; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
     const int begin = int(max(0LL, my_first - u.place - deal.cost));
     const int end = int(min((long long)u.x.tiles, my_end - u.place - deal.cost));
     if (end <= begin) continue;
@@ -476,8 +519,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     // ---- the unit's rows, asked for before the copies so that they do not queue behind them
     const int row0 = u.c * S::kRows, rows = u.x.q_len * a.gamma;   // rows of the request
     const int base = u.x.n - u.x.q_len;                            // position of query 0
-    constexpr int kWords = S::kPart / 8;   // 32-bit words of a lane's quarter of a part
-    uint32_t raw[NT][S::kParts][kWords];
+    // Words of the lane's quarter of each slice, its own slice's first (the others count for the
+    // largest element only).
+    constexpr int kWords = S::kSlice / 8;
+    uint32_t raw[NT][S::kMembers][kWords];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int rho = row0 + nt * 8 + g;
@@ -485,8 +530,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       const int i = real ? rho / a.gamma : 0, j = real ? rho - i * a.gamma : 0;
       const T* src = static_cast<const T*>(a.q) + (int64_t)(u.x.q0 + i) * a.q_stride + (int)a.qhead[u.h * a.gamma + j] * kDim;
 #pragma unroll
-      for (int p = 0; p < S::kParts; ++p) {
-        const uint4* v = reinterpret_cast<const uint4*>(src + p * 128 + t4 * (S::kPart / 4));
+      for (int p = 0; p < S::kMembers; ++p) {
+        const int slice = (member + p) % S::kMembers;
+        const uint4* v = reinterpret_cast<const uint4*>(src + slice / S::kHalves * 128 + t4 * (S::kPart / 4) +
+                                                        slice % S::kHalves * 16);
 #pragma unroll
         for (int x = 0; x < kWords / 4; ++x) {
           const uint4 y = real ? v[x] : make_uint4(0, 0, 0, 0);
@@ -498,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       }
     }
 
-    // ---- the copies.  The lanes know the records of the warp's next 16 tiles: lane 2 i + b the
-    // b-th record of the i-th.
+    // ---- the copies.  The lanes know the records of the team's next 16 tiles: lane 2 i + b the
+    // b-th record of the i-th.  The team's first warp has them copied.
     int it = begin + rank, held = INT_MIN / 2;
     const uint8_t* record = nullptr;
     uint32_t usable = 0;
@@ -526,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       }
       const uint32_t two = (usable >> (2 * src)) & 3u;
       usable_ring = (usable_ring & ~(3u << (2 * s))) | (two << (2 * s));
-      if ((lane >> 1) == src) {
+      if (member == 0 && (lane >> 1) == src) {
         const uint32_t bar = bar0 + 8 * s;
         if ((lane & 1) == 0) ptx::mbar_arrive_expect_tx(bar, two == 3u ? 2 * S::kRecord : two ? S::kRecord : 0);
         if ((two >> (lane & 1)) & 1u)
@@ -540,13 +587,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     __syncwarp();
 
     // ---- the rows as operand B, divided by the power of two of their largest element
-    uint32_t qf[S::kQueryInSmem ? 1 : S::kParts * S::kSteps][NT][2];
+    uint32_t qf[S::kSteps][NT][2];
     float f[NT][2];          // logit factor of rows 2 t4, 2 t4 + 1 of each eight
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float amax = 0.f;
 #pragma unroll
-      for (int p = 0; p < S::kParts; ++p)
+      for (int p = 0; p < S::kMembers; ++p)
 #pragma unroll
         for (int x = 0; x < kWords; ++x) {
           const float2 y = kv::pair_to_float2(raw[nt][p][x], static_cast<const T*>(nullptr));
@@ -559,17 +606,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       e = amax == 0.f ? 0 : max(-126, min(e, 126));
       const float down = __uint_as_float(uint32_t(127 - e) << 23), up = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
-      for (int p = 0; p < S::kParts; ++p)
-#pragma unroll
-        for (int x = 0; x < kWords; ++x) {
-          const float2 y = kv::pair_to_float2(raw[nt][p][x], static_cast<const T*>(nullptr));
-          const uint32_t v = pack_f16(y.x * down, y.y * down);
-          if constexpr (S::kQueryInSmem) {
-            sq[(((p * S::kSteps + x / 2) * NT + nt) * 32 + lane) * 2 + (x & 1)] = v;   // read back by this lane
-          } else {
-            qf[p * S::kSteps + x / 2][nt][x & 1] = v;
-          }
-        }
+      for (int x = 0; x < kWords; ++x) {
+        const float2 y = kv::pair_to_float2(raw[nt][0][x], static_cast<const T*>(nullptr));
+        qf[x / 2][nt][x & 1] = pack_f16(y.x * down, y.y * down);
+      }
 #pragma unroll
       for (int b = 0; b < 2; ++b)   // never 0: it multiplies the -inf of unseen entries
         f[nt][b] = fmaxf(a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4), FLT_MIN);
@@ -582,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     };
 
     // weights are 2^(f s + c) with c = 12 - m; the reference m moves when s passes `limit`
-    float o[S::kParts * S::kSteps][NT][4];
+    float o[S::kSteps][NT][4];
     float c[NT][2], limit[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -592,71 +632,87 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         limit[nt][b] = -FLT_MAX;
         l[nt][b] = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < S::kParts * S::kSteps; ++mt) o[mt][nt][b] = o[mt][nt][b + 2] = 0.f;
+        for (int mt = 0; mt < S::kSteps; ++mt) o[mt][nt][b] = o[mt][nt][b + 2] = 0.f;
       }
 
     // One tile from the records at `rec`; masked: some row does not see some entry of it, or a record of
-    // it may not be looked at (bits of `two`).
-    auto work = [&](auto masked, const uint8_t* rec, int e0, uint32_t two) {
+    // it may not be looked at (bits of `two`).  `late`: this warp's wait for the tile ran out;
+    // returns whether any of the team's did (then nothing is added).
+    auto work = [&](auto masked, const uint8_t* rec, int e0, uint32_t two, bool late) {
       constexpr bool kMasked = decltype(masked)::value;
       // ---- logits: S^T[entry][row]
       float s[2][NT][4];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint8_t* const rb = rec + b * S::kRecord;
+        constexpr int kW = S::kSlice / 32;   // words of a lane's quarter row: 2 or 4
+        uint32_t w[2][kW];
+        __half2 sc[2];                       // scales of the quarter's first and second group
 #pragma unroll
-        for (int p = 0; p < S::kParts; ++p) {
-          constexpr int kW = S::kPart / 32;   // words of a lane's quarter row: 2 or 4
-          uint32_t w[2][kW];
-          __half2 sc[2];                      // scales of the quarter's first and second group
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint8_t* const src = rb + p * (8 * S::kPart) + (g + 8 * half) * (S::kPart / 2) + t4 * (S::kPart / 8);
-            if constexpr (kW == 4) {
-              const uint4 y = *reinterpret_cast<const uint4*>(src);
-              w[half][0] = y.x;
-              w[half][1] = y.y;
-              w[half][2] = y.z;
-              w[half][3] = y.w;
-              sc[half] = as_half2(kv::e4m3x2_to_f16x2(
-                  *reinterpret_cast<const uint16_t*>(rb + kv::k_scale(kDim, g + 8 * half, p * 8 + 2 * t4))));
-            } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(src);
-              w[half][0] = y.x;
-              w[half][1] = y.y;
-              sc[half] = as_half2(kv::e4m3x2_to_f16x2(rb[kv::k_scale(kDim, g + 8 * half, t4)]));
-            }
+        for (int y8 = 0; y8 < 2; ++y8) {
+          const uint8_t* const src = rb + k_at + y8 * (4 * S::kPart);
+          const uint8_t* const scale = rb + ks_at + y8 * (kDim / 2);
+          if constexpr (kW == 4) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src);
+            w[y8][0] = y.x;
+            w[y8][1] = y.y;
+            w[y8][2] = y.z;
+            w[y8][3] = y.w;
+            sc[y8] = as_half2(kv::e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale)));
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            w[y8][0] = y.x;
+            w[y8][1] = y.y;
+            sc[y8] = as_half2(kv::e4m3x2_to_f16x2(*scale));
           }
+        }
 #pragma unroll
-          for (int x = 0; x < kW; ++x) {   // eight dims of the lane: two steps
-            uint32_t x0[4], x1[4];
-            kv::e2m1x8_to_f16(w[0][x], x0);
-            kv::e2m1x8_to_f16(w[1][x], x1);
-            const bool second = kW == 4 && x >= 2;
-            const __half2 s0 = second ? __high2half2(sc[0]) : __low2half2(sc[0]);
-            const __half2 s1 = second ? __high2half2(sc[1]) : __low2half2(sc[1]);
+        for (int x = 0; x < kW; ++x) {   // eight dims of the lane: two steps
+          uint32_t x0[4], x1[4];
+          kv::e2m1x8_to_f16(w[0][x], x0);
+          kv::e2m1x8_to_f16(w[1][x], x1);
+          const bool second = kW == 4 && x >= 2;
+          const __half2 s0 = second ? __high2half2(sc[0]) : __low2half2(sc[0]);
+          const __half2 s1 = second ? __high2half2(sc[1]) : __low2half2(sc[1]);
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              const uint32_t af[4] = {hmul2(x0[2 * st], s0), hmul2(x1[2 * st], s1), hmul2(x0[2 * st + 1], s0),
-                                      hmul2(x1[2 * st + 1], s1)};
-              const int step = p * S::kSteps + 2 * x + st;
+          for (int st = 0; st < 2; ++st) {
+            const uint32_t af[4] = {hmul2(x0[2 * st], s0), hmul2(x1[2 * st], s1), hmul2(x0[2 * st + 1], s0),
+                                    hmul2(x1[2 * st + 1], s1)};
+            const int step = 2 * x + st;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                uint32_t bf[2];
-                if constexpr (S::kQueryInSmem) {
-                  const uint2 y = reinterpret_cast<const uint2*>(sq)[(step * NT + nt) * 32 + lane];
-                  bf[0] = y.x;
-                  bf[1] = y.y;
-                } else {
-                  bf[0] = qf[step][nt][0];
-                  bf[1] = qf[step][nt][1];
-                }
-                if (step == 0) mma_f16_zero(s[b][nt], af, bf);
-                else mma_f16(s[b][nt], af, bf);
-              }
+            for (int nt = 0; nt < NT; ++nt) {
+              if (step == 0) mma_f16_zero(s[b][nt], af, qf[step][nt]);
+              else mma_f16(s[b][nt], af, qf[step][nt]);
             }
           }
         }
+      }
+      if constexpr (S::kMembers > 1) {
+        // the members' logits add up in the same order for all of them
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            exchange[(member * 2 * NT + b * NT + nt) * 32] = make_float4(s[b][nt][0], s[b][nt][1], s[b][nt][2], s[b][nt][3]);
+        if (team_any<S::kMembers>(team, late)) return true;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float4 y = exchange[(b * NT + nt) * 32];
+#pragma unroll
+            for (int p = 1; p < S::kMembers; ++p) {
+              const float4 z = exchange[(p * 2 * NT + b * NT + nt) * 32];
+              y.x += z.x;
+              y.y += z.y;
+              y.z += z.z;
+              y.w += z.w;
+            }
+            s[b][nt][0] = y.x;
+            s[b][nt][1] = y.y;
+            s[b][nt][2] = y.z;
+            s[b][nt][3] = y.w;
+          }
       }
       // ---- weights, in f16 as operand B of the second product
       if constexpr (kMasked) {
@@ -688,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
               limit[nt][b] = x + kLag / f[nt][b];
               l[nt][b] *= k;
 #pragma unroll
-              for (int mt = 0; mt < S::kParts * S::kSteps; ++mt) {
+              for (int mt = 0; mt < S::kSteps; ++mt) {
                 o[mt][nt][b] *= k;
                 o[mt][nt][b + 2] *= k;
               }
@@ -714,57 +770,56 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint8_t* const rb = rec + b * S::kRecord;
+        constexpr int kW = S::kSlice / 64;   // words of a lane's dims of an entry: 1 or 2
+        uint32_t w[2][2][kW];                // [entries 2 t4.. or 2 t4 + 8..][entry of the two]
+        __half2 sc[2];
 #pragma unroll
-        for (int p = 0; p < S::kParts; ++p) {
-          constexpr int kW = S::kPart / 64;   // words of a chunk: 1 or 2
-          uint32_t w[2][2][kW];               // [entries 2 t4.. or 2 t4 + 8..][entry of the two]
-          __half2 sc[2];
+        for (int y8 = 0; y8 < 2; ++y8) {
+          const uint8_t* const src = rb + v_at + y8 * (4 * S::kPart);
+          if constexpr (kW == 2) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src);
+            w[y8][0][0] = y.x;
+            w[y8][0][1] = y.y;
+            w[y8][1][0] = y.z;
+            w[y8][1][1] = y.w;
+          } else if constexpr (S::kHalves == 1) {
+            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            w[y8][0][0] = y.x;
+            w[y8][1][0] = y.y;
+          } else {
+            w[y8][0][0] = *reinterpret_cast<const uint32_t*>(src);
+            w[y8][1][0] = *reinterpret_cast<const uint32_t*>(src + 8);
+          }
+          uint32_t raw_sc = *reinterpret_cast<const uint16_t*>(rb + vs_at + y8 * (S::kPart / 2));
+          if constexpr (kMasked) {
+            // 0 * NaN would reach the rows that do not see the entry: take the scale as 0 and
+            // give the NaN to the rows that do see it below
+            if ((raw_sc & 0x7Fu) == 0x7Fu) {
+              raw_sc &= 0xFF00u;
+              bad = 1;
+            }
+            if ((raw_sc & 0x7F00u) == 0x7F00u) {
+              raw_sc &= 0x00FFu;
+              bad = 1;
+            }
+          }
+          sc[y8] = as_half2(kv::e4m3x2_to_f16x2(uint16_t(raw_sc)));
+        }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint8_t* const src = rb + 8 * kDim + p * (8 * S::kPart) + half * (4 * S::kPart) + lane * (8 * kW);
-            if constexpr (kW == 2) {
-              const uint4 y = *reinterpret_cast<const uint4*>(src);
-              w[half][0][0] = y.x;
-              w[half][0][1] = y.y;
-              w[half][1][0] = y.z;
-              w[half][1][1] = y.w;
-            } else {
-              const uint2 y = *reinterpret_cast<const uint2*>(src);
-              w[half][0][0] = y.x;
-              w[half][1][0] = y.y;
-            }
-            uint32_t raw = *reinterpret_cast<const uint16_t*>(rb + 17 * kDim + p * S::kPart + half * (S::kPart / 2) +
-                                                              (kW == 2 ? g : g >> 1) * 8 + 2 * t4);
-            if constexpr (kMasked) {
-              // 0 * NaN would reach the rows that do not see the entry: take the scale as 0 and
-              // give the NaN to the rows that do see it below
-              if ((raw & 0x7Fu) == 0x7Fu) {
-                raw &= 0xFF00u;
-                bad = 1;
-              }
-              if ((raw & 0x7F00u) == 0x7F00u) {
-                raw &= 0x00FFu;
-                bad = 1;
-              }
-            }
-            sc[half] = as_half2(kv::e4m3x2_to_f16x2(uint16_t(raw)));
+        for (int x = 0; x < kW; ++x) {
+          // low nibbles of both entries side by side (even dims), then the high ones
+          uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+          for (int y8 = 0; y8 < 2; ++y8) {
+            kv::e2m1x8_to_f16(merge_bits(w[y8][0][x], w[y8][1][x] << 4, 0x0F0F0F0Fu), lo[y8]);
+            kv::e2m1x8_to_f16(merge_bits(w[y8][0][x] >> 4, w[y8][1][x], 0x0F0F0F0Fu), hi[y8]);
           }
 #pragma unroll
-          for (int x = 0; x < kW; ++x) {
-            // low nibbles of both entries side by side (even dims), then the high ones
-            uint32_t lo[2][4], hi[2][4];
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t af[4] = {hmul2(lo[0][j], sc[0]), hmul2(hi[0][j], sc[0]), hmul2(lo[1][j], sc[1]),
+                                    hmul2(hi[1][j], sc[1])};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              kv::e2m1x8_to_f16(merge_bits(w[half][0][x], w[half][1][x] << 4, 0x0F0F0F0Fu), lo[half]);
-              kv::e2m1x8_to_f16(merge_bits(w[half][0][x] >> 4, w[half][1][x], 0x0F0F0F0Fu), hi[half]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t af[4] = {hmul2(lo[0][j], sc[0]), hmul2(hi[0][j], sc[0]), hmul2(lo[1][j], sc[1]),
-                                      hmul2(hi[1][j], sc[1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(o[p * S::kSteps + 4 * x + j][nt], af, pf[b][nt]);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * x + j][nt], af, pf[b][nt]);
           }
         }
       }
@@ -772,177 +827,158 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         for (int b = 0; b < 2; ++b)
           for (int row = 0; row < 16; ++row) {
             const int e = e0 + 16 * b + row;
+            const int grp = part * (S::kPart / 16) + (S::kPart == 128 ? g : g >> 1);
+            const bool nan = (rec[b * S::kRecord + kv::v_scale(kDim, row, grp)] & 0x7F) == 0x7F;
 #pragma unroll
-            for (int p = 0; p < S::kParts; ++p) {
-              const int grp = p * (S::kPart / 16) + (S::kPart == 128 ? g : g >> 1);
-              const bool nan = (rec[b * S::kRecord + kv::v_scale(kDim, row, grp)] & 0x7F) == 0x7F;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int d = 0; d < 2; ++d)
+                if (nan && ((two >> b) & 1u) && sees(nt, d, e))
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
-                  if (nan && ((two >> b) & 1u) && sees(nt, d, e))
-#pragma unroll
-                    for (int mt = 0; mt < S::kSteps; ++mt)
-                      o[p * S::kSteps + mt][nt][d] = o[p * S::kSteps + mt][nt][d + 2] = __int_as_float(0x7FFFFFFF);
-            }
+                  for (int mt = 0; mt < S::kSteps; ++mt) o[mt][nt][d] = o[mt][nt][d + 2] = __int_as_float(0x7FFFFFFF);
           }
       }
+      return false;
     };
 
     // tiles [whole0, whole1) lie inside every row's window and before every row's position
     const int whole1 = u.x.sink_t - u.x.lo_t + (p_min + 1) / kTile;
     const int whole0 = u.x.sink_t - u.x.lo_t + (a.window ? (max(0, p_max - a.window + 1) + kTile - 1) / kTile : 0);
     for (int t = begin + rank; t < end; t += group) {
-      const bool late = dead || !ptx::mbar_wait_poll(bar0 + 8 * stage, (phases >> stage) & 1u, a.wait_limit, 64);
-      if (__any_sync(0xFFFFFFFFu, late)) {
-        // a copy did not come in time: no more work, the warp's own copies are waited for
+      const uint32_t parity = (phases >> stage) & 1u;
+      bool late = dead || !ptx::mbar_wait_poll(bar0 + 8 * stage, parity, a.wait_limit, 64);
+      if constexpr (S::kMembers == 1) late = __any_sync(0xFFFFFFFFu, late);
+      if (!dead && (S::kMembers > 1 || !late)) {
+        const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
+        const uint8_t* const rec = ring + stage * S::kStage;
+        if (two == 3u && t >= whole0 && t < whole1) late = work(std::false_type(), rec, 0, two, late);
+        else late = work(std::true_type(), rec, entry_of(t), two, late);
+      }
+      if (late) {
+        // a copy did not come in time: no more work, the team's own copies are waited for
         if (!dead && lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
         dead = true;
         if (in_flight == 0) break;
-        ptx::mbar_wait(bar0 + 8 * stage, (phases >> stage) & 1u, kDefaultWaitCycles);
-      } else {
-        const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
-        const uint8_t* const rec = ring + stage * S::kStage;
-        if (two == 3u && t >= whole0 && t < whole1) work(std::false_type(), rec, 0, two);
-        else work(std::true_type(), rec, entry_of(t), two);
+        ptx::mbar_wait(bar0 + 8 * stage, parity, kDefaultWaitCycles);
       }
       --in_flight;
       phases ^= 1u << stage;
-      __syncwarp();
+      team_sync<S::kMembers>(team);
       issue(stage);
       if (++stage == S::kStages) stage = 0;
     }
 
     // ---- write the unit, or this worker's part of it
     const bool goes_on = end < u.x.tiles, alone = !goes_on && begin == 0;
-    const size_t part = (size_t)2 * worker + (goes_on ? 1 : 0);
+    const size_t slot = (size_t)2 * worker + (goes_on ? 1 : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][b] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][b], d);
-    if (deal.warps) {
-      // straight from the registers: a lane holds the dims of chunk g of its two columns
+    if (deal.teams) {
+      // straight from the registers: a lane holds 2 kSteps dims of its two columns
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int row = nt * 8 + 2 * t4 + b, rho = row0 + row;
           if (rho >= rows) continue;
-          const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
-          const int64_t at = u.x.q0 + qi;
-          const float all = l[nt][b], inv = all == 0.f ? 0.f : a.v_mul / all, m = kWeightExp - c[nt][b];
+          const float all = l[nt][b], m = kWeightExp - c[nt][b];
+          if (alone) {
+            const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
+            const int64_t at = u.x.q0 + qi;
+            const float inv = all == 0.f ? 0.f : a.v_mul / all;
+            uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim0);
 #pragma unroll
-          for (int p = 0; p < S::kParts; ++p) {
-            const int dim = p * 128 + g * (S::kPart / 8);
-            if (alone) {
-              uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim);
+            for (int mt = 0; mt < S::kSteps; mt += 4) {
+              uint32_t w[4];
 #pragma unroll
-              for (int mt = 0; mt < S::kSteps; mt += 4) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  w[i] = kv::float2_to_pair(o[p * S::kSteps + mt + i][nt][b] * inv, o[p * S::kSteps + mt + i][nt][b + 2] * inv,
-                                            static_cast<const T*>(nullptr));
-                *reinterpret_cast<uint4*>(dst + mt) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
-              float* const dst = parts.o + (part * S::kRows + row) * kDim + dim;
-#pragma unroll
-              for (int mt = 0; mt < S::kSteps; mt += 2)
-                *reinterpret_cast<float4*>(dst + 2 * mt) =
-                    make_float4(o[p * S::kSteps + mt][nt][b], o[p * S::kSteps + mt][nt][b + 2],
-                                o[p * S::kSteps + mt + 1][nt][b], o[p * S::kSteps + mt + 1][nt][b + 2]);
+              for (int i = 0; i < 4; ++i)
+                w[i] = kv::float2_to_pair(o[mt + i][nt][b] * inv, o[mt + i][nt][b + 2] * inv, static_cast<const T*>(nullptr));
+              *reinterpret_cast<uint4*>(dst + mt) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          }
-          if (g == 0) {
-            if (!alone) parts.ml[part * S::kRows + row] = make_float2(m, all);
-            else if (a.lse) a.lse[at * a.Hq + head] = lse_of(m, all);
+            if (g == 0 && member == 0 && a.lse) a.lse[at * a.Hq + head] = lse_of(m, all);
+          } else {
+            float* const dst = parts.o + (slot * S::kRows + row) * kDim + dim0;
+#pragma unroll
+            for (int mt = 0; mt < S::kSteps; mt += 2)
+              *reinterpret_cast<float4*>(dst + 2 * mt) =
+                  make_float4(o[mt][nt][b], o[mt][nt][b + 2], o[mt + 1][nt][b], o[mt + 1][nt][b + 2]);
+            if (g == 0 && member == 0) parts.ml[slot * S::kRows + row] = make_float2(m, all);
           }
         }
-      __syncwarp();   // sq is free again, the part is written
       if (!alone)
-        finish_unit<T, kDim, NT>(a, parts, u, deal, worker, lane, 32, [&](int32_t* counter) {
-          int n = 0;
-          __syncwarp();
-          if (lane == 0) n = count_in(counter);
-          return __shfl_sync(0xFFFFFFFFu, n, 0);
+        finish_unit<T, kDim, NT>(a, parts, u, deal, worker, member * 32 + lane, 32 * S::kMembers, [&](int32_t* counter) {
+          team_sync<S::kMembers>(team);
+          if (member == 0 && lane == 0) sh_count[team] = count_in(counter);
+          team_sync<S::kMembers>(team);
+          return *static_cast<volatile int*>(&sh_count[team]);
         });
       continue;
     }
+    if (member == 0 && g == 0) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        if (g == 0) {
-          sh_m[warp][nt * 8 + 2 * t4 + b] = kWeightExp - c[nt][b];
-          sh_l[warp][nt * 8 + 2 * t4 + b] = l[nt][b];
+        for (int b = 0; b < 2; ++b) {
+          sh_m[team][nt * 8 + 2 * t4 + b] = kWeightExp - c[nt][b];
+          sh_l[team][nt * 8 + 2 * t4 + b] = l[nt][b];
         }
+    }
     __syncthreads();
-    float scale[NT][2];
+    if (threadIdx.x < S::kRows) {
+      float top = -FLT_MAX, all = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][threadIdx.x]);
+#pragma unroll
+      for (int w = 0; w < S::kTeams; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx(sh_m[w][threadIdx.x] - top);
+      sh_top[threadIdx.x] = top;
+      sh_all[threadIdx.x] = all;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float scale[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         float top = -FLT_MAX;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][nt * 8 + 2 * t4 + b]);
-        scale[nt][b] = ptx::ex2_approx(kWeightExp - c[nt][b] - top);
+        for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][nt * 8 + 2 * t4 + b]);
+        scale[b] = ptx::ex2_approx(kWeightExp - c[nt][b] - top);
       }
-    if (threadIdx.x < S::kRows) {
-      float top = -FLT_MAX, all = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][threadIdx.x]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx(sh_m[w][threadIdx.x] - top);
-      sh_top[threadIdx.x] = top;
-      sh_all[threadIdx.x] = all;
+      for (int mt = 0; mt < S::kSteps; ++mt) {
+        float* const dst = reinterpret_cast<float*>(join) + (nt * 8 + 2 * t4) * S::kJoinRow + mt * 16 + g * 2;
+        *reinterpret_cast<float2*>(dst) = make_float2(o[mt][nt][0] * scale[0], o[mt][nt][2] * scale[0]);
+        *reinterpret_cast<float2*>(dst + S::kJoinRow) = make_float2(o[mt][nt][1] * scale[1], o[mt][nt][3] * scale[1]);
+      }
     }
-    for (int p = 0; p < S::kParts; ++p) {
-      if (p) __syncthreads();
+    __syncthreads();
+    for (int i = threadIdx.x; i < S::kRows * kDim / 2; i += kThreads) {
+      const int row = i / (kDim / 2), j = i % (kDim / 2) / (S::kSlice / 2), y = i % (S::kSlice / 2);   // y: dims (mt = y / 8, g = y % 8) of slice j
+      const int rho = row0 + row;
+      if (rho >= rows) continue;
+      const int dim = j / S::kHalves * 128 + (y % 8) * (S::kPart / 8) + j % S::kHalves * 8 + 2 * (y / 8);
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < S::kSteps; ++mt) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = o[mt][nt][i];
-            if constexpr (S::kParts == 2)
-              if (p) x[i] = o[S::kSteps + mt][nt][i];
-            x[i] *= scale[nt][i & 1];
-          }
-          float* const dst = reinterpret_cast<float*>(ring) + (nt * 8 + 2 * t4) * S::kJoinRow + mt * 16 + g * 2;
-          *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[2]);
-          *reinterpret_cast<float2*>(dst + S::kJoinRow) = make_float2(x[1], x[3]);
-        }
-      __syncthreads();
-      for (int i = threadIdx.x; i < S::kRows * S::kPart / 2; i += kThreads) {
-        const int row = i / (S::kPart / 2), y = i % (S::kPart / 2);   // y: dims (mt = y / 8, g = y % 8)
-        const int rho = row0 + row;
-        if (rho >= rows) continue;
-        const int dim = p * 128 + (y % 8) * (S::kPart / 8) + 2 * (y / 8);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(smem + w * (S::kStages * S::kStage) +
-                                                            (row * S::kJoinRow + 2 * y) * 4);
-          sum.x += v.x;
-          sum.y += v.y;
-        }
-        const float all = sh_all[row];
-        if (alone) {
-          const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
-          const int64_t at = u.x.q0 + qi;
-          const float inv = all == 0.f ? 0.f : a.v_mul / all;
-          *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim) =
-              kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
-          if (a.lse && p == 0 && y == 0) a.lse[at * a.Hq + head] = lse_of(sh_top[row], all);
-        } else {
-          *reinterpret_cast<float2*>(parts.o + (part * S::kRows + row) * kDim + dim) = sum;
-          if (p == 0 && y == 0) parts.ml[part * S::kRows + row] = make_float2(sh_top[row], all);
-        }
+      for (int w = 0; w < S::kTeams; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(smem + w * S::kRing + j * (S::kRing / S::kMembers) +
+                                                          (row * S::kJoinRow + 2 * y) * 4);
+        sum.x += v.x;
+        sum.y += v.y;
+      }
+      const float all = sh_all[row];
+      if (alone) {
+        const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
+        const int64_t at = u.x.q0 + qi;
+        const float inv = all == 0.f ? 0.f : a.v_mul / all;
+        *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim) =
+            kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
+        if (a.lse && dim == 0) a.lse[at * a.Hq + head] = lse_of(sh_top[row], all);
+      } else {
+        *reinterpret_cast<float2*>(parts.o + (slot * S::kRows + row) * kDim + dim) = sum;
+        if (dim == 0) parts.ml[slot * S::kRows + row] = make_float2(sh_top[row], all);
       }
     }
     // the rings take copies again, sh_m, sh_l, sh_top and sh_all new values
@@ -951,9 +987,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     if (!alone)
       finish_unit<T, kDim, NT>(a, parts, u, deal, worker, threadIdx.x, kThreads, [&](int32_t* counter) {
         __syncthreads();
-        if (threadIdx.x == 0) sh_count = count_in(counter);
+        if (threadIdx.x == 0) sh_count[0] = count_in(counter);
         __syncthreads();
-        return sh_count;
+        return *static_cast<volatile int*>(&sh_count[0]);
       });
   }
 }
