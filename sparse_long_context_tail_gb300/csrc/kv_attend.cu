@@ -39,6 +39,7 @@
 // 2^-11 relative; they are scaled by 2^12 against a reference that may lag the
 // running maximum by 2^3, so that weights down to 2^-26 of the reference keep all
 // their bits.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -97,6 +98,13 @@ __device__ __forceinline__ Request load_request(const KvAttendArgs& a, int r) {
   return x;
 }
 
+// rho / gamma for a row of a request: the quotient is at most 1024 and gamma at most 256,
+// so (rho + 1/2) / gamma is 2^-9 or more away from every integer and the fp32 product,
+// off by under 2^-12, has the same whole part.
+__device__ __forceinline__ int query_of(const KvAttendArgs& a, int rho) {
+  return __float2int_rz((float(rho) + 0.5f) * a.inv_gamma);
+}
+
 __device__ __forceinline__ int chunks_of(const KvAttendArgs& a, const Request& x, int rows) {
   return (x.q_len * a.gamma + rows - 1) / rows;
 }
@@ -111,6 +119,10 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 constexpr int kUnitCostCta = 16, kUnitCostTeam = 4;
 // Workers are teams where units have fewer tiles than this on average.
 constexpr int kShortUnit = 64;
+
+// Where workers are teams, a unit of at most this many tiles is not split: it belongs to
+// the team whose share its first place lies in.
+constexpr int kWholeUnit = 8;
 
 // How the tiles are dealt out.  Along the dealing a unit takes cost + tiles places.
 struct Deal {
@@ -181,6 +193,15 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int teams, int per, lo
 struct Parts {
   float* o;         // [2 * workers][rows][d]
   float2* ml;       // [2 * workers][rows]: reference, sum
+  struct Note* notes;   // [CTAs], or null: no second launch
+};
+
+// Where few units are spread over many CTAs, adding their parts up is left to a second
+// launch, which shares it among as many CTAs as the unit had: for each CTA, the unit
+// that goes on after its share.
+struct Note {
+  int first, last;        // CTAs of the unit (first < 0: no such unit)
+  int h, row0, rows, q0;  // kv head, first row of the chunk, rows of the request, its first row in q
 };
 
 // Parts are counted in by at most kFan workers at a time, so that no worker has to
@@ -286,22 +307,21 @@ __device__ __forceinline__ float lse_of(float top, float all) {
 
 // Adds up n parts of a unit's workers first .. last in order, by `count` threads: those of
 // workers w0, w0 + 1, ... or, if `groups`, those that stand for kFan workers each.
-// The sum goes to out and lse or, if `to` >= 0, to that part.  2^k lanes add up
-// four dims of a row, each every 2^k-th part; what they load does not hang on what
-// they loaded before.
+// Of its outputs (four dims of a row each) from .. to - 1; the sum goes to out and lse
+// or, if `into` >= 0, to that part.  2^k lanes add up one output, each every 2^k-th
+// part; what they load does not hang on what they loaded before.
 template <typename T, int kDim, int NT>
-__device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Unit& u, int first, int last, int w0, int n,
-                          bool groups, int to, int thread, int count) {
+__device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note& u, int w0, int n, bool groups, int into,
+                          int from, int to, int thread, int count) {
   using S = Shape<kDim, NT>;
   constexpr int kBatch = 4;
-  const int row0 = u.c * S::kRows, rows = min(S::kRows, u.x.q_len * a.gamma - row0), outputs = rows * (kDim / 4);
   int lanes = 1;
-  while (lanes < 32 && 2 * lanes * outputs <= count && lanes < n) lanes *= 2;
+  while (lanes < 32 && 2 * lanes * (to - from) <= count && lanes < n) lanes *= 2;
   const int sub = thread & (lanes - 1);
   // every lane makes every round: the shuffles need all of them
-  for (int at0 = 0; at0 < outputs; at0 += count / lanes) {
+  for (int at0 = from; at0 < to; at0 += count / lanes) {
     const int i = at0 + thread / lanes;
-    const bool mine = i < outputs;
+    const bool mine = i < to;
     const int row = mine ? i / (kDim / 4) : 0, j = mine ? i % (kDim / 4) : 0;
     float m = -FLT_MAX, all = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -314,7 +334,7 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Unit&
         ml[x] = make_float2(-FLT_MAX, 0.f);
         v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < n) {   // from L2: other SMs wrote them
-          const size_t at = (size_t)(groups && w < last ? S::group_part(w, first) : 2 * w + (w < last)) * S::kRows + row;
+          const size_t at = (size_t)(groups && w < u.last ? S::group_part(w, u.first) : 2 * w + (w < u.last)) * S::kRows + row;
           ml[x] = __ldcg(parts.ml + at);
           v[x] = __ldcg(reinterpret_cast<const float4*>(parts.o + at * kDim) + j);
         }
@@ -355,14 +375,14 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Unit&
       sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, d);
     }
     if (!mine || sub) continue;
-    if (to >= 0) {
-      const size_t at = (size_t)to * S::kRows + row;
+    if (into >= 0) {
+      const size_t at = (size_t)into * S::kRows + row;
       reinterpret_cast<float4*>(parts.o + at * kDim)[j] = sum;
       if (j == 0) parts.ml[at] = make_float2(m, all);
       continue;
     }
-    const int rho = row0 + row, q = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - q * a.gamma];
-    const int64_t at = u.x.q0 + q;
+    const int rho = u.row0 + row, q = query_of(a, rho), head = a.qhead[u.h * a.gamma + rho - q * a.gamma];
+    const int64_t at = u.q0 + q;
     const float inv = all == 0.f ? 0.f : a.v_mul / all;
     uint2 w;
     w.x = kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
@@ -381,32 +401,35 @@ __device__ __forceinline__ int count_in(int32_t* counter) {
 }
 
 // Counts this worker's part of a unit in; the worker that completes the count adds
-// the parts up.  arrive(counter): everything that the worker's threads wrote is out,
-// and how many came before.
-template <typename T, int kDim, int NT, typename Arrive>
-__device__ void finish_unit(const KvAttendArgs& a, const Parts& parts, const Unit& u, const Deal& deal, int worker, int thread,
-                            int count, Arrive&& arrive) {
+// the parts up.  sync: a barrier of the worker's threads; said: a word of theirs in
+// shared memory.
+template <typename T, int kDim, int NT, typename Sync>
+__device__ __forceinline__ void finish_unit(const KvAttendArgs& a, const Parts& parts, const Unit& u, const Deal& deal, int worker, int thread,
+                            int count, volatile int* said, Sync&& sync) {
   using S = Shape<kDim, NT>;
   const long long place = u.place + deal.cost;
   const int first = int(quotient(place, deal.share)), last = int(quotient(place + u.x.tiles - 1, deal.share));
-  const int n = last - first + 1;
-  int32_t* counter = a.counters + first;
-  int w0 = first, members = n;
-  if (n > kFan) {
-    w0 = first + (worker - first) / kFan * kFan;
-    members = min(kFan, last - w0 + 1);
-    if (members > 1) {
-      if (arrive(a.counters + w0) != members - 1) return;
-      if (thread == 0) a.counters[w0] = 0;
-      add_parts<T, kDim, NT>(a, parts, u, first, last, w0, members, false, S::group_part(w0, first), thread, count);
-    }
-    counter = a.counters + S::kMaxWorkers + first;
-    w0 = first;
-    members = (n + kFan - 1) / kFan;
+  const int n = last - first + 1, row0 = u.c * S::kRows;
+  const Note note{first, last, u.h, row0, u.x.q_len * a.gamma, u.x.q0};
+  const int outputs = min(S::kRows, note.rows - row0) * (kDim / 4);
+  auto arrive = [&](int32_t* counter) {   // how many came before
+    sync();
+    if (thread == 0) *said = count_in(counter);
+    sync();
+    return *said;
+  };
+  // level 0: the runs of kFan workers of a unit with more than that; level 1: the unit
+  for (int level = n > kFan ? 0 : 1; level < 2; ++level) {
+    const bool groups = level == 1 && n > kFan;
+    const int w0 = level == 0 ? first + (worker - first) / kFan * kFan : first;
+    const int members = groups ? (n + kFan - 1) / kFan : min(level == 0 ? kFan : n, last - w0 + 1);
+    if (level == 0 && members == 1) continue;   // its part stands for itself
+    int32_t* const counter = a.counters + (groups ? S::kMaxWorkers : 0) + w0;
+    if (arrive(counter) != members - 1) break;
+    if (thread == 0) *counter = 0;
+    add_parts<T, kDim, NT>(a, parts, note, w0, members, groups, level == 0 ? S::group_part(w0, first) : -1, 0, outputs, thread,
+                           count);
   }
-  if (arrive(counter) != members - 1) return;
-  if (thread == 0) *counter = 0;
-  add_parts<T, kDim, NT>(a, parts, u, first, last, w0, members, n > kFan, -1, thread, count);
 }
 
 // A team's barriers: one warp, or kMembers warps on the named barrier 1 + team.
@@ -436,7 +459,7 @@ __device__ __forceinline__ bool team_any(int team, bool x) {
 }
 
 template <typename T, int kDim, int NT>
-__global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_attend_kernel(const KvAttendArgs a, const Parts parts) {
+__global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_attend_kernel(const __grid_constant__ KvAttendArgs a, const __grid_constant__ Parts parts) {
   using S = Shape<kDim, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[S::kTeams][S::kStages];
@@ -493,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       if (a.lse && i % (kDim / 2) == 0) a.lse[at * a.Hq + h] = -INFINITY;
     }
   }
+  if (parts.notes && threadIdx.x == 0) parts.notes[blockIdx.x].first = -1;
   __syncthreads();
   const long long my_first = worker * deal.share, my_end = min(my_first + deal.share, deal.total);
   if (my_first >= deal.total) return;   // a whole CTA, or a team that meets no other again
@@ -512,8 +536,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   bool dead = false;
 
   for (Unit u = starts[deal.teams ? team : 0]; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
-    const int begin = int(max(0LL, my_first - u.place - deal.cost));
-    const int end = int(min((long long)u.x.tiles, my_end - u.place - deal.cost));
+    int begin = int(max(0LL, my_first - u.place - deal.cost));
+    int end = int(min((long long)u.x.tiles, my_end - u.place - deal.cost));
+    if (deal.teams && u.x.tiles <= kWholeUnit) {
+      begin = 0;
+      end = u.place < my_first ? 0 : u.x.tiles;
+    }
     if (end <= begin) continue;
 
     // ---- the unit's rows, asked for before the copies so that they do not queue behind them
@@ -527,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     for (int nt = 0; nt < NT; ++nt) {
       const int rho = row0 + nt * 8 + g;
       const bool real = rho < rows;
-      const int i = real ? rho / a.gamma : 0, j = real ? rho - i * a.gamma : 0;
+      const int i = real ? query_of(a, rho) : 0, j = real ? rho - i * a.gamma : 0;
       const T* src = static_cast<const T*>(a.q) + (int64_t)(u.x.q0 + i) * a.q_stride + (int)a.qhead[u.h * a.gamma + j] * kDim;
 #pragma unroll
       for (int p = 0; p < S::kMembers; ++p) {
@@ -614,10 +642,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       for (int b = 0; b < 2; ++b)   // never 0: it multiplies the -inf of unseen entries
         f[nt][b] = fmaxf(a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4), FLT_MIN);
     }
-    const int p_min = base + row0 / a.gamma, p_max = base + (min(rows, row0 + S::kRows) - 1) / a.gamma;
+    const int p_min = base + query_of(a, row0), p_max = base + query_of(a, min(rows, row0 + S::kRows) - 1);
     // does row y of this lane's columns (nt, b) see entry e?
     auto sees = [&](int nt, int b, int e) {
-      const int y = row0 + nt * 8 + 2 * t4 + b, p = base + y / a.gamma;
+      const int y = row0 + nt * 8 + 2 * t4 + b, p = base + query_of(a, y);
       return y < rows && e <= p && (a.window == 0 || p - e < a.window || e < a.sinks);
     };
 
@@ -741,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
             if (x > limit[nt][b]) {
               const float c2 = kWeightExp - x * f[nt][b], k = ptx::ex2_approx(c2 - c[nt][b]);
               c[nt][b] = c2;
-              limit[nt][b] = x + kLag / f[nt][b];
+              limit[nt][b] = x + __fdividef(kLag, f[nt][b]);
               l[nt][b] *= k;
 #pragma unroll
               for (int mt = 0; mt < S::kSteps; ++mt) {
@@ -887,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
           if (rho >= rows) continue;
           const float all = l[nt][b], m = kWeightExp - c[nt][b];
           if (alone) {
-            const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
+            const int qi = query_of(a, rho), head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
             const int64_t at = u.x.q0 + qi;
             const float inv = all == 0.f ? 0.f : a.v_mul / all;
             uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim0);
@@ -909,89 +937,104 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
             if (g == 0 && member == 0) parts.ml[slot * S::kRows + row] = make_float2(m, all);
           }
         }
-      if (!alone)
-        finish_unit<T, kDim, NT>(a, parts, u, deal, worker, member * 32 + lane, 32 * S::kMembers, [&](int32_t* counter) {
-          team_sync<S::kMembers>(team);
-          if (member == 0 && lane == 0) sh_count[team] = count_in(counter);
-          team_sync<S::kMembers>(team);
-          return *static_cast<volatile int*>(&sh_count[team]);
-        });
-      continue;
-    }
-    if (member == 0 && g == 0) {
+    } else {
+      if (member == 0 && g == 0) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            sh_m[team][nt * 8 + 2 * t4 + b] = kWeightExp - c[nt][b];
+            sh_l[team][nt * 8 + 2 * t4 + b] = l[nt][b];
+          }
+      }
+      __syncthreads();
+      if (threadIdx.x < S::kRows) {
+        float top = -FLT_MAX, all = 0.f;
+#pragma unroll
+        for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][threadIdx.x]);
+#pragma unroll
+        for (int w = 0; w < S::kTeams; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx(sh_m[w][threadIdx.x] - top);
+        sh_top[threadIdx.x] = top;
+        sh_all[threadIdx.x] = all;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float scale[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          sh_m[team][nt * 8 + 2 * t4 + b] = kWeightExp - c[nt][b];
-          sh_l[team][nt * 8 + 2 * t4 + b] = l[nt][b];
+          float top = -FLT_MAX;
+#pragma unroll
+          for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][nt * 8 + 2 * t4 + b]);
+          scale[b] = ptx::ex2_approx(kWeightExp - c[nt][b] - top);
         }
-    }
-    __syncthreads();
-    if (threadIdx.x < S::kRows) {
-      float top = -FLT_MAX, all = 0.f;
 #pragma unroll
-      for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][threadIdx.x]);
-#pragma unroll
-      for (int w = 0; w < S::kTeams; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx(sh_m[w][threadIdx.x] - top);
-      sh_top[threadIdx.x] = top;
-      sh_all[threadIdx.x] = all;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float scale[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float top = -FLT_MAX;
-#pragma unroll
-        for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][nt * 8 + 2 * t4 + b]);
-        scale[b] = ptx::ex2_approx(kWeightExp - c[nt][b] - top);
+        for (int mt = 0; mt < S::kSteps; ++mt) {
+          float* const dst = reinterpret_cast<float*>(join) + (nt * 8 + 2 * t4) * S::kJoinRow + mt * 16 + g * 2;
+          *reinterpret_cast<float2*>(dst) = make_float2(o[mt][nt][0] * scale[0], o[mt][nt][2] * scale[0]);
+          *reinterpret_cast<float2*>(dst + S::kJoinRow) = make_float2(o[mt][nt][1] * scale[1], o[mt][nt][3] * scale[1]);
+        }
       }
+      __syncthreads();
+      for (int i = threadIdx.x; i < S::kRows * kDim / 2; i += kThreads) {
+        const int row = i / (kDim / 2), j = i % (kDim / 2) / (S::kSlice / 2), y = i % (S::kSlice / 2);   // y: dims (mt = y / 8, g = y % 8) of slice j
+        const int rho = row0 + row;
+        if (rho >= rows) continue;
+        const int dim = j / S::kHalves * 128 + (y % 8) * (S::kPart / 8) + j % S::kHalves * 8 + 2 * (y / 8);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int mt = 0; mt < S::kSteps; ++mt) {
-        float* const dst = reinterpret_cast<float*>(join) + (nt * 8 + 2 * t4) * S::kJoinRow + mt * 16 + g * 2;
-        *reinterpret_cast<float2*>(dst) = make_float2(o[mt][nt][0] * scale[0], o[mt][nt][2] * scale[0]);
-        *reinterpret_cast<float2*>(dst + S::kJoinRow) = make_float2(o[mt][nt][1] * scale[1], o[mt][nt][3] * scale[1]);
+        for (int w = 0; w < S::kTeams; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(smem + w * S::kRing + j * (S::kRing / S::kMembers) +
+                                                            (row * S::kJoinRow + 2 * y) * 4);
+          sum.x += v.x;
+          sum.y += v.y;
+        }
+        const float all = sh_all[row];
+        if (alone) {
+          const int qi = query_of(a, rho), head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
+          const int64_t at = u.x.q0 + qi;
+          const float inv = all == 0.f ? 0.f : a.v_mul / all;
+          *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim) =
+              kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
+          if (a.lse && dim == 0) a.lse[at * a.Hq + head] = lse_of(sh_top[row], all);
+        } else {
+          *reinterpret_cast<float2*>(parts.o + (slot * S::kRows + row) * kDim + dim) = sum;
+          if (dim == 0) parts.ml[slot * S::kRows + row] = make_float2(sh_top[row], all);
+        }
       }
+      // the rings take copies again, sh_m, sh_l, sh_top and sh_all new values
+      ptx::fence_proxy_async_smem();
+      __syncthreads();
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < S::kRows * kDim / 2; i += kThreads) {
-      const int row = i / (kDim / 2), j = i % (kDim / 2) / (S::kSlice / 2), y = i % (S::kSlice / 2);   // y: dims (mt = y / 8, g = y % 8) of slice j
-      const int rho = row0 + row;
-      if (rho >= rows) continue;
-      const int dim = j / S::kHalves * 128 + (y % 8) * (S::kPart / 8) + j % S::kHalves * 8 + 2 * (y / 8);
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < S::kTeams; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(smem + w * S::kRing + j * (S::kRing / S::kMembers) +
-                                                          (row * S::kJoinRow + 2 * y) * 4);
-        sum.x += v.x;
-        sum.y += v.y;
+    if (parts.notes && !deal.teams) {
+      if (goes_on && threadIdx.x == 0) {
+        const long long place = u.place + deal.cost;
+        parts.notes[blockIdx.x] = Note{int(quotient(place, deal.share)), int(quotient(place + u.x.tiles - 1, deal.share)),
+                                       u.h, row0, rows, u.x.q0};
       }
-      const float all = sh_all[row];
-      if (alone) {
-        const int qi = rho / a.gamma, head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
-        const int64_t at = u.x.q0 + qi;
-        const float inv = all == 0.f ? 0.f : a.v_mul / all;
-        *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim) =
-            kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
-        if (a.lse && dim == 0) a.lse[at * a.Hq + head] = lse_of(sh_top[row], all);
-      } else {
-        *reinterpret_cast<float2*>(parts.o + (slot * S::kRows + row) * kDim + dim) = sum;
-        if (dim == 0) parts.ml[slot * S::kRows + row] = make_float2(sh_top[row], all);
-      }
+    } else if (!alone) {
+      finish_unit<T, kDim, NT>(a, parts, u, deal, worker, deal.teams ? member * 32 + lane : threadIdx.x,
+                               deal.teams ? 32 * S::kMembers : kThreads, &sh_count[deal.teams ? team : 0], [&] {
+                                 if (deal.teams) team_sync<S::kMembers>(team);
+                                 else __syncthreads();
+                               });
     }
-    // the rings take copies again, sh_m, sh_l, sh_top and sh_all new values
-    ptx::fence_proxy_async_smem();
-    __syncthreads();
-    if (!alone)
-      finish_unit<T, kDim, NT>(a, parts, u, deal, worker, threadIdx.x, kThreads, [&](int32_t* counter) {
-        __syncthreads();
-        if (threadIdx.x == 0) sh_count[0] = count_in(counter);
-        __syncthreads();
-        return *static_cast<volatile int*>(&sh_count[0]);
-      });
   }
+}
+
+// The second launch: each warp of the CTAs first .. last - 1 of a unit takes its portion
+// of the outputs.
+template <typename T, int kDim, int NT>
+__global__ void __launch_bounds__(kThreads) kv_attend_join_kernel(const __grid_constant__ KvAttendArgs a,
+                                                                  const __grid_constant__ Parts parts) {
+  using S = Shape<kDim, NT>;
+  pdl_wait();
+  const Note u = parts.notes[blockIdx.x];
+  if (u.first < 0) return;
+  const int outputs = min(S::kRows, u.rows - u.row0) * (kDim / 4), portions = (u.last - u.first) * kWarps;
+  const int each = (outputs + portions - 1) / portions;
+  const int from = ((blockIdx.x - u.first) * kWarps + (threadIdx.x >> 5)) * each;
+  add_parts<T, kDim, NT>(a, parts, u, u.first, u.last - u.first + 1, false, -1, from, min(outputs, from + each),
+                         threadIdx.x & 31, 32);
 }
 
 template <int kDim, int NT>
@@ -1007,7 +1050,15 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t s) {
   parts.ml = reinterpret_cast<float2*>(parts.o + part_rows<kDim, NT>() * kDim);
   cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, kDim, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kv_attend_kernel<T, kDim, NT>, S::kCtas, kThreads, S::kSmem, s, true, a, parts);
+  // Most CTAs that can come to work on one unit, if the units are about as long as one another:
+  // all CTAs by the units, or the longest unit by the least share.
+  const long long units = (long long)a.R * a.H * ((a.max_q * a.gamma + S::kRows - 1) / S::kRows);
+  const long long longest = a.window ? (long long)a.window + a.sinks + a.max_q : (long long)a.max_pages << a.page_shift;
+  const bool second = std::min(S::kCtas / units, longest / (kTile * S::kTeams)) > kFan;
+  parts.notes = second ? reinterpret_cast<Note*>(parts.ml + part_rows<kDim, NT>()) : nullptr;
+  e = launch_kernel(kv_attend_kernel<T, kDim, NT>, S::kCtas, kThreads, S::kSmem, s, true, a, parts);
+  if (e != cudaSuccess || !second) return e;
+  return launch_kernel(kv_attend_join_kernel<T, kDim, NT>, S::kCtas, kThreads, 0, s, true, a, parts);
 }
 
 template <int kDim>
@@ -1018,7 +1069,7 @@ cudaError_t launch_dim(const KvAttendArgs& a, bool f16, cudaStream_t s) {
 
 template <int kDim, int NT>
 constexpr size_t ws_bytes() {
-  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2));
+  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2)) + Shape<kDim, NT>::kCtas * sizeof(Note);
 }
 
 template <int kDim>

@@ -1242,6 +1242,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   a.R = query->num_reqs;
   a.Hq = query->num_q_heads;
   a.gamma = gamma;
+  a.inv_gamma = 1.0f / float(gamma);
   a.num_q = query->num_q_tokens;
   a.max_q = query->max_q_len;
   a.q = q;

@@ -222,6 +222,7 @@ struct KvAttendArgs {
   int32_t window, sinks;        // window 0: none
   float scale_log2;             // softmax scale * 2^k_exp * log2 e
   float v_mul;                  // 2^v_exp
+  float inv_gamma;              // 1 / gamma
   int32_t* status;
   int32_t* counters;            // [kKvCounters] of the context, zero between calls
   long long wait_limit;

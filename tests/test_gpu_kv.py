@@ -529,16 +529,20 @@ def test_selected_tokens_are_written_at_their_slots_and_attended():
 
 
 def test_a_wait_that_runs_out_is_reported_and_the_cache_recovers():
-    """The copies' waits limited to one SM cycle, over a 300 MB cache (more than L2 holds): some record is not there
-    that soon.  The kernel reports it, waits for its own copies and returns, and the next calls are right."""
+    """The copies' waits limited to one SM cycle, over a 300 MB cache (more than L2 holds), until some record is not
+    there that soon.  The kernel reports it, waits for its own copies and returns, and the next calls are right."""
     n = 1 << 17
     big = make(n, 8, 128, fill=0)
     q = rand((1, 8, 128), BF16, 1)
     table = torch.randperm(n // 16, generator=torch.Generator().manual_seed(1)).int()[None].to(DEV)
     kv = torch.full((1,), n, dtype=torch.int32, device=DEV)
     B.upf_set_wait_limit(big.ctx, 1)
-    big.attend(q, table, kv, 16)
-    assert big.status() == 6
+    for _ in range(200):
+        big.attend(q, table, kv, 16)
+        status = big.status()
+        if status:
+            break
+    assert status == 6
     B.upf_set_wait_limit(big.ctx, 0)
     got = big.attend(q, table, kv, 16)
     assert big.status() == 0 and not got.out.any() and (got.lse - np.log(n)).abs().max() < 1e-5
