@@ -30,21 +30,18 @@ namespace kv {
 __host__ __device__ constexpr int record_bytes(int d) { return 18 * d; }
 __host__ __device__ constexpr int part_dims(int d) { return d >= 128 ? 128 : d; }
 
-// Byte offset inside a record of the codes of group `grp` (16 dims, 8 bytes) of
-// row `row`: keys, one run of 8 bytes.
-__device__ __forceinline__ int k_codes(int d, int row, int grp) {
-  const int D = part_dims(d), per = D / 16;
-  return (grp / per) * (8 * D) + row * (D / 2) + (grp % per) * 8;
+// Byte offset inside a record of the codes of eight dims (half a group, 4 bytes):
+// dims 8 oct .. 8 oct + 7 of row `row`.
+__device__ __forceinline__ int k_codes(int d, int row, int oct) {
+  const int D = part_dims(d), per = D / 8;
+  return (oct / per) * (8 * D) + row * (D / 2) + (oct % per) * 4;
 }
 
-// Values: at D = 128 a chunk is one group (8 bytes); at D = 64 a group is the
-// two 4-byte chunks 2 grp and 2 grp + 1, v_chunk_stride() apart.
-__device__ __forceinline__ int v_codes(int d, int row, int grp) {
-  const int D = part_dims(d), C = D / 16, per = D / 16;
-  const int chunk = (grp % per) * (8 / C);
-  return 8 * d + (grp / per) * (8 * D) + (row >> 3) * (4 * D) + chunk * (8 * C) + (row & 7) * C;
+// Values: at D = 128 a chunk is two of these, at D = 64 one.
+__device__ __forceinline__ int v_codes(int d, int row, int oct) {
+  const int D = part_dims(d), C = D / 16, per = D / 8, in = oct % per;
+  return 8 * d + (oct / per) * (8 * D) + (row >> 3) * (4 * D) + in * 4 / C * (8 * C) + (row & 7) * C + in * 4 % C;
 }
-__device__ __forceinline__ int v_chunk_stride(int d) { return part_dims(d) / 2; }
 
 __device__ __forceinline__ int k_scale(int d, int row, int grp) { return 16 * d + row * (d / 16) + grp; }
 
@@ -107,6 +104,18 @@ __device__ __forceinline__ float2 pair_to_float2(uint32_t w, const __nv_bfloat16
 }
 __device__ __forceinline__ float2 pair_to_float2(uint32_t w, const __half*) { return half2_bits_to_float2(w); }
 
+// Elementwise the larger magnitude (a NaN where there is one).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, const __nv_bfloat16*) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, const __half*) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t float2_to_pair(float a, float b, const __nv_bfloat16*) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -116,56 +125,55 @@ __device__ __forceinline__ uint32_t float2_to_pair(float a, float b, const __hal
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Quantise one group of 16 values (eight 32-bit words of two).  mul = 2^-exp.
+// Quantise a group of 16 values (eight 32-bit words of two).  mul = 2^-exp.
 //
-// Every decision is the exact one.  The scale: amax * mul is exact (a power of
-// two) and has at most 11 bits, so its quotient by 6, rounded to fp32, lies on
-// a border between two e4m3 numbers only where the exact quotient does.  The
-// codes: x has at most 11 bits and s four, so x / s is either one of the ties
-// 1/4, 3/4, 5/4, ... 5 exactly or at least 2^-13 away from it (for quotients up
-// to 6.5).  t = x * (mul / s) is off by under 2^-20, and adding and taking away
-// 768 rounds it to a multiple of 2^-14, so a tie comes out as a tie and
-// everything else on its own side.
+// Every decision is the exact one, without a division.  The scale: amax * mul is
+// exact (a power of two) and has at most 11 bits; a border between two e4m3
+// numbers has at most five, so amax * mul / 6 is a border or differs from it by
+// 2^-13 of itself or more.  The product with 1/6 is off by under 2^-22 of itself,
+// and rounding it to 16 bits brings it onto a border where the exact quotient is
+// one and leaves everything else on its own side.  The codes: x has at most 11 bits
+// and s four, so x / s is either one of the ties 1/4, 3/4, 5/4, ... 5 exactly or at
+// least 2^-13 away from it (for quotients up to 6.5).  x * (mul / s) is off by under
+// 2^-18, and adding and taking away 768 rounds it to a multiple of 2^-14.
 template <typename T>
 __device__ __forceinline__ uint2 quantise16(const uint32_t (&w)[8], float mul, uint8_t* scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
-  top = max(top & 0xFFFFu, top >> 16);
+  constexpr const T* kT = nullptr;
+  const uint32_t m = max_abs2(max_abs2(max_abs2(w[0], w[1], kT), max_abs2(w[2], w[3], kT), kT),
+                              max_abs2(max_abs2(w[4], w[5], kT), max_abs2(w[6], w[7], kT), kT), kT);
+  const uint32_t top = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);   // of the bit patterns: a NaN is above all
   if (top >= kFirstNonfinite<T>) {   // the whole group reads back as NaN
     *scale = 0x7F;
     return make_uint2(0u, 0u);
   }
-  const float amax = pair_to_float2(top, static_cast<const T*>(nullptr)).x;
-  const uint8_t sb = f32_to_e4m3(fminf(__fdiv_rn(amax * mul, 6.f), 448.f));
+  const float amax = pair_to_float2(top, kT).x;
+  const float want = __uint_as_float((__float_as_uint(amax * mul * (1.f / 6.f)) + 0x80u) & 0xFFFFFF00u);
+  const uint8_t sb = f32_to_e4m3(fminf(want, 448.f));
   const float s = half2_bits_to_float2(e4m3x2_to_f16x2(sb)).x;
-  const float inv = sb ? __fdiv_rn(mul, s) : 0.f;
+  const float inv = sb ? __fdividef(mul, s) : 0.f;
   float x[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 v = pair_to_float2(w[i], static_cast<const T*>(nullptr));
-    x[2 * i] = __fadd_rn(__fadd_rn(__fmul_rn(v.x, inv), 768.f), -768.f);
-    x[2 * i + 1] = __fadd_rn(__fadd_rn(__fmul_rn(v.y, inv), 768.f), -768.f);
+    const float2 v = pair_to_float2(w[i], kT);
+    x[2 * i] = __fadd_rn(__fmaf_rn(v.x, inv, 768.f), -768.f);
+    x[2 * i + 1] = __fadd_rn(__fmaf_rn(v.y, inv, 768.f), -768.f);
   }
   *scale = sb;
   return make_uint2(f32_to_e2m1x8(x), f32_to_e2m1x8(x + 8));
 }
 
-// The 16 values of a group in the output type: codes (two words), scale byte,
-// mul = 2^exp.
+// Eight values in the output type: codes, scale byte, mul = 2^exp.
 template <typename T>
-__device__ __forceinline__ void dequantise16(uint2 codes, uint8_t scale, float mul, uint32_t (&w)[8]) {
+__device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint8_t scale, float mul) {
   const float s = half2_bits_to_float2(e4m3x2_to_f16x2(scale)).x * mul;
-  uint32_t h[4];
+  uint32_t h[4], w[4];
+  e2m1x8_to_f16(codes, h);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    e2m1x8_to_f16(i ? codes.y : codes.x, h);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 v = half2_bits_to_float2(h[j]);
-      w[4 * i + j] = float2_to_pair(v.x * s, v.y * s, static_cast<const T*>(nullptr));
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = half2_bits_to_float2(h[j]);
+    w[j] = float2_to_pair(v.x * s, v.y * s, static_cast<const T*>(nullptr));
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace kv

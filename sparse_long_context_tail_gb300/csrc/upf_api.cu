@@ -746,7 +746,7 @@ upf_status check_ws_bytes(const void* ws, size_t have, size_t need) {
 
 upf_status check_tokens(const upf_kv_cache* c, int32_t num_tokens) {
   if (num_tokens < 0 || num_tokens > (1 << 30)) return fail(UPF_ERR_INVALID_ARG, "num_tokens must be in [0, 2^30]");
-  if ((int64_t)num_tokens * c->num_kv_heads * (c->head_dim / 16) > (1LL << 38))
+  if ((int64_t)num_tokens * c->num_kv_heads * (c->head_dim / 16) > (1LL << 35))   // warps are counted in 32 bits
     return fail(UPF_ERR_UNSUPPORTED, "too many tokens for one call");
   return UPF_OK;
 }
