@@ -372,8 +372,13 @@ typedef enum upf_dtype { UPF_BF16 = 0, UPF_F16 = 1 } upf_dtype;
  * if they are invalid. */
 size_t upf_kv_cache_bytes(const upf_kv_cache* cache);
 
+/* Tokens that upf_kv_write writes without a workspace. */
+#define UPF_KV_FEW_TOKENS 1024
+
 /* Bytes of workspace upf_kv_write needs for num_tokens tokens (scratch, 256-byte
- * aligned, any contents); 0 and the last error if the arguments are invalid. */
+ * aligned, any contents); 0 and the last error if the arguments are invalid.
+ * Calls of at most UPF_KV_FEW_TOKENS tokens use none: ws may be NULL (and this
+ * returns a small positive size). */
 size_t upf_kv_write_workspace_bytes(const upf_kv_cache* cache, int32_t num_tokens);
 
 /* Quantise tokens' keys and values and write them at their slots.

@@ -60,6 +60,7 @@ class UpfKvQuery(ctypes.Structure):
 
 
 UPF_BF16, UPF_F16 = 0, 1
+UPF_KV_FEW_TOKENS = 1024
 
 _SIGNATURES = {
     "upf_version": ([], c_int),
@@ -279,7 +280,7 @@ def upf_kv_write_workspace_bytes(cache: UpfKvCache, num_tokens: int) -> int:
 def upf_kv_write(ctx, cache, dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens, num_tokens_dev, ws, ws_bytes,
                  stream=0):
     _check(load().upf_kv_write(ctx, ctypes.byref(cache), dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens,
-                               num_tokens_dev or None, ws, ws_bytes, stream or None))
+                               num_tokens_dev or None, ws or None, ws_bytes, stream or None))
 
 
 def upf_kv_read(ctx, cache, dtype, slots, num_tokens, num_tokens_dev, k, k_row_stride, v, v_row_stride, stream=0):

@@ -40,6 +40,7 @@
 // running maximum by 2^3, so that weights down to 2^-26 of the reference keep all
 // their bits.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -1048,8 +1049,15 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t s) {
   Parts parts;
   parts.o = static_cast<float*>(a.ws);
   parts.ml = reinterpret_cast<float2*>(parts.o + part_rows<kDim, NT>() * kDim);
-  cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, kDim, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return e;
+  // once a device (setting it twice does no harm)
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << (a.device & 63);
+  cudaError_t e = cudaSuccess;
+  if (a.device > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kv_attend_kernel<T, kDim, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   // Most CTAs that can come to work on one unit, if the units are about as long as one another:
   // all CTAs by the units, or the longest unit by the least share.
   const long long units = (long long)a.R * a.H * ((a.max_q * a.gamma + S::kRows - 1) / S::kRows);

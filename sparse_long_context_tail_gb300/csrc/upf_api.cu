@@ -791,7 +791,7 @@ upf_status check_query(const upf_kv_cache* c, const upf_kv_query* x, bool need_d
 }
 
 size_t write_ws_bytes(const upf_kv_cache* c, int32_t num_tokens) {
-  return num_tokens <= upf::kKvFewTokens ? 256 : align256(size_t(c->num_slots) * sizeof(int32_t));
+  return num_tokens <= UPF_KV_FEW_TOKENS ? 256 : align256(size_t(c->num_slots) * sizeof(int32_t));
 }
 
 }  // namespace
@@ -1158,7 +1158,8 @@ upf_status upf_kv_write(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, 
   if ((st = check_rows("k", k, k_row_stride, cache->num_kv_heads, cache->head_dim)) != UPF_OK) return st;
   if ((st = check_rows("v", v, v_row_stride, cache->num_kv_heads, cache->head_dim)) != UPF_OK) return st;
   if (!slots) return fail(UPF_ERR_INVALID_ARG, "slots is NULL");
-  if ((st = check_ws_bytes(ws, ws_bytes, write_ws_bytes(cache, num_tokens))) != UPF_OK) return st;
+  if (num_tokens > UPF_KV_FEW_TOKENS && (st = check_ws_bytes(ws, ws_bytes, write_ws_bytes(cache, num_tokens))) != UPF_OK)
+    return st;
   if ((st = check_ctx(ctx)) != UPF_OK) return st;
   DeviceGuard guard(ctx->device);
   upf::KvWriteArgs a;
@@ -1175,7 +1176,7 @@ upf_status upf_kv_write(upf_ctx* ctx, const upf_kv_cache* cache, int32_t dtype, 
   a.count = num_tokens_dev;
   a.k_mul = std::ldexp(1.f, -cache->k_exp);
   a.v_mul = std::ldexp(1.f, -cache->v_exp);
-  a.owner = num_tokens <= upf::kKvFewTokens ? nullptr : static_cast<int32_t*>(ws);
+  a.owner = num_tokens <= UPF_KV_FEW_TOKENS ? nullptr : static_cast<int32_t*>(ws);
   a.status = ctx->status_dev;
   UPF_LAUNCH(upf::launch_kv_write(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv write");
   return UPF_OK;
@@ -1266,6 +1267,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
   a.counters = ctx->status_dev + 64;
   a.ws = ws;
+  a.device = ctx->device;
   int fill[upf::kMaxHeads] = {};
   for (int h = 0; h < a.Hq; ++h) {
     const int g = query->kv_of_q ? query->kv_of_q[h] : h / gamma;

@@ -176,7 +176,6 @@ struct HistoryArgs {
 
 // The 4-bit KV cache (layout: kv_layout.cuh).
 constexpr int kKvCounters = 8192;    // words of the context that the cache attention counts in
-constexpr int kKvFewTokens = 1024;   // calls of at most this many tokens write without claiming their slots
 
 struct KvWriteArgs {
   uint8_t* data;
@@ -188,7 +187,7 @@ struct KvWriteArgs {
   const int64_t* slots;         // [T]
   const int32_t* count;         // nullable: tokens to write, read on the device
   float k_mul, v_mul;           // 2^-exp
-  int32_t* owner;               // [num_slots] (nullable: at most kKvFewTokens tokens)
+  int32_t* owner;               // [num_slots] (nullable: at most UPF_KV_FEW_TOKENS tokens)
   int32_t* status;
 };
 
@@ -227,6 +226,7 @@ struct KvAttendArgs {
   int32_t* counters;            // [kKvCounters] of the context, zero between calls
   long long wait_limit;
   void* ws;
+  int32_t device;
   uint8_t qhead[kMaxHeads];     // q heads of kv head g at [g*gamma, (g+1)*gamma)
 };
 

@@ -48,6 +48,7 @@ class QuantKVCache:
         self.device = torch.device("cuda", device or 0)
         self.storage = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if storage is None else storage
         self._cache.data = self.storage.data_ptr()
+        self._ws_bytes = {}      # upf_kv_attend_workspace_bytes by (q heads, new tokens)
         self.ctx = B.upf_create(self.device.index)
 
     def close(self) -> None:
@@ -67,22 +68,26 @@ class QuantKVCache:
         return B.upf_sync_status(self.ctx, self._stream())
 
     # ------------------------------------------------------------------
+    # A call on a few tokens takes a few microseconds on the GPU, so the checks below ask each
+    # tensor for its shape and strides once.
     def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+        # the handle of torch.cuda.current_stream(self.device) without the object
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def _rows(self, name: str, t: torch.Tensor, heads: int) -> None:
+    def _rows(self, name: str, t: torch.Tensor, heads: int) -> int:
+        """Check rows of `heads` heads; return the row stride in elements."""
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         if t.dtype not in _DTYPES:
             raise ValueError(f"{name} must be bfloat16 or float16, not {t.dtype}")
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, {heads}, {self.head_dim}]")
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
+        shape, d = t.shape, self.head_dim
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens, {heads}, {d}]")
+        row, head, dim = t.stride()
+        if dim != 1 or (heads > 1 and head != d):
             raise ValueError(f"{name}: the heads of a row must be contiguous (strides {t.stride()})")
-
-    def _row_stride(self, t: torch.Tensor) -> int:
         # the stride of a single row is never used and may be anything
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * self.head_dim
+        return row if shape[0] > 1 else heads * d
 
     def _ints(self, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, n: int) -> int:
         if t is None:
@@ -97,16 +102,19 @@ class QuantKVCache:
         """Store ``k``, ``v`` [T, H_kv, d] (rows may be strided) at ``slots`` (int64 [T]; negative: skip).
 
         ``num_tokens``: device int32 [1]; only that many first tokens are stored (e.g. ``total_kept``)."""
-        self._rows("k", k, self.num_kv_heads)
-        self._rows("v", v, self.num_kv_heads)
+        ks = self._rows("k", k, self.num_kv_heads)
+        vs = self._rows("v", v, self.num_kv_heads)
         T = k.shape[0]
         if v.shape[0] != T or v.dtype != k.dtype:
             raise ValueError("k and v disagree on the token count or the type")
         sp = self._ints("slots", slots, torch.int64, T)
         np_ = self._ints("num_tokens", num_tokens, torch.int32, 1)
-        ws = torch.empty(B.upf_kv_write_workspace_bytes(self._cache, T), dtype=torch.uint8, device=self.device)
-        B.upf_kv_write(self.ctx, self._cache, _DTYPES[k.dtype], k.data_ptr(), self._row_stride(k), v.data_ptr(),
-                       self._row_stride(v), sp, T, np_, ws.data_ptr(), ws.numel(), self._stream())
+        wp = wn = 0
+        if T > B.UPF_KV_FEW_TOKENS:      # fewer need no workspace
+            ws = torch.empty(B.upf_kv_write_workspace_bytes(self._cache, T), dtype=torch.uint8, device=self.device)
+            wp, wn = ws.data_ptr(), ws.numel()
+        B.upf_kv_write(self.ctx, self._cache, _DTYPES[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs, sp, T, np_, wp, wn,
+                       self._stream())
 
     def read(self, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, num_tokens: Optional[torch.Tensor] = None,
              out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -121,15 +129,17 @@ class QuantKVCache:
             if dtype not in _DTYPES:
                 raise ValueError(f"dtype must be bfloat16 or float16, not {dtype}")
             shape = (T, self.num_kv_heads, self.head_dim)
-            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+            k = torch.empty(shape, dtype=dtype, device=self.device)
+            v = torch.empty(shape, dtype=dtype, device=self.device)
+            ks = vs = self.num_kv_heads * self.head_dim
         else:
             k, v = out
-            self._rows("out[0]", k, self.num_kv_heads)
-            self._rows("out[1]", v, self.num_kv_heads)
+            ks = self._rows("out[0]", k, self.num_kv_heads)
+            vs = self._rows("out[1]", v, self.num_kv_heads)
             if k.shape[0] != T or v.shape[0] != T or k.dtype != v.dtype:
                 raise ValueError("out disagrees with slots on the token count, or its two tensors on the type")
-        B.upf_kv_read(self.ctx, self._cache, _DTYPES[k.dtype], sp, T, np_, k.data_ptr(), self._row_stride(k),
-                      v.data_ptr(), self._row_stride(v), self._stream())
+        B.upf_kv_read(self.ctx, self._cache, _DTYPES[k.dtype], sp, T, np_, k.data_ptr(), ks, v.data_ptr(), vs,
+                      self._stream())
         return k, v
 
     def attend(self, q: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, page_size: int,
@@ -144,29 +154,34 @@ class QuantKVCache:
         keep what ``out`` and ``lse`` hold (anything, in new tensors)."""
         if q.dim() != 3:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, H_q, {self.head_dim}]")
-        N, Hq = q.shape[0], q.shape[1]
-        self._rows("q", q, Hq)
-        if (page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != self.device
-                or page_table.shape[1] < 1 or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-            raise ValueError(f"page_table must be an int32 [requests, pages] tensor with contiguous rows on {self.device}")
-        R = page_table.shape[0]
+        N, Hq, d = q.shape
+        qs = self._rows("q", q, Hq)
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != self.device:
+            raise ValueError(f"page_table must be an int32 [requests, pages] tensor on {self.device}")
+        R, pages = page_table.shape
+        table_row, table_page = page_table.stride()
+        if pages < 1 or (pages > 1 and table_page != 1):
+            raise ValueError("page_table needs a page at least, and the pages of a request side by side")
         lp = self._ints("kv_len", kv_len, torch.int32, R)
         cp = self._ints("cu_q", cu_q, torch.int32, R + 1)
         if out is None:
-            out = torch.empty((N, Hq, self.head_dim), dtype=q.dtype, device=self.device)
+            out = torch.empty((N, Hq, d), dtype=q.dtype, device=self.device)
+            outs = Hq * d
         else:
-            self._rows("out", out, Hq)
+            outs = self._rows("out", out, Hq)
             if out.shape[0] != N or out.dtype != q.dtype:
                 raise ValueError("out disagrees with q on the token count or the type")
         if lse is None:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=self.device)
         elif lse.dtype != torch.float32 or lse.shape != (N, Hq) or not lse.is_contiguous() or lse.device != self.device:
             raise ValueError(f"lse must be a contiguous float32 [{N}, {Hq}] tensor on {self.device}")
-        query, keep = B.make_kv_query(R, Hq, N, lp, page_table.data_ptr(),
-                                      page_table.stride(0) if R > 1 else page_table.shape[1], page_table.shape[1],
+        query, keep = B.make_kv_query(R, Hq, N, lp, page_table.data_ptr(), table_row if R > 1 else pages, pages,
                                       page_size, cp, max_q_len, window, sinks, softmax_scale or 0.0, kv_of_q)
-        ws = torch.empty(B.upf_kv_attend_workspace_bytes(self._cache, query), dtype=torch.uint8, device=self.device)
-        B.upf_kv_attend(self.ctx, self._cache, query, _DTYPES[q.dtype], q.data_ptr(), self._row_stride(q), out.data_ptr(),
-                        self._row_stride(out), lse.data_ptr(), ws.data_ptr(), ws.numel(), self._stream())
+        nbytes = self._ws_bytes.get((Hq, max_q_len))
+        if nbytes is None:               # depends on these alone
+            nbytes = self._ws_bytes[Hq, max_q_len] = B.upf_kv_attend_workspace_bytes(self._cache, query)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        B.upf_kv_attend(self.ctx, self._cache, query, _DTYPES[q.dtype], q.data_ptr(), qs, out.data_ptr(), outs,
+                        lse.data_ptr(), ws.data_ptr(), nbytes, self._stream())
         del keep
         return AttendOutputs(out, lse)

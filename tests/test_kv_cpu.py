@@ -175,8 +175,8 @@ def test_attend_calls_that_are_refused(query, args, word):
 @pytest.mark.parametrize("args,word", [
     (dict(dtype=-1), "dtype"), (dict(k=0), "k "), (dict(k=8), "k "), (dict(ks=128), "stride"), (dict(ks=260), "stride"),
     (dict(v=0), "v "), (dict(vs=0), "stride"), (dict(slots=0), "slots"), (dict(T=-1), "num_tokens"),
-    (dict(T=(1 << 30) + 1), "num_tokens"), (dict(ws=0), "workspace"), (dict(nbytes=0), "workspace"), (dict(T=0), "context"),
-    ({}, "context")])
+    (dict(T=(1 << 30) + 1), "num_tokens"), (dict(T=2000, ws=0), "workspace"), (dict(T=2000, nbytes=0), "workspace"),
+    (dict(T=2000, ws=64), "workspace"), (dict(T=0), "context"), (dict(ws=0, nbytes=0), "context"), ({}, "context")])
 def test_write_calls_that_are_refused(args, word):
     a = dict(dtype=0, k=16, ks=256, v=16, vs=256, slots=8, T=4, ws=256, nbytes=1 << 20)
     a.update(args)
