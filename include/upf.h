@@ -455,6 +455,9 @@ size_t upf_kv_attend_workspace_bytes(const upf_kv_cache* cache, const upf_kv_que
  *         strides >= H_q*head_dim and multiples of 8, 16-byte aligned; out must
  *         not overlap q or the cache.
  * lse:    device float32 [num_q_tokens, H_q] (nullable), natural logarithm.
+ * cu_q, kv_len and page_table must not change while the call runs.  A captured
+ * call may be replayed with other contents of them, as long as the sizes in
+ * `query` hold and the context exists.
  * Lengths or pages out of range set UPF_ERR_INVALID_ARG in the status word:
  * a request whose cu_q entries are not ascending within [0, num_q_tokens], or
  * with more than max_q_len rows, is skipped; one with a bad kv_len gets empty

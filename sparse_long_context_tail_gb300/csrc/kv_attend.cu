@@ -409,7 +409,8 @@ __device__ __forceinline__ void finish_unit(const KvAttendArgs& a, const Parts& 
                             int count, volatile int* said, Sync&& sync) {
   using S = Shape<kDim, NT>;
   const long long place = u.place + deal.cost;
-  const int first = int(quotient(place, deal.share)), last = int(quotient(place + u.x.tiles - 1, deal.share));
+  const int first = int(quotient(place, deal.share));
+  const int last = min(int(quotient(place + u.x.tiles - 1, deal.share)), int(gridDim.x) * (deal.teams ? S::kTeams : 1) - 1);
   const int n = last - first + 1, row0 = u.c * S::kRows;
   const Note note{first, last, u.h, row0, u.x.q_len * a.gamma, u.x.q0};
   const int outputs = min(S::kRows, note.rows - row0) * (kDim / 4);

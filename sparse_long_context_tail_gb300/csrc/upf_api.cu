@@ -15,10 +15,13 @@
 
 #include "upf_internal.cuh"
 
+// Device words of a context: [0] the status, from [64] on the cache attention's counters.
+constexpr size_t kCtxWords = 64 + upf::kKvCounters;
+
 struct upf_ctx {
   int device;
   int num_sms;
-  int32_t* status_dev;  // [64 + kKvCounters] device words; [0] = status, from [64] on the cache attention's counters
+  int32_t* status_dev;  // [kCtxWords] device words
   long long wait_limit = 0;  // pipeline waits of the scoring kernels, cycles (0: default)
   // tracing
   bool profiling = false;
@@ -849,12 +852,11 @@ upf_status upf_create(upf_ctx** out, int device) {
     delete c;
     return fail(UPF_ERR_UNSUPPORTED, "libupf is built for sm_103a; device %d is sm_%d%d", device, major, minor);
   }
-  const size_t words = 64 + upf::kKvCounters;
-  if ((e = cudaMalloc(&c->status_dev, words * sizeof(int32_t))) != cudaSuccess) {
+  if ((e = cudaMalloc(&c->status_dev, kCtxWords * sizeof(int32_t))) != cudaSuccess) {
     delete c;
     return cuda_fail(e, "cudaMalloc(status)");
   }
-  if ((e = cudaMemset(c->status_dev, 0, words * sizeof(int32_t))) != cudaSuccess) {
+  if ((e = cudaMemset(c->status_dev, 0, kCtxWords * sizeof(int32_t))) != cudaSuccess) {
     cudaFree(c->status_dev);
     delete c;
     return cuda_fail(e, "cudaMemset(status)");
@@ -887,7 +889,8 @@ upf_status upf_sync_status(upf_ctx* ctx, void* stream) {
   if ((e = cudaMemcpy(&code, ctx->status_dev, sizeof(code), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return cuda_fail(e, "read status");
   if (code != 0) {
-    if ((e = cudaMemset(ctx->status_dev, 0, sizeof(int32_t))) != cudaSuccess) return cuda_fail(e, "reset status");
+    // the counters too: whatever went wrong, the next call starts from zero
+    if ((e = cudaMemset(ctx->status_dev, 0, kCtxWords * sizeof(int32_t))) != cudaSuccess) return cuda_fail(e, "reset status");
     return fail(static_cast<upf_status>(code), "device reported %s", upf_status_name(static_cast<upf_status>(code)));
   }
   return UPF_OK;

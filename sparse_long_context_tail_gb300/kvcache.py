@@ -29,7 +29,8 @@ class QuantKVCache:
     ``storage``: uint8 tensor of ``upf_kv_cache_bytes`` bytes to use (any contiguous shape);
     by default one is allocated, its slots unwritten.  ``k_exp`` / ``v_exp`` scale the range
     by a power of two.  Calls run on the current stream of the cache's device; one
-    cache must not be used by two streams at the same time."""
+    cache must not be used by two streams at the same time, and has to outlive the graphs that
+    captured calls on it."""
 
     def __init__(self, num_slots: int, num_kv_heads: int, head_dim: int, device: Optional[int] = None, k_exp: int = 0,
                  v_exp: int = 0, storage: Optional[torch.Tensor] = None):

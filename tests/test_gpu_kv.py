@@ -407,6 +407,59 @@ def test_bad_tables_are_reported_and_touch_nothing_else():
         assert b.cache.status() == 1
 
 
+@pytest.mark.parametrize("lens,Hq,H,d", [
+    ([60000] + [100] * 19, 1, 1, 64),        # one unit over most of the CTAs, among others: parts added up in two steps
+    ([6000] + [20] * 100, 4, 1, 128),        # short units, teams as workers, one of them over many teams
+    ([9000] + [33] * 60, 12, 1, 256),        # the same with teams of four warps
+    ([20000, 20000], 4, 1, 128),             # few units over many CTAs: added up by the second launch
+    ([5000, 17, 4000, 900], 32, 2, 128),     # two chunks of rows a kv head
+])
+def test_units_over_many_workers(lens, Hq, H, d):
+    b = Batch(lens, Hq, H, d, page=64)
+    q, cu_q = b.queries([1] * len(lens))
+    ref = K.attend(f64(q), b.k, b.v, cu_q)
+    first = None
+    for _ in range(3):                       # the counters are back at zero after each call
+        got = b.cache.attend(q, b.table, b.kv_len, 64)
+        compare(got, ref, BF16)
+        assert first is None or (torch.equal(first.out, got.out) and torch.equal(first.lse, got.lse))
+        first = got
+    # another shape in between, on the same counters
+    half = b.kv_len // 2
+    got = b.cache.attend(q, b.table, half, 64)
+    n = half.tolist()
+    compare(got, K.attend(f64(q), [k[:m] for k, m in zip(b.k, n)], [v[:m] for v, m in zip(b.v, n)], cu_q), BF16)
+    assert torch.equal(b.cache.attend(q, b.table, b.kv_len, 64).out, first.out) and b.cache.status() == 0
+
+
+def test_requests_that_do_not_begin_at_row_zero():
+    b = Batch([70, 30], 4, 2, 128)
+    q, cu = b.queries([2, 1])
+    shifted = torch.cat([rand((3, 4, 128), BF16, 2), q])
+    out, lse = torch.full_like(shifted, 5.0), torch.full((6, 4), 5.0, device=DEV)
+    b.cache.attend(shifted, b.table, b.kv_len, 16, cu_q=torch.from_numpy(cu + 3).to(DEV), max_q_len=2, out=out, lse=lse)
+    assert (out[:3] == 5).all() and (lse[:3] == 5).all() and b.cache.status() == 0
+    compare((out[3:], lse[3:]), K.attend(f64(q), b.k, b.v, cu), BF16)
+
+
+def test_two_caches_on_two_streams():
+    """Each cache has its own context: their calls may overlap."""
+    work = []
+    for i, (Hq, H, d) in enumerate([(8, 2, 128), (16, 2, 256)]):
+        b = Batch([3000, 500, 40], Hq, H, d, seed=20 + i)
+        q, cu = b.queries([1, 1, 1])
+        work.append((b, q, K.attend(f64(q), b.k, b.v, cu), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for b, q, ref, stream in work:
+            with torch.cuda.stream(stream):
+                outs.append((b.cache.attend(q, b.table, b.kv_len, 16), ref))
+    torch.cuda.synchronize()
+    for got, ref in outs:
+        compare(got, ref, BF16)
+
+
 def test_results_repeat_bit_for_bit():
     b = Batch([3000, 17, 900], 8, 2, 128)
     q, cu = b.queries([2, 1, 2])
