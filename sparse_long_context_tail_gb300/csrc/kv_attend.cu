@@ -133,11 +133,53 @@ struct Deal {
   long long share;     // places of a worker
 };
 
-// Each thread looks at requests [i * per, (i + 1) * per); `before` are the places
-// of the requests before them.
+// The deal from the tiles and units of all requests; `before`: those of the requests
+// before this thread's, turned into places.
+__device__ __forceinline__ Deal make_deal(long long all_t, long long all_u, long long t, long long u, int teams, long long& before) {
+  Deal d;
+  d.teams = all_t < all_u * kShortUnit;
+  d.cost = d.teams ? kUnitCostTeam : kUnitCostCta;
+  d.total = all_t + all_u * d.cost;
+  before = t + u * d.cost;
+  const long long workers = d.teams ? (long long)gridDim.x * teams : gridDim.x;
+  d.share = max(quotient(d.total + workers - 1, workers), (long long)(d.teams ? 1 : teams));
+  return d;
+}
+
+__device__ __forceinline__ void scan_warp(long long& t, long long& u) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, t, s), z = __shfl_up_sync(0xFFFFFFFFu, u, s);
+    if (lane >= s) {
+      t += y;
+      u += z;
+    }
+  }
+}
+
+// At most 32 requests: every warp works the deal out by itself, a request a lane (`mine`).
+__device__ Deal deal_out_few(const KvAttendArgs& a, int rows, int teams, long long& before, Request& mine, bool& empty) {
+  const int lane = threadIdx.x & 31;
+  long long tiles = 0, units = 0;
+  bool none = false;
+  if (lane < a.R) {
+    mine = load_request(a, lane);
+    none = mine.tiles == 0;
+    units = none ? 0 : (long long)a.H * chunks_of(a, mine, rows);
+    tiles = units * mine.tiles;
+  }
+  empty = __any_sync(0xFFFFFFFFu, none);
+  long long t = tiles, u = units;
+  scan_warp(t, u);
+  const long long all_t = __shfl_sync(0xFFFFFFFFu, t, 31), all_u = __shfl_sync(0xFFFFFFFFu, u, 31);
+  return make_deal(all_t, all_u, t - tiles, u - units, teams, before);
+}
+
+// More: the CTA does, thread i looks at requests [i * per, (i + 1) * per).
 // `mine`: the first of the thread's requests; `empty`: some request has no tiles.
-__device__ Deal deal_out(const KvAttendArgs& a, int rows, int teams, int per, longlong2 (&warp_sums)[kWarps], long long& before,
-                         Request& mine, bool& empty) {
+__device__ Deal deal_out_many(const KvAttendArgs& a, int rows, int teams, int per, longlong2 (&warp_sums)[kWarps],
+                              long long& before, Request& mine, bool& empty) {
   long long tiles = 0, units = 0;
   bool none = false;
   for (int j = 0; j < per; ++j) {
@@ -155,14 +197,7 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int teams, int per, lo
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long t = tiles, u = units;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, t, s), z = __shfl_up_sync(0xFFFFFFFFu, u, s);
-    if (lane >= s) {
-      t += y;
-      u += z;
-    }
-  }
+  scan_warp(t, u);
   if (lane == 31) warp_sums[warp] = make_longlong2(t, u);
   empty = __syncthreads_or(none);
   t -= tiles;
@@ -177,14 +212,7 @@ __device__ Deal deal_out(const KvAttendArgs& a, int rows, int teams, int per, lo
     all_t += warp_sums[w].x;
     all_u += warp_sums[w].y;
   }
-  Deal d;
-  d.teams = all_t < all_u * kShortUnit;
-  d.cost = d.teams ? kUnitCostTeam : kUnitCostCta;
-  d.total = all_t + all_u * d.cost;
-  before = t + u * d.cost;
-  const long long workers = d.teams ? (long long)gridDim.x * teams : gridDim.x;
-  d.share = max(quotient(d.total + workers - 1, workers), (long long)(d.teams ? 1 : teams));
-  return d;
+  return make_deal(all_t, all_u, t, u, teams, before);
 }
 
 // The workspace.  A worker has at most two units that others work on too: the one
@@ -286,6 +314,19 @@ struct Unit {
   long long place;    // its first place
   Request x;
 };
+
+// The unit of request r (places from `before` on) that holds place `first`.
+__device__ __forceinline__ Unit unit_at(const KvAttendArgs& a, int r, const Request& x, long long before, long long first,
+                                        int cost, int rows) {
+  const int chunks = chunks_of(a, x, rows), places = x.tiles + cost, unit = int(quotient(first - before, places));
+  Unit u;
+  u.r = r;
+  u.h = unit / chunks;
+  u.c = unit - u.h * chunks;
+  u.place = before + (long long)unit * places;
+  u.x = x;
+  return u;
+}
 
 __device__ __forceinline__ void next_unit(const KvAttendArgs& a, Unit& u, int cost, int rows) {
   u.place += u.x.tiles + cost;
@@ -476,37 +517,47 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   if (member == 0 && lane == 0)
     for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(ptx::smem_u32(&bars[team][s]), 1);
   ptx::fence_barrier_init();
+  __syncthreads();   // the barriers are there for the team's other warps
   pdl_wait();
 
   // ---- this worker's share
-  const int per = (a.R + kThreads - 1) / kThreads;
   long long before;
   Request mine;
   bool empty;
-  const Deal deal = deal_out(a, S::kRows, S::kTeams, per, warp_sums, before, mine, empty);
-  const int lg = deal.teams ? 0 : S::kLogTeams, group = 1 << lg, rank = deal.teams ? 0 : team;   // teams of a worker; which this is
-  const int worker = deal.teams ? blockIdx.x * S::kTeams + team : blockIdx.x;
-  for (int j = 0; j < per; ++j) {
-    // the thread whose requests hold a worker's first place finds its unit
-    const int r = threadIdx.x * per + j;
-    if (r >= a.R) break;
-    Unit u;
-    u.x = j ? load_request(a, r) : mine;
-    if (u.x.tiles == 0) continue;
-    const int chunks = chunks_of(a, u.x, S::kRows), places = u.x.tiles + deal.cost;
-    const long long end = before + (long long)places * a.H * chunks;
-    for (int w = 0; w < S::kTeams / group; ++w) {
-      const long long first = (long long)(blockIdx.x * (S::kTeams / group) + w) * deal.share;
-      if (first < before || first >= end) continue;
-      const int unit = int(quotient(first - before, places));
-      u.r = r;
-      u.h = unit / chunks;
-      u.c = unit % chunks;
-      u.place = before + (long long)unit * places;
-      starts[w] = u;
+  Deal deal;
+  Unit u;
+  int worker;
+  if (a.R <= 32) {
+    deal = deal_out_few(a, S::kRows, S::kTeams, before, mine, empty);
+    worker = deal.teams ? blockIdx.x * S::kTeams + team : blockIdx.x;
+    const long long first = worker * deal.share;
+    // the last request with tiles that begins at or before the first place
+    const uint32_t from = __ballot_sync(0xFFFFFFFFu, lane < a.R && mine.tiles > 0 && before <= first);
+    const int r = from ? 31 - __clz(from) : 0;
+    const long long at = __shfl_sync(0xFFFFFFFFu, before, r);
+    if (first < deal.total) u = unit_at(a, r, load_request(a, r), at, first, deal.cost, S::kRows);
+  } else {
+    const int per = (a.R + kThreads - 1) / kThreads;
+    deal = deal_out_many(a, S::kRows, S::kTeams, per, warp_sums, before, mine, empty);
+    worker = deal.teams ? blockIdx.x * S::kTeams + team : blockIdx.x;
+    const int workers = deal.teams ? S::kTeams : 1;   // of this CTA
+    for (int j = 0; j < per; ++j) {
+      // the thread whose requests hold a worker's first place finds its unit
+      const int r = threadIdx.x * per + j;
+      if (r >= a.R) break;
+      const Request x = j ? load_request(a, r) : mine;
+      if (x.tiles == 0) continue;
+      const long long end = before + (long long)(x.tiles + deal.cost) * a.H * chunks_of(a, x, S::kRows);
+      for (int w = 0; w < workers; ++w) {
+        const long long first = (long long)(blockIdx.x * workers + w) * deal.share;
+        if (first >= before && first < end) starts[w] = unit_at(a, r, x, before, first, deal.cost, S::kRows);
+      }
+      before = end;
     }
-    before = end;
+    __syncthreads();
+    u = starts[deal.teams ? team : 0];
   }
+  const int lg = deal.teams ? 0 : S::kLogTeams, group = 1 << lg, rank = deal.teams ? 0 : team;   // teams of a worker; which this is
   // rows that see nothing because their request has no entries
   for (int r = blockIdx.x; empty && r < a.R; r += gridDim.x) {
     const Request x = load_request(a, r);
@@ -519,7 +570,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     }
   }
   if (parts.notes && threadIdx.x == 0) parts.notes[blockIdx.x].first = -1;
-  __syncthreads();
   const long long my_first = worker * deal.share, my_end = min(my_first + deal.share, deal.total);
   if (my_first >= deal.total) return;   // a whole CTA, or a team that meets no other again
 
@@ -533,11 +583,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   const int v_at = 8 * kDim + part * (8 * S::kPart) + lane * (S::kPart / 8) + half * 4;
   const int vs_at = 17 * kDim + part * S::kPart + (S::kPart == 128 ? g : g >> 1) * 8 + 2 * t4;
   const int dim0 = part * 128 + g * (S::kPart / 8) + half * 8;   // first of the lane's 2 kSteps dims of the output
-  int stage = 0, in_flight = 0;          // next stage to take; stages filled and not taken
-  uint32_t phases = 0, usable_ring = 0;  // a bit per stage; two bits per stage: which of its records may be looked at
+  int stage = 0;                  // next stage to take
+  uint32_t phase = 0;             // of its barrier
+  uint32_t usable_ring = ~0u;     // two bits per stage: which of its records may be looked at
   bool dead = false;
 
-  for (Unit u = starts[deal.teams ? team : 0]; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
+  for (; u.place < my_end; next_unit(a, u, deal.cost, S::kRows)) {
     int begin = int(max(0LL, my_first - u.place - deal.cost));
     int end = int(min((long long)u.x.tiles, my_end - u.place - deal.cost));
     if (deal.teams && u.x.tiles <= kWholeUnit) {
@@ -577,17 +628,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
 
     // ---- the copies.  The lanes know the records of the team's next 16 tiles: lane 2 i + b the
     // b-th record of the i-th.  The team's first warp has them copied.
-    int it = begin + rank, held = INT_MIN / 2;
+    const int todo = dead || begin + rank >= end ? 0 : (end - begin - rank + group - 1) >> lg;   // this team's tiles
+    int left = todo, src = 16, refill = begin + rank;
     const uint8_t* record = nullptr;
     uint32_t usable = 0;
     auto entry_of = [&](int t) { return (t < u.x.sink_t ? t : t - u.x.sink_t + u.x.lo_t) * kTile; };
     auto issue = [&](int s) {   // the next tile into stage s
-      if (it >= end || dead) return;
-      int src = (it - held) >> lg;
-      if (src >= 16) {
-        held = it;
+      if (left == 0) return;
+      --left;
+      if (src == 16) {
         src = 0;
-        const int tile = it + ((lane >> 1) << lg);
+        const int tile = refill + ((lane >> 1) << lg);
+        refill += 16 << lg;
         bool ok = false;
         if (tile < end) {
           const int e0 = entry_of(tile) + (lane & 1) * 16;
@@ -601,19 +653,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         }
         usable = __ballot_sync(0xFFFFFFFFu, ok);
       }
-      const uint32_t two = (usable >> (2 * src)) & 3u;
-      usable_ring = (usable_ring & ~(3u << (2 * s))) | (two << (2 * s));
+      const uint32_t two = usable & 3u;
+      usable >>= 2;
+      if (two != 3u) usable_ring &= ~((two ^ 3u) << (2 * s));
       if (member == 0 && (lane >> 1) == src) {
         const uint32_t bar = bar0 + 8 * s;
         if ((lane & 1) == 0) ptx::mbar_arrive_expect_tx(bar, two == 3u ? 2 * S::kRecord : two ? S::kRecord : 0);
         if ((two >> (lane & 1)) & 1u)
           ptx::bulk_load(ring0 + s * S::kStage + (lane & 1) * S::kRecord, record, S::kRecord, bar);
       }
-      it += group;
-      ++in_flight;
+      ++src;
     };
-    for (int s = 0; s < S::kStages; ++s) issue(s);
-    stage = 0;
+    for (int i = 0, s = stage; i < S::kStages; ++i) {
+      issue(s);
+      if (++s == S::kStages) s = 0;
+    }
     __syncwarp();
 
     // ---- the rows as operand B, divided by the power of two of their largest element
@@ -621,14 +675,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     float f[NT][2];          // logit factor of rows 2 t4, 2 t4 + 1 of each eight
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float amax = 0.f;
+      uint32_t top = 0;
 #pragma unroll
       for (int p = 0; p < S::kMembers; ++p)
 #pragma unroll
-        for (int x = 0; x < kWords; ++x) {
-          const float2 y = kv::pair_to_float2(raw[nt][p][x], static_cast<const T*>(nullptr));
-          amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
-        }
+        for (int x = 0; x < kWords; ++x) top = kv::max_abs2(top, raw[nt][p][x], static_cast<const T*>(nullptr));
+      const float2 tops = kv::pair_to_float2(top, static_cast<const T*>(nullptr));
+      float amax = fmaxf(fabsf(tops.x), fabsf(tops.y));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       // 2^-e and 2^e with e the exponent of the largest element (0 for a row of zeros)
@@ -871,31 +924,41 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       return false;
     };
 
-    // tiles [whole0, whole1) lie inside every row's window and before every row's position
-    const int whole1 = u.x.sink_t - u.x.lo_t + (p_min + 1) / kTile;
+    // tiles [whole0, whole0 + wholes) lie inside every row's window and before every row's position
     const int whole0 = u.x.sink_t - u.x.lo_t + (a.window ? (max(0, p_max - a.window + 1) + kTile - 1) / kTile : 0);
-    for (int t = begin + rank; t < end; t += group) {
-      const uint32_t parity = (phases >> stage) & 1u;
-      bool late = dead || !ptx::mbar_wait_poll(bar0 + 8 * stage, parity, a.wait_limit, 64);
+    const uint32_t wholes = max(0, u.x.sink_t - u.x.lo_t + (p_min + 1) / kTile - whole0);
+    for (int i = 0, t = begin + rank; i < todo; ++i, t += group) {
+      bool late = !ptx::mbar_wait_poll(bar0 + 8 * stage, phase, a.wait_limit, 64);
       if constexpr (S::kMembers == 1) late = __any_sync(0xFFFFFFFFu, late);
-      if (!dead && (S::kMembers > 1 || !late)) {
-        const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
+      if (S::kMembers > 1 || !late) {
         const uint8_t* const rec = ring + stage * S::kStage;
-        if (two == 3u && t >= whole0 && t < whole1) late = work(std::false_type(), rec, 0, two, late);
-        else late = work(std::true_type(), rec, entry_of(t), two, late);
+        const uint32_t two = (usable_ring >> (2 * stage)) & 3u;
+        if (two == 3u && uint32_t(t - whole0) < wholes) {
+          late = work(std::false_type(), rec, 0, 3u, late);
+        } else {
+          late = work(std::true_type(), rec, entry_of(t), two, late);
+          usable_ring |= 3u << (2 * stage);
+        }
       }
       if (late) {
         // a copy did not come in time: no more work, the team's own copies are waited for
-        if (!dead && lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
+        if (lane == 0) set_status(a.status, UPF_ERR_TIMEOUT);
         dead = true;
-        if (in_flight == 0) break;
-        ptx::mbar_wait(bar0 + 8 * stage, parity, kDefaultWaitCycles);
+        for (int flying = todo - left - i; flying > 0; --flying) {
+          ptx::mbar_wait(bar0 + 8 * stage, phase, kDefaultWaitCycles);
+          if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        break;
       }
-      --in_flight;
-      phases ^= 1u << stage;
       team_sync<S::kMembers>(team);
       issue(stage);
-      if (++stage == S::kStages) stage = 0;
+      if (++stage == S::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
 
     // ---- write the unit, or this worker's part of it
