@@ -378,7 +378,7 @@ size_t upf_kv_cache_bytes(const upf_kv_cache* cache);
 /* Bytes of workspace upf_kv_write needs for num_tokens tokens (scratch, 256-byte
  * aligned, any contents); 0 and the last error if the arguments are invalid.
  * Calls of at most UPF_KV_FEW_TOKENS tokens use none: ws may be NULL (and this
- * returns a small positive size). */
+ * returns a small positive size); for more, the size depends on num_slots alone. */
 size_t upf_kv_write_workspace_bytes(const upf_kv_cache* cache, int32_t num_tokens);
 
 /* Quantise tokens' keys and values and write them at their slots.

@@ -279,13 +279,15 @@ def upf_kv_write_workspace_bytes(cache: UpfKvCache, num_tokens: int) -> int:
 
 def upf_kv_write(ctx, cache, dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens, num_tokens_dev, ws, ws_bytes,
                  stream=0):
-    _check(load().upf_kv_write(ctx, ctypes.byref(cache), dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens,
-                               num_tokens_dev or None, ws or None, ws_bytes, stream or None))
+    lib = _lib or load()
+    _check(lib.upf_kv_write(ctx, ctypes.byref(cache), dtype, k, k_row_stride, v, v_row_stride, slots, num_tokens,
+                            num_tokens_dev or None, ws or None, ws_bytes, stream or None))
 
 
 def upf_kv_read(ctx, cache, dtype, slots, num_tokens, num_tokens_dev, k, k_row_stride, v, v_row_stride, stream=0):
-    _check(load().upf_kv_read(ctx, ctypes.byref(cache), dtype, slots, num_tokens, num_tokens_dev or None, k or None,
-                              k_row_stride, v or None, v_row_stride, stream or None))
+    lib = _lib or load()
+    _check(lib.upf_kv_read(ctx, ctypes.byref(cache), dtype, slots, num_tokens, num_tokens_dev or None, k or None,
+                           k_row_stride, v or None, v_row_stride, stream or None))
 
 
 def upf_kv_attend_workspace_bytes(cache: UpfKvCache, query: UpfKvQuery) -> int:
@@ -296,8 +298,9 @@ def upf_kv_attend_workspace_bytes(cache: UpfKvCache, query: UpfKvQuery) -> int:
 
 
 def upf_kv_attend(ctx, cache, query, dtype, q, q_row_stride, out, out_row_stride, lse, ws, ws_bytes, stream=0):
-    _check(load().upf_kv_attend(ctx, ctypes.byref(cache), ctypes.byref(query), dtype, q, q_row_stride, out,
-                                out_row_stride, lse or None, ws, ws_bytes, stream or None))
+    lib = _lib or load()
+    _check(lib.upf_kv_attend(ctx, ctypes.byref(cache), ctypes.byref(query), dtype, q, q_row_stride, out,
+                             out_row_stride, lse or None, ws, ws_bytes, stream or None))
 
 
 NUM_STAGES = 8

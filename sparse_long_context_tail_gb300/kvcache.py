@@ -49,7 +49,7 @@ class QuantKVCache:
         self.device = torch.device("cuda", device or 0)
         self.storage = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if storage is None else storage
         self._cache.data = self.storage.data_ptr()
-        self._ws_bytes = {}      # upf_kv_attend_workspace_bytes by (q heads, new tokens)
+        self._ws_bytes = {}      # of attend, by (q heads, new tokens); of write, by None: they depend on these alone
         self.ctx = B.upf_create(self.device.index)
 
     def close(self) -> None:
@@ -112,8 +112,11 @@ class QuantKVCache:
         np_ = self._ints("num_tokens", num_tokens, torch.int32, 1)
         wp = wn = 0
         if T > B.UPF_KV_FEW_TOKENS:      # fewer need no workspace
-            ws = torch.empty(B.upf_kv_write_workspace_bytes(self._cache, T), dtype=torch.uint8, device=self.device)
-            wp, wn = ws.data_ptr(), ws.numel()
+            wn = self._ws_bytes.get(None)
+            if wn is None:
+                wn = self._ws_bytes[None] = B.upf_kv_write_workspace_bytes(self._cache, T)
+            ws = torch.empty(wn, dtype=torch.uint8, device=self.device)
+            wp = ws.data_ptr()
         B.upf_kv_write(self.ctx, self._cache, _DTYPES[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs, sp, T, np_, wp, wn,
                        self._stream())
 
@@ -179,7 +182,7 @@ class QuantKVCache:
         query, keep = B.make_kv_query(R, Hq, N, lp, page_table.data_ptr(), table_row if R > 1 else pages, pages,
                                       page_size, cp, max_q_len, window, sinks, softmax_scale or 0.0, kv_of_q)
         nbytes = self._ws_bytes.get((Hq, max_q_len))
-        if nbytes is None:               # depends on these alone
+        if nbytes is None:
             nbytes = self._ws_bytes[Hq, max_q_len] = B.upf_kv_attend_workspace_bytes(self._cache, query)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         B.upf_kv_attend(self.ctx, self._cache, query, _DTYPES[q.dtype], q.data_ptr(), qs, out.data_ptr(), outs,
