@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         qf[x / 2][nt][x & 1] = pack_f16(y.x * down, y.y * down);
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b)   // never 0: it multiplies the -inf of unseen entries
-        f[nt][b] = fmaxf(a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4), FLT_MIN);
+      for (int b = 0; b < 2; ++b)   // never 0: it multiplies the -inf of unseen entries; nor infinite: products may be 0
+        f[nt][b] = fminf(fmaxf(a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4), FLT_MIN), FLT_MAX);
     }
     const int p_min = base + query_of(a, row0), p_max = base + query_of(a, min(rows, row0 + S::kRows) - 1);
     // does row y of this lane's columns (nt, b) see entry e?

@@ -329,6 +329,12 @@ def test_scales_head_maps_and_large_and_small_queries():
     check(b, [1, 2], q_scale=64.0)               # a few entries take all the weight
 
 
+def test_zero_logits_stay_zero_where_their_factor_passes_fp32():
+    """Keys of zeros with the largest exponent under huge queries: 2^k_exp times the row's power of two is past 2^128."""
+    for d, Hq in ((64, 4), (256, 20)):
+        check(Batch([1, 40, 700], Hq, 1, d, k_exp=32, scale=0.0), [1, 2, 1], q_scale=2.0 ** 100)
+
+
 def test_one_entry_is_given_back_exactly():
     b = Batch([1, 1], 4, 2, 128)
     q, got, ref = check(b, [1, 1])
