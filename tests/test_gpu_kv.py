@@ -335,6 +335,26 @@ def test_zero_logits_stay_zero_where_their_factor_passes_fp32():
         check(Batch([1, 40, 700], Hq, 1, d, k_exp=32, scale=0.0), [1, 2, 1], q_scale=2.0 ** 100)
 
 
+@pytest.mark.parametrize("Hq,d", [(4, 64), (8, 128), (16, 256)])
+def test_a_row_of_nan_stays_by_itself(Hq, d):
+    """One head of one query is NaN or infinite: the heads and queries that share its unit are as without it."""
+    b = Batch([90, 3000], Hq, 1, d)
+    q, cu_q = b.queries([2, 2])
+    ask = lambda x: b.cache.attend(x, b.table, b.kv_len, b.page, cu_q=torch.from_numpy(cu_q).to(DEV), max_q_len=2)
+    want = ask(q)
+    for x in (float("nan"), float("inf")):
+        odd = q.clone()
+        odd[1, 2, 5], odd[2, 0, d - 1] = x, x
+        got = ask(odd)
+        for g, w in zip(got, want):
+            same = torch.ones_like(g, dtype=torch.bool)
+            same[1, 2] = same[2, 0] = False
+            assert torch.equal(g[same], w[same])
+        if x != x:
+            assert got.out[1, 2].isnan().all() and got.out[2, 0].isnan().all() and got.lse[1, 2].isnan()
+    assert b.cache.status() == 0
+
+
 def test_one_entry_is_given_back_exactly():
     b = Batch([1, 1], 4, 2, 128)
     q, got, ref = check(b, [1, 1])
