@@ -450,7 +450,9 @@ size_t upf_kv_attend_workspace_bytes(const upf_kv_cache* cache, const upf_kv_que
 /* Attention of the new tokens over the cache:
  *   out = sum_e softmax_e(scale * q . k_e) v_e,   lse = ln sum_e exp(scale * q . k_e)
  * over the entries e that the row sees; a row that sees none gets out = 0 and
- * lse = -inf.  Logits are fp32: a row with one past its range may come out as NaN.
+ * lse = -inf.  Weights come from differences of logits, so these may have any
+ * size up to 2^127.  A row whose largest logit is past fp32's range is NaN, and so is one
+ * whose softmax_scale * 2^k_exp * max|q| is, unless its largest logit is 0.
  * q, out: device, row t head h at q + t*q_row_stride + h*head_dim (`dtype`), row
  *         strides >= H_q*head_dim and multiples of 8, 16-byte aligned; out must
  *         not overlap q or the cache.

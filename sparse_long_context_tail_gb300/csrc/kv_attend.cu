@@ -50,7 +50,15 @@
 // weighted sums are fp32.  The one rounding is that of the softmax weights to f16,
 // 2^-11 relative; they are scaled by 2^12 against a reference that may lag the
 // running maximum by 2^3, so that weights down to 2^-26 of the reference keep all
-// their bits.
+// their bits.  (Weights in two f16 parts would double the products over the values for
+// an error that the rounding of a bf16 output hides.)
+//
+// Weights come from differences of a row's products, 2^((s - ref) f + 12) with s and ref
+// as the matrix instructions give them (under 2^22) and f the row's logit factor: what
+// rounds is the difference, whatever the size of the logits.  (With the reference times the
+// factor folded into one constant, its last place is worth more than the f16 range of the
+// weights from logits of about 10^7 on.)  So ref stays in units of s, also in the parts.  A
+// row whose largest logit is past fp32 is NaN (`logit_of`).
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -230,13 +238,29 @@ __device__ Deal deal_out_many(const KvAttendArgs& a, int rows, int teams, int pe
   return make_deal(all_t, all_u, t, u, teams, before);
 }
 
+// A row's logit factor: 2^exp times the mantissa of the scale.  Never 0: it multiplies the -inf
+// of unseen entries; never infinite: the differences it multiplies may be 0.
+__device__ __forceinline__ float factor_of(const KvAttendArgs& a, int exp) {
+  if (exp > 127) return FLT_MAX;
+  return fminf(a.scale_mant * __uint_as_float(uint32_t(max(exp, -126) + 127) << 23), FLT_MAX);
+}
+
+// The largest logit (times log2 e) of a row with factor f and reference s; NaN if it is past
+// fp32, or if the factor is and the logit is not 0.  (The weights are right even then: differences
+// of s are multiples of 2^-34, so that FLT_MAX takes them past the weights' range as the factor would.)
+__device__ __forceinline__ float logit_of(float s, float f) {
+  const float x = s * f;
+  return fabsf(x) <= FLT_MAX && (f < FLT_MAX || s == 0.f) ? x : __int_as_float(0x7FFFFFFF);
+}
+
 // The workspace.  A worker has at most two units that others work on too: the one
 // its share begins in the middle of, and the one that goes on after its share.
 // The part of the latter (or of a unit that does both) is at 2 w + 1, that of the
 // former at 2 w.
 struct Parts {
-  float* o;         // [2 * workers][rows][d]
-  float2* ml;       // [2 * workers][rows]: reference, sum
+  float* o;         // [part slots][rows][d]
+  float2* ml;       // [part slots][rows]: reference, sum
+  float* f;         // [CTAs][rows]: the rows' logit factors, for the second launch
   struct Note* notes;   // [CTAs], or null: no second launch
 };
 
@@ -360,18 +384,23 @@ __device__ __forceinline__ void next_unit(const KvAttendArgs& a, Unit& u, int co
   } while (u.x.tiles == 0);
 }
 
-__device__ __forceinline__ float lse_of(float top, float all) {
-  return all == 0.f ? -INFINITY : (top - kWeightExp + log2f(all)) * kLn2;
+// What a row's weighted sum is multiplied by, and its lse, from its largest logit (`logit_of`)
+// and the sum of its weights.
+__device__ __forceinline__ float inverse_of(const KvAttendArgs& a, float logit, float all) {
+  return all == 0.f ? 0.f : isnan(logit) ? logit : a.v_mul / all;
+}
+__device__ __forceinline__ float lse_of(float logit, float all) {
+  return all == 0.f ? -INFINITY : (logit - kWeightExp + log2f(all)) * kLn2;
 }
 
 // Adds up n parts of a unit's workers first .. last in order, by `count` threads: those of
 // workers w0, w0 + 1, ... or, if `groups`, those that stand for kFan workers each.
 // Of its outputs (four dims of a row each) from .. to - 1; the sum goes to out and lse
-// or, if `into` >= 0, to that part.  2^k lanes add up one output, each every 2^k-th
+// or, if `into` >= 0, to that part.  `factors`: of the unit's rows.  2^k lanes add up one output, each every 2^k-th
 // part; what they load does not hang on what they loaded before.
 template <typename T, int kDim, int NT>
 __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note& u, int w0, int n, bool groups, int into,
-                          int from, int to, int thread, int count) {
+                          const float* factors, int from, int to, int thread, int count) {
   using S = Shape<kDim, NT>;
   constexpr int kBatch = 4;
   int lanes = 1;
@@ -382,6 +411,7 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note&
     const int i = at0 + thread / lanes;
     const bool mine = i < to;
     const int row = mine ? i / (kDim / 4) : 0, j = mine ? i % (kDim / 4) : 0;
+    const float f = factors[row];
     float m = -FLT_MAX, all = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = sub; k0 < n; k0 += kBatch * lanes) {
@@ -401,7 +431,7 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note&
       float top = m;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) top = fmaxf(top, ml[x].x);
-      const float c = ptx::ex2_approx(m - top);
+      const float c = ptx::ex2_approx((m - top) * f);
       m = top;
       all *= c;
       sum.x *= c;
@@ -410,7 +440,7 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note&
       sum.w *= c;
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        const float y = ptx::ex2_approx(ml[x].x - top);
+        const float y = ptx::ex2_approx((ml[x].x - top) * f);
         all += ml[x].y * y;
         sum.x += v[x].x * y;
         sum.y += v[x].y * y;
@@ -420,7 +450,7 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note&
     }
     for (int d = 1; d < lanes; d <<= 1) {
       const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, d), top = fmaxf(m, m2);
-      const float c = ptx::ex2_approx(m - top);
+      const float c = ptx::ex2_approx((m - top) * f);
       m = top;
       all *= c;
       sum.x *= c;
@@ -442,12 +472,12 @@ __device__ void add_parts(const KvAttendArgs& a, const Parts& parts, const Note&
     }
     const int rho = u.row0 + row, q = query_of(a, rho), head = a.qhead[u.h * a.gamma + rho - q * a.gamma];
     const int64_t at = u.q0 + q;
-    const float inv = all == 0.f ? 0.f : a.v_mul / all;
+    const float logit = logit_of(m, f), inv = inverse_of(a, logit, all);
     uint2 w;
     w.x = kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
     w.y = kv::float2_to_pair(sum.z * inv, sum.w * inv, static_cast<const T*>(nullptr));
     reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim)[j] = w;
-    if (a.lse && j == 0) a.lse[at * a.Hq + head] = lse_of(m, all);
+    if (a.lse && j == 0) a.lse[at * a.Hq + head] = lse_of(logit, all);
   }
 }
 
@@ -461,10 +491,10 @@ __device__ __forceinline__ int count_in(int32_t* counter) {
 
 // Counts this worker's part of a unit in; the worker that completes the count adds
 // the parts up.  sync: a barrier of the worker's threads; said: a word of theirs in
-// shared memory.
+// shared memory; factors: of the unit's rows, written by the worker's threads.
 template <typename T, int kDim, int NT, typename Sync>
 __device__ __forceinline__ void finish_unit(const KvAttendArgs& a, const Parts& parts, const Unit& u, const Deal& deal, int worker, int thread,
-                            int count, volatile int* said, Sync&& sync) {
+                            int count, volatile int* said, const float* factors, Sync&& sync) {
   using S = Shape<kDim, NT>;
   const long long place = u.place + deal.cost;
   const int first = int(quotient(place, deal.share));
@@ -487,8 +517,9 @@ __device__ __forceinline__ void finish_unit(const KvAttendArgs& a, const Parts& 
     int32_t* const counter = a.counters + (groups ? S::kMaxWorkers : 0) + w0;
     if (arrive(counter) != members - 1) break;
     if (thread == 0) *counter = 0;
-    add_parts<T, kDim, NT>(a, parts, note, w0, members, groups, level == 0 ? S::group_part(w0, first) : -1, 0, outputs, thread,
-                           count);
+    add_parts<T, kDim, NT>(a, parts, note, w0, members, groups, level == 0 ? S::group_part(w0, first) : -1, factors, 0, outputs,
+                           thread, count);
+    sync();   // the next unit's factors may be written
   }
 }
 
@@ -525,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
   __shared__ __align__(8) uint64_t bars[S::kTeams][S::kStages];
   __shared__ longlong2 warp_sums[kWarps];
   __shared__ Unit starts[S::kTeams];
-  __shared__ float sh_m[S::kTeams][S::kRows], sh_l[S::kTeams][S::kRows], sh_top[S::kRows], sh_all[S::kRows];
+  __shared__ float sh_m[S::kTeams][S::kRows], sh_l[S::kTeams][S::kRows], sh_f[S::kTeams][S::kRows];
+  __shared__ float sh_top[S::kRows], sh_all[S::kRows];
   __shared__ int sh_count[S::kTeams];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = warp / S::kMembers, member = warp % S::kMembers;
@@ -701,18 +733,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       float amax = fmaxf(fabsf(tops.x), fabsf(tops.y));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      // 2^-e and 2^e with e the exponent of the largest element (0 for a row of zeros)
+      // 2^-e with e the exponent of the largest element (0 for a row of zeros)
       int e = int(__float_as_uint(amax) >> 23) - 127;
       e = amax == 0.f ? 0 : max(-126, min(e, 126));
-      const float down = __uint_as_float(uint32_t(127 - e) << 23), up = __uint_as_float(uint32_t(127 + e) << 23);
+      const float down = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
         const float2 y = kv::pair_to_float2(raw[nt][0][x], static_cast<const T*>(nullptr));
         qf[x / 2][nt][x & 1] = pack_f16(y.x * down, y.y * down);
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b)   // never 0: it multiplies the -inf of unseen entries; nor infinite: products may be 0
-        f[nt][b] = fminf(fmaxf(a.scale_log2 * __shfl_sync(0xFFFFFFFFu, up, (2 * t4 + b) * 4), FLT_MIN), FLT_MAX);
+      for (int b = 0; b < 2; ++b) f[nt][b] = factor_of(a, a.scale_exp + __shfl_sync(0xFFFFFFFFu, e, (2 * t4 + b) * 4));
     }
     const int p_min = base + query_of(a, row0), p_max = base + query_of(a, min(rows, row0 + S::kRows) - 1);
     // does row y of this lane's columns (nt, b) see entry e?
@@ -721,15 +752,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       return y < rows && e <= p && (a.window == 0 || p - e < a.window || e < a.sinks);
     };
 
-    // weights are 2^(f s + c) with c = 12 - m; the reference m moves when s passes `limit`
+    // weights are 2^((s - ref) f + 12); the reference moves when s passes `limit`
     float o[S::kSteps][NT][4];
-    float c[NT][2], limit[NT][2], l[NT][2];
+    float ref[NT][2], limit[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        c[nt][b] = FLT_MAX;
-        limit[nt][b] = -FLT_MAX;
+        ref[nt][b] = limit[nt][b] = -FLT_MAX;
         l[nt][b] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < S::kSteps; ++mt) o[mt][nt][b] = o[mt][nt][b + 2] = 0.f;
@@ -839,9 +869,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
             if (x > limit[nt][b]) {
-              const float c2 = kWeightExp - x * f[nt][b], k = ptx::ex2_approx(c2 - c[nt][b]);
-              c[nt][b] = c2;
-              limit[nt][b] = x + __fdividef(kLag, f[nt][b]);
+              const float k = ptx::ex2_approx((ref[nt][b] - x) * f[nt][b]);
+              ref[nt][b] = x;
+              limit[nt][b] = __fadd_rd(x, __fdividef(kLag, f[nt][b]));   // down: the weights' range ends there
               l[nt][b] *= k;
 #pragma unroll
               for (int mt = 0; mt < S::kSteps; ++mt) {
@@ -859,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i] = ptx::ex2_approx(__fmaf_rn(s[b][nt][i], f[nt][i & 1], c[nt][i & 1]));
+            w[i] = ptx::ex2_approx(__fmaf_rn(s[b][nt][i] - ref[nt][i & 1], f[nt][i & 1], kWeightExp));
             l[nt][i & 1] += w[i];
           }
           pf[b][nt][0] = transpose8x8(pack_f16(w[0], w[1]));
@@ -995,11 +1025,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         for (int b = 0; b < 2; ++b) {
           const int row = nt * 8 + 2 * t4 + b, rho = row0 + row;
           if (rho >= rows) continue;
-          const float all = l[nt][b], m = kWeightExp - c[nt][b];
+          const float all = l[nt][b];
           if (alone) {
             const int qi = query_of(a, rho), head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
             const int64_t at = u.x.q0 + qi;
-            const float inv = all == 0.f ? 0.f : a.v_mul / all;
+            const float logit = logit_of(ref[nt][b], f[nt][b]), inv = inverse_of(a, logit, all);
             uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim0);
 #pragma unroll
             for (int mt = 0; mt < S::kSteps; mt += 4) {
@@ -1009,14 +1039,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
                 w[i] = kv::float2_to_pair(o[mt + i][nt][b] * inv, o[mt + i][nt][b + 2] * inv, static_cast<const T*>(nullptr));
               *reinterpret_cast<uint4*>(dst + mt) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (g == 0 && member == 0 && a.lse) a.lse[at * a.Hq + head] = lse_of(m, all);
+            if (g == 0 && member == 0 && a.lse) a.lse[at * a.Hq + head] = lse_of(logit, all);
           } else {
             float* const dst = parts.o + (slot * S::kRows + row) * kDim + dim0;
 #pragma unroll
             for (int mt = 0; mt < S::kSteps; mt += 2)
               *reinterpret_cast<float4*>(dst + 2 * mt) =
                   make_float4(o[mt][nt][b], o[mt][nt][b + 2], o[mt + 1][nt][b], o[mt + 1][nt][b + 2]);
-            if (g == 0 && member == 0) parts.ml[slot * S::kRows + row] = make_float2(m, all);
+            if (g == 0 && member == 0) {
+              parts.ml[slot * S::kRows + row] = make_float2(ref[nt][b], all);
+              sh_f[team][row] = f[nt][b];
+            }
           }
         }
     } else {
@@ -1025,17 +1058,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            sh_m[team][nt * 8 + 2 * t4 + b] = kWeightExp - c[nt][b];
+            sh_m[team][nt * 8 + 2 * t4 + b] = ref[nt][b];
             sh_l[team][nt * 8 + 2 * t4 + b] = l[nt][b];
+            sh_f[team][nt * 8 + 2 * t4 + b] = f[nt][b];   // the same for every team
           }
       }
       __syncthreads();
       if (threadIdx.x < S::kRows) {
+        const float fr = sh_f[0][threadIdx.x];
         float top = -FLT_MAX, all = 0.f;
 #pragma unroll
         for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][threadIdx.x]);
 #pragma unroll
-        for (int w = 0; w < S::kTeams; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx(sh_m[w][threadIdx.x] - top);
+        for (int w = 0; w < S::kTeams; ++w) all += sh_l[w][threadIdx.x] * ptx::ex2_approx((sh_m[w][threadIdx.x] - top) * fr);
         sh_top[threadIdx.x] = top;
         sh_all[threadIdx.x] = all;
       }
@@ -1047,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
           float top = -FLT_MAX;
 #pragma unroll
           for (int w = 0; w < S::kTeams; ++w) top = fmaxf(top, sh_m[w][nt * 8 + 2 * t4 + b]);
-          scale[b] = ptx::ex2_approx(kWeightExp - c[nt][b] - top);
+          scale[b] = ptx::ex2_approx((ref[nt][b] - top) * f[nt][b]);
         }
 #pragma unroll
         for (int mt = 0; mt < S::kSteps; ++mt) {
@@ -1074,13 +1109,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
         if (alone) {
           const int qi = query_of(a, rho), head = a.qhead[u.h * a.gamma + rho - qi * a.gamma];
           const int64_t at = u.x.q0 + qi;
-          const float inv = all == 0.f ? 0.f : a.v_mul / all;
+          const float logit = logit_of(sh_top[row], sh_f[0][row]), inv = inverse_of(a, logit, all);
           *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * a.out_stride + head * kDim + dim) =
               kv::float2_to_pair(sum.x * inv, sum.y * inv, static_cast<const T*>(nullptr));
-          if (a.lse && dim == 0) a.lse[at * a.Hq + head] = lse_of(sh_top[row], all);
+          if (a.lse && dim == 0) a.lse[at * a.Hq + head] = lse_of(logit, all);
         } else {
           *reinterpret_cast<float2*>(parts.o + (slot * S::kRows + row) * kDim + dim) = sum;
-          if (dim == 0) parts.ml[slot * S::kRows + row] = make_float2(sh_top[row], all);
+          if (dim == 0) {
+            parts.ml[slot * S::kRows + row] = make_float2(sh_top[row], all);
+            if (goes_on) parts.f[blockIdx.x * S::kRows + row] = sh_f[0][row];
+          }
         }
       }
       // the rings take copies again, sh_m, sh_l, sh_top and sh_all new values
@@ -1095,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       }
     } else if (!alone) {
       finish_unit<T, kDim, NT>(a, parts, u, deal, worker, deal.teams ? member * 32 + lane : threadIdx.x,
-                               deal.teams ? 32 * S::kMembers : kThreads, &sh_count[deal.teams ? team : 0], [&] {
+                               deal.teams ? 32 * S::kMembers : kThreads, &sh_count[deal.teams ? team : 0], sh_f[deal.teams ? team : 0], [&] {
                                  if (deal.teams) team_sync<S::kMembers>(team);
                                  else __syncthreads();
                                });
@@ -1115,8 +1153,8 @@ __global__ void __launch_bounds__(kThreads) kv_attend_join_kernel(const __grid_c
   const int outputs = min(S::kRows, u.rows - u.row0) * (kDim / 4), portions = (u.last - u.first) * kWarps;
   const int each = (outputs + portions - 1) / portions;
   const int from = ((blockIdx.x - u.first) * kWarps + (threadIdx.x >> 5)) * each;
-  add_parts<T, kDim, NT>(a, parts, u, u.first, u.last - u.first + 1, false, -1, from, min(outputs, from + each),
-                         threadIdx.x & 31, 32);
+  add_parts<T, kDim, NT>(a, parts, u, u.first, u.last - u.first + 1, false, -1, parts.f + u.first * S::kRows, from,
+                         min(outputs, from + each), threadIdx.x & 31, 32);
 }
 
 template <int kDim, int NT>
@@ -1144,7 +1182,8 @@ cudaError_t launch(const KvAttendArgs& a, cudaStream_t s) {
   const long long units = (long long)a.R * a.H * ((a.max_q * a.gamma + S::kRows - 1) / S::kRows);
   const long long longest = a.window ? (long long)a.window + a.sinks + a.max_q : (long long)a.max_pages << a.page_shift;
   const bool second = std::min(S::kCtas / units, longest / (kTile * S::kTeams)) > kFan;
-  parts.notes = second ? reinterpret_cast<Note*>(parts.ml + part_rows<kDim, NT>()) : nullptr;
+  parts.f = reinterpret_cast<float*>(parts.ml + part_rows<kDim, NT>());
+  parts.notes = second ? reinterpret_cast<Note*>(parts.f + S::kCtas * S::kRows) : nullptr;
   e = launch_kernel(kv_attend_kernel<T, kDim, NT>, S::kCtas, kThreads, S::kSmem, s, true, a, parts);
   if (e != cudaSuccess || !second) return e;
   return launch_kernel(kv_attend_join_kernel<T, kDim, NT>, S::kCtas, kThreads, 0, s, true, a, parts);
@@ -1158,7 +1197,8 @@ cudaError_t launch_dim(const KvAttendArgs& a, bool f16, cudaStream_t s) {
 
 template <int kDim, int NT>
 constexpr size_t ws_bytes() {
-  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2)) + Shape<kDim, NT>::kCtas * sizeof(Note);
+  using S = Shape<kDim, NT>;
+  return part_rows<kDim, NT>() * (kDim * sizeof(float) + sizeof(float2)) + S::kCtas * (S::kRows * sizeof(float) + sizeof(Note));
 }
 
 template <int kDim>

@@ -1264,7 +1264,8 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   a.window = query->window < (1 << 30) ? query->window : 0;   // no request has 2^30 entries behind a query
   a.sinks = query->sinks;
   const float scale = query->softmax_scale > 0.f ? query->softmax_scale : 1.0f / std::sqrt(float(cache->head_dim));
-  a.scale_log2 = std::ldexp(scale * 1.4426950408889634f, cache->k_exp);
+  a.scale_mant = float(2.0 * std::frexp(double(scale) * 1.4426950408889634, &a.scale_exp));
+  a.scale_exp += cache->k_exp - 1;
   a.v_mul = std::ldexp(1.f, cache->v_exp);
   a.status = ctx->status_dev;
   a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;

@@ -219,7 +219,8 @@ struct KvAttendArgs {
   int64_t page_stride;
   int32_t max_pages, page_shift;
   int32_t window, sinks;        // window 0: none
-  float scale_log2;             // softmax scale * 2^k_exp * log2 e
+  float scale_mant;             // softmax scale * 2^k_exp * log2 e = scale_mant * 2^scale_exp, scale_mant in [1, 2]
+  int32_t scale_exp;
   float v_mul;                  // 2^v_exp
   float inv_gamma;              // 1 / gamma
   int32_t* status;

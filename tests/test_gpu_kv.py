@@ -626,3 +626,82 @@ def test_a_wait_that_runs_out_is_reported_and_the_cache_recovers():
     got = big.attend(q, table, kv, 16)
     assert big.status() == 0 and not got.out.any() and (got.lse - np.log(n)).abs().max() < 1e-5
     check(Batch([500, 300], 8, 4, 128), [1, 1])
+
+
+# ------------------------------------------------------- logits of any size --
+
+def peaked(lens, Hq, H, d, logit, twice=False, sign=1.0, dtype=BF16, page=16):
+    """Requests in each of which one entry (`twice`: two, with the same keys) has a logit of about `logit` for every head
+    and all others are far below: positive queries, its keys +6, the others' negative.  `sign` -1: every entry's
+    keys are -6 instead.  Returns (batch, q, cu_q, entries that take all the weight)."""
+    b = Batch(lens, Hq, H, d, page=page, dtype=dtype)
+    cut = np.cumsum([0] + b.lens)
+    T = int(cut[-1])
+    k = -rand((T, H, d), dtype, 3).abs().clamp(2.0 ** -4, 6.0)
+    if sign < 0:
+        k = torch.full_like(k, -6.0)
+    top = [sorted({n // 3, max(n - 2, 0)} if twice else {n // 3}) for n in b.lens]
+    for r, at in enumerate(top):
+        for e in at:
+            k[cut[r] + e] = 6.0 * sign
+    v = rand((T, H, d), dtype, 4)
+    b.cache.write(k, v, b.slots.to(DEV))
+    kk, vv = K.cache_values(f64(k), 0), K.cache_values(f64(v), 0)
+    b.k, b.v = [kk[x:y] for x, y in zip(cut, cut[1:])], [vv[x:y] for x, y in zip(cut, cut[1:])]
+    g = torch.Generator().manual_seed(5)
+    q = (1 + torch.rand((len(lens), Hq, d), generator=g)) * (logit / (9 * d ** 0.5))     # scale sum q 6 = 9 sqrt(d) each
+    return b, q.to(dtype).to(DEV), np.arange(len(lens) + 1), top
+
+
+LAYOUTS = [([1, 40, 700], "teams"), ([6000] + [20] * 100, "a unit over many teams"), ([30000], "a second launch"),
+           ([60000] + [100] * 19, "parts added up in two steps")]
+
+
+@pytest.mark.parametrize("Hq,d", [(4, 64), (12, 64), (4, 128), (12, 128), (4, 256), (12, 256)])
+@pytest.mark.parametrize("logit", [1e5, 1e7, 1e9, 1e12, 1e30])
+def test_the_heaviest_entry_is_given_back_whatever_the_logits_size(logit, Hq, d):
+    """Weights come from differences of logits: the entry with the largest one takes all the weight and its values come out
+    exactly; two entries with the same keys share it, wherever they are."""
+    for lens, _ in LAYOUTS if logit == 1e9 else LAYOUTS[:2] if logit == 1e7 else LAYOUTS[:1]:
+        b, q, cu_q, top = peaked(lens, Hq, 1, d, logit)
+        ref = K.attend(f64(q), b.k, b.v, cu_q)
+        got = b.cache.attend(q, b.table, b.kv_len, 16)
+        for r, at in enumerate(top):
+            np.testing.assert_array_equal(f64(got.out[r]), np.broadcast_to(b.v[r][at[0]], (Hq, d)))
+        assert (np.abs(f64(got.lse) - ref[1]) <= _bound(BF16, ref)[1]).all() and b.cache.status() == 0
+        b, q, cu_q, top = peaked(lens, Hq, 1, d, logit, twice=True)
+        got = b.cache.attend(q, b.table, b.kv_len, 16)
+        for r, at in enumerate(top):
+            # equal weights, an fp32 sum of two products and one rounding to bf16
+            mean, size = b.v[r][at].mean(0), np.abs(b.v[r][at]).sum(0)
+            assert (np.abs(f64(got.out[r]) - mean) <= np.abs(mean) * 2.0 ** -8 * (1 + 2.0 ** -10) + size * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("Hq,d", [(4, 64), (12, 128), (4, 256), (12, 256)])
+def test_logits_past_fp32_are_nan_and_stay_by_themselves(Hq, d):
+    """The largest logit of one head is past fp32's range, on either side: that row is NaN, the others are as without it,
+    and a row that sees nothing is empty all the same."""
+    for lens, _ in LAYOUTS[:3]:
+        for sign in (1.0, -1.0):
+            b, q, cu_q, top = peaked(lens, Hq, 1, d, 4.0, sign=sign)
+            want = b.cache.attend(q, b.table, b.kv_len, 16)
+            odd = q.clone()
+            odd[0, 2] = 1e38 * (1.0 if sign > 0 else 1.5)
+            got = b.cache.attend(odd, b.table, b.kv_len, 16)
+            assert got.out[0, 2].isnan().all() and got.lse[0, 2].isnan()
+            for g, w in zip(got, want):
+                same = torch.ones_like(g, dtype=torch.bool)
+                same[0, 2] = False
+                assert torch.equal(g[same], w[same])
+    b = Batch([1, 5], Hq, 1, d, k_exp=32, scale=2.0 ** 32)            # 2^k_exp takes the factor past fp32 before any product
+    q, cu_q = b.queries([2, 1], scale=2.0 ** 110)
+    got = b.cache.attend(q, b.table, b.kv_len, 16, cu_q=torch.from_numpy(cu_q).to(DEV), max_q_len=2)
+    assert not got.out[0].any() and torch.isneginf(got.lse[0]).all()
+    assert got.out[1:].isnan().all() and got.lse[1:].isnan().all() and b.cache.status() == 0
+
+
+def test_scales_at_the_ends_of_fp32():
+    """softmax_scale below the smallest normal fp32 number under large queries, and a large one over small ones."""
+    for scale, size, k_exp in ((2.0 ** -140, 2.0 ** 120, 17), (2.0 ** 120, 2.0 ** -100, -21), (2.0 ** 127, 2.0 ** -126, -2)):
+        b = Batch([77, 200, 1], 6, 3, 128, k_exp=k_exp, scale=2.0 ** k_exp)
+        check(b, [1, 1, 1], scale=scale, q_scale=size)
