@@ -736,7 +736,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
       // 2^-e with e the exponent of the largest element (0 for a row of zeros)
       int e = int(__float_as_uint(amax) >> 23) - 127;
       e = amax == 0.f ? 0 : max(-126, min(e, 126));
-      const float down = __uint_as_float(uint32_t(127 - e) << 23);
+      // An infinite query makes every logit infinite or NaN, and their softmax NaN; where all are -inf, NaN
+      // queries tell that from entries that are not seen.
+      const float down = __uint_as_float(amax <= FLT_MAX ? uint32_t(127 - e) << 23 : 0x7FFFFFFFu);
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
         const float2 y = kv::pair_to_float2(raw[nt][0][x], static_cast<const T*>(nullptr));

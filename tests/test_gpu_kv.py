@@ -705,3 +705,29 @@ def test_scales_at_the_ends_of_fp32():
     for scale, size, k_exp in ((2.0 ** -140, 2.0 ** 120, 17), (2.0 ** 120, 2.0 ** -100, -21), (2.0 ** 127, 2.0 ** -126, -2)):
         b = Batch([77, 200, 1], 6, 3, 128, k_exp=k_exp, scale=2.0 ** k_exp)
         check(b, [1, 1, 1], scale=scale, q_scale=size)
+
+
+@pytest.mark.parametrize("Hq,d", [(4, 64), (12, 128), (16, 256)])
+def test_an_infinite_query_is_nan_wherever_it_sees_something(Hq, d):
+    """Keys of one sign where the query is infinite: every logit is -inf (or +inf), and their softmax is 0 / 0."""
+    b = Batch([1, 300], Hq, 1, d)
+    k = rand((301, 1, d), BF16, 3)
+    k[..., 7] = -k[..., 7].abs().clamp(min=2.0)
+    k[..., 0] = 12.0
+    b.cache.write(k, k, b.slots.to(DEV))
+    assert (b.cache.read(b.slots.to(DEV))[0][..., 7] < 0).all()
+    q, cu_q = b.queries([2, 1])                      # the first query sees nothing
+    ask = lambda x: b.cache.attend(x, b.table, b.kv_len, 16, cu_q=torch.from_numpy(cu_q).to(DEV), max_q_len=2)  # noqa: E731
+    want = ask(q)
+    for x in (float("inf"), float("-inf")):
+        odd = q.clone()
+        odd[0, 1, 7] = odd[1, 2, 7] = odd[2, 3, 7] = x
+        got = ask(odd)
+        assert not got.out[0].any() and torch.isneginf(got.lse[0]).all()
+        for at in ((1, 2), (2, 3)):
+            assert got.out[at].isnan().all() and got.lse[at].isnan()
+        for g, w in zip(got, want):
+            same = torch.ones_like(g, dtype=torch.bool)
+            same[1, 2] = same[2, 3] = False
+            assert torch.equal(g[same], w[same])
+    assert b.cache.status() == 0
