@@ -856,10 +856,18 @@ upf_status upf_create(upf_ctx** out, int device) {
     delete c;
     return cuda_fail(e, "cudaMalloc(status)");
   }
-  if ((e = cudaMemset(c->status_dev, 0, kCtxWords * sizeof(int32_t))) != cudaSuccess) {
+  // Zero before the first call on any stream, and without waiting for work of others: a fill on the
+  // legacy stream would come after what that stream holds, and non-blocking streams do not wait for it.
+  cudaStream_t own = nullptr;
+  if ((e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking)) == cudaSuccess) {
+    e = cudaMemsetAsync(c->status_dev, 0, kCtxWords * sizeof(int32_t), own);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+    cudaStreamDestroy(own);
+  }
+  if (e != cudaSuccess) {
     cudaFree(c->status_dev);
     delete c;
-    return cuda_fail(e, "cudaMemset(status)");
+    return cuda_fail(e, "clear status");
   }
   *out = c;
   return UPF_OK;
@@ -885,12 +893,16 @@ upf_status upf_sync_status(upf_ctx* ctx, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+  // on the caller's stream: the calls after this one come after the reset, and other streams are not waited for
   int32_t code = 0;
-  if ((e = cudaMemcpy(&code, ctx->status_dev, sizeof(code), cudaMemcpyDeviceToHost)) != cudaSuccess)
-    return cuda_fail(e, "read status");
+  e = cudaMemcpyAsync(&code, ctx->status_dev, sizeof(code), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail(e, "read status");
   if (code != 0) {
     // the counters too: whatever went wrong, the next call starts from zero
-    if ((e = cudaMemset(ctx->status_dev, 0, kCtxWords * sizeof(int32_t))) != cudaSuccess) return cuda_fail(e, "reset status");
+    e = cudaMemsetAsync(ctx->status_dev, 0, kCtxWords * sizeof(int32_t), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "reset status");
     return fail(static_cast<upf_status>(code), "device reported %s", upf_status_name(static_cast<upf_status>(code)));
   }
   return UPF_OK;

@@ -731,3 +731,34 @@ def test_an_infinite_query_is_nan_wherever_it_sees_something(Hq, d):
             same[1, 2] = same[2, 3] = False
             assert torch.equal(g[same], w[same])
     assert b.cache.status() == 0
+
+
+def test_a_cache_made_and_used_on_one_stream_while_another_is_busy():
+    """Its device words are zero before the first call on any stream, and its status is read and cleared in order with the
+    caller's stream alone: half a second of work on the default stream neither delays nor undoes anything."""
+    from sparse_long_context_tail_gb300.kvcache import QuantKVCache
+    b = Batch([20000, 20000], 4, 1, 128, page=64)    # units that are added up by their last worker and by a second launch
+    s = Batch([6000] + [20] * 100, 4, 1, 128)
+    work = [(x, x.queries([1] * len(x.lens))[0], x.page) for x in (b, s)]
+    refs = [K.attend(f64(q), x.k, x.v, np.arange(len(x.lens) + 1)) for x, q, _ in work]
+    bad = s.table.clone()
+    bad[5, 0] = -3
+    for x, q, p in work:                             # a kernel's first launch in a process waits for the device
+        x.cache.attend(q, x.table, x.kv_len, p)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(10 ** 9)
+    with torch.cuda.stream(side):
+        made = [QuantKVCache(x.cache.num_slots, 1, 128, storage=x.cache.storage) for x, _, _ in work]
+        got = [[c.attend(q, x.table, x.kv_len, p) for _ in range(3)] for c, (x, q, p) in zip(made, work)]
+        made[1].attend(work[1][1], bad, s.kv_len, 16)
+        reported = made[1].status(), made[1].status(), made[0].status()
+        got[1].append(made[1].attend(work[1][1], s.table, s.kv_len, 16))
+        side.synchronize()
+        busy = not torch.cuda.default_stream().query()
+    torch.cuda.synchronize()
+    assert reported == (1, 0, 0)
+    for outs, ref in zip(got, refs):
+        for x in outs:
+            compare(x, ref, BF16)
+    assert busy, "the calls waited for the default stream"
