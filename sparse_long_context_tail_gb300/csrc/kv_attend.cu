@@ -882,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
               }
             }
           }
+        __syncwarp();   // the matrix instructions below take whole warps
       }
       uint32_t pf[2][NT][2];
 #pragma unroll
@@ -937,6 +938,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
           }
           sc[y8] = as_half2(kv::e4m3x2_to_f16x2(uint16_t(raw_sc)));
         }
+        if constexpr (kMasked) __syncwarp();
 #pragma unroll
         for (int x = 0; x < kW; ++x) {
           // low nibbles of both entries side by side (even dims), then the high ones
@@ -978,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<kDim, NT>::kCtasPerSm)) kv_at
     const uint32_t wholes = max(0, u.x.sink_t - u.x.lo_t + (p_min + 1) / kTile - whole0);
     for (int i = 0, t = begin + rank; i < todo; ++i, t += group) {
       bool late = !ptx::mbar_wait_poll(bar0 + 8 * stage, phase, a.wait_limit, 64);
-      if constexpr (S::kMembers == 1) late = __any_sync(0xFFFFFFFFu, late);
+      late = __any_sync(0xFFFFFFFFu, late);   // one answer, and the lanes together again for the matrix instructions
       if (S::kMembers > 1 || !late) {
         const uint8_t* const rec = ring + stage * S::kStage;
         const uint32_t two = (usable_ring >> (2 * stage)) & 3u;

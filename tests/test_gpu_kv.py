@@ -762,3 +762,26 @@ def test_a_cache_made_and_used_on_one_stream_while_another_is_busy():
         for x in outs:
             compare(x, ref, BF16)
     assert busy, "the calls waited for the default stream"
+
+
+@pytest.mark.parametrize("Hq,H,d", [(4, 4, 256), (64, 4, 256), (128, 8, 128)])
+def test_a_wait_that_runs_out_in_teams_of_several_warps(Hq, H, d):
+    """As above, where two or four warps work on a tile: the warps of a team give up together, whichever lane's wait ran out,
+    and so they do where the cache's units are short and each team is its own worker."""
+    n = (1 << 20) // (H * d // 128)                  # 151 MB
+    big = make(n, H, d, fill=0)
+    table = torch.randperm(n // 16, generator=torch.Generator().manual_seed(1)).int().to(DEV)
+    for R in (1, n // 1024):
+        q = rand((R, Hq, d), BF16, 1)
+        kv = torch.full((R,), n // R, dtype=torch.int32, device=DEV)
+        ask = lambda: big.attend(q, table.view(R, -1), kv, 16)  # noqa: E731
+        B.upf_set_wait_limit(big.ctx, 1)
+        for _ in range(200):
+            ask()
+            status = big.status()
+            if status:
+                break
+        assert status == 6
+        B.upf_set_wait_limit(big.ctx, 0)
+        got = ask()
+        assert big.status() == 0 and not got.out.any() and (got.lse - np.log(n // R)).abs().max() < 1e-5
