@@ -133,6 +133,16 @@ def _check(status: int) -> None:
 
 # ------------------------------------------------------------------ structs --
 
+def _head_map(kv_of_q: Optional[Sequence[int]], num_q_heads: int) -> Optional[np.ndarray]:
+    """The kv head of each q head for the library, which reads num_q_heads entries."""
+    if kv_of_q is None:
+        return None
+    kv = np.ascontiguousarray(kv_of_q, dtype=np.int32)
+    if kv.shape != (num_q_heads,):
+        raise ValueError(f"kv_of_q has shape {kv.shape}, expected a kv head for each of {num_q_heads} q heads")
+    return kv
+
+
 def make_batch(cu_seqlens_dev: int, cu_seqlens_host: np.ndarray, num_q_heads: int, num_kv_heads: int,
                head_dim: int, kv_of_q: Optional[Sequence[int]] = None):
     """Build a upf_batch; returns (struct, keepalive) -- keep both alive during the call."""
@@ -166,7 +176,7 @@ def make_kv_query(num_reqs: int, num_q_heads: int, num_q_tokens: int, kv_len: in
                   max_pages: int, page_size: int, cu_q: int = 0, max_q_len: int = 1, window: int = 0, sinks: int = 0,
                   softmax_scale: float = 0.0, kv_of_q: Optional[Sequence[int]] = None):
     """Build a upf_kv_query; returns (struct, keepalive) -- keep both alive during the call."""
-    kv = None if kv_of_q is None else np.ascontiguousarray(kv_of_q, dtype=np.int32)
+    kv = _head_map(kv_of_q, num_q_heads)
     x = UpfKvQuery(num_reqs, num_q_heads, kv.ctypes.data_as(POINTER(c_int32)) if kv is not None else None,
                    num_q_tokens, max_q_len, cu_q or None, kv_len or None, page_table or None, page_stride, max_pages,
                    page_size, window, sinks, softmax_scale)

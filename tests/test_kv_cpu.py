@@ -249,3 +249,13 @@ def test_front_end_attend_refusals(front):
                 dict(lse=torch.zeros(2, 3)), dict(lse=torch.zeros(2, 4, dtype=torch.float64))):
         with pytest.raises(ValueError):
             front.attend(**{**good, **bad})
+
+
+@pytest.mark.parametrize("heads", [[], [0, 0, 1], [0, 0, 1, 1, 1], [[0, 0], [1, 1]]])
+def test_head_maps_of_another_length_are_refused(front, heads):
+    """The library reads num_q_heads entries of the map: a shorter one would be read past its end."""
+    with pytest.raises(ValueError, match="kv_of_q"):
+        _query(kv_of_q=heads)
+    with pytest.raises(ValueError, match="kv_of_q"):
+        front.attend(_kv(2, 4), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 16, kv_of_q=heads)
+    _query(kv_of_q=torch.tensor([0, 1, 0, 1]))
