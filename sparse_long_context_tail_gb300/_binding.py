@@ -147,7 +147,7 @@ def make_batch(cu_seqlens_dev: int, cu_seqlens_host: np.ndarray, num_q_heads: in
                head_dim: int, kv_of_q: Optional[Sequence[int]] = None):
     """Build a upf_batch; returns (struct, keepalive) -- keep both alive during the call."""
     cu = np.ascontiguousarray(cu_seqlens_host, dtype=np.int32)
-    kv = None if kv_of_q is None else np.ascontiguousarray(kv_of_q, dtype=np.int32)
+    kv = _head_map(kv_of_q, num_q_heads)
     b = UpfBatch(len(cu) - 1, ctypes.c_void_p(cu_seqlens_dev), cu.ctypes.data_as(POINTER(c_int32)),
                  num_q_heads, num_kv_heads, head_dim,
                  kv.ctypes.data_as(POINTER(c_int32)) if kv is not None else POINTER(c_int32)())

@@ -159,3 +159,10 @@ def test_scoring_work_split_is_near_the_best_whole_tile_split(lib):
             cand = range(lo, -(-max(s.lengths) // tile) * tile + tile, tile)
             best = min(_greedy_makespan(s.lengths, s.num_kv_heads, nq, c, ovh, sms) for c in cand)
             assert _greedy_makespan(s.lengths, s.num_kv_heads, nq, ks, ovh, sms) <= 1.02 * best, (name, ks)
+
+
+@pytest.mark.parametrize("heads", [[], [0, 1, 0], [0, 1, 0, 1, 0]])
+def test_head_maps_of_another_length_are_refused(heads):
+    """The library reads num_q_heads entries of the map: a shorter one would be read past its end."""
+    with pytest.raises(ValueError, match="kv_of_q"):
+        _batch([0, 100], Hq=4, Hkv=2, kv=heads)
