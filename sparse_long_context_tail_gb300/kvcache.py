@@ -9,6 +9,7 @@ without a sliding window beside a few first entries.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -154,8 +155,9 @@ class QuantKVCache:
 
         ``page_table``: int32 [R, max_pages]; ``kv_len``: int32 [R], the new tokens' own entries
         included; ``cu_q``: int32 [R + 1], or None for one new token per request; ``window`` 0: no
-        window; ``sinks``: first entries that stay visible beside the window.  Rows of no request
-        keep what ``out`` and ``lse`` hold (anything, in new tensors)."""
+        window; ``sinks``: first entries that stay visible beside the window; ``softmax_scale``:
+        positive, None for 1/sqrt(d).  Rows of no request keep what ``out`` and ``lse`` hold
+        (anything, in new tensors); ``out`` must not overlap ``q`` or the cache."""
         if q.dim() != 3:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, H_q, {self.head_dim}]")
         N, Hq, d = q.shape
@@ -179,6 +181,10 @@ class QuantKVCache:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=self.device)
         elif lse.dtype != torch.float32 or lse.shape != (N, Hq) or not lse.is_contiguous() or lse.device != self.device:
             raise ValueError(f"lse must be a contiguous float32 [{N}, {Hq}] tensor on {self.device}")
+        if softmax_scale is not None:
+            softmax_scale = ctypes.c_float(softmax_scale).value
+            if not softmax_scale > 0:
+                raise ValueError("softmax_scale must be positive in fp32, or None for 1/sqrt(head_dim)")
         query, keep = B.make_kv_query(R, Hq, N, lp, page_table.data_ptr(), table_row if R > 1 else pages, pages,
                                       page_size, cp, max_q_len, window, sinks, softmax_scale or 0.0, kv_of_q)
         nbytes = self._ws_bytes.get((Hq, max_q_len))

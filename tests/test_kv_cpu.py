@@ -259,3 +259,17 @@ def test_head_maps_of_another_length_are_refused(front, heads):
     with pytest.raises(ValueError, match="kv_of_q"):
         front.attend(_kv(2, 4), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 16, kv_of_q=heads)
     _query(kv_of_q=torch.tensor([0, 1, 0, 1]))
+
+
+@pytest.mark.parametrize("scale", [0, 0.0, -0.125, float("nan"), 1e-60])
+def test_scales_that_are_not_positive_are_refused(front, scale):
+    """None selects 1/sqrt(head_dim), which the library takes from a scale that is not positive (1e-60 is 0 in fp32)."""
+    args = _kv(2, 4), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 16
+    front._ws_bytes = {(4, 1): 256}
+    front._stream = lambda: 0
+    with pytest.raises(ValueError, match="softmax_scale"):
+        front.attend(*args, softmax_scale=scale)
+    for good in (None, 0.5, 1e-40):
+        with pytest.raises(B.UpfError) as e:      # past the front end's checks: the library refuses the null context
+            front.attend(*args, softmax_scale=good)
+        assert "softmax_scale" not in e.value.message
