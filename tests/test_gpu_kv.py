@@ -785,3 +785,58 @@ def test_a_wait_that_runs_out_in_teams_of_several_warps(Hq, H, d):
         B.upf_set_wait_limit(big.ctx, 0)
         got = ask()
         assert big.status() == 0 and not got.out.any() and (got.lse - np.log(n // R)).abs().max() < 1e-5
+
+
+# ----------------------------------------------------------- more of the above --
+
+def test_inconsistent_row_ranges_touch_only_the_good_requests():
+    """cu_q that is not ascending, leaves the rows or holds more than max_q_len rows: such a request is skipped, its rows are
+    left as they are and the others are right."""
+    b = Batch([40, 50, 60], 4, 2, 128)
+    q, _ = b.queries([1, 1, 1])
+    lone = [K.attend(f64(q[r:r + 1]), b.k[r:r + 1], b.v[r:r + 1], [0, 1]) for r in range(3)]
+    # the rows of each good request, with the oracle's view of it
+    two = K.attend(f64(q[:2]), b.k[:1], b.v[:1], [0, 2])
+    tail = K.attend(f64(q[2:3]), b.k[2:], b.v[2:], [0, 1])
+    for wrong, kept, good in (([0, 0, 3, 3], [0, 1, 2], []), ([0, -1, 2, 3], [0, 1], [(2, 3, tail)]),
+                              ([0, 1, 2, 9], [2], [(0, 1, lone[0]), (1, 2, lone[1])]),
+                              ([0, 2, 1, 3], [], [(0, 1, [x[:1] for x in two])]),   # row 1 is given to two requests
+                              ([0, 1, 2 ** 31 - 1, 3], [1, 2], [(0, 1, lone[0])]), ([3, 3, 3, 3], [0, 1, 2], [])):
+        out, lse = torch.full_like(q, 5.0), torch.full((3, 4), 5.0, device=DEV)
+        b.cache.attend(q, b.table, b.kv_len, 16, cu_q=torch.tensor(wrong, dtype=torch.int32, device=DEV), max_q_len=2,
+                       out=out, lse=lse)
+        assert b.cache.status() == (0 if wrong == [3, 3, 3, 3] else 1)
+        assert (out[kept] == 5).all() and (lse[kept] == 5).all(), wrong
+        for x, y, ref in good:
+            compare((out[x:y], lse[x:y]), ref, BF16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,d", [(12, 64), (4, 256), (12, 128), (4, 64)])
+@pytest.mark.parametrize("lens", [[60000] + [100] * 19, [6000] + [20] * 100, [20000, 20000]])
+def test_units_over_many_workers_at_every_shape(lens, Hq, d, dtype):
+    """Eight and sixteen rows of each head size: parts added up in two steps, by teams, and by the second launch."""
+    b = Batch(lens, Hq, 1, d, page=64, dtype=dtype)
+    q, got, ref = check(b, [1] * len(lens))
+    again = b.cache.attend(q, b.table, b.kv_len, 64)
+    assert torch.equal(got.out, again.out) and torch.equal(got.lse, again.lse)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_batches(seed):
+    r = np.random.default_rng(1000 + seed)
+    pick = lambda *x: x[r.integers(len(x))]  # noqa: E731
+    Hq, H, d = pick((8, 2, 64), (5, 1, 64), (40, 2, 64), (8, 2, 128), (28, 4, 128), (4, 4, 128), (32, 2, 128), (16, 2, 256),
+                    (9, 1, 256), (24, 2, 256))
+    R = pick(1, 2, 3, 8, 20, 60, 300)
+    top = pick(1, 16, 40, 200, 1000, 3000) if R < 60 else pick(1, 20, 100)
+    lens = r.integers(0, top + 1, R)
+    if r.random() < 0.2:
+        lens[r.integers(R)] = r.integers(2000, 9000)
+    q_len = pick(1, 1, 2, 5, 17, 60) if R <= 20 else pick(1, 2)
+    news = r.integers(0 if q_len > 1 else 1, q_len + 1, R)
+    news[0] = max(news[0], 1)
+    window = int(pick(0, 0, 1, 5, 33, 64, 300, 5000))
+    b = Batch(lens.tolist(), Hq, H, d, page=int(pick(16, 32, 64, 128)), dtype=pick(BF16, F16), seed=seed,
+              k_exp=int(r.integers(-3, 4)), v_exp=int(r.integers(-3, 4)), scale=pick(0.2, 1, 3))
+    check(b, news.tolist(), window=window, sinks=int(pick(0, 1, 4, 17, 100)) if window else 0, q_scale=pick(0.1, 1, 4))
