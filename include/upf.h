@@ -319,7 +319,8 @@ upf_status upf_select_noalloc(const upf_batch* batch, const upf_params* params, 
  * inside the tensor-core scoring kernels is bounded; when one expires the
  * kernel records UPF_ERR_TIMEOUT in the status word, stops issuing work,
  * waits for its outstanding copies and MMAs, frees its tensor memory and
- * returns, so the context stays usable.  This sets the limit of the pipeline
+ * returns, so the context stays usable.  The cache attention's waits for its
+ * copies are bounded in the same way.  This sets the limit of the pipeline
  * waits (a role waiting for another role's data), in SM clock cycles, for
  * later calls on `ctx`; 0 restores the default (4e9 cycles, about 2 s).  The
  * waits that wind a kernel down always keep the default.  A very small limit

@@ -25,9 +25,9 @@
 // in 32 registers a lane (128 dims of eight rows, 64 of sixteen), so that sixteen
 // warps fit an SM at every head size: each multiplies its dims of the queries and
 // keys, the team adds the logits up through shared memory, and each weighs its dims
-// of the values.  (Eight warps an SM with 250 registers instead: 60 against 46 us for 64
-// requests with a window of 1024 at d = 256, 35 against 31 for four drafted tokens
-// each of eight requests.)  Every team has its own ring of records filled by bulk
+// of the values.  (Eight warps an SM with 250 registers instead took a third longer for 64
+// requests with a window of 1024 at d = 256, and an eighth longer for four drafted tokens
+// each of eight requests, when those took 46 and 31 us.)  Every team has its own ring of records filled by bulk
 // copies (two records of 18 d bytes a tile).  A unit that lies in one worker's share is
 // written out at once; of others every worker leaves its part (reference, sum, weighted
 // sum, all fp32) in the workspace, and the last one to do so adds the parts up, in
@@ -37,11 +37,11 @@
 // among others): 16 requests of 4096 to 131072 entries, 521 MB, 96 us, 5.4 TB/s or
 // 0.80 of the copy rate; while tiles stream the SMs take in 6.2 TB/s, the rest is
 // the start (kv_len, then page table, then the first records: 5.6 us) and the end.  One
-// request of 131072 entries: 35 us.  One of 4096 entries with two heads of d = 64:
-// 7.4 us, all of it latency.  Many short units (256 requests of up to 700 entries: 27
+// request of 131072 entries: 35.5 us.  One of 4096 entries with two heads of d = 64:
+// 7.6 us, all of it latency.  Many short units (256 requests of up to 700 entries: 28
 // us) and sixteen rows are bound by instructions: about 560 a warp for a whole tile
 // (128 conversions, 128 scalings, 32 products, 32 to pair the values' entries), 1500
-// for a unit.
+// to 2100 for a unit.
 //
 // Arithmetic.  A code times its scale has at most six significant bits and is
 // exact in f16, and so is a query after division by the power of two of its
@@ -138,14 +138,15 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // Cost of a unit in the dealing, in tiles, beside its tiles: the rows' load, the
 // first copies' latency and the writing out.
 constexpr int kUnitCostCta = 24, kUnitCostTeam = 4;
-// Workers are teams where units have fewer tiles than this on average.  64 requests with a
-// window (34 tiles a unit, d = 256): 42 us as teams, 47 as CTAs; one request of 4096
-// entries (128 tiles a unit): 14 us as teams, 7.5 as CTAs.
+// Workers are teams where units have fewer tiles than this on average.  256 short requests
+// (4 tiles a unit): 28 us as teams, 54 as CTAs; 64 requests with a window (34 tiles, d = 256):
+// 42.6 and 46.8; one request of 4096 entries (128 tiles): 14.5 and 7.7.
 constexpr int kShortUnit = 64;
 
 // Where workers are teams, a unit of at most this many tiles is not split: it belongs to
-// the team whose share its first place lies in.  256 short requests: 31 us, 44 with
-// every unit split where the shares end, 40 with units of up to 24 tiles kept whole.
+// the team whose share its first place lies in.  256 short requests: 28 us, 32 with
+// every unit split where the shares end (parts to add up), 37 with units of up to 24 tiles
+// kept whole (uneven shares).
 constexpr int kWholeUnit = 8;
 
 // How the tiles are dealt out.  Along the dealing a unit takes cost + tiles places.
@@ -266,9 +267,9 @@ struct Parts {
 
 // Where few units are spread over many CTAs, adding their parts up is left to a second
 // launch, which shares it among as many CTAs as the unit had (one request of 131072
-// entries: 40 against 43 us at eight kv heads, 32 against 37 at two of d = 256; with
-// 16 parts a unit or fewer the second launch costs more: 12.3 against 10.3 us for one
-// request of 4096 entries): for each CTA, the unit that goes on after its share.
+// entries: 35.5 against 37.7 us at eight kv heads, 27.7 against 33.8 at two of d = 256; with
+// 16 parts a unit or fewer the second launch costs more: 7.9 against 7.7 us for one
+// request of 4096 entries, 44.7 against 42.6 for 64 with a window): for each CTA, the unit that goes on after its share.
 struct Note {
   int first, last;        // CTAs of the unit (first < 0: no such unit)
   int h, row0, rows, q0;  // kv head, first row of the chunk, rows of the request, its first row in q

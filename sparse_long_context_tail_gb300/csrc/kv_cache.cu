@@ -16,9 +16,11 @@
 // Short calls look for a later token with the same slot; longer ones claim
 // their slots first (owner[slot] = the latest token), in one launch of a cluster
 // of CTAs whose cost goes with the tokens, not with the size of the cache, and
-// which the loads of the writing launch do not wait for.  Measured (8 heads, d = 128),
-// looking against claiming: 64 tokens 2.5 and 3.5 us, 1024 tokens 3.7 and 4.2, 2048
-// tokens 5.3 and 4.5.
+// which the loads of the writing launch do not wait for.  Measured, looking against
+// claiming, us: 8 heads of d = 128: 64 tokens 2.4 and 3.9, 1024 tokens 3.3 and 5.5, 2048 tokens
+// 4.6 and 6.3, 4096 tokens 7.9 and 7.7; one head of d = 64, where the looks are all there is:
+// 64 tokens 2.2 and 3.9, 1024 tokens 7.0 and 5.2, 4096 tokens 11.2 and 5.5.  1024 tokens
+// (UPF_KV_FEW_TOKENS) lie between the two crossings.
 #include "kv_layout.cuh"
 #include "sm100_ptx.cuh"
 #include "upf_internal.cuh"

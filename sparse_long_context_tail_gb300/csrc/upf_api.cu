@@ -22,7 +22,7 @@ struct upf_ctx {
   int device;
   int num_sms;
   int32_t* status_dev;  // [kCtxWords] device words
-  long long wait_limit = 0;  // pipeline waits of the scoring kernels, cycles (0: default)
+  long long wait_limit = 0;  // pipeline waits of the scoring kernels and the cache attention, cycles (0: default)
   // tracing
   bool profiling = false;
   int32_t launches[UPF_NUM_STAGES] = {};
