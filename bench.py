@@ -477,6 +477,24 @@ def run_per_config(torch, B, sel, names, dev, stream, flush, peaks, peak_kind, s
     return out
 
 
+def seven_digits(x):
+    """x with its floats cut to seven significant digits (whole numbers stay as they are)."""
+    if isinstance(x, float):
+        return int(x) if x.is_integer() else float(f"{x:.7g}")
+    if isinstance(x, dict):
+        return {k: seven_digits(v) for k, v in x.items()}
+    return [seven_digits(v) for v in x] if isinstance(x, list) else x
+
+
+def result_line(line):
+    """The benchmark's one JSON line, under 3.6 KB, so that readers that keep only the end of the output
+    see all of it: stages that did not run and the roofline's second copy of its kernel are left out."""
+    roofline = dict(line["roofline"])
+    roofline["passes"] = {k: v for k, v in roofline["passes"].items() if k != roofline["kernel"]}
+    return json.dumps(seven_digits(dict(line, roofline=roofline,
+                                        stages={k: v for k, v in line["stages"].items() if v["launches"]})))
+
+
 PER_CONFIG = ["small-L4096", "llama8b-L32768", "llama8b-batch16"] + list(wl.SWEEP_NAMES)
 
 
@@ -588,12 +606,12 @@ def main():
         gather_p1 = run_gather_p1(torch, sel, spec, w, cu, cu_dev, hid_dev, pos_dev, slot_dev, out, peaks)
 
     # the other workloads (one GPU only: they are not the headline)
-    per_config = None
     if rank == 0 and world == 1 and not args.no_per_config:
         del x
         torch.cuda.empty_cache()
         names = [n for n in PER_CONFIG if n != spec.name]
         per_config = run_per_config(torch, B, sel, names, dev, stream, flush, peaks, peak_kind)
+        log("[bench] per_config " + json.dumps(seven_digits(per_config)))
 
     cpu = None
     if rank == 0 and world == 1 and not args.no_cpu_baseline:
@@ -608,9 +626,9 @@ def main():
                             "traced_mean": statistics.mean(traced), "stage_sum": sum(stage_ms) / args.steps},
                 "kept_tokens": kept_total, "kept_fraction": kept_total / T,
                 "roofline": roofline, "stages": stages, "cpu_baseline": cpu, "e2e": e2e, "gather_p1": gather_p1,
-                "graph": graph, "per_config": per_config,
+                "graph": graph,
                 "gpu_launches": int(sum(launches)), "clocks": clk, "wall_s": wall}
-        print(json.dumps(line), flush=True)
+        print(result_line(line), flush=True)
     sel.close()
     if world > 1:
         dist.destroy_process_group()

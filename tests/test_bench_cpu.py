@@ -85,3 +85,48 @@ def test_reference_arm_prints_one_line_on_rank_zero_only():
 @pytest.mark.parametrize("every,layers,want", [(4, 12, [3, 7, 11]), (6, 12, [5, 11])])
 def test_stack_schedules_place_the_full_attention_layers(every, layers, want):
     assert bench.full_attention_layers(layers, every) == want
+
+
+def test_the_result_line_is_short_and_whole():
+    """With every key of a run the line stays under 3.6 KB, and the contract's numbers are all there."""
+    third = 1 / 3
+    entry = {"bound": "tensor", "kernel": "score_pass1", "achieved": 1e3 * third, "peak": 1897.7, "unit": "TFLOP/s",
+             "frac": third, "peak_source": "measured bf16_tflops (burst)", "traffic": None, "us_per_launch": 100 * third,
+             "algorithmic_bytes_per_launch": 269484032.0, "algorithmic_flops_per_launch": 137372368896.0,
+             "tflops": 1e3 * third, "gbs": 1e4 * third, "frac_of_sustained_peak": third}
+    passes = {"score_pass1": entry, "score_pass2": dict(entry, kernel="score_pass2")}
+    stage = {"launches": 20, "ms_per_launch": third, "share": third, "tflops": 1e3 * third, "gbs": 1e4 * third}
+    stages = {n: dict(stage, launches=20 if n in ("score_pass1", "score_pass2", "select", "compact_gather") else 0)
+              for n in bench.STAGES}
+    spec = wl.named_spec("llama8b-L131072")
+
+    class W:
+        total_tokens = 131072
+
+    class Args:
+        gpus, no_flush = 1, False
+
+    line = {"metric": bench.METRIC, "value": 6e8 * third, "unit": bench.UNIT, "n_gpus": 1, "steps": 20, "warmup": 5,
+            "ms_per_step": third, "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+            "data": "synthetic (seeded bf16 N(0,1) + planted blocks)",
+            "config": bench.config_of(spec, W, Args),
+            "step_ms": {k: third for k in ("median", "min", "max", "traced_mean", "stage_sum")}, "kept_tokens": 1088,
+            "kept_fraction": third, "roofline": dict(entry, passes=passes), "stages": stages,
+            "cpu_baseline": {"value": 1e5 * third, "unit": "tokens/s", "cores": 16, "kind": "oracle", "sample": "s" * 150},
+            "e2e": {"value": 9e7 * third, "unit": "tokens/s", "h2d_bytes_per_step": 278414344, "d2h_bytes_per_step": 8946704,
+                    "ms_per_step": third, "steps": 5, "serial_ms_per_step": third, "note": "n" * 450},
+            "gather_p1": {k: 1e4 * third for k in ("kept_tokens", "bytes_per_launch", "gather_ms_per_launch", "achieved_gbs",
+                                                   "peak_gbs", "frac", "compaction_ms_per_launch")},
+            "graph": {"ms_per_step": third, "median_ms": third, "steps": 20}, "gpu_launches": 80,
+            "clocks": {"sm_mhz": 2070.0, "sm_max_mhz": 2070.0, "reasons": [], "samples": 3}, "wall_s": third}
+    text = bench.result_line(line)
+    assert len(text) < 3600 and "\n" not in text
+    got = json.loads(text)
+    assert set(got) == set(line)
+    for k in ("metric", "unit", "n_gpus", "steps", "warmup", "higher_is_better", "scaling", "dtype", "data", "config",
+              "gpu_launches", "clocks", "vs_baseline"):
+        assert got[k] == line[k]
+    assert got["value"] == pytest.approx(line["value"], rel=1e-6) and got["e2e"]["h2d_bytes_per_step"] == 278414344
+    assert got["roofline"]["algorithmic_flops_per_launch"] == 137372368896
+    assert list(got["stages"]) == ["score_pass1", "score_pass2", "select", "compact_gather"]
+    assert list(got["roofline"]["passes"]) == ["score_pass2"]
