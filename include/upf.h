@@ -453,8 +453,9 @@ size_t upf_kv_attend_workspace_bytes(const upf_kv_cache* cache, const upf_kv_que
  * over the entries e that the row sees; a row that sees none gets out = 0 and
  * lse = -inf.  Weights come from differences of logits, so these may have any
  * size up to 2^127.  A row whose largest logit is past fp32's range is NaN, and so is one
- * whose softmax_scale * 2^k_exp * max|q| is, unless its largest logit is 0.  An infinity or
- * a NaN in q makes its row NaN (if it sees an entry) and no other.
+ * whose softmax_scale * 2^k_exp * max|q| is, unless its largest logit is 0 (both may be NaN
+ * from 2^127 on).  An infinity or a NaN in q makes its row NaN (if it sees an entry) and no
+ * other.
  * q, out: device, row t head h at q + t*q_row_stride + h*head_dim (`dtype`), row
  *         strides >= H_q*head_dim and multiples of 8, 16-byte aligned; out must
  *         not overlap q or the cache.
