@@ -840,3 +840,85 @@ def test_random_batches(seed):
     b = Batch(lens.tolist(), Hq, H, d, page=int(pick(16, 32, 64, 128)), dtype=pick(BF16, F16), seed=seed,
               k_exp=int(r.integers(-3, 4)), v_exp=int(r.integers(-3, 4)), scale=pick(0.2, 1, 3))
     check(b, news.tolist(), window=window, sinks=int(pick(0, 1, 4, 17, 100)) if window else 0, q_scale=pick(0.1, 1, 4))
+
+
+# ------------------------------------------- calls at the ends of what is allowed --
+
+def test_outputs_that_may_be_left_out():
+    """upf_kv_read of keys or values alone, and upf_kv_attend without lse, give what the full calls give."""
+    b = Batch([300, 40], 8, 2, 128)
+    c, slots = b.cache, b.slots.to(DEV)
+    T, width = len(slots), 2 * 128
+    k, v = c.read(slots)
+    for of in range(2):
+        out = [torch.full_like(k, 3.0), torch.full_like(v, 3.0)]
+        ptr = [x.data_ptr() if i == of else 0 for i, x in enumerate(out)]
+        B.upf_kv_read(c.ctx, c._cache, B.UPF_BF16, slots.data_ptr(), T, 0, ptr[0], width, ptr[1], width, c._stream())
+        assert torch.equal(out[of], (k, v)[of]) and (out[1 - of] == 3).all()
+    q, _ = b.queries([1, 1])
+    want = c.attend(q, b.table, b.kv_len, 16)
+    query, keep = B.make_kv_query(2, 8, 2, b.kv_len.data_ptr(), b.table.data_ptr(), b.table.shape[1], b.table.shape[1], 16)
+    ws = torch.empty(B.upf_kv_attend_workspace_bytes(c._cache, query), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(q)
+    B.upf_kv_attend(c.ctx, c._cache, query, B.UPF_BF16, q.data_ptr(), 8 * 128, out.data_ptr(), 8 * 128, 0, ws.data_ptr(),
+                    ws.numel(), c._stream())
+    assert torch.equal(out, want.out) and c.status() == 0
+
+
+def test_a_captured_long_write_with_other_slots_and_counts():
+    """More tokens than a call without a workspace takes, captured once: replays follow slots, count and values."""
+    T, H, d = 3000, 2, 64
+    c = make(16 * 300, H, d, fill=0)
+    k, v = rand((T, H, d), BF16, 1), rand((T, H, d), BF16, 2)
+    slots = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    count = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c.write(k, v, slots, count)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.write(k, v, slots, count)
+    held = {}
+    for step, n in enumerate((T, 17, 0, 2500)):
+        s = torch.randint(-2, c.num_slots, (T,), generator=torch.Generator().manual_seed(step))
+        k.copy_(rand((T, H, d), BF16, 10 + step))
+        v.copy_(rand((T, H, d), BF16, 20 + step))
+        slots.copy_(s)
+        count.fill_(n)
+        g.replay()
+        kk, vv = K.cache_values(f64(k), 0), K.cache_values(f64(v), 0)
+        for t in range(n):
+            if s[t] >= 0:
+                held[int(s[t])] = kk[t], vv[t]
+        at = list(held)
+        got = c.read(torch.tensor(at, device=DEV))
+        for of in range(2):
+            np.testing.assert_array_equal(f64(got[of]), np.stack([held[x][of] for x in at]))
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("Hq,H,d,lens,news", [
+    (256, 256, 64, [70, 1, 0], [2, 1, 1]),             # as many kv heads as there may be
+    (256, 1, 64, [70, 33], [1, 3]),                    # all q heads on one
+    (8, 2, 64, [1500, 1024, 600], [1024, 1024, 1024]),  # as many new tokens as there may be: some rows see nothing
+    (4, 2, 128, [2100], [1024]),
+])
+def test_the_largest_head_counts_and_prompt_chunks(Hq, H, d, lens, news):
+    b = Batch(lens, Hq, H, d)
+    check(b, news)
+    check(b, news, window=50, sinks=3)
+
+
+def test_thousands_of_requests():
+    rng = np.random.default_rng(6)
+    check(Batch(rng.integers(0, 25, 3000).tolist(), 2, 1, 64), [1] * 3000)
+    check(Batch(rng.integers(0, 100, 700).tolist(), 4, 1, 256), [1] * 700, window=20, sinks=2)
+
+
+def test_windows_first_tokens_and_pages_as_large_as_they_come():
+    b = Batch([1000, 40, 3], 8, 2, 128)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 30, 2 ** 31 - 1), (2 ** 30 - 1, 1), (7, 2 ** 31 - 1)):
+        check(b, [2, 1, 5], window=window, sinks=sinks)
+    check(Batch([70000], 2, 1, 64, page=65536, spare=0), [3], window=66000, sinks=100)
+    full = Batch([64, 32], 4, 2, 128, page=32)          # kv_len fills the table
+    full.table = full.table[:, :2].contiguous()
+    check(full, [1, 1])
