@@ -167,8 +167,16 @@ def make_compact_io(row_bytes=0, hidden_in=0, hidden_out=0, pos_in=0, pos_out=0,
                         total_kept or None, layer_id, history_cap, history or None, history_len or None)
 
 
+def _check_int32(**sizes: int) -> None:
+    """ctypes cuts a larger number down to its low bits without a word."""
+    for name, value in sizes.items():
+        if not -2 ** 31 <= value < 2 ** 31:
+            raise ValueError(f"{name} {value} does not fit 32 bits")
+
+
 def make_kv_cache(data: int, num_slots: int, num_kv_heads: int, head_dim: int, k_exp: int = 0,
                   v_exp: int = 0) -> UpfKvCache:
+    _check_int32(num_kv_heads=num_kv_heads, head_dim=head_dim, k_exp=k_exp, v_exp=v_exp)
     return UpfKvCache(data or None, num_slots, num_kv_heads, head_dim, k_exp, v_exp)
 
 
@@ -176,6 +184,7 @@ def make_kv_query(num_reqs: int, num_q_heads: int, num_q_tokens: int, kv_len: in
                   max_pages: int, page_size: int, cu_q: int = 0, max_q_len: int = 1, window: int = 0, sinks: int = 0,
                   softmax_scale: float = 0.0, kv_of_q: Optional[Sequence[int]] = None):
     """Build a upf_kv_query; returns (struct, keepalive) -- keep both alive during the call."""
+    _check_int32(max_q_len=max_q_len, page_size=page_size, window=window, sinks=sinks)
     kv = _head_map(kv_of_q, num_q_heads)
     x = UpfKvQuery(num_reqs, num_q_heads, kv.ctypes.data_as(POINTER(c_int32)) if kv is not None else None,
                    num_q_tokens, max_q_len, cu_q or None, kv_len or None, page_table or None, page_stride, max_pages,

@@ -273,3 +273,17 @@ def test_scales_that_are_not_positive_are_refused(front, scale):
         with pytest.raises(B.UpfError) as e:      # past the front end's checks: the library refuses the null context
             front.attend(*args, softmax_scale=good)
         assert "softmax_scale" not in e.value.message
+
+
+@pytest.mark.parametrize("name", ["max_q_len", "page_size", "window", "sinks"])
+def test_sizes_past_32_bits_are_refused(front, name):
+    """The C structure holds 32 bits: a larger number would be cut down to another one."""
+    args = dict(q=_kv(2, 4), page_table=torch.zeros(2, 4, dtype=torch.int32), kv_len=torch.zeros(2, dtype=torch.int32), page_size=16)
+    for value in (2 ** 32 + 16, -2 ** 32 + 16, 2 ** 31):
+        with pytest.raises(ValueError, match=name):
+            front.attend(**{**args, name: value})
+        with pytest.raises(ValueError, match=name):
+            _query(**{name: value})
+    for field in ("num_kv_heads", "head_dim", "k_exp", "v_exp"):
+        with pytest.raises(ValueError, match=field):
+            _cache(**{field: 2 ** 32 + 64})
