@@ -184,7 +184,8 @@ def make_kv_query(num_reqs: int, num_q_heads: int, num_q_tokens: int, kv_len: in
                   max_pages: int, page_size: int, cu_q: int = 0, max_q_len: int = 1, window: int = 0, sinks: int = 0,
                   softmax_scale: float = 0.0, kv_of_q: Optional[Sequence[int]] = None):
     """Build a upf_kv_query; returns (struct, keepalive) -- keep both alive during the call."""
-    _check_int32(max_q_len=max_q_len, page_size=page_size, window=window, sinks=sinks)
+    if (max_q_len | page_size | window | sinks) >> 31:      # one is negative or too large
+        _check_int32(max_q_len=max_q_len, page_size=page_size, window=window, sinks=sinks)
     kv = _head_map(kv_of_q, num_q_heads)
     x = UpfKvQuery(num_reqs, num_q_heads, kv.ctypes.data_as(POINTER(c_int32)) if kv is not None else None,
                    num_q_tokens, max_q_len, cu_q or None, kv_len or None, page_table or None, page_stride, max_pages,
