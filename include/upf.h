@@ -472,6 +472,164 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
                          const void* q, int64_t q_row_stride, void* out, int64_t out_row_stride, float* lse, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* Attention weight that entries of the cache have drawn, for upf_kv_evict:
+ *   weights_out[r, e] = decay * weights_in[r, e] + sum exp(scale * q . k_e - lse)
+ * over the rows (new tokens of request r, q heads) that see entry e, for all e < kv_len[r];
+ * weights of later entries are left as they are, and those of a request without new tokens.
+ * Added up in fp32, in the same order at every call.
+ * query:   as for upf_kv_attend.
+ * q, lse:  what upf_kv_attend was given and gave back.  An error of lse is a relative error of
+ *          the weights: in fp32 |lse| * 2^-24 and more.
+ * decay:   in [0, 1]; 1 adds.
+ * weights_in (nullable: zeros), weights_out: device float32, request r entry e at
+ *    r*weights_stride + e, `weights_cols` entries a row; they may be the same.
+ * A row whose lse is -inf adds nothing (it saw nothing); one whose lse is a NaN or +inf, or with
+ * a NaN or an infinity in q, adds nothing and sets UPF_ERR_NONFINITE in the status word.
+ * An entry whose key holds a NaN gets a NaN.  Errors in device tables as for upf_kv_attend:
+ * the request is skipped (also with kv_len[r] > weights_cols); an entry of a bad page is not seen.
+ * ws: upf_kv_accumulate_workspace_bytes() bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
+                             const void* q, int64_t q_row_stride, const float* lse, float decay,
+                             const float* weights_in, float* weights_out, int64_t weights_stride,
+                             int32_t weights_cols, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace upf_kv_accumulate needs (scratch, 256-byte aligned, any contents;
+ * depends on the sizes alone); 0 and the last error if the arguments are invalid. */
+size_t upf_kv_accumulate_workspace_bytes(const upf_kv_cache* cache, const upf_kv_query* query);
+
+/* Eviction: requests with more than `trigger` entries keep `budget` of them.
+ * num_reqs, kv_len, page_table, page_stride, max_pages, page_size: as in upf_kv_query.
+ * trigger, budget: 1 <= budget <= trigger.  A request with kv_len[r] <= trigger keeps all.
+ * sinks, recent: the first `sinks` and the last `recent` entries stay (sinks + recent <= budget);
+ *    of the others the heaviest do, of equally heavy ones the lower entries.
+ * The kept entries stay in order and lie together: entry j is what was entry kept[r, j].
+ * page_table_out: device int32 (nullable): where the kept entries go.  NULL: they stay in the
+ *    request's own pages, from the first on.  Otherwise the table has rows of page_stride_out and
+ *    max_pages_out pages and may name a page of page_table only in the same place of the same
+ *    request; no other page may be named twice.  All entries of requests that keep theirs are
+ *    copied too.  Pages that several requests share have to be evicted into others.
+ * kv_len_out: device int32 [R]: the new lengths; may be kv_len.
+ * weights: device float32, request r entry e at r*weights_stride + e, `weights_cols` a row.
+ * weights_out: (same with its own stride and cols; may be weights, with its stride): the kept entries'
+ *    weights, together, and zeros from the new length up to the old one.  Requests whose entries all stay
+ *    where they are keep theirs (copied if weights_out is another array).
+ * kept: device int32 (nullable): request r's at r*kept_stride, `budget` entries; -1 past the new length
+ *    and for a skipped request.
+ * A negative, infinite or NaN weight in a request to be cut sets UPF_ERR_NONFINITE; a bad kv_len
+ * (also one above weights_cols), a bad page among the request's entries or new places, or more
+ * entries to keep than places (of max_pages_out or weights_out_cols) set UPF_ERR_INVALID_ARG.  Such a
+ * request is skipped: nothing of it is moved, kv_len_out[r] is kv_len[r], or 0 where page_table_out is given. */
+typedef struct upf_kv_eviction {
+  int32_t num_reqs;
+  const int32_t* kv_len;
+  int32_t* kv_len_out;
+  const int32_t* page_table;
+  int64_t page_stride;
+  int32_t max_pages;
+  int32_t page_size;
+  const int32_t* page_table_out;
+  int64_t page_stride_out;
+  int32_t max_pages_out;
+  int32_t budget;
+  int32_t trigger;
+  int32_t sinks;
+  int32_t recent;
+  const float* weights;
+  int64_t weights_stride;
+  int32_t weights_cols;
+  int32_t weights_out_cols;
+  float* weights_out;
+  int64_t weights_out_stride;
+  int32_t* kept;
+  int64_t kept_stride;
+} upf_kv_eviction;
+
+/* Bytes of workspace upf_kv_evict needs (scratch, 256-byte aligned, any contents; depends on
+ * the sizes alone); 0 and the last error if the arguments are invalid. */
+size_t upf_kv_evict_workspace_bytes(const upf_kv_cache* cache, const upf_kv_eviction* eviction);
+
+/* Run an eviction.  kv_len, the page tables and weights must not change while the call runs; a captured call
+ * may be replayed with other contents.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+upf_status upf_kv_evict(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_eviction* eviction, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions
+ * ------------------------------------------------------------------------
+ * Queries and keys as upf_select_tokens and upf_kv_write take them carry their
+ * position as a rotation; pos_out of upf_compact are the positions of the kept
+ * tokens.  Pair i of a head, (a, b), at position p turns by the angle p * f_i:
+ *   a' = m (a cos - b sin),   b' = m (b cos + a sin),
+ * computed in fp32 and rounded once.  The frequency f_i is base^(-2i / rotary_dim)
+ * radians per position, changed for long contexts as `scaling` says, m a magnitude.
+ *
+ * head_dim:    64, 128 or 256.
+ * rotary_dim:  even, 2 to head_dim: the first rotary_dim dims of a head turn, the
+ *              others are left as they are.
+ * interleaved: 0: pair i is dims (i, i + rotary_dim/2); 1: dims (2i, 2i + 1).
+ * scaling:     how f_i is changed, with s = factor and L0 = original_len:
+ *   UPF_ROPE_NONE    not at all (factor, original_len, low and high are not read)
+ *   UPF_ROPE_LINEAR  f_i / s: positions are interpolated
+ *   UPF_ROPE_BASE    base becomes base * s^(rotary_dim / (rotary_dim - 2))
+ *   UPF_ROPE_YARN    between f_i / s and f_i along a ramp over the pair's index
+ *                    from the one that makes `high` turns in L0 positions (kept) to the
+ *                    one that makes `low` (divided); ends rounded outwards
+ *   UPF_ROPE_BANDS   pairs that make more than `high` turns in L0 positions are kept,
+ *                    those that make fewer than `low` divided, in between
+ *                    f_i ((1 - k) / s + k) with k = (turns - low) / (high - low)
+ * base > 0 (and not 1 with UPF_ROPE_YARN), factor > 0, original_len > 0, 0 < low < high.
+ * divisors:    host [rotary_dim / 2], nullable: f_i is divided by divisors[i] (> 0) too.
+ * magnitude:   m; 0 selects 0.1 ln s + 1 with UPF_ROPE_YARN and s > 1, otherwise 1. */
+typedef enum upf_rope_scaling {
+  UPF_ROPE_NONE = 0,
+  UPF_ROPE_LINEAR = 1,
+  UPF_ROPE_BASE = 2,
+  UPF_ROPE_YARN = 3,
+  UPF_ROPE_BANDS = 4
+} upf_rope_scaling;
+
+typedef struct upf_rope {
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t scaling;
+  double base;
+  double factor;
+  double original_len;
+  double low;
+  double high;
+  const double* divisors;
+  double magnitude;
+} upf_rope;
+
+/* The rotation's table (host only, no GPU): turns[i] (host, rotary_dim / 2) is
+ * f_i / (2 pi) as a fraction of a turn in units of 2^-64, modulo one turn, so that
+ * position * turns[i] modulo 2^64 is the angle, at any position to 2^-53 of
+ * position * f_i.  The caller copies it to the device.  magnitude: receives m
+ * (nullable).  Errors: INVALID_ARG, UNSUPPORTED. */
+upf_status upf_rope_turns(const upf_rope* rope, uint64_t* turns, double* magnitude);
+
+/* Rotate queries and keys.
+ * rope:      head_dim, rotary_dim, interleaved; the rest only as far as it gives the magnitude.
+ * turns_dev: device uint64 [rotary_dim / 2], as upf_rope_turns gives it (or the caller's own).
+ * inverse:   not 0: turn back and divide by the magnitude.
+ * positions: device int64 [num_tokens], any value.
+ * num_tokens_dev: device int32 [1] (nullable): only the first
+ *    min(num_tokens, *num_tokens_dev) tokens are done (e.g. total_kept); rows past them
+ *    keep what the outputs hold.
+ * q, k:      device, token t head h at q + t*q_row_stride + h*head_dim (`dtype`);
+ *    row strides in elements, >= heads*head_dim and multiples of 8, 16-byte aligned.
+ *    With num_q_heads or num_kv_heads 0 the pointers are not read; at most 65536 heads each.
+ * q_out, k_out: the same layout with strides of their own.  An output may be its own
+ *    input, with the same stride; otherwise no output may overlap an input or the other output.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+upf_status upf_rope_apply(upf_ctx* ctx, const upf_rope* rope, const uint64_t* turns_dev, int32_t inverse,
+                          int32_t dtype, const int64_t* positions, int32_t num_tokens, const int32_t* num_tokens_dev,
+                          const void* q, int64_t q_row_stride, void* q_out, int64_t q_out_row_stride,
+                          int32_t num_q_heads, const void* k, int64_t k_row_stride, void* k_out,
+                          int64_t k_out_row_stride, int32_t num_kv_heads, void* stream);
+
 /* Tracing (per-stage device timing).  Stages, in launch order:
  * 0 describe (batch descriptor; upf_select_tokens launches none for batches
  * whose descriptor travels in the kernel parameters), 1 score pass 1, 2 score

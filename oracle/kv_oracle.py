@@ -129,3 +129,44 @@ def attend(q: np.ndarray, k: Sequence[np.ndarray], v: Sequence[np.ndarray], cu_q
                 reach[a + i, h] = scale * (np.abs(ke) @ np.abs(row)).max()
                 flat[a + i, h] = scale * np.abs(row).max() * np.abs(ke).sum(1).max()
     return out, lse, spread, total, reach, flat, seen
+
+
+def accumulate(q: np.ndarray, lse: np.ndarray, k: Sequence[np.ndarray], cu_q: Sequence[int], window: int = 0,
+               sinks: int = 0, scale: Optional[float] = None, kv_of_q: Optional[Sequence[int]] = None):
+    """Per request, float64 [n_r]: what each entry draws, sum exp(scale q.k_e - lse) over the rows that see it, and the
+    sums over the same rows of that times the terms a tolerance is made of: ``reach`` = scale sum_j |q_j k_ej|,
+    ``flat`` = scale max|q| sum_j |k_ej|, ``far`` = |lse|, and ``one``.  Rows whose lse is not finite add nothing."""
+    q = np.asarray(q, dtype=np.float64)
+    lse = np.asarray(lse, dtype=np.float64)
+    Hq, d = q.shape[1:]
+    scale = d ** -0.5 if scale is None else scale
+    drawn, slack = [], []
+    for r in range(len(cu_q) - 1):
+        n, a, b = len(k[r]), cu_q[r], cu_q[r + 1]
+        w = np.zeros(n)
+        s = {name: np.zeros(n) for name in ("reach", "flat", "far", "one")}
+        for i in range(b - a):
+            e = visible(n, b - a, i, window, sinks)
+            for h in range(Hq):
+                if not len(e) or not np.isfinite(lse[a + i, h]):
+                    continue
+                g = h // (Hq // k[r].shape[1]) if kv_of_q is None else kv_of_q[h]
+                ke, row = k[r][e, g], q[a + i, h]
+                x = np.exp(scale * (ke @ row) - lse[a + i, h])
+                w[e] += x
+                s["reach"][e] += x * scale * (np.abs(ke) @ np.abs(row))
+                s["flat"][e] += x * scale * np.abs(row).max() * np.abs(ke).sum(1)
+                s["far"][e] += x * abs(lse[a + i, h])
+                s["one"][e] += x
+        drawn.append(w)
+        slack.append(s)
+    return drawn, slack
+
+
+def evict(w: Sequence[float], budget: int, trigger: int, sinks: int, recent: int) -> List[int]:
+    """Numbers of the entries that stay, of a request whose entries have the weights w."""
+    n = len(w)
+    if n <= trigger:
+        return list(range(n))
+    left = sorted(range(sinks, n - recent), key=lambda e: (-w[e], e))[:budget - sinks - recent]
+    return list(range(sinks)) + sorted(left) + list(range(n - recent, n))

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 from typing import Optional, Sequence
 
 import numpy as np
@@ -59,7 +59,23 @@ class UpfKvQuery(ctypes.Structure):
                 ("window", c_int32), ("sinks", c_int32), ("softmax_scale", c_float)]
 
 
+class UpfKvEviction(ctypes.Structure):
+    _fields_ = [("num_reqs", c_int32), ("kv_len", c_void_p), ("kv_len_out", c_void_p), ("page_table", c_void_p),
+                ("page_stride", c_int64), ("max_pages", c_int32), ("page_size", c_int32), ("page_table_out", c_void_p),
+                ("page_stride_out", c_int64), ("max_pages_out", c_int32), ("budget", c_int32), ("trigger", c_int32),
+                ("sinks", c_int32), ("recent", c_int32), ("weights", c_void_p), ("weights_stride", c_int64),
+                ("weights_cols", c_int32), ("weights_out_cols", c_int32), ("weights_out", c_void_p),
+                ("weights_out_stride", c_int64), ("kept", c_void_p), ("kept_stride", c_int64)]
+
+
+class UpfRope(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("rotary_dim", c_int32), ("interleaved", c_int32), ("scaling", c_int32),
+                ("base", c_double), ("factor", c_double), ("original_len", c_double), ("low", c_double),
+                ("high", c_double), ("divisors", POINTER(c_double)), ("magnitude", c_double)]
+
+
 UPF_BF16, UPF_F16 = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "bands": 4}
 UPF_KV_FEW_TOKENS = 1024
 
 _SIGNATURES = {
@@ -96,6 +112,15 @@ _SIGNATURES = {
     "upf_kv_attend_workspace_bytes": ([POINTER(UpfKvCache), POINTER(UpfKvQuery)], c_size_t),
     "upf_kv_attend": ([c_void_p, POINTER(UpfKvCache), POINTER(UpfKvQuery), c_int32, c_void_p, c_int64, c_void_p,
                        c_int64, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
+    "upf_kv_accumulate_workspace_bytes": ([POINTER(UpfKvCache), POINTER(UpfKvQuery)], c_size_t),
+    "upf_kv_accumulate": ([c_void_p, POINTER(UpfKvCache), POINTER(UpfKvQuery), c_int32, c_void_p, c_int64, c_void_p,
+                           c_float, c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_size_t, c_void_p], c_int),
+    "upf_kv_evict_workspace_bytes": ([POINTER(UpfKvCache), POINTER(UpfKvEviction)], c_size_t),
+    "upf_kv_evict": ([c_void_p, POINTER(UpfKvCache), POINTER(UpfKvEviction), c_void_p, c_size_t, c_void_p], c_int),
+    "upf_rope_turns": ([POINTER(UpfRope), POINTER(c_uint64), POINTER(c_double)], c_int),
+    "upf_rope_apply": ([c_void_p, POINTER(UpfRope), c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                        c_int64, c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p],
+                       c_int),
     "upf_stage_name": ([c_int32], c_char_p),
     "upf_profile_enable": ([c_void_p, c_int32], c_int),
     "upf_profile_read": ([c_void_p, c_void_p, c_void_p, c_int32], c_int),
@@ -191,6 +216,36 @@ def make_kv_query(num_reqs: int, num_q_heads: int, num_q_tokens: int, kv_len: in
                    num_q_tokens, max_q_len, cu_q or None, kv_len or None, page_table or None, page_stride, max_pages,
                    page_size, window, sinks, softmax_scale)
     return x, kv
+
+
+def make_kv_eviction(num_reqs: int, kv_len: int, kv_len_out: int, page_table: int, page_stride: int, max_pages: int,
+                     page_size: int, weights: int, weights_stride: int, weights_cols: int, weights_out: int,
+                     weights_out_stride: int, weights_out_cols: int, budget: int, trigger: int, sinks: int = 0,
+                     recent: int = 0, page_table_out: int = 0, page_stride_out: int = 0, max_pages_out: int = 0,
+                     kept: int = 0, kept_stride: int = 0) -> UpfKvEviction:
+    _check_int32(page_size=page_size, budget=budget, trigger=trigger, sinks=sinks, recent=recent,
+                 weights_cols=weights_cols, weights_out_cols=weights_out_cols)
+    return UpfKvEviction(num_reqs, kv_len or None, kv_len_out or None, page_table or None, page_stride, max_pages,
+                         page_size, page_table_out or None, page_stride_out, max_pages_out, budget, trigger, sinks,
+                         recent, weights or None, weights_stride, weights_cols, weights_out_cols, weights_out or None,
+                         weights_out_stride, kept or None, kept_stride)
+
+
+def make_rope(head_dim: int, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+              factor: float = 1.0, original_len: float = 0.0, low: float = 0.0, high: float = 0.0,
+              divisors: Optional[Sequence[float]] = None, magnitude: float = 0.0):
+    """Build a upf_rope; returns (struct, keepalive) -- keep both alive during the calls."""
+    _check_int32(head_dim=head_dim, rotary_dim=rotary_dim)
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, not {scaling!r}")
+    div = None
+    if divisors is not None:
+        div = np.ascontiguousarray(divisors, dtype=np.float64)
+        if div.shape != (rotary_dim // 2,):
+            raise ValueError(f"divisors has shape {div.shape}, expected one for each of {rotary_dim // 2} pairs")
+    x = UpfRope(head_dim, rotary_dim, 1 if interleaved else 0, ROPE_SCALINGS[scaling], base, factor, original_len, low,
+                high, div.ctypes.data_as(POINTER(c_double)) if div is not None else None, magnitude)
+    return x, div
 
 
 # ------------------------------------------------------- entry points (C ABI) --
@@ -321,6 +376,50 @@ def upf_kv_attend(ctx, cache, query, dtype, q, q_row_stride, out, out_row_stride
     lib = _lib or load()
     _check(lib.upf_kv_attend(ctx, ctypes.byref(cache), ctypes.byref(query), dtype, q, q_row_stride, out,
                              out_row_stride, lse or None, ws, ws_bytes, stream or None))
+
+
+def upf_kv_accumulate_workspace_bytes(cache: UpfKvCache, query: UpfKvQuery) -> int:
+    n = load().upf_kv_accumulate_workspace_bytes(ctypes.byref(cache), ctypes.byref(query))
+    if n == 0:
+        raise UpfError(1, upf_last_error())
+    return n
+
+
+def upf_kv_accumulate(ctx, cache, query, dtype, q, q_row_stride, lse, decay, weights_in, weights_out, weights_stride,
+                      weights_cols, ws, ws_bytes, stream=0):
+    lib = _lib or load()
+    _check(lib.upf_kv_accumulate(ctx, ctypes.byref(cache), ctypes.byref(query), dtype, q, q_row_stride, lse, decay,
+                                 weights_in or None, weights_out, weights_stride, weights_cols, ws, ws_bytes,
+                                 stream or None))
+
+
+def upf_kv_evict_workspace_bytes(cache: UpfKvCache, eviction: UpfKvEviction) -> int:
+    n = load().upf_kv_evict_workspace_bytes(ctypes.byref(cache), ctypes.byref(eviction))
+    if n == 0:
+        raise UpfError(1, upf_last_error())
+    return n
+
+
+def upf_kv_evict(ctx, cache, eviction, ws, ws_bytes, stream=0):
+    lib = _lib or load()
+    _check(lib.upf_kv_evict(ctx, ctypes.byref(cache), ctypes.byref(eviction), ws, ws_bytes, stream or None))
+
+
+def upf_rope_turns(rope: UpfRope):
+    """(turns as numpy uint64 [rotary_dim / 2], magnitude)."""
+    turns = np.zeros(max(1, rope.rotary_dim // 2), dtype=np.uint64)
+    m = c_double()
+    _check(load().upf_rope_turns(ctypes.byref(rope), turns.ctypes.data_as(POINTER(c_uint64)), ctypes.byref(m)))
+    return turns, m.value
+
+
+def upf_rope_apply(ctx, rope, turns_dev, inverse, dtype, positions, num_tokens, num_tokens_dev, q, q_row_stride, q_out,
+                   q_out_row_stride, num_q_heads, k, k_row_stride, k_out, k_out_row_stride, num_kv_heads, stream=0):
+    lib = _lib or load()
+    _check(lib.upf_rope_apply(ctx, ctypes.byref(rope), turns_dev, inverse, dtype, positions, num_tokens,
+                              num_tokens_dev or None, q or None, q_row_stride, q_out or None, q_out_row_stride,
+                              num_q_heads, k or None, k_row_stride, k_out or None, k_out_row_stride, num_kv_heads,
+                              stream or None))
 
 
 NUM_STAGES = 8

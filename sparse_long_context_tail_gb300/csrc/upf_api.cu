@@ -793,6 +793,138 @@ upf_status check_query(const upf_kv_cache* c, const upf_kv_query* x, bool need_d
   return UPF_OK;
 }
 
+// No byte of `rows` rows of wa bytes from a on, sa bytes apart, is one of the rows of wb bytes from b on.
+bool rows_disjoint(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t rows) {
+  if (rows < 1) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (x + uintptr_t((rows - 1) * sa + wa) <= y || y + uintptr_t((rows - 1) * sb + wb) <= x) return true;
+  if (rows == 1 || sa != sb) return false;
+  const int64_t off = int64_t((x < y ? y - x : x - y) % uintptr_t(sa));   // of the later rows' starts behind the others'
+  return x < y ? off >= wa && off + wb <= sa : off >= wb && off + wa <= sa;
+}
+
+// scale * 2^k_exp * log2 e = mant * 2^exp with mant in [1, 2)
+void split_scale(float softmax_scale, const upf_kv_cache* c, float* mant, int32_t* exp) {
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(float(c->head_dim));
+  *mant = float(2.0 * std::frexp(double(scale) * 1.4426950408889634, exp));
+  *exp += c->k_exp - 1;
+}
+
+int log2_of(int32_t page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) s++;
+  return s;
+}
+
+// The q heads of each kv head, one kv head after another.
+void fill_heads(uint8_t* qhead, const upf_kv_query* x, int gamma) {
+  int fill[upf::kMaxHeads] = {};
+  for (int h = 0; h < x->num_q_heads; ++h) {
+    const int g = x->kv_of_q ? x->kv_of_q[h] : h / gamma;
+    qhead[g * gamma + fill[g]++] = uint8_t(h);
+  }
+}
+
+upf_status check_weights(const char* name, const void* p, int64_t stride, int64_t cols) {
+  if (!p || reinterpret_cast<uintptr_t>(p) % 4) return fail(UPF_ERR_INVALID_ARG, "%s must be set and 4-byte aligned", name);
+  if (cols < 1 || stride < cols)
+    return fail(UPF_ERR_INVALID_ARG, "%s needs 1 <= cols <= stride (got %lld, %lld)", name, (long long)cols, (long long)stride);
+  return UPF_OK;
+}
+
+upf_status check_eviction(const upf_kv_cache* c, const upf_kv_eviction* x, bool need_data) {
+  if (!x) return fail(UPF_ERR_INVALID_ARG, "eviction is NULL");
+  if (x->num_reqs < 1) return fail(UPF_ERR_INVALID_ARG, "num_reqs must be >= 1 (got %d)", x->num_reqs);
+  if (x->num_reqs > (1 << 20)) return fail(UPF_ERR_UNSUPPORTED, "num_reqs above 2^20");
+  if (x->page_size < 16 || x->page_size > 65536 || (x->page_size & (x->page_size - 1)))
+    return fail(UPF_ERR_INVALID_ARG, "page_size must be a power of two from 16 to 65536 (got %d)", x->page_size);
+  if (x->max_pages < 1 || (int64_t)x->max_pages * x->page_size > (1LL << 30))
+    return fail(UPF_ERR_INVALID_ARG, "max_pages must be >= 1 and max_pages * page_size at most 2^30");
+  if (x->budget < 1 || x->trigger < x->budget)
+    return fail(UPF_ERR_INVALID_ARG, "need 1 <= budget <= trigger (got %d, %d)", x->budget, x->trigger);
+  if (x->sinks < 0 || x->recent < 0 || (int64_t)x->sinks + x->recent > x->budget)
+    return fail(UPF_ERR_INVALID_ARG, "sinks and recent must be >= 0 and together at most budget (got %d, %d)", x->sinks, x->recent);
+  const int64_t places = std::min<int64_t>((int64_t)x->max_pages * x->page_size, x->trigger);
+  if ((places + 63) / 64 * c->num_kv_heads * x->num_reqs > INT32_MAX || places * x->num_reqs > (1LL << 36))
+    return fail(UPF_ERR_UNSUPPORTED, "too many entries may stay for one call: fewer requests or a smaller trigger");
+  if (!need_data) return UPF_OK;
+  if (!x->kv_len || !x->kv_len_out || !x->page_table)
+    return fail(UPF_ERR_INVALID_ARG, "kv_len, kv_len_out and page_table are required");
+  if (x->page_stride < x->max_pages) return fail(UPF_ERR_INVALID_ARG, "page_stride must be >= max_pages");
+  if (x->page_table_out) {
+    if (x->max_pages_out < 1 || (int64_t)x->max_pages_out * x->page_size > (1LL << 30))
+      return fail(UPF_ERR_INVALID_ARG, "max_pages_out must be >= 1 and max_pages_out * page_size at most 2^30");
+    if (x->page_stride_out < x->max_pages_out) return fail(UPF_ERR_INVALID_ARG, "page_stride_out must be >= max_pages_out");
+  }
+  upf_status st;
+  if ((st = check_weights("weights", x->weights, x->weights_stride, x->weights_cols)) != UPF_OK) return st;
+  if ((st = check_weights("weights_out", x->weights_out, x->weights_out_stride, x->weights_out_cols)) != UPF_OK) return st;
+  if (!(x->weights == x->weights_out && (x->num_reqs == 1 || x->weights_stride == x->weights_out_stride)) &&
+      !rows_disjoint(x->weights, x->weights_stride * 4, (int64_t)x->weights_cols * 4, x->weights_out,
+                     x->weights_out_stride * 4, (int64_t)x->weights_out_cols * 4, x->num_reqs))
+    return fail(UPF_ERR_INVALID_ARG, "weights_out must be weights (with its stride) or not overlap it");
+  if (x->kept && x->kept_stride < x->budget) return fail(UPF_ERR_INVALID_ARG, "kept_stride must be >= budget");
+  return UPF_OK;
+}
+
+upf::KvEvictArgs evict_args(const upf_kv_cache* c, const upf_kv_eviction* x) {
+  upf::KvEvictArgs a = {};
+  a.data = static_cast<uint8_t*>(c->data);
+  a.num_slots = c->num_slots;
+  a.H = c->num_kv_heads;
+  a.d = c->head_dim;
+  a.R = x->num_reqs;
+  a.kv_len = x->kv_len;
+  a.len_out = x->kv_len_out;
+  a.table = x->page_table;
+  a.table_out = x->page_table_out;
+  a.table_stride = x->page_stride;
+  a.table_out_stride = x->page_stride_out;
+  a.max_pages = x->max_pages;
+  a.max_pages_out = x->max_pages_out;
+  a.page_shift = log2_of(x->page_size);
+  a.budget = x->budget;
+  a.trigger = x->trigger;
+  a.sinks = x->sinks;
+  a.recent = x->recent;
+  a.w = x->weights;
+  a.w_out = x->weights_out;
+  a.w_stride = x->weights_stride;
+  a.w_out_stride = x->weights_out_stride;
+  a.w_cols = x->weights_cols;
+  a.w_out_cols = x->weights_out_cols;
+  a.kept = x->kept;
+  a.kept_stride = x->kept_stride;
+  return a;
+}
+
+upf_status check_rope(const upf_rope* x) {
+  if (!x) return fail(UPF_ERR_INVALID_ARG, "rope is NULL");
+  if (x->head_dim != 64 && x->head_dim != 128 && x->head_dim != 256)
+    return fail(UPF_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", x->head_dim);
+  if (x->rotary_dim < 2 || x->rotary_dim > x->head_dim || x->rotary_dim % 2)
+    return fail(UPF_ERR_INVALID_ARG, "rotary_dim must be even, from 2 to head_dim (got %d)", x->rotary_dim);
+  if (x->interleaved != 0 && x->interleaved != 1) return fail(UPF_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (x->scaling < UPF_ROPE_NONE || x->scaling > UPF_ROPE_BANDS)
+    return fail(UPF_ERR_INVALID_ARG, "scaling must be one of upf_rope_scaling (got %d)", x->scaling);
+  if (!(x->base > 0) || !std::isfinite(x->base)) return fail(UPF_ERR_INVALID_ARG, "base must be positive");
+  if (!(x->magnitude >= 0) || x->magnitude > 1e30 || (x->magnitude > 0 && x->magnitude < 1e-30))
+    return fail(UPF_ERR_INVALID_ARG, "magnitude must be 0, or from 1e-30 to 1e30");
+  if (x->scaling == UPF_ROPE_NONE) return UPF_OK;
+  if (!(x->factor > 0) || x->factor > 1e30 || x->factor < 1e-30) return fail(UPF_ERR_INVALID_ARG, "factor must be positive");
+  if (x->scaling < UPF_ROPE_YARN) return UPF_OK;
+  if (!(x->original_len > 0) || !std::isfinite(x->original_len))
+    return fail(UPF_ERR_INVALID_ARG, "original_len must be positive");
+  if (!(x->low > 0) || !(x->high > x->low) || !std::isfinite(x->high)) return fail(UPF_ERR_INVALID_ARG, "need 0 < low < high");
+  if (x->scaling == UPF_ROPE_YARN && x->base == 1) return fail(UPF_ERR_INVALID_ARG, "base must not be 1 with UPF_ROPE_YARN");
+  return UPF_OK;
+}
+
+double rope_magnitude(const upf_rope* x) {
+  if (x->magnitude > 0) return x->magnitude;
+  return x->scaling == UPF_ROPE_YARN && x->factor > 1 ? 0.1 * std::log(x->factor) + 1 : 1.0;
+}
+
 size_t write_ws_bytes(const upf_kv_cache* c, int32_t num_tokens) {
   return num_tokens <= UPF_KV_FEW_TOKENS ? 256 : align256(size_t(c->num_slots) * sizeof(int32_t));
 }
@@ -1271,25 +1403,201 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
   a.page_table = query->page_table;
   a.page_stride = query->page_stride;
   a.max_pages = query->max_pages;
-  a.page_shift = 0;
-  while ((1 << a.page_shift) < query->page_size) a.page_shift++;
+  a.page_shift = log2_of(query->page_size);
   a.window = query->window < (1 << 30) ? query->window : 0;   // no request has 2^30 entries behind a query
   a.sinks = query->sinks;
-  const float scale = query->softmax_scale > 0.f ? query->softmax_scale : 1.0f / std::sqrt(float(cache->head_dim));
-  a.scale_mant = float(2.0 * std::frexp(double(scale) * 1.4426950408889634, &a.scale_exp));
-  a.scale_exp += cache->k_exp - 1;
+  split_scale(query->softmax_scale, cache, &a.scale_mant, &a.scale_exp);
   a.v_mul = std::ldexp(1.f, cache->v_exp);
   a.status = ctx->status_dev;
   a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
   a.counters = ctx->status_dev + 64;
   a.ws = ws;
   a.device = ctx->device;
-  int fill[upf::kMaxHeads] = {};
-  for (int h = 0; h < a.Hq; ++h) {
-    const int g = query->kv_of_q ? query->kv_of_q[h] : h / gamma;
-    a.qhead[g * gamma + fill[g]++] = uint8_t(h);
-  }
+  fill_heads(a.qhead, query, gamma);
   UPF_LAUNCH(upf::launch_kv_attend(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv attend");
+  return UPF_OK;
+}
+
+size_t upf_kv_accumulate_workspace_bytes(const upf_kv_cache* cache, const upf_kv_query* query) {
+  if (check_cache(cache, false) != UPF_OK || check_query(cache, query, false) != UPF_OK) return 0;
+  return upf::kv_accumulate_workspace_bytes(query->num_q_heads, query->num_q_tokens, cache->head_dim);
+}
+
+upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
+                             const void* q, int64_t q_row_stride, const float* lse, float decay,
+                             const float* weights_in, float* weights_out, int64_t weights_stride,
+                             int32_t weights_cols, void* ws, size_t ws_bytes, void* stream) {
+  upf_status st;
+  if ((st = check_cache(cache, true)) != UPF_OK) return st;
+  if ((st = check_dtype(dtype)) != UPF_OK) return st;
+  if ((st = check_query(cache, query, true)) != UPF_OK) return st;
+  if (!(decay >= 0.f && decay <= 1.f)) return fail(UPF_ERR_INVALID_ARG, "decay must be in [0, 1]");
+  if ((st = check_weights("weights_out", weights_out, weights_stride, weights_cols)) != UPF_OK) return st;
+  if (weights_in && (st = check_weights("weights_in", weights_in, weights_stride, weights_cols)) != UPF_OK) return st;
+  if (weights_in && weights_in != weights_out &&
+      !rows_disjoint(weights_in, weights_stride * 4, (int64_t)weights_cols * 4, weights_out, weights_stride * 4,
+                     (int64_t)weights_cols * 4, query->num_reqs))
+    return fail(UPF_ERR_INVALID_ARG, "weights_out must be weights_in or not overlap it");
+  if (query->num_q_tokens == 0) return check_ctx(ctx);
+  if ((st = check_rows("q", q, q_row_stride, query->num_q_heads, cache->head_dim)) != UPF_OK) return st;
+  if (!lse || reinterpret_cast<uintptr_t>(lse) % 4) return fail(UPF_ERR_INVALID_ARG, "lse must be set and 4-byte aligned");
+  const size_t need = upf::kv_accumulate_workspace_bytes(query->num_q_heads, query->num_q_tokens, cache->head_dim);
+  if ((st = check_ws_bytes(ws, ws_bytes, need)) != UPF_OK) return st;
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  DeviceGuard guard(ctx->device);
+  upf::KvAccumulateArgs a;
+  a.data = static_cast<const uint8_t*>(cache->data);
+  a.num_slots = cache->num_slots;
+  a.H = cache->num_kv_heads;
+  a.d = cache->head_dim;
+  a.R = query->num_reqs;
+  a.Hq = query->num_q_heads;
+  a.gamma = query->num_q_heads / cache->num_kv_heads;
+  a.num_q = query->num_q_tokens;
+  a.max_q = query->max_q_len;
+  a.q = q;
+  a.lse = lse;
+  a.q_stride = q_row_stride;
+  a.cu_q = query->cu_q;
+  a.kv_len = query->kv_len;
+  a.page_table = query->page_table;
+  a.page_stride = query->page_stride;
+  a.max_pages = query->max_pages;
+  a.page_shift = log2_of(query->page_size);
+  a.window = query->window < (1 << 30) ? query->window : 0;   // no request has 2^30 entries behind a query
+  a.sinks = query->sinks;
+  split_scale(query->softmax_scale, cache, &a.scale_mant, &a.scale_exp);
+  a.decay = decay;
+  a.w_in = decay > 0.f ? weights_in : nullptr;
+  a.w_out = weights_out;
+  a.w_stride = weights_stride;
+  a.w_cols = weights_cols;
+  a.status = ctx->status_dev;
+  a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
+  a.ws = ws;
+  fill_heads(a.qhead, query, a.gamma);
+  UPF_LAUNCH(upf::launch_kv_accumulate(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "kv accumulate");
+  return UPF_OK;
+}
+
+size_t upf_kv_evict_workspace_bytes(const upf_kv_cache* cache, const upf_kv_eviction* eviction) {
+  if (check_cache(cache, false) != UPF_OK || check_eviction(cache, eviction, false) != UPF_OK) return 0;
+  upf::KvEvictArgs a = evict_args(cache, eviction);
+  return upf::kv_evict_workspace(a, nullptr);
+}
+
+upf_status upf_kv_evict(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_eviction* eviction, void* ws,
+                        size_t ws_bytes, void* stream) {
+  upf_status st;
+  if ((st = check_cache(cache, true)) != UPF_OK) return st;
+  if ((st = check_eviction(cache, eviction, true)) != UPF_OK) return st;
+  upf::KvEvictArgs a = evict_args(cache, eviction);
+  if ((st = check_ws_bytes(ws, ws_bytes, upf::kv_evict_workspace(a, nullptr))) != UPF_OK) return st;
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  DeviceGuard guard(ctx->device);
+  upf::kv_evict_workspace(a, ws);
+  a.status = ctx->status_dev;
+  a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
+  UPF_LAUNCH(upf::launch_kv_evict(a, static_cast<cudaStream_t>(stream)), "kv evict");
+  return UPF_OK;
+}
+
+upf_status upf_rope_turns(const upf_rope* rope, uint64_t* turns, double* magnitude) {
+  upf_status st;
+  if ((st = check_rope(rope)) != UPF_OK) return st;
+  if (!turns) return fail(UPF_ERR_INVALID_ARG, "turns is NULL");
+  const int pairs = rope->rotary_dim / 2;
+  const double n = rope->rotary_dim, s = rope->factor, two_pi = 6.283185307179586;
+  double base = rope->base, from = 0, to = 0;
+  if (rope->scaling == UPF_ROPE_BASE && pairs > 1) base *= std::pow(s, n / (n - 2));
+  if (rope->scaling == UPF_ROPE_YARN) {
+    // the pair that makes t turns in original_len positions
+    auto pair_of = [&](double t) { return n * std::log(rope->original_len / (t * two_pi)) / (2 * std::log(base)); };
+    from = std::max(std::floor(pair_of(rope->high)), 0.0);
+    to = std::min(std::ceil(pair_of(rope->low)), n - 1);
+  }
+  // all or nothing: the table is filled when every frequency is known to be one
+  uint64_t table[128];
+  for (int i = 0; i < pairs; ++i) {
+    double f = std::pow(base, -2.0 * i / n);
+    if (rope->scaling == UPF_ROPE_LINEAR) f /= s;
+    if (rope->scaling == UPF_ROPE_YARN) {
+      const double ramp = std::min(std::max((i - from) / std::max(to - from, 0.001), 0.0), 1.0);
+      f = f / s * ramp + f * (1 - ramp);
+    }
+    if (rope->scaling == UPF_ROPE_BANDS) {
+      const double keep = std::min(std::max((rope->original_len * f / two_pi - rope->low) / (rope->high - rope->low), 0.0), 1.0);
+      f = f * keep + f / s * (1 - keep);
+    }
+    if (rope->divisors) {
+      if (!(rope->divisors[i] > 0)) return fail(UPF_ERR_INVALID_ARG, "divisors[%d] must be positive", i);
+      f /= rope->divisors[i];
+    }
+    if (!(f >= 0) || !std::isfinite(f)) return fail(UPF_ERR_INVALID_ARG, "the frequency of pair %d is not finite", i);
+    const double turn = std::fmod(f / two_pi, 1.0);
+    table[i] = turn >= 1.0 - 0x1p-53 ? 0 : uint64_t(std::ldexp(turn, 64));
+  }
+  std::copy(table, table + pairs, turns);
+  if (magnitude) *magnitude = rope_magnitude(rope);
+  return UPF_OK;
+}
+
+upf_status upf_rope_apply(upf_ctx* ctx, const upf_rope* rope, const uint64_t* turns_dev, int32_t inverse,
+                          int32_t dtype, const int64_t* positions, int32_t num_tokens, const int32_t* num_tokens_dev,
+                          const void* q, int64_t q_row_stride, void* q_out, int64_t q_out_row_stride,
+                          int32_t num_q_heads, const void* k, int64_t k_row_stride, void* k_out,
+                          int64_t k_out_row_stride, int32_t num_kv_heads, void* stream) {
+  upf_status st;
+  if ((st = check_rope(rope)) != UPF_OK) return st;
+  if ((st = check_dtype(dtype)) != UPF_OK) return st;
+  if (num_tokens < 0 || num_tokens > (1 << 30)) return fail(UPF_ERR_INVALID_ARG, "num_tokens must be in [0, 2^30]");
+  if (num_q_heads < 0 || num_q_heads > 65536 || num_kv_heads < 0 || num_kv_heads > 65536)
+    return fail(UPF_ERR_INVALID_ARG, "num_q_heads and num_kv_heads must be in [0, 65536] (got %d, %d)", num_q_heads, num_kv_heads);
+  if (num_q_heads + num_kv_heads == 0) return fail(UPF_ERR_INVALID_ARG, "q or k must have heads");
+  if (num_tokens == 0) return check_ctx(ctx);
+  const int d = rope->head_dim;
+  struct Side {
+    const char* name;
+    const char* out_name;
+    const void* in;
+    void* out;
+    int64_t stride, out_stride;
+    int heads;
+  } sides[2] = {{"q", "q_out", q, q_out, q_row_stride, q_out_row_stride, num_q_heads},
+                {"k", "k_out", k, k_out, k_row_stride, k_out_row_stride, num_kv_heads}};
+  for (const Side& x : sides) {
+    if (!x.heads) continue;
+    if ((st = check_rows(x.name, x.in, x.stride, x.heads, d)) != UPF_OK) return st;
+    if ((st = check_rows(x.out_name, x.out, x.out_stride, x.heads, d)) != UPF_OK) return st;
+  }
+  for (const Side& x : sides)
+    for (const Side& y : sides) {
+      if (!x.heads || !y.heads) continue;
+      const int64_t wx = (int64_t)x.heads * d * 2, wy = (int64_t)y.heads * d * 2;
+      const bool same = &x == &y && x.out == x.in && (num_tokens == 1 || x.out_stride == x.stride);
+      if (!same && !rows_disjoint(x.out, x.out_stride * 2, wx, y.in, y.stride * 2, wy, num_tokens))
+        return fail(UPF_ERR_INVALID_ARG, "%s overlaps %s: an output is its own input, or overlaps none", x.out_name, y.name);
+      if (&x != &y && !rows_disjoint(x.out, x.out_stride * 2, wx, y.out, y.out_stride * 2, wy, num_tokens))
+        return fail(UPF_ERR_INVALID_ARG, "q_out and k_out overlap");
+    }
+  if (!positions) return fail(UPF_ERR_INVALID_ARG, "positions is NULL");
+  if (!turns_dev || !aligned16(turns_dev)) return fail(UPF_ERR_INVALID_ARG, "turns_dev must be set and 16-byte aligned");
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  DeviceGuard guard(ctx->device);
+  upf::RopeArgs a = {};
+  a.q = {q, q_out, q_row_stride, q_out_row_stride, num_q_heads};
+  a.k = {k, k_out, k_row_stride, k_out_row_stride, num_kv_heads};
+  a.turns = turns_dev;
+  a.positions = positions;
+  a.count = num_tokens_dev;
+  a.T = num_tokens;
+  a.d = d;
+  a.rotary = rope->rotary_dim;
+  a.interleaved = rope->interleaved;
+  const double m = rope_magnitude(rope);
+  a.magnitude = float(inverse ? 1.0 / m : m);
+  a.sign = inverse ? -1.f : 1.f;
+  UPF_LAUNCH(upf::launch_rope(a, dtype == UPF_F16, static_cast<cudaStream_t>(stream)), "rope");
   return UPF_OK;
 }
 

@@ -231,6 +231,80 @@ struct KvAttendArgs {
   uint8_t qhead[kMaxHeads];     // q heads of kv head g at [g*gamma, (g+1)*gamma)
 };
 
+// One of queries and keys in the rotation.
+struct RopeRows {
+  const void* in;
+  void* out;
+  int64_t in_stride, out_stride;   // elements between tokens
+  int32_t heads;
+};
+
+struct RopeArgs {
+  RopeRows q, k;
+  const uint64_t* turns;        // [rotary / 2]
+  const int64_t* positions;     // [T]
+  const int32_t* count;         // nullable
+  int32_t T, d, rotary, interleaved;
+  float magnitude, sign;
+  int32_t runs, groups, heads_each;   // set by the launcher: work of a token
+};
+
+// Accumulated attention weights of cache entries.
+struct KvAccumulateArgs {
+  const uint8_t* data;
+  int64_t num_slots;
+  int32_t H, d, R, Hq, gamma;
+  int32_t num_q, max_q;
+  const void* q;
+  const float* lse;
+  int64_t q_stride;
+  const int32_t* cu_q;          // nullable: one new token per request
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t page_stride;
+  int32_t max_pages, page_shift;
+  int32_t window, sinks;        // window 0: none
+  float scale_mant;             // as in KvAttendArgs
+  int32_t scale_exp;
+  float decay;
+  const float* w_in;            // nullable: zeros
+  float* w_out;
+  int64_t w_stride;
+  int32_t w_cols;
+  int32_t* status;
+  long long wait_limit;
+  void* ws;
+  uint8_t qhead[kMaxHeads];     // q heads of kv head g at [g*gamma, (g+1)*gamma)
+};
+
+struct KvEvictArgs {
+  uint8_t* data;
+  int64_t num_slots;
+  int32_t H, d, R;
+  const int32_t* kv_len;
+  int32_t* len_out;
+  const int32_t* table;
+  const int32_t* table_out;     // nullable: in place
+  int64_t table_stride, table_out_stride;
+  int32_t max_pages, max_pages_out, page_shift;
+  int32_t budget, trigger, sinks, recent;
+  const float* w;
+  float* w_out;
+  int64_t w_stride, w_out_stride;
+  int32_t w_cols, w_out_cols;
+  int32_t* kept;                // nullable
+  int64_t kept_stride;
+  int32_t cap;                  // most entries that a request can have afterwards
+  int32_t* status;
+  long long wait_limit;
+  // workspace
+  struct KvEvictPlan* plan;     // [R]
+  int32_t* list;                // [R][cap] old numbers of the entries
+  float* list_w;                // [R][cap] their weights
+  int32_t* read;                // [R][H][chunks of cap]: that chunk has been read
+  int32_t* ticket;
+};
+
 // Programmatic dependent launch.  Kernels launched after the first one of an
 // API call may start while their predecessor is finishing; each kernel lets its
 // own dependent start early and waits for its predecessor (full completion and
@@ -302,5 +376,11 @@ cudaError_t launch_kv_write(const KvWriteArgs& a, bool f16, cudaStream_t s);
 cudaError_t launch_kv_read(const KvReadArgs& a, bool f16, cudaStream_t s);
 cudaError_t launch_kv_attend(const KvAttendArgs& a, bool f16, cudaStream_t s);
 size_t kv_attend_workspace_bytes(int gamma, int max_q, int d);
+cudaError_t launch_rope(const RopeArgs& a, bool f16, cudaStream_t s);
+cudaError_t launch_kv_accumulate(const KvAccumulateArgs& a, bool f16, cudaStream_t s);
+size_t kv_accumulate_workspace_bytes(int Hq, int num_q, int d);
+// `a` with the sizes set; fills in the workspace pointers where ws is given.
+size_t kv_evict_workspace(KvEvictArgs& a, void* ws);
+cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s);
 
 }  // namespace upf

@@ -5,7 +5,8 @@ has the format).  It takes what the selection hands out: ``write`` stores kept
 tokens at their slot ids (``SelectOutputs.slot_out``, with ``total_kept`` as the
 device-side count), ``read`` gives entries back, and ``attend`` runs the attention
 of new tokens over ``kv_len`` entries per request (``upf_history_kv_len``), with or
-without a sliding window beside a few first entries.
+without a sliding window beside a few first entries.  ``accumulate`` adds up the attention
+weight that each entry draws, and ``evict`` keeps the heaviest of a request that has grown too long.
 """
 from __future__ import annotations
 
@@ -50,7 +51,9 @@ class QuantKVCache:
         self.device = torch.device("cuda", device or 0)
         self.storage = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if storage is None else storage
         self._cache.data = self.storage.data_ptr()
-        self._ws_bytes = {}      # of attend, by (q heads, new tokens); of write, by None: they depend on these alone
+        # of attend, by (q heads, new tokens); of write, by None; of accumulate and evict, by their names and sizes:
+        # they depend on these alone
+        self._ws_bytes = {}
         self.ctx = B.upf_create(self.device.index)
 
     def close(self) -> None:
@@ -195,3 +198,113 @@ class QuantKVCache:
                         lse.data_ptr(), ws.data_ptr(), nbytes, self._stream())
         del keep
         return AttendOutputs(out, lse)
+
+    def _table(self, name: str, t: torch.Tensor, reqs: Optional[int] = None) -> Tuple[int, int, int]:
+        """Check a page table; return its requests, pages and row stride."""
+        if t.dim() != 2 or t.dtype != torch.int32 or t.device != self.device:
+            raise ValueError(f"{name} must be an int32 [requests, pages] tensor on {self.device}")
+        R, pages = t.shape
+        row, page = t.stride()
+        if pages < 1 or (pages > 1 and page != 1):
+            raise ValueError(f"{name} needs a page at least, and the pages of a request side by side")
+        if reqs is not None and R != reqs:
+            raise ValueError(f"{name} has {R} requests, expected {reqs}")
+        return R, pages, row if R > 1 else pages
+
+    def _weights(self, name: str, t: torch.Tensor, reqs: int) -> Tuple[int, int]:
+        """Check weights of entries; return the entries of a row and the row stride."""
+        if t.dim() != 2 or t.dtype != torch.float32 or t.device != self.device or t.shape[0] != reqs:
+            raise ValueError(f"{name} must be a float32 [{reqs}, entries] tensor on {self.device}")
+        cols = t.shape[1]
+        row, col = t.stride()
+        if cols < 1 or (cols > 1 and col != 1):
+            raise ValueError(f"{name} needs an entry at least, and the entries of a request side by side")
+        return cols, row if reqs > 1 else cols
+
+    def accumulate(self, q: torch.Tensor, lse: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                   page_size: int, weights: Optional[torch.Tensor], cu_q: Optional[torch.Tensor] = None,
+                   max_q_len: int = 1, window: int = 0, sinks: int = 0, softmax_scale: Optional[float] = None,
+                   kv_of_q: Optional[Sequence[int]] = None, decay: float = 1.0,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Add to ``weights`` (float32 [R, entries]) the attention weight that each entry draws from ``q``.
+
+        ``q`` and the arguments that ``attend`` has too are what it was given, ``lse`` (float32 [tokens, H_q]) is what
+        it gave back.  Entry e of request r becomes decay * weights[r, e] + the sum of its softmax weights over the
+        new tokens and q heads that see it, for e < kv_len[r]; later entries and requests without new tokens
+        keep what ``out`` holds.  ``out``: where the sums go (None: into ``weights``); with ``weights`` None they start
+        from zero.  Returns ``out``."""
+        if q.dim() != 3:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, H_q, {self.head_dim}]")
+        N, Hq, _ = q.shape
+        qs = self._rows("q", q, Hq)
+        if lse.dtype != torch.float32 or lse.shape != (N, Hq) or not lse.is_contiguous() or lse.device != self.device:
+            raise ValueError(f"lse must be a contiguous float32 [{N}, {Hq}] tensor on {self.device}")
+        R, pages, table_row = self._table("page_table", page_table)
+        lp = self._ints("kv_len", kv_len, torch.int32, R)
+        cp = self._ints("cu_q", cu_q, torch.int32, R + 1)
+        if out is None:
+            if weights is None:
+                raise ValueError("weights or out must be given")
+            out = weights
+        cols, row = self._weights("out", out, R)
+        if weights is not None and weights is not out and self._weights("weights", weights, R) != (cols, row):
+            raise ValueError("out must have the shape and strides of weights")
+        if softmax_scale is not None:
+            softmax_scale = ctypes.c_float(softmax_scale).value
+            if not softmax_scale > 0:
+                raise ValueError("softmax_scale must be positive in fp32, or None for 1/sqrt(head_dim)")
+        query, keep = B.make_kv_query(R, Hq, N, lp, page_table.data_ptr(), table_row, pages, page_size, cp, max_q_len,
+                                      window, sinks, softmax_scale or 0.0, kv_of_q)
+        key = ("accumulate", Hq, N)
+        nbytes = self._ws_bytes.get(key)
+        if nbytes is None:
+            nbytes = self._ws_bytes[key] = B.upf_kv_accumulate_workspace_bytes(self._cache, query)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        B.upf_kv_accumulate(self.ctx, self._cache, query, _DTYPES[q.dtype], q.data_ptr(), qs, lse.data_ptr(), decay,
+                            0 if weights is None else weights.data_ptr(), out.data_ptr(), row, cols, ws.data_ptr(),
+                            nbytes, self._stream())
+        del keep
+        return out
+
+    def evict(self, weights: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, page_size: int, budget: int,
+              trigger: Optional[int] = None, sinks: int = 0, recent: int = 0,
+              page_table_out: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+              kv_len_out: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Cut requests of more than ``trigger`` entries (None: ``budget``) down to ``budget`` of them.
+
+        The first ``sinks`` and the last ``recent`` entries stay, and of the others those with the largest ``weights``
+        (float32 [R, entries]; of equal ones the earlier).  The kept ones stay in order and are moved to the first places
+        of the request's own pages, or of those of ``page_table_out`` (where the entries of uncut requests are
+        copied too).  ``kv_len`` and ``weights`` follow, in place or into ``kv_len_out`` and ``weights_out``; weights
+        from the new length up to the old one become zero.  Returns ``kept``, int32 [R, budget]: what number the entry
+        had that is number j now; -1 past the new length.  Pages that several requests share have to be
+        evicted into others."""
+        R, pages, table_row = self._table("page_table", page_table)
+        op = ostride = opages = 0
+        if page_table_out is not None:
+            _, opages, ostride = self._table("page_table_out", page_table_out, R)
+            op = page_table_out.data_ptr()
+        lp = self._ints("kv_len", kv_len, torch.int32, R)
+        lop = lp if kv_len_out is None else self._ints("kv_len_out", kv_len_out, torch.int32, R)
+        cols, row = self._weights("weights", weights, R)
+        if weights_out is None:
+            weights_out = weights
+        ocols, orow = self._weights("weights_out", weights_out, R)
+        trigger = budget if trigger is None else trigger
+        if budget < 1:
+            raise ValueError(f"budget must be at least 1 (got {budget})")
+        if kept is None:
+            kept = torch.empty((R, budget), dtype=torch.int32, device=self.device)
+        elif kept.dtype != torch.int32 or kept.shape != (R, budget) or kept.device != self.device or \
+                not kept.is_contiguous():
+            raise ValueError(f"kept must be a contiguous int32 [{R}, {budget}] tensor on {self.device}")
+        ev = B.make_kv_eviction(R, lp, lop, page_table.data_ptr(), table_row, pages, page_size, weights.data_ptr(), row,
+                                cols, weights_out.data_ptr(), orow, ocols, budget, trigger, sinks, recent, op, ostride,
+                                opages, kept.data_ptr(), budget)
+        key = ("evict", R, min(pages * page_size, trigger))
+        nbytes = self._ws_bytes.get(key)
+        if nbytes is None:
+            nbytes = self._ws_bytes[key] = B.upf_kv_evict_workspace_bytes(self._cache, ev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        B.upf_kv_evict(self.ctx, self._cache, ev, ws.data_ptr(), nbytes, self._stream())
+        return kept
