@@ -14,6 +14,7 @@
 // 64 places in a row at most, which two chunks hold.  Chunks are taken by ticket, so those that
 // a CTA waits for have been taken before by CTAs that wait for nothing to read them.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kv_layout.cuh"
@@ -33,8 +34,11 @@ namespace {
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
+constexpr int kMaxHeld = 40;          // weights of a thread that stay in shared memory (160 KB a CTA)
 constexpr int kChunk = 64;            // places of a moving CTA
-constexpr int kMoveThreads = 128;
+// Threads of a moving CTA.
+constexpr int move_threads(int d) { return d == 256 ? 256 : 128; }
+static_assert(move_threads(64) >= kChunk, "a thread for each entry of a chunk");
 
 __host__ __device__ constexpr int64_t chunks_of(int64_t places) { return (places + kChunk - 1) / kChunk; }
 
@@ -45,10 +49,29 @@ __device__ __forceinline__ int64_t slot_of(const int32_t* row, int e, int shift,
   return page >= 0 && slot < num_slots ? slot : -1;
 }
 
+// This variable in another CTA of the cluster, which has written it before a barrier of the cluster.
 __device__ __forceinline__ int32_t ld_cluster(const int32_t* mine, uint32_t rank) {
   int32_t v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::mapa_shared(ptx::smem_u32(mine), rank)) : "memory");
   return v;
+}
+__device__ __forceinline__ int2 ld_cluster2(const int32_t* mine, uint32_t rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(ptx::mapa_shared(ptx::smem_u32(mine), rank))
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
 
 // Sum over the threads before this one.
@@ -73,12 +96,16 @@ __device__ __forceinline__ int block_scan(int v, int* scratch) {
 }
 static_assert(kSelWarps == 32, "a warp scans the warps' sums");
 
-// A cluster of `ctas` CTAs a request.  A warp has a run of entries of its own, 32 at a time, the first
-// kHeld times in registers through all passes (131072 entries of a request; of more, the rest is read again).
-__global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEvictArgs a, const uint32_t ctas) {
-  constexpr int kHeld = 16, kPasses = 3;
-  __shared__ int32_t hist[kPasses][kBins];
-  __shared__ int32_t scratch[kPasses][32], found[kPasses][2], bad_here, counts[2], warp_counts[kSelWarps][2];
+// A cluster of `ctas` CTAs a request.  A warp has a run of entries of its own, 32 at a time, the first `held`
+// times in shared memory through all passes (the rest is read again).  Loops stay rolled: every instruction of a launch runs
+// a few times only, so that fetching long unrolled ones costs more than it saves (weights in
+// registers, 16 times unrolled: 1088 entries 22 us against NN).
+__global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEvictArgs a, const uint32_t ctas,
+                                                                    const int held) {
+  constexpr int kPasses = 3;
+  extern __shared__ uint32_t held_bits[];    // [held][kSelThreads]
+  __shared__ __align__(8) int32_t hist[kPasses][kBins], counts[2];
+  __shared__ int32_t scratch[kPasses][32], found[kPasses][2], bad_here, warp_counts[kSelWarps][2];
   const uint32_t rank = blockIdx.x % ctas;   // in the request's cluster
   const int r = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = rank * kSelThreads + tid, stride = ctas * kSelThreads;   // of the cluster's threads
@@ -87,6 +114,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     else __syncthreads();
   };
   auto of_cta = [&](const int32_t* mine, uint32_t c) { return ctas > 1 ? ld_cluster(mine, c) : *mine; };
+  auto of_cta2 = [&](const int32_t* mine, uint32_t c) { return ctas > 1 ? ld_cluster2(mine, c) : *reinterpret_cast<const int2*>(mine); };
   const int n = a.kv_len[r];
   const float* const w = a.w + r * a.w_stride;
   const int32_t* const row = a.table + r * a.table_stride;
@@ -110,40 +138,46 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   const float* const m = w + a.sinks;
   const int runs = cut ? (middle + 32 * kSelWarps * int(ctas) - 1) / (32 * kSelWarps * int(ctas)) : 0;   // of 32 entries, a warp
   const int from = (rank * kSelWarps + warp) * runs * 32 + lane;    // under 2^30 + 2^15
-  uint32_t held[kHeld];
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) held[k] = k < runs && from + 32 * k < middle ? __float_as_uint(m[from + 32 * k]) : 0u;
-  // f(k, bits): entry from + 32 k of the middle, where there is one (`there`)
+  uint32_t* const mine = held_bits + tid;
+#pragma unroll 4
+  for (int k = 0; k < min(runs, held); ++k)
+    if (from + 32 * k < middle) copy_async4(mine + k * kSelThreads, m + from + 32 * k);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  // f(k, bits, there): entry from + 32 k of the middle, where there is one; four at a time, so that their
+  // votes and loads do not wait for one another
   auto each = [&](auto&& f) {
+    const int whole = min(runs, held) & ~3;
+#pragma unroll 1
+    for (int k0 = 0; k0 < whole; k0 += 4)
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (k < runs) f(k, held[k], from + 32 * k < middle);
-    for (int k = kHeld; k < runs; ++k) {
+      for (int k = 0; k < 4; ++k) {
+        const bool there = from + 32 * (k0 + k) < middle;
+        f(k0 + k, there ? mine[(k0 + k) * kSelThreads] : 0u, there);
+      }
+#pragma unroll 1
+    for (int k = whole; k < runs; ++k) {
       const bool there = from + 32 * k < middle;
-      f(k, there ? __float_as_uint(m[from + 32 * k]) : 0u, there);
+      f(k, !there ? 0u : k < held ? mine[k * kSelThreads] : __float_as_uint(m[from + 32 * k]), there);
     }
   };
   // Of a weight's bits: the order of weights.  -0 is 0.
   constexpr uint32_t kMagnitude = 0x7FFFFFFFu, kInfinity = 0x7F800000u;
   auto is_bad = [&](uint32_t bits) { return (bits & kMagnitude) >= kInfinity || bits > 0x80000000u; };
   // One to the bin of each entry whose upper bits are those of `least`.
-  auto count = [&](int pass, uint32_t least) {
-    const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0, bits = pass == 0 ? 11 : 10;
+  auto count = [&](int pass, uint32_t least, int& bad) {
+    const int shift = 20 - 10 * pass, bits = pass == 0 ? 11 : 10;
     each([&](int, uint32_t raw, bool there) {
       const uint32_t key = raw & kMagnitude;
+      if (is_bad(raw)) bad |= 2;
       const bool on = there && (pass == 0 || (key >> (shift + bits)) == (least >> (shift + bits)));
-      const int digit = on ? int(key >> shift & ((1u << bits) - 1)) : -1;
-      // equal digits of a warp wait for one another: those of zeros, and of warps with one digit, go together
+      if (pass > 0 && !__any_sync(0xFFFFFFFFu, on)) return;
+      // equal digits of a warp wait for one another: those of zeros, of which there may be many, go together
       const uint32_t zeros = __ballot_sync(0xFFFFFFFFu, on && key == 0);
-      if (__all_sync(0xFFFFFFFFu, digit == __shfl_sync(0xFFFFFFFFu, digit, 0))) {
-        if (lane == 0 && on) atomicAdd(&hist[pass][digit], 32);
-      } else {
-        if (lane == 0 && zeros) atomicAdd(&hist[pass][0], __popc(zeros));
-        if (on && key != 0) atomicAdd(&hist[pass][digit], 1);
-      }
+      if (lane == 0 && zeros) atomicAdd(&hist[pass][0], __popc(zeros));
+      if (on && key != 0) atomicAdd(&hist[pass][key >> shift & ((1u << bits) - 1)], 1);
     });
   };
-  __syncthreads();
+  __syncthreads();   // the bins are empty
   if (fine) {
     const int page = 1 << a.page_shift;
     int bad = 0;
@@ -155,16 +189,14 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     if (cut) {
       for (int e = first; e < a.sinks + a.recent; e += stride)
         if (is_bad(__float_as_uint(w[e < a.sinks ? e : e + middle]))) bad |= 2;
-      each([&](int, uint32_t raw, bool) {
-        if (is_bad(raw)) bad |= 2;
-      });
-      if (want > 0) count(0, 0);
+      asm volatile("cp.async.wait_all;" ::: "memory");   // a thread reads its own copies only
+      count(0, 0, bad);
     }
     if (bad) atomicOr(&bad_here, bad);
   }
   sync();
-  int bad = 0;
-  for (uint32_t c = 0; c < ctas; ++c) bad |= of_cta(&bad_here, c);
+  // a lane or an unrolled step for each CTA: the loads from other SMs do not wait for one another
+  int bad = __reduce_or_sync(0xFFFFFFFFu, lane < ctas ? of_cta(&bad_here, lane) : 0);
   if (!fine || bad) {
     if (first == 0) set_status(a.status, !fine || (bad & 1) ? UPF_ERR_INVALID_ARG : UPF_ERR_NONFINITE);
     fine = false;
@@ -172,6 +204,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   int32_t* const list = a.list + (int64_t)r * a.cap;
   float* const list_w = a.list_w + (int64_t)r * a.cap;
   int32_t* const kept = a.kept ? a.kept + r * a.kept_stride : nullptr;
+  int32_t* const bounds = a.bounds + r * (chunks_of(a.cap) + 1);
   if (!fine || !cut) {
     const int now = fine ? left : a.table_out ? 0 : n;
     if (first == 0) {
@@ -182,6 +215,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     for (int j = first; fine && move && j < left; j += stride) {
       list[j] = j;
       list_w[j] = w[j];
+      if (j % kChunk == 0) bounds[j / kChunk] = j;
     }
     sync();   // no CTA leaves while others read its words
     return;
@@ -192,21 +226,27 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   if (want > 0) {
     least = 0;
     need = want;
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < kPasses; ++pass) {
-      const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0, bins = pass == 0 ? 2048 : 1024;
+      const int shift = 20 - 10 * pass, bins = pass == 0 ? 2048 : 1024;
       if (pass > 0) {
-        count(pass, least);
+        count(pass, least, bad);
         sync();
       }
       // thread t: bin bins - 1 - 2 t and the one below it (from the heaviest on)
       const int top = bins - 1 - 2 * tid;
+      int2 part[kMaxCluster];
+#pragma unroll
+      for (uint32_t k = 0; k < kMaxCluster; ++k) {
+        part[k] = make_int2(0, 0);
+        if (top > 0 && k < ctas) part[k] = of_cta2(&hist[pass][top - 1], k);
+      }
       int c[2] = {0, 0};
-      if (top > 0)
-        for (uint32_t k = 0; k < ctas; ++k) {
-          c[0] += of_cta(&hist[pass][top], k);
-          c[1] += of_cta(&hist[pass][top - 1], k);
-        }
+#pragma unroll
+      for (uint32_t k = 0; k < kMaxCluster; ++k) {
+        c[0] += part[k].y;
+        c[1] += part[k].x;
+      }
       const int before = block_scan(c[0] + c[1], scratch[pass]);
       if (top > 0 && before < need && before + c[0] + c[1] >= need) {
         const bool second = before + c[0] < need;
@@ -244,10 +284,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   }
   if (ctas > 1) {
     ptx::cluster_sync();
-    for (uint32_t c = 0; c < rank; ++c) {
-      above += ld_cluster(&counts[0], c);
-      equal += ld_cluster(&counts[1], c);
-    }
+    const int2 c = lane < rank ? ld_cluster2(counts, lane) : make_int2(0, 0);
+    above += __reduce_add_sync(0xFFFFFFFFu, c.x);
+    equal += __reduce_add_sync(0xFFFFFFFFu, c.y);
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // this CTA has read the others' words
   }
   // ---- the list
@@ -256,39 +295,31 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     list_w[j] = x;
     if (kept) kept[j] = e;
   };
+  // of the places' chunks: how many kept entries lie before them now
+  auto bound = [&](int j, int e) {
+    if (e % kChunk == 0 && e < left + kChunk) bounds[e / kChunk] = j;
+  };
   const uint32_t before_lane = (1u << lane) - 1;
   each([&](int k, uint32_t raw, bool there) {
     const uint32_t key = raw & kMagnitude;
     const uint32_t more = __ballot_sync(0xFFFFFFFFu, there && key > least), same = __ballot_sync(0xFFFFFFFFu, there && key == least);
-    const int rank_same = equal + __popc(same & before_lane);
-    if (there && (key > least || (key == least && rank_same < need)))
-      put(a.sinks + above + __popc(more & before_lane) + min(rank_same, need), a.sinks + from + 32 * k, __uint_as_float(raw));
+    const int rank_same = equal + __popc(same & before_lane), e = a.sinks + from + 32 * k;
+    const int j = a.sinks + above + __popc(more & before_lane) + min(rank_same, need);   // kept entries before this one
+    if (there && (key > least || (key == least && rank_same < need))) put(j, e, __uint_as_float(raw));
+    if (there) bound(j, e);
     above += __popc(more);
     equal += __popc(same);
   });
   for (int j = first; j < a.sinks + a.recent; j += stride) {
     const int e = j < a.sinks ? j : j + middle;
     put(j < a.sinks ? j : j + want, e, w[e]);
+    bound(j < a.sinks ? j : j + want, e);
   }
   if (first == 0) {
     a.plan[r] = KvEvictPlan{n, left, 1, 0};
     a.len_out[r] = left;
   }
   if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");   // no CTA leaves while others read its words
-}
-
-// First place of list[0 .. n) (ascending) whose entry is at or above e, by a warp.
-__device__ __forceinline__ int first_at(const int32_t* list, int n, int e) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;        // the answer is in [lo, hi]
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const int below = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && list[at] < e));   // of the probes
-    if (below == 0) return lo;
-    lo += (below - 1) * step + 1;
-    hi = min(hi, lo + step - 1);
-  }
-  return lo;
 }
 
 __device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
@@ -300,130 +331,125 @@ __device__ __forceinline__ void store_release(int32_t* p, int32_t v) {
   asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-
+// A CTA per chunk.  Of a record a row's keys are one run of bytes, its values eight (64 bytes apart at d = 128) and its
+// scales one and many: lanes side by side take the pieces of one entry, which lie in a few lines, while
+// the kept entries may lie anywhere.
 template <int kDim>
-__global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const KvEvictArgs a, const int64_t units) {
+__global__ void __launch_bounds__(move_threads(kDim)) kv_evict_move_kernel(const KvEvictArgs a) {
   constexpr int kRecord = kv::record_bytes(kDim), kD = kv::part_dims(kDim), kParts = kDim / kD, kC = kD / 16;
-  constexpr int kRecords = kChunk / 16, kGroups = kDim / 16;
+  constexpr int kRecords = kChunk / 16, kGroups = kDim / 16, kThreads = move_threads(kDim);
   __shared__ __align__(128) uint8_t rec[kRecords * kRecord];
   __shared__ const uint8_t* base[kChunk];   // records of the entries
   __shared__ uint8_t old_row[kChunk];       // and their rows in them
   __shared__ uint8_t* place[kRecords];      // records of the places
-  __shared__ int32_t said[4];
+  __shared__ uint32_t said;
   const int tid = threadIdx.x;
+  const uint32_t per = a.R * a.H;
   const int64_t per_head = chunks_of(a.cap);
   pdl_wait();
-  if (tid == 0) said[0] = atomicAdd(a.ticket, 1);
+  if (tid == 0) said = atomicAdd(a.ticket, 1);
   __syncthreads();
-  // ticket -> chunk first, so that tickets of one request and head ascend with the chunk
-  const uint32_t u = said[0], per = a.R * a.H;
-  if (u >= units) return;
+  // chunk first, so that tickets of one request and head ascend with the chunk
+  const uint32_t u = said;
   const int c = int(u / per), rh = int(u - c * per), r = rh / a.H, h = rh - r * a.H;
+  const int j0 = c * kChunk;
+  const int64_t at = (int64_t)r * a.cap + j0;
   const KvEvictPlan plan = a.plan[r];
+  const int mine = tid < kChunk && j0 + tid < a.cap ? a.list[at + tid] : 0;
+  const int64_t bound = r * (per_head + 1) + c;
+  const int lo = a.bounds[bound], next = a.bounds[bound + 1];
   if (!plan.move) return;
-  const int j0 = c * kChunk, places = min(kChunk, plan.left - j0);
-  const int32_t* const list = a.list + (int64_t)r * a.cap;
+  const int places = min(kChunk, plan.left - j0);
   // ---- weights: this chunk's, and this chunk's share of the places that fall free
   if (h == 0) {
     float* const w = a.w_out + r * a.w_out_stride;
-    if (tid < places) w[j0 + tid] = a.list_w[(int64_t)r * a.cap + j0 + tid];
+    if (tid < places) w[j0 + tid] = a.list_w[at + tid];
     const int end = min(plan.n, a.w_out_cols), chunks = max(1, int(chunks_of(plan.left)));
     if (c < chunks)
-      for (int64_t e = plan.left + (int64_t)c * kMoveThreads + tid; e < end; e += (int64_t)chunks * kMoveThreads) w[e] = 0.f;
+      for (int64_t e = plan.left + (int64_t)c * kThreads + tid; e < end; e += (int64_t)chunks * kThreads) w[e] = 0.f;
   }
   if (places <= 0) return;
-  int32_t* const mark = a.read + ((int64_t)r * a.H + h) * per_head;
-  // ---- nothing to do where all entries stay where they are: then list[j] = j up to here
-  const bool in_place = !a.table_out || a.table_out == a.table;
-  if (in_place && list[j0 + places - 1] == j0 + places - 1) {
-    if (tid == 0) store_release(mark + c, 1);
-    return;
-  }
+  int32_t* const mark = a.read + rh * per_head;
   auto record_of = [&](int64_t slot) { return a.data + ((slot >> 4) * a.H + h) * (int64_t)kRecord; };
   const int whole = (places + 15) / 16;
   if (tid < places) {
-    const int64_t slot = slot_of(a.table + r * a.table_stride, list[j0 + tid], a.page_shift, a.num_slots);
+    const int64_t slot = slot_of(a.table + r * a.table_stride, mine, a.page_shift, a.num_slots);
     base[tid] = record_of(slot);
     old_row[tid] = uint8_t(slot & 15);
   }
-  if (tid >= 64 && tid < 64 + whole)
-    place[tid - 64] = record_of(slot_of(a.table_out ? a.table_out + r * a.table_out_stride : a.table + r * a.table_stride,
-                                        j0 + (tid - 64) * 16, a.page_shift, a.num_slots));
-  __syncthreads();
+  if (const int k = kThreads - 1 - tid; k < whole)
+    place[k] = record_of(slot_of(a.table_out ? a.table_out + r * a.table_out_stride : a.table + r * a.table_stride, j0 + k * 16,
+                                 a.page_shift, a.num_slots));
+  // ---- nothing to move where all entries stay where they are: list[j] >= j, so that the last one tells
+  const bool in_place = !a.table_out || a.table_out == a.table;
+  if (__syncthreads_or(in_place && tid == places - 1 && mine == j0 + tid)) {
+    if (tid == 0) store_release(mark + c, 1);
+    return;
+  }
   // ---- read.  V scales are bytes, through registers; the rest goes to shared memory by itself
-  constexpr int kBytes = kChunk * kGroups / kMoveThreads;
-  const int j = tid % kChunk;                  // a thread has one entry's scales
-  const uint8_t* const mine = base[j < places ? j : 0];
-  const int mine_row = old_row[j < places ? j : 0];
+  constexpr int kBytes = kChunk * kGroups / kThreads;
   uint8_t scale[kBytes];
 #pragma unroll
-  for (int i = 0; i < kBytes; ++i) scale[i] = mine[kv::v_scale(kDim, mine_row, tid / kChunk + i * (kMoveThreads / kChunk))];
+  for (int i = 0; i < kBytes; ++i) {
+    const int k = (i * kThreads + tid) / kGroups;
+    scale[i] = k < places ? base[k][kv::v_scale(kDim, old_row[k], tid % kGroups)] : 0;
+  }
   // the record that the request ends in keeps its other rows
   if (places & 15) {
-    for (int i = tid; i < kRecord / 16; i += kMoveThreads)
+    for (int i = tid; i < kRecord / 16; i += kThreads)
       reinterpret_cast<uint4*>(rec + (whole - 1) * kRecord)[i] = reinterpret_cast<const uint4*>(place[whole - 1])[i];
     __syncthreads();
   }
   constexpr int kKeyVecs = kD / 32;    // 16-byte vectors of a row's keys in a part
 #pragma unroll
-  for (int i0 = 0; i0 < kChunk * kParts * kKeyVecs; i0 += kMoveThreads) {
-    const int i = i0 + tid, j = i / (kParts * kKeyVecs), v = i % (kParts * kKeyVecs), p = v / kKeyVecs, x = v % kKeyVecs;
-    const int at = p * 8 * kD + x * 16;
-    if (j < places) copy_async16(rec + (j >> 4) * kRecord + at + (j & 15) * (kD / 2), base[j] + at + old_row[j] * (kD / 2));
-  }
-  if (j < places) {   // rows side by side are likely to come from rows side by side
-#pragma unroll
-    for (int i = 0; i < kChunk * kParts * 8 / kMoveThreads; ++i) {
-      const int x = tid / kChunk + i * (kMoveThreads / kChunk), p = x / 8, y = x % 8;
-      auto at = [&](int s) { return 8 * kDim + p * 8 * kD + (s >> 3) * 4 * kD + y * 8 * kC + (s & 7) * kC; };
-      uint8_t* const dst = rec + (j >> 4) * kRecord + at(j & 15);
-      if constexpr (kC == 8) copy_async8(dst, mine + at(mine_row));
-      else copy_async4(dst, mine + at(mine_row));
-    }
+  for (int i0 = 0; i0 < kChunk * kParts * kKeyVecs; i0 += kThreads) {
+    const int i = i0 + tid, k = i / (kParts * kKeyVecs), v = i % (kParts * kKeyVecs), p = v / kKeyVecs, y = v % kKeyVecs;
+    const int off = p * 8 * kD + y * 16;
+    if (k < places) copy_async16(rec + (k >> 4) * kRecord + off + (k & 15) * (kD / 2), base[k] + off + old_row[k] * (kD / 2));
   }
 #pragma unroll
-  for (int i0 = 0; i0 < kChunk * kGroups / 4; i0 += kMoveThreads) {
-    const int i = i0 + tid, j = i / (kGroups / 4), x = i % (kGroups / 4) * 4;
-    if (j < places && i < kChunk * kGroups / 4)
-      copy_async4(rec + (j >> 4) * kRecord + kv::k_scale(kDim, j & 15, x), base[j] + kv::k_scale(kDim, old_row[j], x));
+  for (int i0 = 0; i0 < kChunk * kParts * 8; i0 += kThreads) {
+    const int i = i0 + tid, k = i / (kParts * 8), z = i % (kParts * 8), p = z / 8, y = z % 8;
+    auto off = [&](int s) { return 8 * kDim + p * 8 * kD + (s >> 3) * 4 * kD + y * 8 * kC + (s & 7) * kC; };
+    if (k >= places) continue;
+    uint8_t* const dst = rec + (k >> 4) * kRecord + off(k & 15);
+    if constexpr (kC == 8) copy_async8(dst, base[k] + off(old_row[k]));
+    else copy_async4(dst, base[k] + off(old_row[k]));
   }
-  // which of the kept entries lie in this chunk's places
-  if (tid < 64) {
-    const int at = first_at(list, plan.left, tid < 32 ? j0 : j0 + kChunk);
-    if ((tid & 31) == 0) said[2 + tid / 32] = at;
-  }
-  if (j < places) {
 #pragma unroll
-    for (int i = 0; i < kBytes; ++i)
-      rec[(j >> 4) * kRecord + kv::v_scale(kDim, j & 15, tid / kChunk + i * (kMoveThreads / kChunk))] = scale[i];
+  for (int i0 = 0; i0 < kChunk * kGroups / 4; i0 += kThreads) {
+    const int i = i0 + tid, k = i / (kGroups / 4), y = i % (kGroups / 4) * 4;
+    if (i < kChunk * kGroups / 4 && k < places)
+      copy_async4(rec + (k >> 4) * kRecord + kv::k_scale(kDim, k & 15, y), base[k] + kv::k_scale(kDim, old_row[k], y));
+  }
+#pragma unroll
+  for (int i = 0; i < kBytes; ++i) {
+    const int k = (i * kThreads + tid) / kGroups;
+    if (k < places) rec[(k >> 4) * kRecord + kv::v_scale(kDim, k & 15, tid % kGroups)] = scale[i];
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  // ---- say so, and wait until the entries in these places have been read
+  // ---- say that it has been read, and wait until the entries in these places have been
   __syncthreads();
   if (tid == 0) {
     store_release(mark + c, 1);
-    const int lo = said[2], hi = said[3];
+    const int hi = j0 + kChunk >= plan.n ? plan.left : next;   // entries lo .. hi - 1 of the list lie in the places
     bool ok = true;
     const long long t0 = clock64();
     for (int k = lo / kChunk; lo < hi && k <= (hi - 1) / kChunk && k < c && ok; ++k)
       while (ok && load_acquire(mark + k) == 0) ok = clock64() - t0 < a.wait_limit;
     if (!ok) set_status(a.status, UPF_ERR_TIMEOUT);
-    said[1] = ok;
+    said = ok;
   }
   __syncthreads();
-  if (!said[1]) return;
-  for (int k = 0; k < whole; ++k)
-    for (int i = tid; i < kRecord / 16; i += kMoveThreads)
-      reinterpret_cast<uint4*>(place[k])[i] = reinterpret_cast<const uint4*>(rec + k * kRecord)[i];
+  if (!said) return;
+  for (int i = tid; i < whole * (kRecord / 16); i += kThreads)
+    reinterpret_cast<uint4*>(place[i / (kRecord / 16)])[i % (kRecord / 16)] = reinterpret_cast<const uint4*>(rec)[i];
+}
+
+template <int kDim>
+cudaError_t launch_move(const KvEvictArgs& a, cudaStream_t s) {
+  const int64_t units = (int64_t)a.R * a.H * chunks_of(a.cap);   // under 2^31 (checked by the caller)
+  return launch_kernel(kv_evict_move_kernel<kDim>, dim3(unsigned(units)), move_threads(kDim), 0, s, true, a);
 }
 
 // CTAs of a request's cluster.
@@ -450,14 +476,27 @@ size_t kv_evict_workspace(KvEvictArgs& a, void* ws) {
   a.list = static_cast<int32_t*>(take(sizeof(int32_t) * a.R * a.cap));
   a.list_w = static_cast<float*>(take(sizeof(float) * a.R * a.cap));
   a.read = static_cast<int32_t*>(take(sizeof(int32_t) * a.R * a.H * chunks_of(a.cap)));
+  a.bounds = static_cast<int32_t*>(take(sizeof(int32_t) * a.R * (chunks_of(a.cap) + 1)));
   return off;
 }
 
 cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
   const int ctas = cluster_of(a);
+  const int64_t most = std::min<int64_t>((int64_t)a.max_pages << a.page_shift, a.w_cols);
+  const int held = int(std::min<int64_t>(kMaxHeld, (most + (int64_t)ctas * kSelThreads - 1) / ((int64_t)ctas * kSelThreads)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas) * unsigned(a.R));
   cfg.blockDim = kSelThreads;
+  cfg.dynamicSmemBytes = size_t(held) * kSelThreads * 4;
+  // once per device and process (and before the first capture, or in it: this launches nothing)
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << (a.device & 63);
+  if (a.device > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMaxHeld * kSelThreads * 4);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -465,13 +504,9 @@ cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_select_kernel, a, uint32_t(ctas));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_select_kernel, a, uint32_t(ctas), held);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)a.R * a.H * chunks_of(a.cap);
-  const dim3 grid = dim3(unsigned(units));
-  return a.d == 64    ? launch_kernel(kv_evict_move_kernel<64>, grid, kMoveThreads, 0, s, true, a, units)
-         : a.d == 128 ? launch_kernel(kv_evict_move_kernel<128>, grid, kMoveThreads, 0, s, true, a, units)
-                      : launch_kernel(kv_evict_move_kernel<256>, grid, kMoveThreads, 0, s, true, a, units);
+  return a.d == 64 ? launch_move<64>(a, s) : a.d == 128 ? launch_move<128>(a, s) : launch_move<256>(a, s);
 }
 
 }  // namespace upf

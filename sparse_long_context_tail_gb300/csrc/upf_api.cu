@@ -1496,6 +1496,7 @@ upf_status upf_kv_evict(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_ev
   if ((st = check_ctx(ctx)) != UPF_OK) return st;
   DeviceGuard guard(ctx->device);
   upf::kv_evict_workspace(a, ws);
+  a.device = ctx->device;
   a.status = ctx->status_dev;
   a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
   UPF_LAUNCH(upf::launch_kv_evict(a, static_cast<cudaStream_t>(stream)), "kv evict");

@@ -295,6 +295,7 @@ struct KvEvictArgs {
   int32_t* kept;                // nullable
   int64_t kept_stride;
   int32_t cap;                  // most entries that a request can have afterwards
+  int32_t device;
   int32_t* status;
   long long wait_limit;
   // workspace
@@ -302,6 +303,7 @@ struct KvEvictArgs {
   int32_t* list;                // [R][cap] old numbers of the entries
   float* list_w;                // [R][cap] their weights
   int32_t* read;                // [R][H][chunks of cap]: that chunk has been read
+  int32_t* bounds;              // [R][chunks of cap + 1]: kept entries before entry 64 c
   int32_t* ticket;
 };
 
