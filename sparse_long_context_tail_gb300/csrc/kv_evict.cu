@@ -15,6 +15,7 @@
 // a CTA waits for have been taken before by CTAs that wait for nothing to read them.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "kv_layout.cuh"
@@ -33,8 +34,9 @@ namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
-constexpr int kMaxHeld = 40;          // weights of a thread that stay in shared memory (160 KB a CTA)
+constexpr int kUnroll = 2;
+constexpr int kPasses = 3, kBins = 2048, kOwnBins = 4;   // digits; bins of a digit; of a thread
+constexpr int kMaxHeld = 9;           // fours of weights of a thread that stay in shared memory (144 KB a CTA)
 constexpr int kChunk = 64;            // places of a moving CTA
 // Threads of a moving CTA.
 constexpr int move_threads(int d) { return d == 256 ? 256 : 128; }
@@ -63,6 +65,12 @@ __device__ __forceinline__ int2 ld_cluster2(const int32_t* mine, uint32_t rank) 
                : "memory");
   return v;
 }
+__device__ __forceinline__ void add_cluster(int32_t* mine, uint32_t rank, int32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(ptx::mapa_shared(ptx::smem_u32(mine), rank)), "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 __device__ __forceinline__ void copy_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
@@ -85,27 +93,22 @@ __device__ __forceinline__ int block_scan(int v, int* scratch) {
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  const int s = scratch[lane];
-  int t = s;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, t, d);
-    if (lane >= d) t += y;
-  }
-  return __shfl_sync(0xFFFFFFFFu, t - s, warp) + x - v;
+  return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scratch[lane] : 0) + x - v;
 }
-static_assert(kSelWarps == 32, "a warp scans the warps' sums");
+static_assert(kSelWarps <= 32, "a warp adds up the warps' sums");
 
-// A cluster of `ctas` CTAs a request.  A warp has a run of entries of its own, 32 at a time, the first `held`
-// times in shared memory through all passes (the rest is read again).  Loops stay rolled: every instruction of a launch runs
-// a few times only, so that fetching long unrolled ones costs more than it saves (weights in
-// registers, 16 times unrolled: 1088 entries 22 us against NN).
+// A cluster of `ctas` CTAs a request.  A warp has a run of entries of its own, `held` times 128 of them
+// in shared memory through all passes (327680 entries of a request; of more, the rest is read again).
+// What bounds it is the instructions of few SMs: four entries a lane at a time.  Loops stay rolled: the instructions of a launch run
+// a few times only, so that fetching long unrolled ones costs more than it saves (weights in registers,
+// 16 times unrolled: 22 us for 1088 entries, 10 rolled).
 __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEvictArgs a, const uint32_t ctas,
                                                                     const int held) {
-  constexpr int kPasses = 3;
-  extern __shared__ uint32_t held_bits[];    // [held][kSelThreads]
-  __shared__ __align__(8) int32_t hist[kPasses][kBins], counts[2];
+  extern __shared__ int4 held_bits[];    // [warp][held at most][lane], and before it, in a cluster, [kPasses][kBins] sums
+  __shared__ __align__(16) int32_t hist[kPasses][kBins];     // entries of this CTA by digit
+  __shared__ __align__(8) int32_t counts[2];
   __shared__ int32_t scratch[kPasses][32], found[kPasses][2], bad_here, warp_counts[kSelWarps][2];
+  int32_t* const sums = ctas > 1 ? reinterpret_cast<int32_t*>(held_bits) : &hist[0][0];    // of all CTAs
   const uint32_t rank = blockIdx.x % ctas;   // in the request's cluster
   const int r = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = rank * kSelThreads + tid, stride = ctas * kSelThreads;   // of the cluster's threads
@@ -114,12 +117,15 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     else __syncthreads();
   };
   auto of_cta = [&](const int32_t* mine, uint32_t c) { return ctas > 1 ? ld_cluster(mine, c) : *mine; };
-  auto of_cta2 = [&](const int32_t* mine, uint32_t c) { return ctas > 1 ? ld_cluster2(mine, c) : *reinterpret_cast<const int2*>(mine); };
   const int n = a.kv_len[r];
   const float* const w = a.w + r * a.w_stride;
   const int32_t* const row = a.table + r * a.table_stride;
-  for (int i = tid; i < kPasses * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < kPasses * kBins / 4; i += kSelThreads) {
+    reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+    if (ctas > 1) reinterpret_cast<int4*>(sums)[i] = make_int4(0, 0, 0, 0);
+  }
   if (tid == 0) bad_here = 0;
+  if (ctas > 1) cluster_arrive();        // the others may add to the sums
   pdl_trigger();
   // the second launch's ticket and marks
   if (r == 0 && first == 0) *a.ticket = 0;
@@ -133,49 +139,55 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   const bool move = cut || a.table_out || a.w_out != a.w;
   if (move) fine = fine && left <= a.w_out_cols && (!a.table_out || left <= ((int64_t)a.max_pages_out << a.page_shift));
 
-  // ---- the weights between the ends
+  // ---- the weights between the ends: a warp has 128 `its` of them, a lane four side by side at a time
   const int middle = n - a.sinks - a.recent, want = a.budget - a.sinks - a.recent;
   const float* const m = w + a.sinks;
-  const int runs = cut ? (middle + 32 * kSelWarps * int(ctas) - 1) / (32 * kSelWarps * int(ctas)) : 0;   // of 32 entries, a warp
-  const int from = (rank * kSelWarps + warp) * runs * 32 + lane;    // under 2^30 + 2^15
-  uint32_t* const mine = held_bits + tid;
-#pragma unroll 4
-  for (int k = 0; k < min(runs, held); ++k)
-    if (from + 32 * k < middle) copy_async4(mine + k * kSelThreads, m + from + 32 * k);
+  const int its = cut ? (middle + 128 * kSelWarps * int(ctas) - 1) / (128 * kSelWarps * int(ctas)) : 0;
+  const int from = (rank * kSelWarps + warp) * its * 128;           // under 2^30 + 2^18
+  const int in_smem = min(its, held);
+  int4* const mine = held_bits + (ctas > 1 ? kPasses * kBins / 4 : 0) + warp * in_smem * 32;
+  for (int k = lane; k < 128 * in_smem && from + k < middle; k += 32) copy_async4(reinterpret_cast<int32_t*>(mine) + k, m + from + k);
   asm volatile("cp.async.commit_group;" ::: "memory");
-  // f(k, bits, there): entry from + 32 k of the middle, where there is one; four at a time, so that their
-  // votes and loads do not wait for one another
-  auto each = [&](auto&& f) {
-    const int whole = min(runs, held) & ~3;
-#pragma unroll 1
-    for (int k0 = 0; k0 < whole; k0 += 4)
+  // Bits of a weight as a signed number: their order is that of the weights; -0 is 0, and an entry that
+  // is not there -1, which no kept weight is or is below.
+  auto key_of = [&](int bits) { return bits == INT_MIN ? 0 : bits; };
+  auto fetch = [&](int it) {
+    int v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool there = from + 32 * (k0 + k) < middle;
-        f(k0 + k, there ? mine[(k0 + k) * kSelThreads] : 0u, there);
-      }
-#pragma unroll 1
-    for (int k = whole; k < runs; ++k) {
-      const bool there = from + 32 * k < middle;
-      f(k, !there ? 0u : k < held ? mine[k * kSelThreads] : __float_as_uint(m[from + 32 * k]), there);
+    for (int y = 0; y < 4; ++y) {
+      const int i = from + it * 128 + lane * 4 + y;
+      v[y] = i >= middle ? -1 : key_of(it < in_smem ? reinterpret_cast<const int32_t*>(mine)[it * 128 + lane * 4 + y] : __float_as_int(m[i]));
     }
+    return make_int4(v[0], v[1], v[2], v[3]);
   };
-  // Of a weight's bits: the order of weights.  -0 is 0.
-  constexpr uint32_t kMagnitude = 0x7FFFFFFFu, kInfinity = 0x7F800000u;
-  auto is_bad = [&](uint32_t bits) { return (bits & kMagnitude) >= kInfinity || bits > 0x80000000u; };
+  // f(iteration, the lane's four): entries from + 128 iteration + 4 lane ..
+  auto each = [&](auto&& f) {
+#pragma unroll kUnroll
+    for (int it = 0; it < its; ++it) f(it, it < in_smem ? mine[it * 32 + lane] : fetch(it));
+  };
   // One to the bin of each entry whose upper bits are those of `least`.
-  auto count = [&](int pass, uint32_t least, int& bad) {
-    const int shift = 20 - 10 * pass, bits = pass == 0 ? 11 : 10;
-    each([&](int, uint32_t raw, bool there) {
-      const uint32_t key = raw & kMagnitude;
-      if (is_bad(raw)) bad |= 2;
-      const bool on = there && (pass == 0 || (key >> (shift + bits)) == (least >> (shift + bits)));
-      if (pass > 0 && !__any_sync(0xFFFFFFFFu, on)) return;
-      // equal digits of a warp wait for one another: those of zeros, of which there may be many, go together
-      const uint32_t zeros = __ballot_sync(0xFFFFFFFFu, on && key == 0);
-      if (lane == 0 && zeros) atomicAdd(&hist[pass][0], __popc(zeros));
-      if (on && key != 0) atomicAdd(&hist[pass][key >> shift & ((1u << bits) - 1)], 1);
+  auto count = [&](int pass, int least) {
+    const int shift = 20 - 10 * pass, bits = pass == 0 ? 11 : 10, mask = (1 << bits) - 1;
+    int zeros = 0;     // they may be many, and equal bins wait for one another
+    each([&](int, int4 v) {
+      const int x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const bool on = pass == 0 ? x[y] >= 0 : x[y] >> (shift + bits) == least >> (shift + bits);
+        if (on && x[y] != 0) atomicAdd(&hist[pass][x[y] >> shift & mask], 1);
+        zeros += on && x[y] == 0;
+      }
     });
+    zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
+    if (lane == 0 && zeros) atomicAdd(&hist[pass][0], zeros);
+    if (ctas == 1) return;
+    // what this CTA has found goes to all CTAs' sums: few bins have entries
+    __syncthreads();
+    if (pass == 0) cluster_wait();
+#pragma unroll 1
+    for (int i = tid; i <= mask; i += kSelThreads)
+      if (const int x = hist[pass][i])
+        for (uint32_t k = 0; k < ctas; ++k) add_cluster(sums + pass * kBins + i, k, x);
   };
   __syncthreads();   // the bins are empty
   if (fine) {
@@ -186,16 +198,26 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     if (a.table_out)
       for (int p = first; p < (left + page - 1) / page; p += stride)
         bad |= slot_of(a.table_out + r * a.table_out_stride, p << a.page_shift, a.page_shift, a.num_slots) < 0;
+    auto is_bad = [&](int bits) { return key_of(bits) < 0 || bits >= 0x7F800000; };
     if (cut) {
       for (int e = first; e < a.sinks + a.recent; e += stride)
-        if (is_bad(__float_as_uint(w[e < a.sinks ? e : e + middle]))) bad |= 2;
-      asm volatile("cp.async.wait_all;" ::: "memory");   // a thread reads its own copies only
-      count(0, 0, bad);
+        if (is_bad(__float_as_int(w[e < a.sinks ? e : e + middle]))) bad |= 2;
+      // the lanes' own copies, and the others': as keys from here on
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+#pragma unroll kUnroll
+      for (int it = 0; it < its; ++it) {
+        const int4 v = fetch(it);
+        const int last = middle - (from + it * 128 + lane * 4);   // of the four, those that are there
+        if ((last > 0 && is_bad(v.x)) || (last > 1 && is_bad(v.y)) || (last > 2 && is_bad(v.z)) || (last > 3 && is_bad(v.w))) bad |= 2;
+        if (it < in_smem) mine[it * 32 + lane] = v;
+      }
+      if (want > 0) count(0, 0);
     }
     if (bad) atomicOr(&bad_here, bad);
   }
+  if (ctas > 1 && !(fine && cut && want > 0)) cluster_wait();   // as in the first count
   sync();
-  // a lane or an unrolled step for each CTA: the loads from other SMs do not wait for one another
   int bad = __reduce_or_sync(0xFFFFFFFFu, lane < ctas ? of_cta(&bad_here, lane) : 0);
   if (!fine || bad) {
     if (first == 0) set_status(a.status, !fine || (bad & 1) ? UPF_ERR_INVALID_ARG : UPF_ERR_NONFINITE);
@@ -221,8 +243,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     return;
   }
   // ---- the least kept weight
-  uint32_t least = kMagnitude;   // its bits, as far as they are known; none to be kept: above every weight
-  int need = 0;                  // how many of the entries as heavy as it are kept
+  int least = INT_MAX;     // its bits, as far as they are known; none to be kept: above every weight
+  int need = 0;            // how many of the entries as heavy as it are kept
   if (want > 0) {
     least = 0;
     need = want;
@@ -230,48 +252,50 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     for (int pass = 0; pass < kPasses; ++pass) {
       const int shift = 20 - 10 * pass, bins = pass == 0 ? 2048 : 1024;
       if (pass > 0) {
-        count(pass, least, bad);
+        count(pass, least);
         sync();
       }
-      // thread t: bin bins - 1 - 2 t and the one below it (from the heaviest on)
-      const int top = bins - 1 - 2 * tid;
-      int2 part[kMaxCluster];
+      // thread t: kOwnBins bins below bins - kOwnBins t, from the heaviest on
+      const int first_bin = bins - kOwnBins * (tid + 1);
+      int c[kOwnBins] = {}, mine_all = 0;
+      if (first_bin >= 0)
 #pragma unroll
-      for (uint32_t k = 0; k < kMaxCluster; ++k) {
-        part[k] = make_int2(0, 0);
-        if (top > 0 && k < ctas) part[k] = of_cta2(&hist[pass][top - 1], k);
-      }
-      int c[2] = {0, 0};
+        for (int y = 0; y < kOwnBins; y += 4) {
+          const int4 v = *reinterpret_cast<const int4*>(sums + pass * kBins + first_bin + y);
+          c[y] = v.x, c[y + 1] = v.y, c[y + 2] = v.z, c[y + 3] = v.w;
+          mine_all += v.x + v.y + v.z + v.w;
+        }
+      int before = block_scan(mine_all, scratch[pass]);
+      if (before < need && before + mine_all >= need) {
 #pragma unroll
-      for (uint32_t k = 0; k < kMaxCluster; ++k) {
-        c[0] += part[k].y;
-        c[1] += part[k].x;
-      }
-      const int before = block_scan(c[0] + c[1], scratch[pass]);
-      if (top > 0 && before < need && before + c[0] + c[1] >= need) {
-        const bool second = before + c[0] < need;
-        found[pass][0] = second ? top - 1 : top;
-        found[pass][1] = need - before - (second ? c[0] : 0);
+        for (int y = kOwnBins - 1; y >= 0; --y) {
+          if (before < need && before + c[y] >= need) {
+            found[pass][0] = first_bin + y;
+            found[pass][1] = need - before;
+          }
+          before += c[y];
+        }
       }
       __syncthreads();
-      least |= uint32_t(found[pass][0]) << shift;
+      least |= found[pass][0] << shift;
       need = found[pass][1];
     }
   }
   // ---- entries above it and as heavy: before this warp, before this CTA
   int above = 0, equal = 0;
-  each([&](int, uint32_t raw, bool there) {
-    const uint32_t key = raw & kMagnitude;
-    above += __popc(__ballot_sync(0xFFFFFFFFu, there && key > least));
-    equal += __popc(__ballot_sync(0xFFFFFFFFu, there && key == least));
+  each([&](int, int4 v) {
+    above += (v.x > least) + (v.y > least) + (v.z > least) + (v.w > least);
+    equal += (v.x == least) + (v.y == least) + (v.z == least) + (v.w == least);
   });
+  above = __reduce_add_sync(0xFFFFFFFFu, above);
+  equal = __reduce_add_sync(0xFFFFFFFFu, equal);
   if (lane == 0) {
     warp_counts[warp][0] = above;
     warp_counts[warp][1] = equal;
   }
   __syncthreads();
   {
-    const int x = warp_counts[lane][0], y = warp_counts[lane][1];
+    const int x = lane < kSelWarps ? warp_counts[lane][0] : 0, y = lane < kSelWarps ? warp_counts[lane][1] : 0;
     above = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
     equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0);
     if (warp == 0) {
@@ -287,7 +311,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     const int2 c = lane < rank ? ld_cluster2(counts, lane) : make_int2(0, 0);
     above += __reduce_add_sync(0xFFFFFFFFu, c.x);
     equal += __reduce_add_sync(0xFFFFFFFFu, c.y);
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // this CTA has read the others' words
+    cluster_arrive();   // this CTA has read the others' words
   }
   // ---- the list
   auto put = [&](int j, int e, float x) {
@@ -300,15 +324,26 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     if (e % kChunk == 0 && e < left + kChunk) bounds[e / kChunk] = j;
   };
   const uint32_t before_lane = (1u << lane) - 1;
-  each([&](int k, uint32_t raw, bool there) {
-    const uint32_t key = raw & kMagnitude;
-    const uint32_t more = __ballot_sync(0xFFFFFFFFu, there && key > least), same = __ballot_sync(0xFFFFFFFFu, there && key == least);
-    const int rank_same = equal + __popc(same & before_lane), e = a.sinks + from + 32 * k;
-    const int j = a.sinks + above + __popc(more & before_lane) + min(rank_same, need);   // kept entries before this one
-    if (there && (key > least || (key == least && rank_same < need))) put(j, e, __uint_as_float(raw));
-    if (there) bound(j, e);
-    above += __popc(more);
-    equal += __popc(same);
+  each([&](int it, int4 v) {
+    const int x[4] = {v.x, v.y, v.z, v.w};
+    int over = above, same = equal;        // before the lane
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, x[y] > least), s = __ballot_sync(0xFFFFFFFFu, x[y] == least);
+      over += __popc(m & before_lane);
+      same += __popc(s & before_lane);
+      above += __popc(m);
+      equal += __popc(s);
+    }
+    const int e0 = a.sinks + from + it * 128 + lane * 4;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int j = a.sinks + over + min(same, need);   // kept entries before this one
+      if (x[y] > least || (x[y] == least && same < need)) put(j, e0 + y, __int_as_float(x[y]));
+      if (x[y] >= 0) bound(j, e0 + y);
+      over += x[y] > least;
+      same += x[y] == least;
+    }
   });
   for (int j = first; j < a.sinks + a.recent; j += stride) {
     const int e = j < a.sinks ? j : j + middle;
@@ -319,7 +354,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     a.plan[r] = KvEvictPlan{n, left, 1, 0};
     a.len_out[r] = left;
   }
-  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");   // no CTA leaves while others read its words
+  if (ctas > 1) cluster_wait();   // no CTA leaves while others read its words
 }
 
 __device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
@@ -483,17 +518,17 @@ size_t kv_evict_workspace(KvEvictArgs& a, void* ws) {
 cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
   const int ctas = cluster_of(a);
   const int64_t most = std::min<int64_t>((int64_t)a.max_pages << a.page_shift, a.w_cols);
-  const int held = int(std::min<int64_t>(kMaxHeld, (most + (int64_t)ctas * kSelThreads - 1) / ((int64_t)ctas * kSelThreads)));
+  const int held = int(std::min<int64_t>(kMaxHeld, (most + 4LL * ctas * kSelThreads - 1) / (4LL * ctas * kSelThreads)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas) * unsigned(a.R));
   cfg.blockDim = kSelThreads;
-  cfg.dynamicSmemBytes = size_t(held) * kSelThreads * 4;
+  cfg.dynamicSmemBytes = size_t(held) * kSelThreads * 16 + (ctas > 1 ? kPasses * kBins * 4 : 0);
   // once per device and process (and before the first capture, or in it: this launches nothing)
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = 1ull << (a.device & 63);
   if (a.device > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxHeld * kSelThreads * 4);
+                                               kMaxHeld * kSelThreads * 16 + kPasses * kBins * 4);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
