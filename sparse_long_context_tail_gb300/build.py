@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["upf_api.cu", "score_simt.cu", "score_tc.cu", "score_pair.cu", "select.cu", "tail.cu", "compact.cu",
            "layers.cu", "select_noalloc.cu", "kv_cache.cu", "kv_attend.cu",
-           "kv_accumulate.cu", "kv_evict.cu", "rope.cu"]
+           "kv_accumulate.cu", "kv_accumulate_tc.cu", "kv_evict.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I" + INCLUDE, "-I" + CSRC,
               "--expt-relaxed-constexpr"]

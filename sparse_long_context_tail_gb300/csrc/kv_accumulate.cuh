@@ -1,0 +1,202 @@
+// What the kernels of the accumulated attention weights share: requests and what their rows see of them,
+// how work is dealt out over the requests, and what turns a row's products into weights.
+#pragma once
+
+#include <cfloat>
+
+#include "kv_layout.cuh"
+#include "sm100_ptx.cuh"
+#include "upf_internal.cuh"
+
+namespace upf {
+namespace acc {
+
+struct Request {
+  int q0, q_len, n;     // first row, rows, entries; no rows: nothing to do
+};
+
+__device__ __forceinline__ Request load_request(const KvAccumulateArgs& a, int r) {
+  Request x{r, 1, a.kv_len[r]};
+  bool ok = x.n >= 0 && x.n <= ((int64_t)a.max_pages << a.page_shift) && x.n <= a.w_cols;
+  if (a.cu_q) {
+    x.q0 = a.cu_q[r];
+    const int q1 = a.cu_q[r + 1];
+    ok = ok && x.q0 >= 0 && q1 >= x.q0 && q1 <= a.num_q && q1 - x.q0 <= a.max_q;
+    x.q_len = q1 - x.q0;
+  }
+  if (!ok) {
+    set_status(a.status, UPF_ERR_INVALID_ARG);
+    x.q0 = x.q_len = x.n = 0;
+  }
+  return x;
+}
+
+template <int kDim>
+struct Shape {
+  static constexpr int kPart = kDim >= 128 ? 128 : kDim;
+  static constexpr int kParts = kDim / kPart;
+  static constexpr int kPartWords = kPart / 32;            // words of codes of a lane's quarter row of a part
+  static constexpr int kWords = kDim / 32;
+  static constexpr int kSteps = kDim / 16;
+  static constexpr int kRecord = kv::record_bytes(kDim);
+};
+
+// What of a request's entries its rows see.
+struct View {
+  int base;        // position of query 0
+  int w0, sinks;   // first entry inside some row's window; first entries that stay visible before it
+};
+__device__ __forceinline__ View view_of(const KvAccumulateArgs& a, const Request& x) {
+  View v;
+  v.base = x.n - x.q_len;
+  v.w0 = a.window ? int(max((int64_t)0, (int64_t)v.base - a.window + 1)) : 0;
+  v.sinks = min(a.sinks, v.w0);
+  return v;
+}
+
+// Keys of head 0 of the 16 entries from e on, or null if no row sees one of them or their page is bad.
+template <int kDim>
+__device__ __forceinline__ const uint8_t* record_at(const KvAccumulateArgs& a, int r, const Request& x, const View& v, int e) {
+  if (e >= x.n || (e + 15 < v.w0 && e >= v.sinks)) return nullptr;
+  const int page = a.page_table[(int64_t)r * a.page_stride + (e >> a.page_shift)];
+  const int64_t b = ((int64_t)page << (a.page_shift - 4)) + ((e & ((1 << a.page_shift) - 1)) >> 4);
+  if (page >= 0 && b < (a.num_slots >> 4)) return a.data + b * a.H * Shape<kDim>::kRecord;
+  set_status(a.status, UPF_ERR_INVALID_ARG);
+  return nullptr;
+}
+
+// Does query i of the request (-1: none) see entry e?
+__device__ __forceinline__ bool sees(const KvAccumulateArgs& a, const View& v, int i, int e) {
+  const int p = v.base + i;
+  return i >= 0 && e <= p && (a.window == 0 || p - e < a.window || e < a.sinks);
+}
+
+// Does every row see all entries [e0, e1)?
+__device__ __forceinline__ bool all_seen(const KvAccumulateArgs& a, const Request& x, const View& v, int e0, int e1) {
+  return e1 <= v.base + 1 && (a.window == 0 || e0 > v.base + x.q_len - 1 - a.window);
+}
+
+// ------------------------------------------------------------- dealing out --
+// Units of all requests in order, count(request) of each; thread i has looked at requests [i * per, (i + 1) * per).
+
+struct Deal {
+  long long total;
+  int per;
+};
+template <int kThreads>
+struct Starts {
+  long long starts[kThreads + 1];        // units before each thread's requests
+  long long warp_sums[kThreads / 32];
+};
+
+template <int kThreads, typename Count>
+__device__ __forceinline__ Deal deal_out(const KvAccumulateArgs& a, Starts<kThreads>& s, Count&& count) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Deal d;
+  d.per = (a.R + kThreads - 1) / kThreads;
+  long long sum = 0;
+  for (int j = 0; j < d.per; ++j) {
+    const int r = threadIdx.x * d.per + j;
+    if (r < a.R) sum += count(load_request(a, r));
+  }
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, k);
+    if (lane >= k) sum += y;
+  }
+  if (lane == 31) s.warp_sums[warp] = sum;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) sum += s.warp_sums[w];
+  s.starts[threadIdx.x + 1] = sum;
+  if (threadIdx.x == 0) s.starts[0] = 0;
+  __syncthreads();
+  d.total = s.starts[kThreads];
+  return d;
+}
+
+// The request that unit u belongs to, and the units before it; false if the lengths have changed under the call.
+template <int kThreads, typename Count>
+__device__ __forceinline__ bool find_request(const KvAccumulateArgs& a, const Starts<kThreads>& s, const Deal& d, long long u, int& r,
+                                             Request& x, long long& first, Count&& count) {
+  // the thread whose run of requests holds it, then along that run
+  int lo = 0, hi = kThreads;      // starts[lo] <= u < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.starts[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  first = s.starts[lo];
+  for (r = lo * d.per; r < a.R; ++r) {
+    x = load_request(a, r);
+    const int mine = count(x);
+    if (u < first + mine) return true;
+    first += mine;
+  }
+  return false;
+}
+
+// Entries behind the window, where no unit is, fade too: [from, to) of each request, which range() gives.
+template <int kThreads, typename Range>
+__device__ __forceinline__ void fade_unseen(const KvAccumulateArgs& a, Range&& range) {
+  if (!a.window || (a.w_in == a.w_out && a.decay == 1.f)) return;
+  for (int r = 0; r < a.R; ++r) {
+    const Request x = load_request(a, r);
+    if (!x.q_len) continue;
+    int from, to;
+    range(x, from, to);
+    for (int64_t e = from + (int64_t)blockIdx.x * kThreads + threadIdx.x; e < to; e += (int64_t)gridDim.x * kThreads) {
+      const int64_t at = r * a.w_stride + e;
+      a.w_out[at] = a.w_in ? a.decay * a.w_in[at] : 0.f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- rows --
+
+__device__ __forceinline__ __half2 as_half2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(as_half2(a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// A row's logit factor 2^exp * mantissa of the scale, within fp32.
+__device__ __forceinline__ float factor_of(const KvAccumulateArgs& a, int exp) {
+  if (exp > 127) return FLT_MAX;
+  return fminf(a.scale_mant * __uint_as_float(uint32_t(max(exp, -126) + 127) << 23), FLT_MAX);
+}
+
+// A weight is 2^(s f - hi) lift, with s the product of the key and of the row divided by a power of two
+// (times `down`).  hi and what its rounding leaves (in `lift`) are lse * log2 e: the rounding of one number would be
+// that of every weight of the row.
+struct RowConstants {
+  bool on, bad;      // does it count; is it not finite
+  int e;             // the power of two
+  float down, f, hi, lift;
+};
+
+// `amax`: bits of the row's largest magnitude in fp32 (at and above those of infinity if it has a NaN or an infinity).
+__device__ __forceinline__ RowConstants row_constants(const KvAccumulateArgs& a, bool real, uint32_t amax, float lse) {
+  constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.9259629911266174e-8f;   // their sum is log2 e to 2^-49
+  RowConstants c;
+  c.bad = real && (amax >= 0x7F800000u || !(lse < INFINITY));
+  c.on = real && !c.bad && lse > -INFINITY;
+  c.e = !c.on || amax == 0 ? 0 : max(-126, min(int(amax >> 23) - 127, 126));
+  c.down = __uint_as_float(uint32_t(127 - c.e) << 23);
+  c.f = factor_of(a, a.scale_exp + c.e);
+  c.hi = lse * kLog2e;
+  c.lift = ptx::ex2_approx(-(__fmaf_rn(lse, kLog2e, -c.hi) + lse * kLog2eLow));
+  return c;
+}
+
+}  // namespace acc
+
+cudaError_t launch_kv_accumulate_tc(const KvAccumulateArgs& a, bool f16, cudaStream_t s);
+size_t kv_accumulate_tc_workspace_bytes(int H, int gamma, int num_q, int R, int d);
+
+}  // namespace upf

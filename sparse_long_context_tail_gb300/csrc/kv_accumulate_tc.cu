@@ -1,0 +1,467 @@
+// Attention weight that cache entries have drawn, for more than eight rows a kv head: prompts' last queries, drafted
+// tokens, wide groups of q heads.
+//
+// Per 128 entries and kv head the logits are one tcgen05 product, S = K Q^T: the keys are operand A, the rows operand B,
+// an entry is a TMEM lane, so that an entry's sum over the rows is a thread's sum along its lane.  Codes times
+// scales go to TMEM straight from the registers that worked them out (tcgen05.st), as f16; from shared memory both
+// operands of an M128 N128 product would take more of its bandwidth than there is.  The rows
+// are made ready once by a launch of their own, in the swizzled layout that the product reads, and copied in bulk.
+//
+// What bounds it: with n rows a kv head every entry and head costs 2 d n flop, n exponentials and one pass over
+// its codes.  At d = 128 and 128 rows the three units need about the same time.
+//
+// A CTA (one an SM) has a run of 128-entry blocks of one request after another.  For each head and chunk of rows it goes
+// through its blocks, so that rows are copied once a run; the entries' sums wait in shared memory.  Warps: eight work
+// out keys (four for every other block), eight add up weights (a half of the columns each), one issues
+// the products, one the copies.
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+
+#include "kv_accumulate.cuh"
+#include "sm100_ptx.cuh"
+
+namespace upf {
+
+namespace {
+
+using namespace acc;
+
+constexpr int kBlock = 128;                    // entries of a product
+constexpr int kRows = 128;                     // most rows of a product
+constexpr int kRun = 16;                       // blocks whose sums are in shared memory at once
+constexpr int kKeyWarps = 8, kSumWarps = 8, kMmaWarp = 16, kTcWarps = 18 /* the last one copies */, kTcThreads = 32 * kTcWarps;
+constexpr uint32_t kSlots = 2;                 // of keys, of rows, of sums
+
+// The rows of all requests as operand B.  Those of request r and kv head h, padded to a multiple of 16, begin at row
+// first_row(r) + h * padded; of d dims every 64 are a slab of their own, 128 bytes a row.
+__host__ __device__ constexpr int pad16(int rows) { return (rows + 15) / 16 * 16; }
+__device__ __forceinline__ int64_t first_row(const KvAccumulateArgs& a, int q0, int r) {
+  return (int64_t)a.H * 16 * (((int64_t)a.gamma * q0) / 16 + r);
+}
+struct RowsMem {
+  uint8_t* q;        // [rows][d] f16: per request and head [slab][row][64 dims], 16-byte pieces swizzled
+  float* f;          // [rows] logit factors
+  float* lse;        // [rows] -lse * log2 e
+  float* lift;       // [rows] 2^ what that was rounded by
+  int32_t* i;        // [rows] queries; -1: none
+  int64_t rows;
+};
+__host__ __device__ inline RowsMem rows_mem(void* ws, int H, int gamma, int num_q, int R, int d) {
+  RowsMem m;
+  m.rows = (int64_t)H * 16 * ((int64_t)gamma * num_q / 16 + R + 1);
+  m.q = static_cast<uint8_t*>(ws);
+  m.f = reinterpret_cast<float*>(m.q + m.rows * d * 2);
+  m.lse = m.f + m.rows;
+  m.lift = m.lse + m.rows;
+  m.i = reinterpret_cast<int32_t*>(m.lift + m.rows);
+  return m;
+}
+
+// A warp per row of a request and kv head, the padding's among them.
+template <typename T, int kDim>
+__global__ void __launch_bounds__(256) kv_accumulate_rows_kernel(const KvAccumulateArgs a, const RowsMem m) {
+  constexpr const T* kT = nullptr;
+  constexpr int kEach = kDim / 32;             // dims of a lane
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.y; r < a.R; r += gridDim.y) {
+    const Request x = load_request(a, r);
+    const int rows = x.q_len * a.gamma, padded = pad16(rows);
+    for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < (int64_t)a.H * padded; w += (int64_t)gridDim.x * 8) {
+      const int h = int(w / padded), rho = int(w - (int64_t)h * padded);
+      const int64_t region = first_row(a, x.q0, r) + (int64_t)h * padded;
+      const bool real = rho < rows;
+      const int i = real ? rho / a.gamma : 0, head = a.qhead[h * a.gamma + (real ? rho - i * a.gamma : 0)];
+      const int64_t at = x.q0 + i;
+      uint32_t q[kEach / 2];
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < kEach / 2; ++k) {
+        q[k] = real ? reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + at * a.q_stride + head * kDim)[lane * (kEach / 2) + k] : 0u;
+        top = kv::max_abs2(top, q[k], kT);
+      }
+      const float2 tops = kv::pair_to_float2(top, kT);
+      const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(fabsf(tops.x)), __float_as_uint(fabsf(tops.y))));
+      const RowConstants c = row_constants(a, real, amax, real ? a.lse[at * a.Hq + head] : -INFINITY);
+      if (c.bad && lane == 0) set_status(a.status, UPF_ERR_NONFINITE);
+      uint32_t v[kEach / 2];
+#pragma unroll
+      for (int k = 0; k < kEach / 2; ++k) {
+        const float2 y = kv::pair_to_float2(q[k], kT);
+        v[k] = c.on ? pack_f16(y.x * c.down, y.y * c.down) : 0u;
+      }
+      // dims lane * kEach ..: slab, and the byte within the row's 128
+      const int dim = lane * kEach, slab = dim / 64, byte = dim % 64 * 2;
+      uint8_t* const dst = m.q + (region * kDim + ((int64_t)slab * padded + rho) * 64) * 2 + ((byte >> 4 ^ rho & 7) << 4) + (byte & 15);
+      if constexpr (kEach == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+      else if constexpr (kEach == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = v[0];
+      if (lane == 0) {
+        m.f[region + rho] = c.on ? c.f : 0.f;
+        m.lse[region + rho] = c.on ? -c.hi : -INFINITY;
+        m.lift[region + rho] = c.on ? c.lift : 0.f;
+        m.i[region + rho] = c.on ? i : -1;
+      }
+    }
+  }
+}
+
+template <int kDim>
+struct TcShape {
+  static constexpr int kSlabs = kDim / 64;
+  static constexpr int kKeyCols = kDim / 2;                    // TMEM columns of a block's keys
+  static constexpr int kRowBytes = kRows * kDim * 2;           // of a chunk of rows
+  static constexpr int kConstBytes = kRows * 16;
+  static constexpr int kSumCol = kSlots * kKeyCols;            // first TMEM column of the sums
+  static_assert(kSumCol + kSlots * kRows <= 512, "tensor memory");
+  // rows (1024-byte aligned), their constants, the entries' sums (a column half each)
+  static constexpr int kConstAt = kSlots * kRowBytes, kSumAt = kConstAt + kSlots * kConstBytes;
+  static constexpr int kSmem = kSumAt + 2 * kRun * kBlock * 4 + 1024;
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 8 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, f16 inputs, fp32 accumulation.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// As ptx::idesc_bf16_f32 with f16 operands.
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t n) { return (1u << 4) | (n >> 3 << 17) | (kBlock >> 4 << 24); }
+
+// A request's blocks that some row sees: [0, sink_b) and [lo_b, ..).
+struct Blocks {
+  int sink_b, lo_b, count;
+  __device__ __forceinline__ int entry(int b) const { return (b < sink_b ? b : b - sink_b + lo_b) * kBlock; }
+};
+__device__ __forceinline__ Blocks blocks_of(const KvAccumulateArgs& a, const Request& x) {
+  const View v = view_of(a, x);
+  Blocks b;
+  b.lo_b = v.w0 / kBlock;
+  b.sink_b = min((v.sinks + kBlock - 1) / kBlock, b.lo_b);
+  b.count = x.q_len ? b.sink_b + (x.n + kBlock - 1) / kBlock - b.lo_b : 0;
+  return b;
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const KvAccumulateArgs a, const RowsMem m) {
+  using S = Shape<kDim>;
+  using C = TcShape<kDim>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (1024 - (ptx::smem_u32(smem_raw) & 1023)) % 1024;
+  float* const sums = reinterpret_cast<float*>(smem + C::kSumAt);      // [2][kRun * kBlock]
+  __shared__ Starts<kTcThreads> starts;
+  __shared__ __align__(8) uint64_t bars[5 * kSlots];
+  __shared__ uint32_t tmem_word;
+  __shared__ int failed;
+  __shared__ uint32_t row_copies, products;      // begun so far
+  __shared__ const uint8_t* records[kRun][kBlock / 16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto keys_full = [&](uint32_t s) { return bar0 + 8 * s; };
+  auto keys_free = [&](uint32_t s) { return bar0 + 8 * (kSlots + s); };
+  auto rows_full = [&](uint32_t s) { return bar0 + 8 * (2 * kSlots + s); };
+  auto rows_free = [&](uint32_t s) { return bar0 + 8 * (3 * kSlots + s); };
+  auto sums_full = [&](uint32_t s) { return bar0 + 8 * (4 * kSlots + s); };
+  // sums_free: an entry sum slot is read by all sum warps
+  __shared__ __align__(8) uint64_t bars_free[kSlots];
+  auto sums_free = [&](uint32_t s) { return ptx::smem_u32(bars_free) + 8 * s; };
+  if (tid == 0) {
+    for (uint32_t s = 0; s < kSlots; ++s) {
+      ptx::mbar_init(keys_full(s), 4);
+      ptx::mbar_init(keys_free(s), 1);
+      ptx::mbar_init(rows_full(s), 1);
+      ptx::mbar_init(rows_free(s), 1 + kSumWarps);
+      ptx::mbar_init(sums_full(s), 1);
+      ptx::mbar_init(sums_free(s), kSumWarps);
+    }
+    failed = 0;
+    row_copies = products = 0;
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_word), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::fence_barrier_init();
+  const Deal deal = deal_out<kTcThreads>(a, starts, [&](const Request& x) { return blocks_of(a, x).count; });   // barriers inside
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_word;
+  fade_unseen<kTcThreads>(a, [&](const Request& x, int& from, int& to) {
+    const Blocks b = blocks_of(a, x);
+    from = b.sink_b * kBlock;
+    to = b.lo_b * kBlock;
+  });
+  const long long share = (deal.total + gridDim.x - 1) / gridDim.x;
+  long long u = blockIdx.x * share;
+  const long long end = min(u + share, deal.total);
+  // phases of the rings, each role its own
+  uint32_t key_n = 0, row_n = 0, sum_n = 0;      // blocks, chunks, products so far
+  auto wait = [&](uint32_t bar, uint32_t phase) {
+    if (*reinterpret_cast<volatile int*>(&failed)) return false;
+    if (ptx::mbar_wait(bar, phase, a.wait_limit)) return true;
+    *reinterpret_cast<volatile int*>(&failed) = 1;
+    set_status(a.status, UPF_ERR_TIMEOUT);
+    return false;
+  };
+  bool rows_waited = false;
+  int r = 0;
+  Request x{};
+  long long first = 0;
+  if (u < end && !find_request<kTcThreads>(a, starts, deal, u, r, x, first, [&](const Request& y) { return blocks_of(a, y).count; })) u = end;
+  while (u < end) {
+    const Blocks blocks = blocks_of(a, x);
+    const View view = view_of(a, x);
+    const int begin = int(u - first), stop = int(min(end - first, (long long)blocks.count));
+    const int rows = x.q_len * a.gamma, padded = pad16(rows), chunks = (padded + kRows - 1) / kRows;
+    const int64_t region = first_row(a, x.q0, r);
+    for (int run0 = begin; run0 < stop; run0 += kRun) {
+      const int run = min(kRun, stop - run0);
+      for (int i = tid; i < run * (kBlock / 16); i += kTcThreads)
+        records[i / (kBlock / 16)][i % (kBlock / 16)] = record_at<kDim>(a, r, x, view, blocks.entry(run0 + i / (kBlock / 16)) + i % (kBlock / 16) * 16);
+      for (int i = tid; i < 2 * kRun * kBlock; i += kTcThreads) sums[i] = 0.f;
+      __syncthreads();
+      if (warp < kKeyWarps) {
+        // ---- keys: this warp's 32 entries of every other block, an entry a lane
+        const int quarter = warp & 3;
+        const uint32_t slot = warp >> 2;
+        uint4 codes[kDim / 32];
+        uint32_t scales[kDim / 64];          // four groups each
+        auto fetch = [&](int h, int b) {
+          const int row = (lane & 15), tile = quarter * 2 + (lane >> 4);
+          const uint8_t* const rec = records[b][tile];
+#pragma unroll
+          for (int k = 0; k < kDim / 32; ++k) codes[k] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < kDim / 64; ++k) scales[k] = 0;
+          if (!rec) return;
+          const uint8_t* const src = rec + (int64_t)h * S::kRecord;
+#pragma unroll
+          for (int k = 0; k < kDim / 32; ++k)        // 32 dims
+            codes[k] = __ldg(reinterpret_cast<const uint4*>(src + k / (S::kPart / 32) * (8 * S::kPart) + row * (S::kPart / 2)) + k % (S::kPart / 32));
+#pragma unroll
+          for (int k = 0; k < kDim / 64; ++k)
+            scales[k] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kDim + row * (kDim / 16)) + k);
+        };
+        const int total = a.H * chunks * run;        // products of the run; the i-th is block i % run
+        // the group's products: those whose number from the kernel's start is its slot modulo two
+        int i = int((slot - key_n) & 1);
+        if (i < total) fetch(i / run / chunks, i % run);
+        for (; i < total; i += 2) {
+          const uint32_t n = key_n + i;
+          if (!__all_sync(0xFFFFFFFFu, wait(keys_free(slot), (n / kSlots & 1) ^ 1))) break;   // all lanes or none
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int half = 0; half < kDim / 64; ++half) {    // 64 dims: 32 columns
+            uint32_t v[32];
+            const uint32_t s01 = kv::e4m3x2_to_f16x2(uint16_t(scales[half])), s23 = kv::e4m3x2_to_f16x2(uint16_t(scales[half] >> 16));
+            const __half2 s[4] = {__low2half2(as_half2(s01)), __high2half2(as_half2(s01)), __low2half2(as_half2(s23)), __high2half2(as_half2(s23))};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint4 c = codes[half * 2 + k];
+              const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint32_t hh[4];
+                kv::e2m1x8_to_f16(w[y], hh);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[k * 16 + y * 4 + z] = hmul2(hh[z], s[k * 2 + y / 2]);
+              }
+            }
+            tmem_st32(tmem + (uint32_t(quarter * 32) << 16) + slot * C::kKeyCols + half * 32, v);
+          }
+          if (i + 2 < total) fetch((i + 2) / run / chunks, (i + 2) % run);
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(keys_full(slot));
+        }
+      } else if (warp < kKeyWarps + kSumWarps) {
+        // ---- weights: this warp's 32 entries, half of the columns
+        const int quarter = warp & 3, half = (warp - kKeyWarps) >> 2;
+        uint32_t rn = row_n, sn = sum_n;
+        bool ok = true;
+        for (int hc = 0; hc < a.H * chunks && ok; ++hc, ++rn) {
+          const int c = hc % chunks, cols = min(kRows, padded - c * kRows);
+          // columns [from, to) of the chunk, in steps of 8
+          const int mid = (cols / 2 + 7) / 8 * 8, from = half ? mid : 0, to = half ? cols : mid;
+          const uint32_t rs = rn % kSlots;
+          ok = __all_sync(0xFFFFFFFFu, wait(rows_full(rs), rn / kSlots & 1));
+          const float* const cf = reinterpret_cast<const float*>(smem + C::kConstAt + rs * C::kConstBytes);
+          for (int b = 0; b < run && ok; ++b, ++sn) {
+            const uint32_t ss = sn % kSlots;
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), sn / kSlots & 1)))) break;
+            ptx::tc_fence_after();
+            const int e0 = blocks.entry(run0 + b), e = e0 + quarter * 32 + lane;
+            const bool whole = all_seen(a, x, view, e0, e0 + kBlock);
+            const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + C::kSumCol + ss * kRows;
+            float total = 0.f;
+            for (int j = from; j < to; j += 8) {
+              float v[8];
+              tmem_ld8(at + j, v);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 8; k += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(cf + j + k), l = *reinterpret_cast<const float4*>(cf + kRows + j + k);
+                const float4 g = *reinterpret_cast<const float4*>(cf + 2 * kRows + j + k);
+                float w0 = ptx::ex2_approx(__fmaf_rn(v[k], f.x, l.x)), w1 = ptx::ex2_approx(__fmaf_rn(v[k + 1], f.y, l.y));
+                float w2 = ptx::ex2_approx(__fmaf_rn(v[k + 2], f.z, l.z)), w3 = ptx::ex2_approx(__fmaf_rn(v[k + 3], f.w, l.w));
+                if (!whole) {
+                  const int4 i = *reinterpret_cast<const int4*>(cf + 3 * kRows + j + k);
+                  w0 = sees(a, view, i.x, e) ? w0 : 0.f;
+                  w1 = sees(a, view, i.y, e) ? w1 : 0.f;
+                  w2 = sees(a, view, i.z, e) ? w2 : 0.f;
+                  w3 = sees(a, view, i.w, e) ? w3 : 0.f;
+                }
+                total = __fmaf_rn(w0, g.x, __fmaf_rn(w1, g.y, __fmaf_rn(w2, g.z, __fmaf_rn(w3, g.w, total))));
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sums_free(ss));
+            sums[half * kRun * kBlock + b * kBlock + quarter * 32 + lane] += total;
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(rows_free(rs));
+        }
+      } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+          uint32_t kn = key_n, rn = row_n, sn = sum_n;
+          bool ok = true;
+          for (int hc = 0; hc < a.H * chunks && ok; ++hc, ++rn) {
+            const int c = hc % chunks, cols = min(kRows, padded - c * kRows);
+            const uint32_t rs = rn % kSlots, idesc = idesc_f16(cols);
+            if (!(ok = wait(rows_full(rs), rn / kSlots & 1))) break;
+            for (int b = 0; b < run; ++b, ++kn, ++sn) {
+              const uint32_t ks = kn % kSlots, ss = sn % kSlots;
+              if (!(ok = wait(keys_full(ks), kn / kSlots & 1) && wait(sums_free(ss), (sn / kSlots & 1) ^ 1))) break;
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < kDim / 16; ++k)
+                mma_f16_ts(tmem + C::kSumCol + ss * kRows, tmem + ks * C::kKeyCols + k * 8,
+                           ptx::sdesc_kmajor_sw128(ptx::smem_u32(smem + rs * C::kRowBytes) + k / 4 * (cols * 128) + k % 4 * 32), idesc, k > 0);
+              ptx::mma_commit(keys_free(ks));
+              ptx::mma_commit(sums_full(ss));
+              products = sn + 1;
+              if (b == run - 1) ptx::mma_commit(rows_free(rs));
+            }
+          }
+        }
+        __syncwarp();
+      } else {
+        // ---- copies of the rows and their constants
+        if (lane == 0) {
+          if (!rows_waited) pdl_wait();
+          rows_waited = true;
+          for (int hc = 0; hc < a.H * chunks; ++hc) {
+            const uint32_t n = row_n + hc, rs = n % kSlots;
+            const int h = hc / chunks, c = hc - h * chunks, cols = min(kRows, padded - c * kRows);
+            if (!wait(rows_free(rs), (n / kSlots & 1) ^ 1)) break;
+            const int64_t row0 = region + (int64_t)h * padded;
+            ptx::mbar_arrive_expect_tx(rows_full(rs), cols * (kDim * 2 + 16));
+            for (int s = 0; s < C::kSlabs; ++s)
+              ptx::bulk_load(ptx::smem_u32(smem + rs * C::kRowBytes) + s * cols * 128,
+                             m.q + (row0 * kDim + ((int64_t)s * padded + c * kRows) * 64) * 2, cols * 128, rows_full(rs));
+            const uint32_t dst = ptx::smem_u32(smem + C::kConstAt + rs * C::kConstBytes);
+            const int64_t at = row0 + c * kRows;
+            ptx::bulk_load(dst, m.f + at, cols * 4, rows_full(rs));
+            ptx::bulk_load(dst + kRows * 4, m.lse + at, cols * 4, rows_full(rs));
+            ptx::bulk_load(dst + kRows * 8, m.lift + at, cols * 4, rows_full(rs));
+            ptx::bulk_load(dst + kRows * 12, m.i + at, cols * 4, rows_full(rs));
+            row_copies = n + 1;
+          }
+        }
+        __syncwarp();
+      }
+      key_n += a.H * chunks * run;
+      sum_n += a.H * chunks * run;
+      row_n += a.H * chunks;
+      __syncthreads();
+      if (failed) break;
+      for (int i = tid; i < run * kBlock; i += kTcThreads) {
+        const int e = blocks.entry(run0 + i / kBlock) + i % kBlock;
+        if (e >= x.n) continue;
+        const float v = records[i / kBlock][i % kBlock / 16] ? sums[i] + sums[kRun * kBlock + i] : 0.f;
+        const int64_t at = r * a.w_stride + e;
+        a.w_out[at] = a.w_in ? __fmaf_rn(a.decay, a.w_in[at], v) : v;
+      }
+      __syncthreads();      // records and sums are the next run's
+    }
+    if (failed) break;
+    u = first + stop;
+    first += blocks.count;
+    for (++r; u < end && r < a.R; ++r) {
+      x = load_request(a, r);
+      const int count = blocks_of(a, x).count;
+      if (u < first + count) break;
+      first += count;
+    }
+    if (r >= a.R) break;
+  }
+  __syncthreads();
+  // a wait that ran out leaves copies and products on their way: they are waited for as long as waits may take by default
+  if (failed && tid == 0)
+    for (uint32_t k = 1; k <= kSlots; ++k) {
+      if (row_copies >= k) ptx::mbar_wait(rows_full((row_copies - k) % kSlots), (row_copies - k) / kSlots & 1, kDefaultWaitCycles);
+      if (products >= k) ptx::mbar_wait(sums_full((products - k) % kSlots), (products - k) / kSlots & 1, kDefaultWaitCycles);
+    }
+  __syncthreads();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int kDim>
+cudaError_t launch(const KvAccumulateArgs& a, cudaStream_t s) {
+  const RowsMem m = rows_mem(a.ws, a.H, a.gamma, a.num_q, a.R, kDim);
+  // once per device and process: this launches nothing
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << (a.device & 63);
+  cudaError_t e;
+  if (a.device > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kv_accumulate_tc_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<kDim>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int per = int(std::min<int64_t>(((int64_t)a.H * pad16(a.gamma * a.max_q) + 7) / 8, 4 * kPlanSMs));
+  e = launch_kernel(kv_accumulate_rows_kernel<T, kDim>, dim3(per, std::min(a.R, std::max(1, 8 * kPlanSMs / per))), 256, 0, s, false, a, m);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)a.R * ((((int64_t)a.max_pages << a.page_shift) + kBlock - 1) / kBlock);
+  return launch_kernel(kv_accumulate_tc_kernel<kDim>, dim3(unsigned(std::min<long long>(kPlanSMs, blocks))), kTcThreads, TcShape<kDim>::kSmem, s, true, a, m);
+}
+
+}  // namespace
+
+size_t kv_accumulate_tc_workspace_bytes(int H, int gamma, int num_q, int R, int d) {
+  return size_t(rows_mem(nullptr, H, gamma, num_q, R, d).rows) * (2 * d + 16);
+}
+
+cudaError_t launch_kv_accumulate_tc(const KvAccumulateArgs& a, bool f16, cudaStream_t s) {
+  if (f16) return a.d == 64 ? launch<__half, 64>(a, s) : a.d == 128 ? launch<__half, 128>(a, s) : launch<__half, 256>(a, s);
+  return a.d == 64 ? launch<__nv_bfloat16, 64>(a, s) : a.d == 128 ? launch<__nv_bfloat16, 128>(a, s) : launch<__nv_bfloat16, 256>(a, s);
+}
+
+}  // namespace upf

@@ -925,6 +925,11 @@ double rope_magnitude(const upf_rope* x) {
   return x->scaling == UPF_ROPE_YARN && x->factor > 1 ? 0.1 * std::log(x->factor) + 1 : 1.0;
 }
 
+size_t accumulate_ws_bytes(const upf_kv_cache* c, const upf_kv_query* x) {
+  return upf::kv_accumulate_workspace_bytes(c->num_kv_heads, x->num_q_heads / c->num_kv_heads, x->max_q_len, x->num_q_tokens,
+                                            x->num_reqs, c->head_dim);
+}
+
 size_t write_ws_bytes(const upf_kv_cache* c, int32_t num_tokens) {
   return num_tokens <= UPF_KV_FEW_TOKENS ? 256 : align256(size_t(c->num_slots) * sizeof(int32_t));
 }
@@ -1420,7 +1425,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
 
 size_t upf_kv_accumulate_workspace_bytes(const upf_kv_cache* cache, const upf_kv_query* query) {
   if (check_cache(cache, false) != UPF_OK || check_query(cache, query, false) != UPF_OK) return 0;
-  return upf::kv_accumulate_workspace_bytes(query->num_q_heads, query->num_q_tokens, cache->head_dim);
+  return accumulate_ws_bytes(cache, query);
 }
 
 upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
@@ -1441,8 +1446,7 @@ upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_
   if (query->num_q_tokens == 0) return check_ctx(ctx);
   if ((st = check_rows("q", q, q_row_stride, query->num_q_heads, cache->head_dim)) != UPF_OK) return st;
   if (!lse || reinterpret_cast<uintptr_t>(lse) % 4) return fail(UPF_ERR_INVALID_ARG, "lse must be set and 4-byte aligned");
-  const size_t need = upf::kv_accumulate_workspace_bytes(query->num_q_heads, query->num_q_tokens, cache->head_dim);
-  if ((st = check_ws_bytes(ws, ws_bytes, need)) != UPF_OK) return st;
+  if ((st = check_ws_bytes(ws, ws_bytes, accumulate_ws_bytes(cache, query))) != UPF_OK) return st;
   if ((st = check_ctx(ctx)) != UPF_OK) return st;
   DeviceGuard guard(ctx->device);
   upf::KvAccumulateArgs a;
@@ -1472,6 +1476,7 @@ upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_
   a.w_out = weights_out;
   a.w_stride = weights_stride;
   a.w_cols = weights_cols;
+  a.device = ctx->device;
   a.status = ctx->status_dev;
   a.wait_limit = ctx->wait_limit > 0 ? ctx->wait_limit : upf::kDefaultWaitCycles;
   a.ws = ws;

@@ -271,6 +271,7 @@ struct KvAccumulateArgs {
   float* w_out;
   int64_t w_stride;
   int32_t w_cols;
+  int32_t device;
   int32_t* status;
   long long wait_limit;
   void* ws;
@@ -380,7 +381,7 @@ cudaError_t launch_kv_attend(const KvAttendArgs& a, bool f16, cudaStream_t s);
 size_t kv_attend_workspace_bytes(int gamma, int max_q, int d);
 cudaError_t launch_rope(const RopeArgs& a, bool f16, cudaStream_t s);
 cudaError_t launch_kv_accumulate(const KvAccumulateArgs& a, bool f16, cudaStream_t s);
-size_t kv_accumulate_workspace_bytes(int Hq, int num_q, int d);
+size_t kv_accumulate_workspace_bytes(int H, int gamma, int max_q, int num_q, int R, int d);
 // `a` with the sizes set; fills in the workspace pointers where ws is given.
 size_t kv_evict_workspace(KvEvictArgs& a, void* ws);
 cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s);

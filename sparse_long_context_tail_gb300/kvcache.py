@@ -255,7 +255,7 @@ class QuantKVCache:
                 raise ValueError("softmax_scale must be positive in fp32, or None for 1/sqrt(head_dim)")
         query, keep = B.make_kv_query(R, Hq, N, lp, page_table.data_ptr(), table_row, pages, page_size, cp, max_q_len,
                                       window, sinks, softmax_scale or 0.0, kv_of_q)
-        key = ("accumulate", Hq, N)
+        key = ("accumulate", Hq, N, R, max_q_len)
         nbytes = self._ws_bytes.get(key)
         if nbytes is None:
             nbytes = self._ws_bytes[key] = B.upf_kv_accumulate_workspace_bytes(self._cache, query)
