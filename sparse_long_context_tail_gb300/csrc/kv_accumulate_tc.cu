@@ -16,7 +16,7 @@
 // the products, one the copies.
 #include <algorithm>
 #include <atomic>
-#include <cfloat>
+#include <type_traits>
 
 #include "kv_accumulate.cuh"
 #include "sm100_ptx.cuh"
@@ -115,10 +115,22 @@ struct TcShape {
   static constexpr int kConstBytes = kRows * 16;
   static constexpr int kSumCol = kSlots * kKeyCols;            // first TMEM column of the sums
   static_assert(kSumCol + kSlots * kRows <= 512, "tensor memory");
-  // rows (1024-byte aligned), their constants, the entries' sums (a column half each)
+  // a key warp's ring: of two tiles the codes, then the scales; 16-byte pieces
+  static constexpr int kPieces = 2 * kDim / 2, kRowPieces = Shape<kDim>::kPart / 32;
+  static constexpr int kRingItem = 2 * 9 * kDim, kAhead = kDim == 64 ? 6 : kDim == 128 ? 4 : 2, kRingBytes = kAhead * kRingItem;
+  static_assert(kRingItem == kPieces * 16 + 2 * kDim, "codes and scales");
+  // rows side by side begin at the same bank every 128 bytes: a row's pieces are swapped by that
+  __device__ static constexpr int swap(int row) { return row / (4 / (kRowPieces / 2)) % kRowPieces; }
+  // rows (1024-byte aligned), their constants, the entries' sums (a column half each), the rings
   static constexpr int kConstAt = kSlots * kRowBytes, kSumAt = kConstAt + kSlots * kConstBytes;
-  static constexpr int kSmem = kSumAt + 2 * kRun * kBlock * 4 + 1024;
+  static constexpr int kRingAt = kSumAt + 2 * kRun * kBlock * 4;
+  static constexpr int kSmem = kRingAt + kKeyWarps * kRingBytes + 1024;
+  static_assert(kSmem <= 224 * 1024, "shared memory");
 };
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -250,40 +262,76 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
         // ---- keys: this warp's 32 entries of every other block, an entry a lane
         const int quarter = warp & 3;
         const uint32_t slot = warp >> 2;
-        uint4 codes[kDim / 32];
-        uint32_t scales[kDim / 64];          // four groups each
-        auto fetch = [&](int h, int b) {
-          const int row = (lane & 15), tile = quarter * 2 + (lane >> 4);
-          const uint8_t* const rec = records[b][tile];
-#pragma unroll
-          for (int k = 0; k < kDim / 32; ++k) codes[k] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int k = 0; k < kDim / 64; ++k) scales[k] = 0;
-          if (!rec) return;
-          const uint8_t* const src = rec + (int64_t)h * S::kRecord;
-#pragma unroll
-          for (int k = 0; k < kDim / 32; ++k)        // 32 dims
-            codes[k] = __ldg(reinterpret_cast<const uint4*>(src + k / (S::kPart / 32) * (8 * S::kPart) + row * (S::kPart / 2)) + k % (S::kPart / 32));
-#pragma unroll
-          for (int k = 0; k < kDim / 64; ++k)
-            scales[k] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kDim + row * (kDim / 16)) + k);
-        };
-        const int total = a.H * chunks * run;        // products of the run; the i-th is block i % run
+        uint8_t* const ring = smem + C::kRingAt + warp * C::kRingBytes;
+        const int total = a.H * chunks * run;        // products of the run; the i-th is of block i % run
         // the group's products: those whose number from the kernel's start is its slot modulo two
-        int i = int((slot - key_n) & 1);
-        if (i < total) fetch(i / run / chunks, i % run);
-        for (; i < total; i += 2) {
-          const uint32_t n = key_n + i;
+        const int i0 = int((slot - key_n) & 1);
+        struct At {
+          int i, b, c, h;      // product; its block, chunk of rows and head
+        };
+        auto next = [&](At& x) {
+          x.i += 2;
+          x.b += 2;
+          while (x.b >= run) {
+            x.b -= run;
+            if (++x.c == chunks) {
+              x.c = 0;
+              ++x.h;
+            }
+          }
+        };
+        // ---- copies of the warp's two tiles' codes and scales, kAhead products before they are worked out.  A lane's
+        // pieces lie side by side in the cache; in the ring those of a row are swapped so that lanes
+        // that read one piece of 32 rows meet all banks.
+        At to{i0 - 2, i0 - 2, 0, 0};
+        next(to);
+        int to_slot = 0;
+        auto copy = [&] {
+          if (to.i < total) {
+            const uint32_t dst = ptx::smem_u32(ring + to_slot * C::kRingItem);
+            const int64_t head = (int64_t)to.h * S::kRecord;
+#pragma unroll
+            for (int k = 0; k < C::kPieces; k += 32) {
+              const int p = k + lane, tile = p / (C::kPieces / 2), q = p % (C::kPieces / 2);      // piece of a tile's codes
+              const int part = q / (S::kPart / 2), row = q % (S::kPart / 2) / C::kRowPieces, piece = q % C::kRowPieces;
+              const uint8_t* const rec = records[to.b][quarter * 2 + tile];
+              if (rec) copy_async16(dst + ((tile * S::kParts + part) * 16 + row) * (S::kPart / 2) + (piece ^ C::swap(row)) * 16, rec + head + q * 16);
+            }
+            if (lane < kDim / 8) {
+              const int tile = lane / (kDim / 16), q = lane % (kDim / 16);
+              const uint8_t* const rec = records[to.b][quarter * 2 + tile];
+              if (rec) copy_async16(dst + 16 * kDim + lane * 16, rec + head + 16 * kDim + q * 16);
+            }
+            if (++to_slot == C::kAhead) to_slot = 0;
+            next(to);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < C::kAhead; ++k) copy();
+        int from_slot = 0;
+        const int row = lane & 15;
+        At x{i0 - 2, i0 - 2, 0, 0};
+        for (next(x); x.i < total; next(x)) {
+          const uint32_t n = key_n + x.i;
+          asm volatile("cp.async.wait_group %0;" ::"n"(C::kAhead - 1) : "memory");
+          __syncwarp();
+          const bool there = records[x.b][quarter * 2 + (lane >> 4)] != nullptr;
+          const uint8_t* const item = ring + from_slot * C::kRingItem;
+          if (++from_slot == C::kAhead) from_slot = 0;
           if (!__all_sync(0xFFFFFFFFu, wait(keys_free(slot), (n / kSlots & 1) ^ 1))) break;   // all lanes or none
           ptx::tc_fence_after();
 #pragma unroll
           for (int half = 0; half < kDim / 64; ++half) {    // 64 dims: 32 columns
             uint32_t v[32];
-            const uint32_t s01 = kv::e4m3x2_to_f16x2(uint16_t(scales[half])), s23 = kv::e4m3x2_to_f16x2(uint16_t(scales[half] >> 16));
+            const uint32_t scales = there ? *reinterpret_cast<const uint32_t*>(item + 16 * kDim + (lane >> 4) * kDim + row * (kDim / 16) + half * 4) : 0u;
+            const uint32_t s01 = kv::e4m3x2_to_f16x2(uint16_t(scales)), s23 = kv::e4m3x2_to_f16x2(uint16_t(scales >> 16));
             const __half2 s[4] = {__low2half2(as_half2(s01)), __high2half2(as_half2(s01)), __low2half2(as_half2(s23)), __high2half2(as_half2(s23))};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint4 c = codes[half * 2 + k];
+              const int piece = half * 2 + k, part = piece / C::kRowPieces;
+              const uint4 c = *reinterpret_cast<const uint4*>(item + (((lane >> 4) * S::kParts + part) * 16 + row) * (S::kPart / 2) +
+                                                              (piece % C::kRowPieces ^ C::swap(row)) * 16);
               const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
@@ -295,12 +343,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             }
             tmem_st32(tmem + (uint32_t(quarter * 32) << 16) + slot * C::kKeyCols + half * 32, v);
           }
-          if (i + 2 < total) fetch((i + 2) / run / chunks, (i + 2) % run);
+          __syncwarp();      // the item may be copied over
+          copy();
           tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(keys_full(slot));
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
       } else if (warp < kKeyWarps + kSumWarps) {
         // ---- weights: this warp's 32 entries, half of the columns
         const int quarter = warp & 3, half = (warp - kKeyWarps) >> 2;
@@ -320,31 +370,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const int e0 = blocks.entry(run0 + b), e = e0 + quarter * 32 + lane;
             const bool whole = all_seen(a, x, view, e0, e0 + kBlock);
             const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + C::kSumCol + ss * kRows;
-            float total = 0.f;
-            for (int j = from; j < to; j += 8) {
+            uint64_t total = 0;      // over the even and over the odd columns
+            // four logits as weights, added up
+            auto add = [&](auto masked, const float* v, int j) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cf + j), l = *reinterpret_cast<const ulonglong2*>(cf + kRows + j);
+              const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(cf + 2 * kRows + j);
+              float w[4];
+              ptx::unpack2(ptx::fma2(ptx::pack2(v[0], v[1]), f.x, l.x), w[0], w[1]);
+              ptx::unpack2(ptx::fma2(ptx::pack2(v[2], v[3]), f.y, l.y), w[2], w[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = ptx::ex2_approx(w[k]);
+              if constexpr (decltype(masked)::value) {
+                const int4 i = *reinterpret_cast<const int4*>(cf + 3 * kRows + j);
+                w[0] = sees(a, view, i.x, e) ? w[0] : 0.f;
+                w[1] = sees(a, view, i.y, e) ? w[1] : 0.f;
+                w[2] = sees(a, view, i.z, e) ? w[2] : 0.f;
+                w[3] = sees(a, view, i.w, e) ? w[3] : 0.f;
+              }
+              total = ptx::fma2(ptx::pack2(w[0], w[1]), g.x, total);
+              total = ptx::fma2(ptx::pack2(w[2], w[3]), g.y, total);
+            };
+            int j = from;
+            if (whole) {
+              for (; j + 32 <= to; j += 32) {
+                float v[32];
+                ptx::tmem_ld32(at + j, v);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) add(std::false_type(), v + k, j + k);
+              }
+            }
+            for (; j < to; j += 8) {
               float v[8];
               tmem_ld8(at + j, v);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 8; k += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(cf + j + k), l = *reinterpret_cast<const float4*>(cf + kRows + j + k);
-                const float4 g = *reinterpret_cast<const float4*>(cf + 2 * kRows + j + k);
-                float w0 = ptx::ex2_approx(__fmaf_rn(v[k], f.x, l.x)), w1 = ptx::ex2_approx(__fmaf_rn(v[k + 1], f.y, l.y));
-                float w2 = ptx::ex2_approx(__fmaf_rn(v[k + 2], f.z, l.z)), w3 = ptx::ex2_approx(__fmaf_rn(v[k + 3], f.w, l.w));
-                if (!whole) {
-                  const int4 i = *reinterpret_cast<const int4*>(cf + 3 * kRows + j + k);
-                  w0 = sees(a, view, i.x, e) ? w0 : 0.f;
-                  w1 = sees(a, view, i.y, e) ? w1 : 0.f;
-                  w2 = sees(a, view, i.z, e) ? w2 : 0.f;
-                  w3 = sees(a, view, i.w, e) ? w3 : 0.f;
-                }
-                total = __fmaf_rn(w0, g.x, __fmaf_rn(w1, g.y, __fmaf_rn(w2, g.z, __fmaf_rn(w3, g.w, total))));
-              }
+              for (int k = 0; k < 8; k += 4) add(std::true_type(), v + k, j + k);
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(sums_free(ss));
-            sums[half * kRun * kBlock + b * kBlock + quarter * 32 + lane] += total;
+            float even, odd;
+            ptx::unpack2(total, even, odd);
+            sums[half * kRun * kBlock + b * kBlock + quarter * 32 + lane] += even + odd;
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(rows_free(rs));
