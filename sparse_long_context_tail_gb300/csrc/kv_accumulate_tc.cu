@@ -31,7 +31,7 @@ constexpr int kBlock = 128;                    // entries of a product
 constexpr int kRows = 128;                     // most rows of a product
 constexpr int kRun = 16;                       // blocks whose sums are in shared memory at once
 constexpr int kKeyWarps = 8, kSumWarps = 8, kMmaWarp = 16, kTcWarps = 18 /* the last one copies */, kTcThreads = 32 * kTcWarps;
-constexpr uint32_t kSlots = 2;                 // of keys, of rows, of sums
+constexpr uint32_t kSlots = 2;                 // of rows, of sums (of keys: TcShape)
 
 // The rows of all requests as operand B.  Those of request r and kv head h, padded to a multiple of 16, begin at row
 // first_row(r) + h * padded; of d dims every 64 are a slab of their own, 128 bytes a row.
@@ -113,14 +113,16 @@ struct TcShape {
   static constexpr int kKeyCols = kDim / 2;                    // TMEM columns of a block's keys
   static constexpr int kRowBytes = kRows * kDim * 2;           // of a chunk of rows
   static constexpr int kConstBytes = kRows * 16;
-  static constexpr int kSumCol = kSlots * kKeyCols;            // first TMEM column of the sums
+  // Four slots of keys where tensor memory has room: a group works out its next block while the products with the last
+  // are under way.
+  static constexpr uint32_t kKeySlots = kDim == 256 ? 2 : 4;
+  static constexpr int kSumCol = kKeySlots * kKeyCols;         // first TMEM column of the sums
   static_assert(kSumCol + kSlots * kRows <= 512, "tensor memory");
   // a key warp's ring: of two tiles the codes, then the scales; 16-byte pieces
-  static constexpr int kPieces = 2 * kDim / 2, kRowPieces = Shape<kDim>::kPart / 32;
+  static constexpr int kRowPieces = Shape<kDim>::kPart / 32;
   static constexpr int kRingItem = 2 * 9 * kDim, kAhead = kDim == 64 ? 6 : kDim == 128 ? 4 : 2, kRingBytes = kAhead * kRingItem;
-  static_assert(kRingItem == kPieces * 16 + 2 * kDim, "codes and scales");
   // rows side by side begin at the same bank every 128 bytes: a row's pieces are swapped by that
-  __device__ static constexpr int swap(int row) { return row / (4 / (kRowPieces / 2)) % kRowPieces; }
+  __host__ __device__ static constexpr int swap(int row) { return row / (4 / (kRowPieces / 2)) % kRowPieces; }
   // rows (1024-byte aligned), their constants, the entries' sums (a column half each), the rings
   static constexpr int kConstAt = kSlots * kRowBytes, kSumAt = kConstAt + kSlots * kConstBytes;
   static constexpr int kRingAt = kSumAt + 2 * kRun * kBlock * 4;
@@ -155,13 +157,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, f16 inputs, fp32 accumulation.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] = A[tmem] * B[smem]^T, f16 inputs, fp32 accumulation; kAdd: += .
+template <bool kAdd>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "n"(kAdd ? 1 : 0)
       : "memory");
 }
 // As ptx::idesc_bf16_f32 with f16 operands.
@@ -189,25 +192,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
   uint8_t* const smem = smem_raw + (1024 - (ptx::smem_u32(smem_raw) & 1023)) % 1024;
   float* const sums = reinterpret_cast<float*>(smem + C::kSumAt);      // [2][kRun * kBlock]
   __shared__ Starts<kTcThreads> starts;
-  __shared__ __align__(8) uint64_t bars[5 * kSlots];
+  __shared__ __align__(8) uint64_t bars[2 * C::kKeySlots + 4 * kSlots];
   __shared__ uint32_t tmem_word;
   __shared__ int failed;
   __shared__ uint32_t row_copies, products;      // begun so far
-  __shared__ const uint8_t* records[kRun][kBlock / 16];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ unsigned long long records[kRun][kBlock / 16];     // bit 0: there is none, and the cache's first stands in
+  // from a shuffle, so that what depends on the warp alone is known to be the same in all lanes
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto keys_full = [&](uint32_t s) { return bar0 + 8 * s; };
-  auto keys_free = [&](uint32_t s) { return bar0 + 8 * (kSlots + s); };
-  auto rows_full = [&](uint32_t s) { return bar0 + 8 * (2 * kSlots + s); };
-  auto rows_free = [&](uint32_t s) { return bar0 + 8 * (3 * kSlots + s); };
-  auto sums_full = [&](uint32_t s) { return bar0 + 8 * (4 * kSlots + s); };
-  // sums_free: an entry sum slot is read by all sum warps
-  __shared__ __align__(8) uint64_t bars_free[kSlots];
-  auto sums_free = [&](uint32_t s) { return ptx::smem_u32(bars_free) + 8 * s; };
+  auto keys_free = [&](uint32_t s) { return bar0 + 8 * (C::kKeySlots + s); };
+  const uint32_t bar1 = bar0 + 16 * C::kKeySlots;
+  auto rows_full = [&](uint32_t s) { return bar1 + 8 * s; };
+  auto rows_free = [&](uint32_t s) { return bar1 + 8 * (kSlots + s); };
+  auto sums_full = [&](uint32_t s) { return bar1 + 8 * (2 * kSlots + s); };
+  auto sums_free = [&](uint32_t s) { return bar1 + 8 * (3 * kSlots + s); };
   if (tid == 0) {
-    for (uint32_t s = 0; s < kSlots; ++s) {
+    for (uint32_t s = 0; s < C::kKeySlots; ++s) {
       ptx::mbar_init(keys_full(s), 4);
       ptx::mbar_init(keys_free(s), 1);
+    }
+    for (uint32_t s = 0; s < kSlots; ++s) {
       ptx::mbar_init(rows_full(s), 1);
       ptx::mbar_init(rows_free(s), 1 + kSumWarps);
       ptx::mbar_init(sums_full(s), 1);
@@ -235,11 +240,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
   // phases of the rings, each role its own
   uint32_t key_n = 0, row_n = 0, sum_n = 0;      // blocks, chunks, products so far
   auto wait = [&](uint32_t bar, uint32_t phase) {
-    if (*reinterpret_cast<volatile int*>(&failed)) return false;
-    if (ptx::mbar_wait(bar, phase, a.wait_limit)) return true;
-    *reinterpret_cast<volatile int*>(&failed) = 1;
-    set_status(a.status, UPF_ERR_TIMEOUT);
-    return false;
+    if (ptx::mbar_try_wait(bar, phase)) return true;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait_hint(bar, phase, 200)) {
+      if (*reinterpret_cast<volatile int*>(&failed)) return false;
+      if (clock64() - t0 > a.wait_limit) {
+        *reinterpret_cast<volatile int*>(&failed) = 1;
+        set_status(a.status, UPF_ERR_TIMEOUT);
+        return false;
+      }
+    }
+    return true;
   };
   bool rows_waited = false;
   int r = 0;
@@ -254,18 +265,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
     const int64_t region = first_row(a, x.q0, r);
     for (int run0 = begin; run0 < stop; run0 += kRun) {
       const int run = min(kRun, stop - run0);
-      for (int i = tid; i < run * (kBlock / 16); i += kTcThreads)
-        records[i / (kBlock / 16)][i % (kBlock / 16)] = record_at<kDim>(a, r, x, view, blocks.entry(run0 + i / (kBlock / 16)) + i % (kBlock / 16) * 16);
+      for (int i = tid; i < run * (kBlock / 16); i += kTcThreads) {
+        const uint8_t* const rec = record_at<kDim>(a, r, x, view, blocks.entry(run0 + i / (kBlock / 16)) + i % (kBlock / 16) * 16);
+        records[i / (kBlock / 16)][i % (kBlock / 16)] = reinterpret_cast<unsigned long long>(rec ? rec : a.data) | !rec;
+      }
       for (int i = tid; i < 2 * kRun * kBlock; i += kTcThreads) sums[i] = 0.f;
       __syncthreads();
       if (warp < kKeyWarps) {
         // ---- keys: this warp's 32 entries of every other block, an entry a lane
         const int quarter = warp & 3;
-        const uint32_t slot = warp >> 2;
+        const uint32_t team = warp >> 2;
         uint8_t* const ring = smem + C::kRingAt + warp * C::kRingBytes;
         const int total = a.H * chunks * run;        // products of the run; the i-th is of block i % run
-        // the group's products: those whose number from the kernel's start is its slot modulo two
-        const int i0 = int((slot - key_n) & 1);
+        // the group's products: those whose number from the kernel's start is its team's modulo two
+        const int i0 = int((team - key_n) & 1);
         struct At {
           int i, b, c, h;      // product; its block, chunk of rows and head
         };
@@ -283,24 +296,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
         // ---- copies of the warp's two tiles' codes and scales, kAhead products before they are worked out.  A lane's
         // pieces lie side by side in the cache; in the ring those of a row are swapped so that lanes
         // that read one piece of 32 rows meet all banks.
+        // a run of 512 bytes has the pieces of whole rows, and rows in the same place of it are swapped alike
+        static_assert(C::swap(512 / (S::kPart / 2)) == 0, "swaps repeat");
+        const uint32_t codes_to = ptx::smem_u32(ring) + (lane / C::kRowPieces * C::kRowPieces + (lane % C::kRowPieces ^ C::swap(lane / C::kRowPieces))) * 16;
+        const uint32_t scales_to = ptx::smem_u32(ring) + 16 * kDim + lane * 16;
         At to{i0 - 2, i0 - 2, 0, 0};
         next(to);
         int to_slot = 0;
         auto copy = [&] {
           if (to.i < total) {
-            const uint32_t dst = ptx::smem_u32(ring + to_slot * C::kRingItem);
-            const int64_t head = (int64_t)to.h * S::kRecord;
+            const uint32_t dst = codes_to + to_slot * C::kRingItem;
+            const int64_t from = to.h * S::kRecord + lane * 16;
 #pragma unroll
-            for (int k = 0; k < C::kPieces; k += 32) {
-              const int p = k + lane, tile = p / (C::kPieces / 2), q = p % (C::kPieces / 2);      // piece of a tile's codes
-              const int part = q / (S::kPart / 2), row = q % (S::kPart / 2) / C::kRowPieces, piece = q % C::kRowPieces;
-              const uint8_t* const rec = records[to.b][quarter * 2 + tile];
-              if (rec) copy_async16(dst + ((tile * S::kParts + part) * 16 + row) * (S::kPart / 2) + (piece ^ C::swap(row)) * 16, rec + head + q * 16);
-            }
-            if (lane < kDim / 8) {
-              const int tile = lane / (kDim / 16), q = lane % (kDim / 16);
-              const uint8_t* const rec = records[to.b][quarter * 2 + tile];
-              if (rec) copy_async16(dst + 16 * kDim + lane * 16, rec + head + 16 * kDim + q * 16);
+            for (int tile = 0; tile < 2; ++tile) {
+              const uint8_t* const src = reinterpret_cast<const uint8_t*>(records[to.b][quarter * 2 + tile] & ~1ull) + from;
+#pragma unroll
+              for (int k = 0; k < 8 * kDim; k += 512) copy_async16(dst + tile * 8 * kDim + k, src + k);
+              if (lane < kDim / 16) copy_async16(scales_to + to_slot * C::kRingItem + tile * kDim, src + 16 * kDim);
             }
             if (++to_slot == C::kAhead) to_slot = 0;
             next(to);
@@ -313,14 +325,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
         const int row = lane & 15;
         At x{i0 - 2, i0 - 2, 0, 0};
         for (next(x); x.i < total; next(x)) {
-          const uint32_t n = key_n + x.i;
+          const uint32_t n = key_n + x.i, slot = n % C::kKeySlots;
           asm volatile("cp.async.wait_group %0;" ::"n"(C::kAhead - 1) : "memory");
           __syncwarp();
-          const bool there = records[x.b][quarter * 2 + (lane >> 4)] != nullptr;
+          const bool there = !(records[x.b][quarter * 2 + (lane >> 4)] & 1);
           const uint8_t* const item = ring + from_slot * C::kRingItem;
           if (++from_slot == C::kAhead) from_slot = 0;
-          if (!__all_sync(0xFFFFFFFFu, wait(keys_free(slot), (n / kSlots & 1) ^ 1))) break;   // all lanes or none
-          ptx::tc_fence_after();
+          bool ok = true;
 #pragma unroll
           for (int half = 0; half < kDim / 64; ++half) {    // 64 dims: 32 columns
             uint32_t v[32];
@@ -341,8 +352,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
                 for (int z = 0; z < 4; ++z) v[k * 16 + y * 4 + z] = hmul2(hh[z], s[k * 2 + y / 2]);
               }
             }
+            if (half == 0) {      // the first 64 dims are worked out before the slot is free
+              ok = __all_sync(0xFFFFFFFFu, wait(keys_free(slot), (n / C::kKeySlots & 1) ^ 1));   // all lanes or none
+              if (!ok) break;
+              ptx::tc_fence_after();
+            }
             tmem_st32(tmem + (uint32_t(quarter * 32) << 16) + slot * C::kKeyCols + half * 32, v);
           }
+          if (!ok) break;
           __syncwarp();      // the item may be copied over
           copy();
           tmem_wait_st();
@@ -425,20 +442,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const int c = hc % chunks, cols = min(kRows, padded - c * kRows);
             const uint32_t rs = rn % kSlots, idesc = idesc_f16(cols);
             if (!(ok = wait(rows_full(rs), rn / kSlots & 1))) break;
-            for (int b = 0; b < run; ++b, ++kn, ++sn) {
-              const uint32_t ks = kn % kSlots, ss = sn % kSlots;
-              if (!(ok = wait(keys_full(ks), kn / kSlots & 1) && wait(sums_free(ss), (sn / kSlots & 1) ^ 1))) break;
-              ptx::tc_fence_after();
+            uint64_t rows_at[C::kSlabs];         // a step of 16 dims is two further on (of 16 bytes)
 #pragma unroll
-              for (int k = 0; k < kDim / 16; ++k)
-                mma_f16_ts(tmem + C::kSumCol + ss * kRows, tmem + ks * C::kKeyCols + k * 8,
-                           ptx::sdesc_kmajor_sw128(ptx::smem_u32(smem + rs * C::kRowBytes) + k / 4 * (cols * 128) + k % 4 * 32), idesc, k > 0);
+            for (int s = 0; s < C::kSlabs; ++s) rows_at[s] = ptx::sdesc_kmajor_sw128(ptx::smem_u32(smem + rs * C::kRowBytes) + s * cols * 128);
+            for (int b = 0; b < run; ++b, ++kn, ++sn) {
+              const uint32_t ks = kn % C::kKeySlots, ss = sn % kSlots;
+              if (!(ok = wait(sums_free(ss), (sn / kSlots & 1) ^ 1) && wait(keys_full(ks), kn / C::kKeySlots & 1))) break;
+              ptx::tc_fence_after();
+              const uint32_t to = tmem + C::kSumCol + ss * kRows, keys = tmem + ks * C::kKeyCols;
+              mma_f16_ts<false>(to, keys, rows_at[0], idesc);
+#pragma unroll
+              for (int k = 1; k < kDim / 16; ++k) mma_f16_ts<true>(to, keys + k * 8, rows_at[k / 4] + k % 4 * 2, idesc);
               ptx::mma_commit(keys_free(ks));
               ptx::mma_commit(sums_full(ss));
-              products = sn + 1;
-              if (b == run - 1) ptx::mma_commit(rows_free(rs));
             }
+            if (ok) ptx::mma_commit(rows_free(rs));
           }
+          products = sn;
         }
         __syncwarp();
       } else {
@@ -474,7 +494,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
       for (int i = tid; i < run * kBlock; i += kTcThreads) {
         const int e = blocks.entry(run0 + i / kBlock) + i % kBlock;
         if (e >= x.n) continue;
-        const float v = records[i / kBlock][i % kBlock / 16] ? sums[i] + sums[kRun * kBlock + i] : 0.f;
+        const float v = records[i / kBlock][i % kBlock / 16] & 1 ? 0.f : sums[i] + sums[kRun * kBlock + i];
         const int64_t at = r * a.w_stride + e;
         a.w_out[at] = a.w_in ? __fmaf_rn(a.decay, a.w_in[at], v) : v;
       }
