@@ -175,9 +175,9 @@ __device__ __forceinline__ float factor_of(const KvAccumulateArgs& a, int exp) {
 // (times `down`).  hi and what its rounding leaves (in `lift`) are lse * log2 e: the rounding of one number would be
 // that of every weight of the row.
 struct RowConstants {
-  bool on, bad;      // does it count; is it not finite
-  int e;             // the power of two
-  float down, f, hi, lift;
+  bool on, bad, zero;      // does it count; is it not finite; is it all zeros
+  int e;                   // the power of two
+  float down, f, hi, low, lift;
 };
 
 // `amax`: bits of the row's largest magnitude in fp32 (at and above those of infinity if it has a NaN or an infinity).
@@ -186,11 +186,13 @@ __device__ __forceinline__ RowConstants row_constants(const KvAccumulateArgs& a,
   RowConstants c;
   c.bad = real && (amax >= 0x7F800000u || !(lse < INFINITY));
   c.on = real && !c.bad && lse > -INFINITY;
-  c.e = !c.on || amax == 0 ? 0 : max(-126, min(int(amax >> 23) - 127, 126));
+  c.zero = amax == 0;
+  c.e = !c.on || c.zero ? 0 : max(-126, min(int(amax >> 23) - 127, 126));
   c.down = __uint_as_float(uint32_t(127 - c.e) << 23);
   c.f = factor_of(a, a.scale_exp + c.e);
   c.hi = lse * kLog2e;
-  c.lift = ptx::ex2_approx(-(__fmaf_rn(lse, kLog2e, -c.hi) + lse * kLog2eLow));
+  c.low = __fmaf_rn(lse, kLog2e, -c.hi) + lse * kLog2eLow;
+  c.lift = ptx::ex2_approx(-c.low);
   return c;
 }
 

@@ -16,6 +16,7 @@
 // the products, one the copies.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "kv_accumulate.cuh"
@@ -29,6 +30,7 @@ using namespace acc;
 
 constexpr int kBlock = 128;                    // entries of a product
 constexpr int kRows = 128;                     // most rows of a product
+constexpr int kRowWarps = 32;                  // of a CTA that makes them ready
 constexpr int kRun = 16;                       // blocks whose sums are in shared memory at once
 constexpr int kKeyWarps = 8, kSumWarps = 8, kMmaWarp = 16, kTcWarps = 18 /* the last one copies */, kTcThreads = 32 * kTcWarps;
 constexpr uint32_t kSlots = 2;                 // of rows, of sums (of keys: TcShape)
@@ -43,7 +45,6 @@ struct RowsMem {
   uint8_t* q;        // [rows][d] f16: per request and head [slab][row][64 dims], 16-byte pieces swizzled
   float* f;          // [rows] logit factors
   float* lse;        // [rows] -lse * log2 e
-  float* lift;       // [rows] 2^ what that was rounded by
   int32_t* i;        // [rows] queries; -1: none
   int64_t rows;
 };
@@ -53,55 +54,98 @@ __host__ __device__ inline RowsMem rows_mem(void* ws, int H, int gamma, int num_
   m.q = static_cast<uint8_t*>(ws);
   m.f = reinterpret_cast<float*>(m.q + m.rows * d * 2);
   m.lse = m.f + m.rows;
-  m.lift = m.lse + m.rows;
-  m.i = reinterpret_cast<int32_t*>(m.lift + m.rows);
+  m.i = reinterpret_cast<int32_t*>(m.lse + m.rows);
   return m;
 }
 
-// A warp per row of a request and kv head, the padding's among them.
+// A CTA per chunk of rows of a request and kv head, the padding's among them.
+//
+// Rows are divided by a power of two so that f16 holds them: one of the whole chunk, which makes its largest element
+// 2^14 to 2^15, so that a logit factor is the same for all columns.  f16 reaches 2^-24, so elements down to
+// 2^-16 of a row 2^15 smaller than the largest keep eight bits.  Where rows are further apart
+// each has its own power.
 template <typename T, int kDim>
-__global__ void __launch_bounds__(256) kv_accumulate_rows_kernel(const KvAccumulateArgs a, const RowsMem m) {
+__global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(const KvAccumulateArgs a, const RowsMem m) {
   constexpr const T* kT = nullptr;
   constexpr int kEach = kDim / 32;             // dims of a lane
+  constexpr int kTop = 14;                     // exponent of the largest element
+  constexpr int kOwn = kRows / kRowWarps;      // rows of a warp
+  __shared__ int most, least;                  // of the exponents of the rows that count
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int r = blockIdx.y; r < a.R; r += gridDim.y) {
     const Request x = load_request(a, r);
-    const int rows = x.q_len * a.gamma, padded = pad16(rows);
-    for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < (int64_t)a.H * padded; w += (int64_t)gridDim.x * 8) {
-      const int h = int(w / padded), rho = int(w - (int64_t)h * padded);
+    const int rows = x.q_len * a.gamma, padded = pad16(rows), chunks = (padded + kRows - 1) / kRows;
+    for (int hc = blockIdx.x; hc < a.H * chunks; hc += gridDim.x) {
+      const int h = hc / chunks, row0 = (hc - h * chunks) * kRows, row1 = min(padded, row0 + kRows);
       const int64_t region = first_row(a, x.q0, r) + (int64_t)h * padded;
-      const bool real = rho < rows;
-      const int i = real ? rho / a.gamma : 0, head = a.qhead[h * a.gamma + (real ? rho - i * a.gamma : 0)];
-      const int64_t at = x.q0 + i;
-      uint32_t q[kEach / 2];
-      uint32_t top = 0;
+      // the warp's rows, all on their way before the first is looked at
+      uint32_t q[kOwn][kEach / 2];
+      float lse[kOwn];
+      int query[kOwn];
 #pragma unroll
-      for (int k = 0; k < kEach / 2; ++k) {
-        q[k] = real ? reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + at * a.q_stride + head * kDim)[lane * (kEach / 2) + k] : 0u;
-        top = kv::max_abs2(top, q[k], kT);
-      }
-      const float2 tops = kv::pair_to_float2(top, kT);
-      const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(fabsf(tops.x)), __float_as_uint(fabsf(tops.y))));
-      const RowConstants c = row_constants(a, real, amax, real ? a.lse[at * a.Hq + head] : -INFINITY);
-      if (c.bad && lane == 0) set_status(a.status, UPF_ERR_NONFINITE);
-      uint32_t v[kEach / 2];
+      for (int y = 0; y < kOwn; ++y) {
+        const int rho = row0 + warp + y * kRowWarps;
+        const bool real = rho < rows;
+        query[y] = real ? rho / a.gamma : -1;
+        const int i = max(query[y], 0), head = a.qhead[h * a.gamma + (real ? rho - i * a.gamma : 0)];
+        const int64_t at = x.q0 + i;
+        lse[y] = real ? a.lse[at * a.Hq + head] : -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kEach / 2; ++k) {
-        const float2 y = kv::pair_to_float2(q[k], kT);
-        v[k] = c.on ? pack_f16(y.x * c.down, y.y * c.down) : 0u;
+        for (int k = 0; k < kEach / 2; ++k)
+          q[y][k] = real ? reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + at * a.q_stride + head * kDim)[lane * (kEach / 2) + k] : 0u;
       }
-      // dims lane * kEach ..: slab, and the byte within the row's 128
-      const int dim = lane * kEach, slab = dim / 64, byte = dim % 64 * 2;
-      uint8_t* const dst = m.q + (region * kDim + ((int64_t)slab * padded + rho) * 64) * 2 + ((byte >> 4 ^ rho & 7) << 4) + (byte & 15);
-      if constexpr (kEach == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
-      else if constexpr (kEach == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = v[0];
-      if (lane == 0) {
-        m.f[region + rho] = c.on ? c.f : 0.f;
-        m.lse[region + rho] = c.on ? -c.hi : -INFINITY;
-        m.lift[region + rho] = c.on ? c.lift : 0.f;
-        m.i[region + rho] = c.on ? i : -1;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        most = INT_MIN;
+        least = INT_MAX;
+      }
+      __syncthreads();
+      RowConstants c[kOwn];
+      int hi = INT_MIN, lo = INT_MAX;
+#pragma unroll
+      for (int y = 0; y < kOwn; ++y) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kEach / 2; ++k) top = kv::max_abs2(top, q[y][k], kT);
+        const float2 tops = kv::pair_to_float2(top, kT);
+        const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(__float_as_uint(fabsf(tops.x)), __float_as_uint(fabsf(tops.y))));
+        c[y] = row_constants(a, query[y] >= 0, amax, lse[y]);
+        if (c[y].bad && lane == 0) set_status(a.status, UPF_ERR_NONFINITE);
+        if (!c[y].on || c[y].zero) continue;
+        hi = max(hi, c[y].e);
+        lo = min(lo, c[y].e);
+      }
+      if (lane == 0 && hi >= lo) {
+        atomicMax(&most, hi);
+        atomicMin(&least, lo);
+      }
+      __syncthreads();
+      const bool same = most < least || most - least <= 15;       // none, or near one another
+#pragma unroll
+      for (int y = 0; y < kOwn; ++y) {
+        const int rho = row0 + warp + y * kRowWarps;
+        if (rho >= row1) break;
+        const int e = (same ? (most < least ? 0 : most) : c[y].e) - kTop;
+        // 2^-e in two factors: it may be past fp32
+        const float down0 = __uint_as_float(uint32_t(127 - e / 2) << 23), down1 = __uint_as_float(uint32_t(127 - (e - e / 2)) << 23);
+        uint32_t v[kEach / 2];
+#pragma unroll
+        for (int k = 0; k < kEach / 2; ++k) {
+          const float2 z = kv::pair_to_float2(q[y][k], kT);
+          v[k] = c[y].on ? pack_f16(z.x * down0 * down1, z.y * down0 * down1) : 0u;
+        }
+        // dims lane * kEach ..: slab, and the byte within the row's 128
+        const int dim = lane * kEach, slab = dim / 64, byte = dim % 64 * 2;
+        uint8_t* const dst = m.q + (region * kDim + ((int64_t)slab * padded + rho) * 64) * 2 + ((byte >> 4 ^ (rho & 7)) << 4) + (byte & 15);
+        if constexpr (kEach == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+        else if constexpr (kEach == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = v[0];
+        if (lane == 0) {
+          m.f[region + rho] = factor_of(a, a.scale_exp + e);
+          m.lse[region + rho] = c[y].on ? -(c[y].hi + c[y].low) : -INFINITY;      // a row that does not count has the weight 0
+          m.i[region + rho] = c[y].on ? query[y] : -1;
+        }
       }
     }
   }
@@ -112,7 +156,7 @@ struct TcShape {
   static constexpr int kSlabs = kDim / 64;
   static constexpr int kKeyCols = kDim / 2;                    // TMEM columns of a block's keys
   static constexpr int kRowBytes = kRows * kDim * 2;           // of a chunk of rows
-  static constexpr int kConstBytes = kRows * 16;
+  static constexpr int kConstBytes = kRows * 12;
   // Four slots of keys where tensor memory has room: a group works out its next block while the products with the last
   // are under way.
   static constexpr uint32_t kKeySlots = kDim == 256 ? 2 : 4;
@@ -380,6 +424,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
           const uint32_t rs = rn % kSlots;
           ok = __all_sync(0xFFFFFFFFu, wait(rows_full(rs), rn / kSlots & 1));
           const float* const cf = reinterpret_cast<const float*>(smem + C::kConstAt + rs * C::kConstBytes);
+          // a broadcast from shared memory takes as long as it has words, so the factor is one where the rows allow it
+          bool same = true;
+          for (int j = from + lane; ok && j < to; j += 32) same = same && cf[j] == cf[from];
+          same = __all_sync(0xFFFFFFFFu, same);
+          const uint64_t one_f = ok && from < to ? ptx::pack2(cf[from], cf[from]) : 0;
           for (int b = 0; b < run && ok; ++b, ++sn) {
             const uint32_t ss = sn % kSlots;
             if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), sn / kSlots & 1)))) break;
@@ -389,40 +438,54 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + C::kSumCol + ss * kRows;
             uint64_t total = 0;      // over the even and over the odd columns
             // four logits as weights, added up
-            auto add = [&](auto masked, const float* v, int j) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cf + j), l = *reinterpret_cast<const ulonglong2*>(cf + kRows + j);
-              const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(cf + 2 * kRows + j);
+            auto add = [&](auto plain, const float* v, int j) {      // plain: one factor, all seen
+              constexpr bool kPlain = decltype(plain)::value;
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(cf + kRows + j);
+              ulonglong2 f;
+              if constexpr (kPlain) f = make_ulonglong2(one_f, one_f);
+              else f = *reinterpret_cast<const ulonglong2*>(cf + j);
               float w[4];
               ptx::unpack2(ptx::fma2(ptx::pack2(v[0], v[1]), f.x, l.x), w[0], w[1]);
               ptx::unpack2(ptx::fma2(ptx::pack2(v[2], v[3]), f.y, l.y), w[2], w[3]);
 #pragma unroll
               for (int k = 0; k < 4; ++k) w[k] = ptx::ex2_approx(w[k]);
-              if constexpr (decltype(masked)::value) {
-                const int4 i = *reinterpret_cast<const int4*>(cf + 3 * kRows + j);
+              if constexpr (!kPlain) {
+                const int4 i = *reinterpret_cast<const int4*>(cf + 2 * kRows + j);
                 w[0] = sees(a, view, i.x, e) ? w[0] : 0.f;
                 w[1] = sees(a, view, i.y, e) ? w[1] : 0.f;
                 w[2] = sees(a, view, i.z, e) ? w[2] : 0.f;
                 w[3] = sees(a, view, i.w, e) ? w[3] : 0.f;
               }
-              total = ptx::fma2(ptx::pack2(w[0], w[1]), g.x, total);
-              total = ptx::fma2(ptx::pack2(w[2], w[3]), g.y, total);
+              total = ptx::add2(total, ptx::add2(ptx::pack2(w[0], w[1]), ptx::pack2(w[2], w[3])));
             };
+            const bool plain = whole && same;
             int j = from;
-            if (whole) {
-              for (; j + 32 <= to; j += 32) {
-                float v[32];
-                ptx::tmem_ld32(at + j, v);
+            if (plain && j + 64 <= to) {      // 32 columns are on their way while others are added up
+              float v0[32], v1[32];
+              ptx::tmem_ld32(at + j, v0);
+              ptx::tmem_wait_ld();
+              ptx::tmem_ld32(at + j + 32, v1);
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) add(std::true_type(), v0 + k, j + k);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) add(std::true_type(), v1 + k, j + 32 + k);
+              j += 64;
+            }
+            if (plain)
+              for (; j < to; j += 8) {
+                float v[8];
+                tmem_ld8(at + j, v);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) add(std::false_type(), v + k, j + k);
+                for (int k = 0; k < 8; k += 4) add(std::true_type(), v + k, j + k);
               }
-            }
             for (; j < to; j += 8) {
               float v[8];
               tmem_ld8(at + j, v);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 8; k += 4) add(std::true_type(), v + k, j + k);
+              for (int k = 0; k < 8; k += 4) add(std::false_type(), v + k, j + k);
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -435,31 +498,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
           if (lane == 0) ptx::mbar_arrive(rows_free(rs));
         }
       } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-          uint32_t kn = key_n, rn = row_n, sn = sum_n;
-          bool ok = true;
-          for (int hc = 0; hc < a.H * chunks && ok; ++hc, ++rn) {
-            const int c = hc % chunks, cols = min(kRows, padded - c * kRows);
-            const uint32_t rs = rn % kSlots, idesc = idesc_f16(cols);
-            if (!(ok = wait(rows_full(rs), rn / kSlots & 1))) break;
-            uint64_t rows_at[C::kSlabs];         // a step of 16 dims is two further on (of 16 bytes)
+        // the whole warp runs the loops, so that what the products take is known to be the same in all lanes
+        uint32_t kn = key_n, rn = row_n, sn = sum_n;
+        bool ok = true;
+        for (int hc = 0, c = 0; hc < a.H * chunks && ok; ++hc, ++rn) {
+          const int cols = min(kRows, padded - c * kRows);
+          if (++c == chunks) c = 0;
+          const uint32_t rs = rn % kSlots, idesc = idesc_f16(cols);
+          if (!(ok = __all_sync(0xFFFFFFFFu, wait(rows_full(rs), rn / kSlots & 1)))) break;
+          uint64_t rows_at[C::kSlabs];         // a step of 16 dims is two further on (of 16 bytes)
 #pragma unroll
-            for (int s = 0; s < C::kSlabs; ++s) rows_at[s] = ptx::sdesc_kmajor_sw128(ptx::smem_u32(smem + rs * C::kRowBytes) + s * cols * 128);
-            for (int b = 0; b < run; ++b, ++kn, ++sn) {
-              const uint32_t ks = kn % C::kKeySlots, ss = sn % kSlots;
-              if (!(ok = wait(sums_free(ss), (sn / kSlots & 1) ^ 1) && wait(keys_full(ks), kn / C::kKeySlots & 1))) break;
-              ptx::tc_fence_after();
-              const uint32_t to = tmem + C::kSumCol + ss * kRows, keys = tmem + ks * C::kKeyCols;
+          for (int s = 0; s < C::kSlabs; ++s) rows_at[s] = ptx::sdesc_kmajor_sw128(ptx::smem_u32(smem + rs * C::kRowBytes) + s * cols * 128);
+          for (int b = 0; b < run; ++b, ++kn, ++sn) {
+            const uint32_t ks = kn % C::kKeySlots, ss = sn % kSlots;
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_free(ss), (sn / kSlots & 1) ^ 1) && wait(keys_full(ks), kn / C::kKeySlots & 1)))) break;
+            ptx::tc_fence_after();
+            const uint32_t to = tmem + C::kSumCol + ss * kRows, keys = tmem + ks * C::kKeyCols;
+            if (ptx::elect_one()) {
               mma_f16_ts<false>(to, keys, rows_at[0], idesc);
 #pragma unroll
               for (int k = 1; k < kDim / 16; ++k) mma_f16_ts<true>(to, keys + k * 8, rows_at[k / 4] + k % 4 * 2, idesc);
               ptx::mma_commit(keys_free(ks));
               ptx::mma_commit(sums_full(ss));
+              if (b == run - 1) ptx::mma_commit(rows_free(rs));
             }
-            if (ok) ptx::mma_commit(rows_free(rs));
+            __syncwarp();
           }
-          products = sn;
         }
+        if (lane == 0) products = sn;
         __syncwarp();
       } else {
         // ---- copies of the rows and their constants
@@ -471,7 +537,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const int h = hc / chunks, c = hc - h * chunks, cols = min(kRows, padded - c * kRows);
             if (!wait(rows_free(rs), (n / kSlots & 1) ^ 1)) break;
             const int64_t row0 = region + (int64_t)h * padded;
-            ptx::mbar_arrive_expect_tx(rows_full(rs), cols * (kDim * 2 + 16));
+            ptx::mbar_arrive_expect_tx(rows_full(rs), cols * (kDim * 2 + 12));
             for (int s = 0; s < C::kSlabs; ++s)
               ptx::bulk_load(ptx::smem_u32(smem + rs * C::kRowBytes) + s * cols * 128,
                              m.q + (row0 * kDim + ((int64_t)s * padded + c * kRows) * 64) * 2, cols * 128, rows_full(rs));
@@ -479,8 +545,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const int64_t at = row0 + c * kRows;
             ptx::bulk_load(dst, m.f + at, cols * 4, rows_full(rs));
             ptx::bulk_load(dst + kRows * 4, m.lse + at, cols * 4, rows_full(rs));
-            ptx::bulk_load(dst + kRows * 8, m.lift + at, cols * 4, rows_full(rs));
-            ptx::bulk_load(dst + kRows * 12, m.i + at, cols * 4, rows_full(rs));
+            ptx::bulk_load(dst + kRows * 8, m.i + at, cols * 4, rows_full(rs));
             row_copies = n + 1;
           }
         }
@@ -534,8 +599,8 @@ cudaError_t launch(const KvAccumulateArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int per = int(std::min<int64_t>(((int64_t)a.H * pad16(a.gamma * a.max_q) + 7) / 8, 4 * kPlanSMs));
-  e = launch_kernel(kv_accumulate_rows_kernel<T, kDim>, dim3(per, std::min(a.R, std::max(1, 8 * kPlanSMs / per))), 256, 0, s, false, a, m);
+  const int per = int(std::min<int64_t>((int64_t)a.H * ((pad16(a.gamma * a.max_q) + kRows - 1) / kRows), 4 * kPlanSMs));
+  e = launch_kernel(kv_accumulate_rows_kernel<T, kDim>, dim3(per, std::min(a.R, std::max(1, 2 * kPlanSMs / per))), 32 * kRowWarps, 0, s, false, a, m);
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)a.R * ((((int64_t)a.max_pages << a.page_shift) + kBlock - 1) / kBlock);
   return launch_kernel(kv_accumulate_tc_kernel<kDim>, dim3(unsigned(std::min<long long>(kPlanSMs, blocks))), kTcThreads, TcShape<kDim>::kSmem, s, true, a, m);
@@ -544,7 +609,7 @@ cudaError_t launch(const KvAccumulateArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t kv_accumulate_tc_workspace_bytes(int H, int gamma, int num_q, int R, int d) {
-  return size_t(rows_mem(nullptr, H, gamma, num_q, R, d).rows) * (2 * d + 16);
+  return size_t(rows_mem(nullptr, H, gamma, num_q, R, d).rows) * (2 * d + 12);
 }
 
 cudaError_t launch_kv_accumulate_tc(const KvAccumulateArgs& a, bool f16, cudaStream_t s) {
