@@ -16,6 +16,7 @@ import numpy as np
 import torch
 
 from . import _binding as B
+from .rotary import RotaryEmbedding
 
 
 @dataclasses.dataclass
@@ -30,6 +31,8 @@ class SelectOutputs:
     hidden_out: Optional[torch.Tensor] = None
     pos_out: Optional[torch.Tensor] = None
     slot_out: Optional[torch.Tensor] = None
+    q_out: Optional[torch.Tensor] = None   # with a rotary embedding: q and k turned by their positions
+    k_out: Optional[torch.Tensor] = None
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -95,9 +98,18 @@ class TokenSelector:
                       slots: Optional[torch.Tensor] = None, layer_id: int = 0,
                       history: Optional[torch.Tensor] = None, history_len: Optional[torch.Tensor] = None,
                       params: Optional[B.UpfParams] = None, kv_of_q: Optional[Sequence[int]] = None,
-                      out: Optional[SelectOutputs] = None) -> SelectOutputs:
-        """q: bf16 [T, H_q, d] (rows may be strided), k: bf16 [T, H_kv, d]; hidden: [T, hidden]."""
+                      out: Optional[SelectOutputs] = None,
+                      rope: Optional[RotaryEmbedding] = None) -> SelectOutputs:
+        """q: bf16 [T, H_q, d] (rows may be strided), k: bf16 [T, H_kv, d]; hidden: [T, hidden].
+
+        ``rope``: q and k come before their rotary positions; they are turned by ``positions`` first (into
+        ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored."""
         params = params or B.make_params()
+        if rope is not None:
+            if positions is None:
+                raise ValueError("rope needs positions")
+            turned = None if out is None else (out.q_out, out.k_out)
+            q, k = rope.apply(q, k, positions, out=turned)
         batch, keep = B.make_batch(cu_seqlens_dev.data_ptr(), cu_seqlens_host, num_q_heads, num_kv_heads,
                                    head_dim, kv_of_q)
         nbytes = B.upf_workspace_bytes(batch, params)
@@ -112,6 +124,8 @@ class TokenSelector:
             total_kept=_ptr(out.total_kept), layer_id=layer_id,
             history_cap=0 if history is None else history.shape[1], history=_ptr(history),
             history_len=_ptr(history_len))
+        if rope is not None:
+            out.q_out, out.k_out = q, k
         stream = torch.cuda.current_stream(self.device).cuda_stream
         B.upf_select_tokens(self.ctx, batch, params, q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
                             _ptr(out.scores), _ptr(out.block_scores), _ptr(out.keep_bits), _ptr(out.kept_count),

@@ -221,3 +221,59 @@ def test_what_the_front_end_refuses():
     for bad in (dict(head_dim=96), dict(head_dim=128, rotary_dim=3), dict(head_dim=128, scaling="yarn", factor=2.0)):
         with pytest.raises(B.UpfError):
             rotation(**bad)
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_drawn_rotations(seed):
+    g = np.random.default_rng(800 + seed)
+    d = int(g.choice([64, 128, 256]))
+    n = 2 * int(g.integers(1, d // 2 + 1)) if seed % 2 else 16 * int(g.integers(1, d // 16 + 1))
+    T, heads = int(np.exp(g.uniform(0, np.log(3000)))), [int(x) for x in g.integers(0, 12, 2)]
+    heads[0] += sum(heads) == 0
+    interleaved, inverse = bool(g.integers(2)), bool(g.integers(2))
+    rope = rotation(d, n, base=float(10 ** g.uniform(1, 7)), interleaved=interleaved,
+                    magnitude=float(g.uniform(0.5, 2)))
+    pos = places(T, seed, 2 ** 40)
+    q, k = (rand((T, h, d), BF16 if seed % 3 else F16, seed) if h else None for h in heads)
+    for x, y in zip((q, k), rope.apply(q, k, pos, inverse=inverse)):
+        if x is not None:
+            check(y, x, rope, pos, interleaved, inverse)
+
+
+def test_rows_past_32_bits_of_bytes():
+    """Rows 4 GiB apart."""
+    rope = rotation(64)
+    room = torch.empty(2 ** 32 + 256, dtype=BF16, device=DEV)
+    x = room.as_strided((3, 2, 64), (2 ** 31, 64, 1))
+    x.copy_(rand((3, 2, 64), BF16, 1))
+    pos = torch.tensor([5, 2 ** 40, -3], device=DEV)
+    want = rope.apply(x.contiguous(), None, pos)[0]
+    assert rope.apply(x, None, pos, out=(x, None))[0] is x
+    assert torch.equal(x, want)
+
+
+def test_selection_of_rows_that_are_not_turned_yet():
+    from sparse_long_context_tail_gb300.selector import TokenSelector
+    T, Hq, H, d = 700, 8, 2, 128
+    rope, sel = rotation(d, 64), TokenSelector(0)
+    rows = rand((T, Hq + 2 * H, d), BF16, 3)
+    q, k = rows[:, :Hq], rows[:, Hq:Hq + H]
+    pos = places(T, 4)
+    cu = np.array([0, 300, T], np.int32)
+    cu_dev = torch.from_numpy(cu).to(DEV)
+    kw = dict(hidden=rows.reshape(T, -1), positions=pos, params=B.make_params(32, 16, 32, 32, 0.6))
+    q2, k2 = rope.apply(q, k, pos)
+    want = sel.select_tokens(q2, k2, cu, cu_dev, Hq, H, d, **kw)
+    got = sel.select_tokens(q, k, cu, cu_dev, Hq, H, d, rope=rope, **kw)
+    assert want.q_out is None and torch.equal(got.q_out, q2) and torch.equal(got.k_out, k2)
+    n = int(want.total_kept)
+    assert 0 < n < T and torch.equal(got.scores, want.scores) and int(got.total_kept) == n
+    assert torch.equal(got.kept_index[:n], want.kept_index[:n]) and torch.equal(got.pos_out[:n], want.pos_out[:n])
+    assert torch.equal(got.hidden_out[:n], want.hidden_out[:n])
+    # in place
+    got.q_out, got.k_out = q, k
+    again = sel.select_tokens(q, k, cu, cu_dev, Hq, H, d, rope=rope, out=got, **kw)
+    assert again is got and again.q_out is q and torch.equal(q, q2) and torch.equal(k, k2) and int(got.total_kept) == n
+    with pytest.raises(ValueError, match="positions"):
+        sel.select_tokens(q, k, cu, cu_dev, Hq, H, d, rope=rope, params=kw["params"])
+    assert sel.status() == 0
