@@ -509,7 +509,7 @@ size_t upf_kv_accumulate_workspace_bytes(const upf_kv_cache* cache, const upf_kv
  *    max_pages_out pages and may name a page of page_table only in the same place of the same
  *    request; no other page may be named twice.  All entries of requests that keep theirs are
  *    copied too.  Pages that several requests share have to be evicted into others.
- * kv_len_out: device int32 [R]: the new lengths; may be kv_len.
+ * kv_len_out: device int32 [R]: the new lengths; kv_len itself, or an array that does not overlap it.
  * weights: device float32, request r entry e at r*weights_stride + e, `weights_cols` a row.
  * weights_out: (same with its own stride and cols; may be weights, with its stride): the kept entries'
  *    weights, together, and zeros from the new length up to the old one.  Requests whose entries all stay

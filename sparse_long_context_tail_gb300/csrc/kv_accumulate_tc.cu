@@ -61,9 +61,10 @@ __host__ __device__ inline RowsMem rows_mem(void* ws, int H, int gamma, int num_
 // A CTA per chunk of rows of a request and kv head, the padding's among them.
 //
 // Rows are divided by a power of two so that f16 holds them: one of the whole chunk, which makes its largest element
-// 2^14 to 2^15, so that a logit factor is the same for all columns.  f16 reaches 2^-24, so elements down to
-// 2^-16 of a row 2^15 smaller than the largest keep eight bits.  Where rows are further apart
-// each has its own power.
+// 2^14 to 2^15, so that a logit factor is the same for all columns (32 queries of 131072 entries: 57 us with a factor
+// a column, 53 with one).  f16 ends at 2^-24, so the rounding of a row 2^14 smaller, whose
+// largest element is 1 to 2, is 2^-25 of that at most, as it is where each row has its own power.
+// Rows further apart do have their own.
 template <typename T, int kDim>
 __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(const KvAccumulateArgs a, const RowsMem m) {
   constexpr const T* kT = nullptr;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
         atomicMin(&least, lo);
       }
       __syncthreads();
-      const bool same = most < least || most - least <= 15;       // none, or near one another
+      const bool same = most < least || most - least <= kTop;     // none, or near one another
 #pragma unroll
       for (int y = 0; y < kOwn; ++y) {
         const int rho = row0 + warp + y * kRowWarps;
@@ -576,6 +577,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
     }
     if (r >= a.R) break;
   }
+  // the workspace is the caller's again only when the rows' launch is over, whether or not this CTA had any work
+  if (tid == 32 * (kTcWarps - 1) && !rows_waited) pdl_wait();
   __syncthreads();
   // a wait that ran out leaves copies and products on their way: they are waited for as long as waits may take by default
   if (failed && tid == 0)

@@ -863,6 +863,8 @@ upf_status check_eviction(const upf_kv_cache* c, const upf_kv_eviction* x, bool 
       !rows_disjoint(x->weights, x->weights_stride * 4, (int64_t)x->weights_cols * 4, x->weights_out,
                      x->weights_out_stride * 4, (int64_t)x->weights_out_cols * 4, x->num_reqs))
     return fail(UPF_ERR_INVALID_ARG, "weights_out must be weights (with its stride) or not overlap it");
+  if (x->kv_len_out != x->kv_len && !rows_disjoint(x->kv_len, 4, 4, x->kv_len_out, 4, 4, x->num_reqs))
+    return fail(UPF_ERR_INVALID_ARG, "kv_len_out must be kv_len or not overlap it");
   if (x->kept && x->kept_stride < x->budget) return fail(UPF_ERR_INVALID_ARG, "kept_stride must be >= budget");
   return UPF_OK;
 }

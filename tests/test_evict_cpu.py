@@ -80,7 +80,8 @@ POINTERS = [(dict(kv_len=0), "kv_len"), (dict(kv_len_out=0), "kv_len_out"), (dic
             (dict(weights=0), "weights"), (dict(weights=0x10002), "weights"), (dict(weights_cols=0), "cols"),
             (dict(weights_cols=65), "cols"), (dict(weights_out=0), "weights_out"), (dict(weights_out_cols=65), "cols"),
             (dict(weights_out_stride=80), "weights_out"), (dict(weights_out=0x10004), "weights_out"),
-            (dict(weights_out=0x10000 + 256), "weights_out"), (dict(kept=0x400, kept_stride=31), "kept_stride")]
+            (dict(weights_out=0x10000 + 256), "weights_out"), (dict(kv_len_out=0x104), "kv_len_out"),
+            (dict(kv_len_out=0xFE), "kv_len_out"), (dict(kept=0x400, kept_stride=31), "kept_stride")]
 
 
 @pytest.mark.parametrize("bad,word", SIZES)
@@ -116,6 +117,7 @@ def test_eviction_workspaces():
 # rows side by side in one array, and another array: these get as far as the missing context
 @pytest.mark.parametrize("good", [dict(weights_stride=200, weights_out_stride=200, weights_out=0x10000 + 400),
                                   dict(weights_out=0x20000, weights_out_stride=90), dict(num_reqs=1, weights_out_stride=100),
+                                  dict(kv_len_out=0x108), dict(kv_len_out=0xF8),
                                   dict(page_table_out=0x200, page_stride_out=4, max_pages_out=4)])
 def test_evictions_that_are_not_refused(good):
     with pytest.raises(B.UpfError, match="context"):

@@ -90,8 +90,10 @@ def close(got, old, decay, drawn, slack, d, rows):
 
 
 def check_accumulate(b, news, Hq, dtype=BF16, window=0, sinks=0, decay=1.0, scale=None, kv_of_q=None, plain=False, seed=5,
-                     q_scale=1.0):
+                     q_scale=1.0, rows=None):
     q, cu = queries(news, Hq, b.d, dtype, seed, q_scale * 2.0 ** -b.k_exp)
+    if rows is not None:          # what each row is multiplied by
+        q = q * rows.to(q)[:, :, None]
     cuq = None if plain else cu
     kw = dict(cu_q=cuq, max_q_len=max(max(news), 1), window=window, sinks=sinks, softmax_scale=scale, kv_of_q=kv_of_q)
     lse = b.cache.attend(q, b.table, b.kv_len, b.page, **kw).lse
@@ -160,6 +162,59 @@ def test_page_sizes(page):
 def test_many_requests():
     lens = [(7 * i) % 40 for i in range(700)]
     check_accumulate(Batch(lens, 1, 64, seed=10), [i % 3 for i in range(700)], 2)
+
+
+@pytest.mark.parametrize("Hq,H,d", [(5, 5, 64), (7, 7, 128), (24, 24, 64), (25, 25, 64), (32, 32, 128), (64, 64, 64), (49, 7, 128),
+                                    (24, 3, 256), (200, 100, 64), (256, 32, 64), (11, 11, 256)])
+def test_few_rows_of_any_number_of_heads(Hq, H, d):
+    check_accumulate(Batch([130, 1, 700, 16], H, d, seed=50), [1] * 4, Hq, window=300, sinks=20)
+
+
+@pytest.mark.parametrize("Hq,H,d", [(9, 1, 64), (64, 1, 128), (128, 1, 256), (256, 1, 64), (256, 2, 128), (20, 2, 256), (45, 5, 64)])
+def test_many_rows_of_one_new_token(Hq, H, d):
+    check_accumulate(Batch([130, 1, 2500, 16, 0, 129], H, d, seed=51), [1] * 6, Hq, plain=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("low", [-14, -15, -40])
+@pytest.mark.parametrize("news,Hq", [([3, 20, 1], 16), ([70, 5, 33], 8), ([1, 1, 1], 4)])
+def test_rows_far_apart(news, Hq, low, d):
+    """Largest elements of a request's rows 2^14 apart, just further, and much further; some rows of zeros."""
+    g = torch.Generator().manual_seed(52)
+    rows = torch.exp2(torch.randint(low, 1, (sum(news), Hq), generator=g).float())
+    rows[torch.rand(rows.shape, generator=g) < 0.1] = 0.0
+    check_accumulate(Batch([300, 40, 129], 2, d, seed=53), news, Hq, rows=rows)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_drawn_batches(seed):
+    g = np.random.default_rng(600 + seed)
+    d, H = int(g.choice([64, 128, 256])), int(g.integers(1, 9))
+    Hq = H * int(g.integers(1, 9))
+    R = int(g.integers(1, 9))
+    lens = [int(x) for x in np.floor(np.exp(g.uniform(0, np.log(3000), R)))]
+    most = int(g.choice([1, 2, 6, 60]))
+    news = [int(x) for x in g.integers(0, most + 1, R)]
+    if sum(news) == 0:
+        news[0] = 1
+    window = int(g.choice([0, 0, 1, 17, 128, 500]))
+    b = Batch(lens, H, d, page=int(g.choice([16, 32, 128])), dtype=BF16 if seed % 2 else F16, seed=seed, k_exp=int(g.integers(-2, 3)))
+    check_accumulate(b, news, Hq, dtype=BF16 if seed % 2 else F16, window=window, sinks=int(g.integers(0, 40)),
+                     decay=float(g.choice([0.0, 0.5, 1.0])), seed=seed)
+
+
+def test_a_wait_of_an_accumulation_that_runs_out_is_reported():
+    """With a limit of one cycle the kernel gives up and says so; the context stays usable."""
+    b = Batch([3000, 200], 2, 128, seed=54)
+    q, cu = queries([40, 9], 8, 128, BF16, 55)
+    kw = dict(cu_q=cu, max_q_len=40)
+    lse = b.cache.attend(q, b.table, b.kv_len, 16, **kw).lse
+    assert b.cache.status() == 0
+    B.upf_set_wait_limit(b.cache.ctx, 1)
+    b.cache.accumulate(q, lse, b.table, b.kv_len, 16, torch.zeros(2, 3000, device=DEV), **kw)
+    assert b.cache.status() == 6
+    B.upf_set_wait_limit(b.cache.ctx, 0)
+    check_accumulate(b, [40, 9], 8)
 
 
 def test_weights_of_a_row_add_up_to_one():
@@ -266,6 +321,67 @@ def test_weights_with_strides_and_accumulate_in_a_graph():
         assert torch.equal(w, 2 * once)
 
 
+def test_two_graphs_of_many_rows_on_two_streams():
+    b = Batch([700, 90], 2, 64, seed=56)
+    graphs, want = [], []
+    for i, news in enumerate(([20, 3], [2, 31])):
+        q, cu = queries(news, 8, 64, BF16, 57 + i)
+        kw = dict(cu_q=cu, max_q_len=31)
+        lse = b.cache.attend(q, b.table, b.kv_len, 16, **kw).lse
+        want.append(b.cache.accumulate(q, lse, b.table, b.kv_len, 16, torch.zeros(2, 704, device=DEV), **kw))
+        w = torch.zeros(2, 704, device=DEV)
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            w.zero_()
+            b.cache.accumulate(q, lse, b.table, b.kv_len, 16, w, **kw)
+        graphs.append((graph, stream, w, (q, cu, lse)))
+    for _ in range(20):
+        for graph, stream, _, _ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(graphs, want):
+            assert torch.equal(x[2], y)
+            x[2].fill_(9.0)
+    assert b.cache.status() == 0
+
+
+def test_a_cache_and_weights_past_32_bits_of_bytes():
+    """The same entries near the start and at the far end of a cache of 5 GB, weights 8 GiB apart."""
+    from sparse_long_context_tail_gb300.kvcache import QuantKVCache
+    H, d, n, page = 8, 128, 300, 16
+    cache = QuantKVCache(1 << 22, H, d)
+    assert cache.storage.numel() > 2 ** 32
+    need, last = -(-n // page), (1 << 22) // page - 1
+    near, far = torch.arange(need), last - torch.arange(need)
+    table = torch.stack([near, far]).int().to(DEV)
+    g = torch.Generator().manual_seed(58)
+    k, v = torch.randn(n, H, d, generator=g).to(BF16).to(DEV), torch.randn(n, H, d, generator=g).to(BF16).to(DEV)
+    e = torch.arange(n, device=DEV)
+    slots = [table[r, e // page].long() * page + e % page for r in range(2)]
+    for s in slots:
+        cache.write(k, v, s)
+    kv_len = torch.full((2,), n, dtype=torch.int32, device=DEV)
+    room = torch.empty(2 ** 31 + 512, device=DEV)
+    w = room.as_strided((2, 304), (2 ** 31, 1))
+    for news in (1, 5):
+        q, _ = queries([news], 32, d, BF16, 59)
+        q = torch.cat([q, q])
+        kw = dict(cu_q=torch.tensor([0, news, 2 * news], dtype=torch.int32, device=DEV), max_q_len=news)
+        lse = cache.attend(q, table, kv_len, page, **kw).lse
+        w.zero_()
+        cache.accumulate(q, lse, table, kv_len, page, w, **kw)
+        assert torch.equal(w[0], w[1]) and float(w[0, :n].sum()) > 31 * news and not w[:, n:].any()
+    old = w.clone()
+    kept = cache.evict(w, table, kv_len, page, 100, recent=10)
+    assert cache.status() == 0 and torch.equal(kept[0], kept[1]) and kv_len.tolist() == [100, 100]
+    want = K.evict(old[0, :n].tolist(), 100, 100, 0, 10)
+    assert kept[0].tolist() == want and torch.equal(w[0], w[1])
+    (k0, v0), (k1, v1) = (cache.read(s[:100]) for s in slots)
+    assert torch.equal(k0, k1) and torch.equal(v0, v1)
+
+
 # ------------------------------------------------------------------ eviction --
 
 def weights_of(lens, cols, seed, kind="mixed"):
@@ -369,6 +485,21 @@ def test_long_requests(n, budget, H, d, page, kind):
 def test_many_requests_are_cut():
     lens = [(13 * i) % 90 for i in range(1500)]
     check_evict(Batch(lens, 1, 64, seed=23), 33, 40, 1, 5)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_evictions(seed):
+    g = np.random.default_rng(700 + seed)
+    d, H, R = int(g.choice([64, 128, 256])), int(g.integers(1, 9)), int(g.integers(1, 12))
+    lens = [int(x) for x in np.floor(np.exp(g.uniform(0, np.log(9000), R)))]
+    budget = int(np.exp(g.uniform(0, np.log(max(lens) + 1))))
+    sinks = int(g.integers(0, budget + 1))
+    recent = int(g.integers(0, budget - sinks + 1)) if seed % 3 else 0
+    elsewhere = bool(seed % 2)
+    trigger = budget + int(g.integers(0, 50))
+    page = int(g.choice([16, 64]))
+    b = Batch(lens, H, d, page=page, seed=seed, spare=R * -(-min(trigger, max(lens)) // page) + 3)
+    check_evict(b, budget, trigger, sinks, recent, str(g.choice(["mixed", "near", "tiny", "zero"])), elsewhere, seed=seed)
 
 
 def test_evicting_again_and_again():
