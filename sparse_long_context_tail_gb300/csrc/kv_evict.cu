@@ -33,7 +33,7 @@ struct KvEvictPlan {
 namespace {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16, kManyCluster = 8;    // of few requests, of many
 constexpr int kUnroll = 2;
 constexpr int kPasses = 3, kBins = 2048, kOwnBins = 4;   // digits; bins of a digit; of a thread
 constexpr int kMaxHeld = 9;           // fours of weights of a thread that stay in shared memory (144 KB a CTA)
@@ -51,22 +51,21 @@ __device__ __forceinline__ int64_t slot_of(const int32_t* row, int e, int shift,
   return page >= 0 && slot < num_slots ? slot : -1;
 }
 
-// This variable in another CTA of the cluster, which has written it before a barrier of the cluster.
-__device__ __forceinline__ int32_t ld_cluster(const int32_t* mine, uint32_t rank) {
-  int32_t v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::mapa_shared(ptx::smem_u32(mine), rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ int2 ld_cluster2(const int32_t* mine, uint32_t rank) {
-  int2 v;
-  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
+// In the shared memory of the cluster's CTA `rank`, at the place that `mine` has in this one's.
+__device__ __forceinline__ int4 ld_cluster4(const int32_t* mine, uint32_t rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(ptx::mapa_shared(ptx::smem_u32(mine), rank))
                : "memory");
   return v;
 }
 __device__ __forceinline__ void add_cluster(int32_t* mine, uint32_t rank, int32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(ptx::mapa_shared(ptx::smem_u32(mine), rank)), "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ void or_cluster(int32_t* mine, uint32_t rank, int32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(ptx::mapa_shared(ptx::smem_u32(mine), rank)), "r"(v)
                : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -98,7 +97,7 @@ __device__ __forceinline__ int block_scan(int v, int* scratch) {
 static_assert(kSelWarps <= 32, "a warp adds up the warps' sums");
 
 // A cluster of `ctas` CTAs a request.  A warp has a run of entries of its own, `held` times 128 of them
-// in shared memory through all passes (327680 entries of a request; of more, the rest is read again).
+// in shared memory through all passes (294912 entries with eight CTAs, 589824 with 16; of more, the rest is read again).
 // What bounds it is the instructions of few SMs: four entries a lane at a time.  Loops stay rolled: the instructions of a launch run
 // a few times only, so that fetching long unrolled ones costs more than it saves (weights in registers,
 // 16 times unrolled: 22 us for 1088 entries, 10 rolled).
@@ -106,9 +105,10 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
                                                                     const int held) {
   extern __shared__ int4 held_bits[];    // [warp][held at most][lane], and before it, in a cluster, [kPasses][kBins] sums
   __shared__ __align__(16) int32_t hist[kPasses][kBins];     // entries of this CTA by digit
-  __shared__ __align__(8) int32_t counts[2];
-  __shared__ int32_t scratch[kPasses][32], found[kPasses][2], bad_here, warp_counts[kSelWarps][2];
-  int32_t* const sums = ctas > 1 ? reinterpret_cast<int32_t*>(held_bits) : &hist[0][0];    // of all CTAs
+  __shared__ int32_t scratch[kPasses][32], found[kPasses][2], warp_counts[kSelWarps][2];
+  __shared__ int32_t bad_any, counts[2];                     // of all CTAs; of those before this one
+  // of all CTAs, each CTA a run of the bins
+  int32_t* const sums = ctas > 1 ? reinterpret_cast<int32_t*>(held_bits) : &hist[0][0];
   const uint32_t rank = blockIdx.x % ctas;   // in the request's cluster
   const int r = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = rank * kSelThreads + tid, stride = ctas * kSelThreads;   // of the cluster's threads
@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     if (ctas > 1) ptx::cluster_sync();
     else __syncthreads();
   };
-  auto of_cta = [&](const int32_t* mine, uint32_t c) { return ctas > 1 ? ld_cluster(mine, c) : *mine; };
   const int n = a.kv_len[r];
   const float* const w = a.w + r * a.w_stride;
   const int32_t* const row = a.table + r * a.table_stride;
@@ -124,8 +123,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     if (ctas > 1) reinterpret_cast<int4*>(sums)[i] = make_int4(0, 0, 0, 0);
   }
-  if (tid == 0) bad_here = 0;
-  if (ctas > 1) cluster_arrive();        // the others may add to the sums
+  if (tid == 0) bad_any = counts[0] = counts[1] = 0;
+  if (ctas > 1) cluster_arrive();        // the others may add to these
   pdl_trigger();
   // the second launch's ticket and marks
   if (r == 0 && first == 0) *a.ticket = 0;
@@ -142,9 +141,17 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   // ---- the weights between the ends: a warp has 128 `its` of them, a lane four side by side at a time
   const int middle = n - a.sinks - a.recent, want = a.budget - a.sinks - a.recent;
   const float* const m = w + a.sinks;
-  const int its = cut ? (middle + 128 * kSelWarps * int(ctas) - 1) / (128 * kSelWarps * int(ctas)) : 0;
+  const int its = fine && cut ? (middle + 128 * kSelWarps * int(ctas) - 1) / (128 * kSelWarps * int(ctas)) : 0;
   const int from = (rank * kSelWarps + warp) * its * 128;           // under 2^30 + 2^18
   const int in_smem = min(its, held);
+  // what is looked at once is on its way first: a load takes longer than counting does
+  const int page = 1 << a.page_shift, ends = fine && cut ? a.sinks + a.recent : 0;
+  const int pages = fine && (cut || a.table_out) ? (n + page - 1) / page : 0;
+  const int pages_out = fine && a.table_out ? (left + page - 1) / page : 0;
+  const int32_t* const row_out = a.table_out + r * a.table_out_stride;
+  auto end_weight = [&](int e) { return __float_as_int(w[e < a.sinks ? e : e + middle]); };
+  const int32_t page0 = first < pages ? row[first] : 0, page_out0 = first < pages_out ? row_out[first] : 0;
+  const int end0 = first < ends ? end_weight(first) : 0;
   int4* const mine = held_bits + (ctas > 1 ? kPasses * kBins / 4 : 0) + warp * in_smem * 32;
   for (int k = lane; k < 128 * in_smem && from + k < middle; k += 32) copy_async4(reinterpret_cast<int32_t*>(mine) + k, m + from + k);
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -181,27 +188,26 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
     if (lane == 0 && zeros) atomicAdd(&hist[pass][0], zeros);
     if (ctas == 1) return;
-    // what this CTA has found goes to all CTAs' sums: few bins have entries
+    // what this CTA has found goes to the sums (all of them in every CTA, as 16 additions a bin: 3 us more at 131072 entries)
     __syncthreads();
     if (pass == 0) cluster_wait();
 #pragma unroll 1
     for (int i = tid; i <= mask; i += kSelThreads)
-      if (const int x = hist[pass][i])
-        for (uint32_t k = 0; k < ctas; ++k) add_cluster(sums + pass * kBins + i, k, x);
+      if (const int x = hist[pass][i]) add_cluster(sums + pass * kBins + i, uint32_t(i) * ctas >> bits, x);
   };
   __syncthreads();   // the bins are empty
+  int bad = 0;
   if (fine) {
-    const int page = 1 << a.page_shift;
-    int bad = 0;
-    if (cut || a.table_out)
-      for (int p = first; p < (n + page - 1) / page; p += stride) bad |= slot_of(row, p << a.page_shift, a.page_shift, a.num_slots) < 0;
-    if (a.table_out)
-      for (int p = first; p < (left + page - 1) / page; p += stride)
-        bad |= slot_of(a.table_out + r * a.table_out_stride, p << a.page_shift, a.page_shift, a.num_slots) < 0;
+    // is the p-th page, of `all` entries, outside the cache?  (The cache may end inside a page, behind the entries.)
+    auto bad_page = [&](int32_t id, int p, int all) {
+      return id < 0 || ((int64_t)id << a.page_shift) + min(page, all - (p << a.page_shift)) > a.num_slots;
+    };
+    for (int p = first; p < pages; p += stride) bad |= bad_page(p == first ? page0 : row[p], p, n);
+    for (int p = first; p < pages_out; p += stride) bad |= bad_page(p == first ? page_out0 : row_out[p], p, left);
     auto is_bad = [&](int bits) { return key_of(bits) < 0 || bits >= 0x7F800000; };
     if (cut) {
-      for (int e = first; e < a.sinks + a.recent; e += stride)
-        if (is_bad(__float_as_int(w[e < a.sinks ? e : e + middle]))) bad |= 2;
+      for (int e = first; e < ends; e += stride)
+        if (is_bad(e == first ? end0 : end_weight(e))) bad |= 2;
       // the lanes' own copies, and the others': as keys from here on
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
@@ -214,11 +220,14 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
       }
       if (want > 0) count(0, 0);
     }
-    if (bad) atomicOr(&bad_here, bad);
   }
   if (ctas > 1 && !(fine && cut && want > 0)) cluster_wait();   // as in the first count
+  if (bad) {
+    if (ctas == 1) atomicOr(&bad_any, bad);
+    for (uint32_t k = 0; ctas > 1 && k < ctas; ++k) or_cluster(&bad_any, k, bad);
+  }
   sync();
-  int bad = __reduce_or_sync(0xFFFFFFFFu, lane < ctas ? of_cta(&bad_here, lane) : 0);
+  bad = bad_any;
   if (!fine || bad) {
     if (first == 0) set_status(a.status, !fine || (bad & 1) ? UPF_ERR_INVALID_ARG : UPF_ERR_NONFINITE);
     fine = false;
@@ -239,7 +248,6 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
       list_w[j] = w[j];
       if (j % kChunk == 0) bounds[j / kChunk] = j;
     }
-    sync();   // no CTA leaves while others read its words
     return;
   }
   // ---- the least kept weight
@@ -261,7 +269,8 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
       if (first_bin >= 0)
 #pragma unroll
         for (int y = 0; y < kOwnBins; y += 4) {
-          const int4 v = *reinterpret_cast<const int4*>(sums + pass * kBins + first_bin + y);
+          const int32_t* const at = sums + pass * kBins + first_bin + y;
+          const int4 v = ctas > 1 ? ld_cluster4(at, uint32_t(first_bin) * ctas / bins) : *reinterpret_cast<const int4*>(at);
           c[y] = v.x, c[y + 1] = v.y, c[y + 2] = v.z, c[y + 3] = v.w;
           mine_all += v.x + v.y + v.z + v.w;
         }
@@ -300,18 +309,16 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0);
     if (warp == 0) {
       const int all_x = __reduce_add_sync(0xFFFFFFFFu, x), all_y = __reduce_add_sync(0xFFFFFFFFu, y);
-      if (lane == 0) {
-        counts[0] = all_x;
-        counts[1] = all_y;
+      if (lane > rank && lane < ctas) {
+        add_cluster(&counts[0], lane, all_x);
+        add_cluster(&counts[1], lane, all_y);
       }
     }
   }
   if (ctas > 1) {
-    ptx::cluster_sync();
-    const int2 c = lane < rank ? ld_cluster2(counts, lane) : make_int2(0, 0);
-    above += __reduce_add_sync(0xFFFFFFFFu, c.x);
-    equal += __reduce_add_sync(0xFFFFFFFFu, c.y);
-    cluster_arrive();   // this CTA has read the others' words
+    ptx::cluster_sync();      // the last: no CTA reads or writes another's words from here on
+    above += counts[0];
+    equal += counts[1];
   }
   // ---- the list
   auto put = [&](int j, int e, float x) {
@@ -354,7 +361,6 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     a.plan[r] = KvEvictPlan{n, left, 1, 0};
     a.len_out[r] = left;
   }
-  if (ctas > 1) cluster_wait();   // no CTA leaves while others read its words
 }
 
 __device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
@@ -487,11 +493,14 @@ cudaError_t launch_move(const KvEvictArgs& a, cudaStream_t s) {
   return launch_kernel(kv_evict_move_kernel<kDim>, dim3(unsigned(units)), move_threads(kDim), 0, s, true, a);
 }
 
-// CTAs of a request's cluster.
+// CTAs of a request's cluster: one per 8192 entries that there may be, up to kMaxCluster for at most four
+// requests.  A GPC holds one cluster of 16, and seven are there at once: 7 requests of 131072 entries take 34.5 us with
+// 16 CTAs and 35.5 with 8, 8 requests 54.8 and 37.2.  One request: 262144 entries 37 and 43 us, 10^6 82 and 126.
 int cluster_of(const KvEvictArgs& a) {
   const int64_t most = std::min<int64_t>((int64_t)a.max_pages << a.page_shift, a.w_cols);
+  const int limit = a.R <= 4 ? kMaxCluster : kManyCluster;
   int c = 1;
-  while (c < kMaxCluster && most > (int64_t)c * 8192) c *= 2;
+  while (c < limit && most > (int64_t)c * 8192) c *= 2;
   return c;
 }
 
@@ -527,8 +536,9 @@ cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = 1ull << (a.device & 63);
   if (a.device > 63 || !(ready.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxHeld * kSelThreads * 16 + kPasses * kBins * 4);
+    cudaError_t e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMaxHeld * kSelThreads * 16 + kPasses * kBins * 4);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }

@@ -83,7 +83,7 @@ class RotaryEmbedding:
         if t.shape[0] != T:
             raise ValueError(f"{name} has {t.shape[0]} tokens, positions {T}")
         if out is None:
-            out = torch.empty(t.shape, dtype=dtype, device=self.device)
+            out = torch.empty_like(t, memory_format=torch.contiguous_format)
             out_stride = t.shape[1] * self.head_dim
         elif out is t:
             out_stride = stride

@@ -587,6 +587,29 @@ def test_requests_that_cannot_be_cut_are_left_alone():
     assert len_out.tolist() == [100, 90, 80]
 
 
+def test_a_cache_that_ends_inside_a_page():
+    """48 slots and pages of 32: entries of page 1 are in the cache up to slot 48."""
+    from sparse_long_context_tail_gb300.kvcache import QuantKVCache
+    g = torch.Generator().manual_seed(62)
+    for in_place in (True, False):
+        for n, status in ((16, 0), (15, 0), (17, 1), (32, 1)):
+            cache = QuantKVCache(48, 2, 64)
+            k = torch.randn(32, 2, 64, generator=g).to(BF16).to(DEV)
+            cache.write(k, k, torch.arange(32, device=DEV))
+            table = torch.tensor([[1 if in_place else 0]], dtype=torch.int32, device=DEV)
+            kw = {} if in_place else dict(page_table_out=torch.ones_like(table))
+            kv_len = torch.tensor([n if in_place else 32], dtype=torch.int32, device=DEV)
+            w = weights_of([32], 32, 63, "rising")
+            storage = cache.storage.clone()
+            cache.evict(w, table, kv_len, 32, 10 if in_place else n, **kw)
+            assert cache.status() == status
+            if status:
+                assert torch.equal(cache.storage, storage)
+            elif not in_place:
+                want = cache.read(torch.arange(32 - n, 32, device=DEV))[0]
+                assert torch.equal(cache.read(torch.arange(32, 32 + n, device=DEV))[0], want)
+
+
 def test_captured_evictions():
     """One graph serves lengths below and above the trigger."""
     b = Batch([100, 70], 2, 64, seed=31)
