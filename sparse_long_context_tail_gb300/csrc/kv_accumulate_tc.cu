@@ -33,7 +33,7 @@ constexpr int kRows = 128;                     // most rows of a product
 constexpr int kRowWarps = 32;                  // of a CTA that makes them ready
 constexpr int kRun = 16;                       // blocks whose sums are in shared memory at once
 constexpr int kKeyWarps = 8, kSumWarps = 8, kMmaWarp = 16, kTcWarps = 18 /* the last one copies */, kTcThreads = 32 * kTcWarps;
-constexpr uint32_t kSlots = 2;                 // of rows, of sums (of keys: TcShape)
+constexpr uint32_t kSlots = 2;                 // of rows
 
 // The rows of all requests as operand B.  Those of request r and kv head h, padded to a multiple of 16, begin at row
 // first_row(r) + h * padded; of d dims every 64 are a slab of their own, 128 bytes a row.
@@ -160,9 +160,9 @@ struct TcShape {
   static constexpr int kConstBytes = kRows * 12;
   // Four slots of keys where tensor memory has room: a group works out its next block while the products with the last
   // are under way.
-  static constexpr uint32_t kKeySlots = kDim == 256 ? 2 : 4;
+  static constexpr uint32_t kKeySlots = kDim == 64 ? 4 : 2, kSumSlots = kDim == 256 ? 2 : 3;
   static constexpr int kSumCol = kKeySlots * kKeyCols;         // first TMEM column of the sums
-  static_assert(kSumCol + kSlots * kRows <= 512, "tensor memory");
+  static_assert(kSumCol + kSumSlots * kRows <= 512, "tensor memory");
   // a key warp's ring: of two tiles the codes, then the scales; 16-byte pieces
   static constexpr int kRowPieces = Shape<kDim>::kPart / 32;
   static constexpr int kRingItem = 2 * 9 * kDim, kAhead = kDim == 64 ? 6 : kDim == 128 ? 4 : 2, kRingBytes = kAhead * kRingItem;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
   uint8_t* const smem = smem_raw + (1024 - (ptx::smem_u32(smem_raw) & 1023)) % 1024;
   float* const sums = reinterpret_cast<float*>(smem + C::kSumAt);      // [2][kRun * kBlock]
   __shared__ Starts<kTcThreads> starts;
-  __shared__ __align__(8) uint64_t bars[2 * C::kKeySlots + 4 * kSlots];
+  __shared__ __align__(8) uint64_t bars[2 * C::kKeySlots + 2 * kSlots + 2 * C::kSumSlots];
   __shared__ uint32_t tmem_word;
   __shared__ int failed;
   __shared__ uint32_t row_copies, products;      // begun so far
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
   auto rows_full = [&](uint32_t s) { return bar1 + 8 * s; };
   auto rows_free = [&](uint32_t s) { return bar1 + 8 * (kSlots + s); };
   auto sums_full = [&](uint32_t s) { return bar1 + 8 * (2 * kSlots + s); };
-  auto sums_free = [&](uint32_t s) { return bar1 + 8 * (3 * kSlots + s); };
+  auto sums_free = [&](uint32_t s) { return bar1 + 8 * (2 * kSlots + C::kSumSlots + s); };
   if (tid == 0) {
     for (uint32_t s = 0; s < C::kKeySlots; ++s) {
       ptx::mbar_init(keys_full(s), 4);
@@ -260,8 +260,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
     for (uint32_t s = 0; s < kSlots; ++s) {
       ptx::mbar_init(rows_full(s), 1);
       ptx::mbar_init(rows_free(s), 1 + kSumWarps);
+    }
+    for (uint32_t s = 0; s < C::kSumSlots; ++s) {
       ptx::mbar_init(sums_full(s), 1);
-      ptx::mbar_init(sums_free(s), kSumWarps);
+      ptx::mbar_init(sums_free(s), kSumWarps / 2);
     }
     failed = 0;
     row_copies = products = 0;
@@ -414,25 +416,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
       } else if (warp < kKeyWarps + kSumWarps) {
-        // ---- weights: this warp's 32 entries, half of the columns
-        const int quarter = warp & 3, half = (warp - kKeyWarps) >> 2;
+        // ---- weights: this warp's 32 entries of its team's products, every other one
+        const int quarter = warp & 3, team = (warp - kKeyWarps) >> 2;
         uint32_t rn = row_n, sn = sum_n;
         bool ok = true;
         for (int hc = 0; hc < a.H * chunks && ok; ++hc, ++rn) {
           const int c = hc % chunks, cols = min(kRows, padded - c * kRows);
-          // columns [from, to) of the chunk, in steps of 8
-          const int mid = (cols / 2 + 7) / 8 * 8, from = half ? mid : 0, to = half ? cols : mid;
           const uint32_t rs = rn % kSlots;
           ok = __all_sync(0xFFFFFFFFu, wait(rows_full(rs), rn / kSlots & 1));
           const float* const cf = reinterpret_cast<const float*>(smem + C::kConstAt + rs * C::kConstBytes);
           // a broadcast from shared memory takes as long as it has words, so the factor is one where the rows allow it
           bool same = true;
-          for (int j = from + lane; ok && j < to; j += 32) same = same && cf[j] == cf[from];
+          for (int j = lane; ok && j < cols; j += 32) same = same && cf[j] == cf[0];
           same = __all_sync(0xFFFFFFFFu, same);
-          const uint64_t one_f = ok && from < to ? ptx::pack2(cf[from], cf[from]) : 0;
+          const uint64_t one_f = ok ? ptx::pack2(cf[0], cf[0]) : 0;
           for (int b = 0; b < run && ok; ++b, ++sn) {
-            const uint32_t ss = sn % kSlots;
-            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), sn / kSlots & 1)))) break;
+            if (int(sn & 1) != team) continue;
+            const uint32_t ss = sn % C::kSumSlots;
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), sn / C::kSumSlots & 1)))) break;
             ptx::tc_fence_after();
             const int e0 = blocks.entry(run0 + b), e = e0 + quarter * 32 + lane;
             const bool whole = all_seen(a, x, view, e0, e0 + kBlock);
@@ -460,28 +461,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
               total = ptx::add2(total, ptx::add2(ptx::pack2(w[0], w[1]), ptx::pack2(w[2], w[3])));
             };
             const bool plain = whole && same;
-            int j = from;
-            if (plain && j + 64 <= to) {      // 32 columns are on their way while others are added up
+            int j = 0;
+            if (plain && cols == kRows) {      // 32 columns are on their way while others are added up
               float v0[32], v1[32];
-              ptx::tmem_ld32(at + j, v0);
-              ptx::tmem_wait_ld();
-              ptx::tmem_ld32(at + j + 32, v1);
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) add(std::true_type(), v0 + k, j + k);
+              ptx::tmem_ld32(at, v0);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) add(std::true_type(), v1 + k, j + 32 + k);
-              j += 64;
+              for (j = 0; j < kRows; j += 64) {
+                ptx::tmem_ld32(at + j + 32, v1);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) add(std::true_type(), v0 + k, j + k);
+                ptx::tmem_wait_ld();
+                if (j + 64 < kRows) ptx::tmem_ld32(at + j + 64, v0);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) add(std::true_type(), v1 + k, j + 32 + k);
+                ptx::tmem_wait_ld();
+              }
             }
             if (plain)
-              for (; j < to; j += 8) {
-                float v[8];
-                tmem_ld8(at + j, v);
+              for (; j < cols; j += 16) {
+                float v[16];
+                ptx::tmem_ld16(at + j, v);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; k += 4) add(std::true_type(), v + k, j + k);
+                for (int k = 0; k < 16; k += 4) add(std::true_type(), v + k, j + k);
               }
-            for (; j < to; j += 8) {
+            for (; j < cols; j += 8) {
               float v[8];
               tmem_ld8(at + j, v);
               ptx::tmem_wait_ld();
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             if (lane == 0) ptx::mbar_arrive(sums_free(ss));
             float even, odd;
             ptx::unpack2(total, even, odd);
-            sums[half * kRun * kBlock + b * kBlock + quarter * 32 + lane] += even + odd;
+            sums[team * kRun * kBlock + b * kBlock + quarter * 32 + lane] += even + odd;
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(rows_free(rs));
@@ -511,8 +516,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
 #pragma unroll
           for (int s = 0; s < C::kSlabs; ++s) rows_at[s] = ptx::sdesc_kmajor_sw128(ptx::smem_u32(smem + rs * C::kRowBytes) + s * cols * 128);
           for (int b = 0; b < run; ++b, ++kn, ++sn) {
-            const uint32_t ks = kn % C::kKeySlots, ss = sn % kSlots;
-            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_free(ss), (sn / kSlots & 1) ^ 1) && wait(keys_full(ks), kn / C::kKeySlots & 1)))) break;
+            const uint32_t ks = kn % C::kKeySlots, ss = sn % C::kSumSlots;
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_free(ss), (sn / C::kSumSlots & 1) ^ 1) && wait(keys_full(ks), kn / C::kKeySlots & 1)))) break;
             ptx::tc_fence_after();
             const uint32_t to = tmem + C::kSumCol + ss * kRows, keys = tmem + ks * C::kKeyCols;
             if (ptx::elect_one()) {
@@ -582,9 +587,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
   __syncthreads();
   // a wait that ran out leaves copies and products on their way: they are waited for as long as waits may take by default
   if (failed && tid == 0)
-    for (uint32_t k = 1; k <= kSlots; ++k) {
-      if (row_copies >= k) ptx::mbar_wait(rows_full((row_copies - k) % kSlots), (row_copies - k) / kSlots & 1, kDefaultWaitCycles);
-      if (products >= k) ptx::mbar_wait(sums_full((products - k) % kSlots), (products - k) / kSlots & 1, kDefaultWaitCycles);
+    for (uint32_t k = 1; k <= C::kSumSlots; ++k) {
+      if (k <= kSlots && row_copies >= k) ptx::mbar_wait(rows_full((row_copies - k) % kSlots), (row_copies - k) / kSlots & 1, kDefaultWaitCycles);
+      if (products >= k) ptx::mbar_wait(sums_full((products - k) % C::kSumSlots), (products - k) / C::kSumSlots & 1, kDefaultWaitCycles);
     }
   __syncthreads();
   if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
