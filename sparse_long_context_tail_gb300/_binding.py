@@ -223,8 +223,9 @@ def make_kv_eviction(num_reqs: int, kv_len: int, kv_len_out: int, page_table: in
                      weights_out_stride: int, weights_out_cols: int, budget: int, trigger: int, sinks: int = 0,
                      recent: int = 0, page_table_out: int = 0, page_stride_out: int = 0, max_pages_out: int = 0,
                      kept: int = 0, kept_stride: int = 0) -> UpfKvEviction:
-    _check_int32(page_size=page_size, budget=budget, trigger=trigger, sinks=sinks, recent=recent,
-                 weights_cols=weights_cols, weights_out_cols=weights_out_cols)
+    if (page_size | budget | trigger | sinks | recent | weights_cols | weights_out_cols) >> 31:   # as in make_kv_query
+        _check_int32(page_size=page_size, budget=budget, trigger=trigger, sinks=sinks, recent=recent,
+                     weights_cols=weights_cols, weights_out_cols=weights_out_cols)
     return UpfKvEviction(num_reqs, kv_len or None, kv_len_out or None, page_table or None, page_stride, max_pages,
                          page_size, page_table_out or None, page_stride_out, max_pages_out, budget, trigger, sinks,
                          recent, weights or None, weights_stride, weights_cols, weights_out_cols, weights_out or None,

@@ -427,16 +427,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
           const float* const cf = reinterpret_cast<const float*>(smem + C::kConstAt + rs * C::kConstBytes);
           // a broadcast from shared memory takes as long as it has words, so the factor is one where the rows allow it
           bool same = true;
-          for (int j = lane; ok && j < cols; j += 32) same = same && cf[j] == cf[0];
+          if (ok && lane * 4 < cols) {
+            const float4 f = *reinterpret_cast<const float4*>(cf + lane * 4);
+            same = f.x == cf[0] && f.y == f.x && f.z == f.x && f.w == f.x;
+          }
           same = __all_sync(0xFFFFFFFFu, same);
           const uint64_t one_f = ok ? ptx::pack2(cf[0], cf[0]) : 0;
-          for (int b = 0; b < run && ok; ++b, ++sn) {
-            if (int(sn & 1) != team) continue;
-            const uint32_t ss = sn % C::kSumSlots;
-            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), sn / C::kSumSlots & 1)))) break;
-            ptx::tc_fence_after();
+          for (int b = int((team - sn) & 1); b < run && ok; b += 2) {
+            const uint32_t n = sn + b, ss = n % C::kSumSlots;
             const int e0 = blocks.entry(run0 + b), e = e0 + quarter * 32 + lane;
             const bool whole = all_seen(a, x, view, e0, e0 + kBlock);
+            if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), n / C::kSumSlots & 1)))) break;
+            ptx::tc_fence_after();
             const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + C::kSumCol + ss * kRows;
             uint64_t total = 0;      // over the even and over the odd columns
             // four logits as weights, added up
@@ -500,6 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             ptx::unpack2(total, even, odd);
             sums[team * kRun * kBlock + b * kBlock + quarter * 32 + lane] += even + odd;
           }
+          sn += run;
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(rows_free(rs));
         }
