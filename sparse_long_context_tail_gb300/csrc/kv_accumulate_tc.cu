@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
   constexpr int kTop = 14;                     // exponent of the largest element
   constexpr int kOwn = kRows / kRowWarps;      // rows of a warp
   __shared__ int most, least;                  // of the exponents of the rows that count
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();         // only now: the second launch reads and writes what launches before this one do
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int r = blockIdx.y; r < a.R; r += gridDim.y) {
     const Request x = load_request(a, r);
@@ -611,7 +612,7 @@ cudaError_t launch(const KvAccumulateArgs& a, cudaStream_t s) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   const int per = int(std::min<int64_t>((int64_t)a.H * ((pad16(a.gamma * a.max_q) + kRows - 1) / kRows), 4 * kPlanSMs));
-  e = launch_kernel(kv_accumulate_rows_kernel<T, kDim>, dim3(per, std::min(a.R, std::max(1, 2 * kPlanSMs / per))), 32 * kRowWarps, 0, s, false, a, m);
+  e = launch_kernel(kv_accumulate_rows_kernel<T, kDim>, dim3(per, std::min(a.R, std::max(1, 2 * kPlanSMs / per))), 32 * kRowWarps, 0, s, true, a, m);
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)a.R * ((((int64_t)a.max_pages << a.page_shift) + kBlock - 1) / kBlock);
   return launch_kernel(kv_accumulate_tc_kernel<kDim>, dim3(unsigned(std::min<long long>(kPlanSMs, blocks))), kTcThreads, TcShape<kDim>::kSmem, s, true, a, m);

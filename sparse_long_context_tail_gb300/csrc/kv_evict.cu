@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
     if (ctas > 1) ptx::cluster_sync();
     else __syncthreads();
   };
-  const int n = a.kv_len[r];
   const float* const w = a.w + r * a.w_stride;
   const int32_t* const row = a.table + r * a.table_stride;
   for (int i = tid; i < kPasses * kBins / 4; i += kSelThreads) {
@@ -125,7 +124,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   }
   if (tid == 0) bad_any = counts[0] = counts[1] = 0;
   if (ctas > 1) cluster_arrive();        // the others may add to these
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();         // only now: the second launch writes what launches before this one may read
+  const int n = a.kv_len[r];
   // the second launch's ticket and marks
   if (r == 0 && first == 0) *a.ticket = 0;
   const int64_t marks = a.H * chunks_of(a.cap);
@@ -543,12 +544,14 @@ cudaError_t launch_kv_evict(const KvEvictArgs& a, cudaStream_t s) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_select_kernel, a, uint32_t(ctas), held);
   if (e != cudaSuccess) return e;
   return a.d == 64 ? launch_move<64>(a, s) : a.d == 128 ? launch_move<128>(a, s) : launch_move<256>(a, s);

@@ -56,6 +56,7 @@ __device__ __forceinline__ void rotate8(uint4& x, uint4& y, const float2 (&cs)[8
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   const uint32_t per = a.runs * a.groups;
+  pdl_wait();
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, t = i / per;
   if (t >= a.T) return;
   if (a.count && t >= *a.count) return;
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_any_kernel(const RopeArgs a) {
   constexpr const T* kT = nullptr;
+  pdl_wait();
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, t = i / a.runs;
   if (t >= a.T) return;
   if (a.count && t >= *a.count) return;
@@ -137,7 +139,7 @@ cudaError_t launch(RopeArgs a, cudaStream_t s) {
   if (a.rotary % 16) {
     a.runs = dims / 2;
     const int64_t blocks = ((int64_t)a.T * a.runs + kThreads - 1) / kThreads;
-    return launch_kernel(rope_any_kernel<T>, dim3(unsigned(blocks)), kThreads, 0, s, false, a);
+    return launch_kernel(rope_any_kernel<T>, dim3(unsigned(blocks)), kThreads, 0, s, true, a);
   }
   a.runs = dims / 16;
   // All heads by one thread, so that its sines serve all of them, unless that leaves SMs without
@@ -150,7 +152,7 @@ cudaError_t launch(RopeArgs a, cudaStream_t s) {
   a.heads_each = (most + groups - 1) / groups * kHeads;
   a.groups = (heads + a.heads_each - 1) / a.heads_each;
   const int64_t blocks = (mine * a.groups + kThreads - 1) / kThreads;
-  return launch_kernel(rope_kernel<T>, dim3(unsigned(blocks)), kThreads, 0, s, false, a);
+  return launch_kernel(rope_kernel<T>, dim3(unsigned(blocks)), kThreads, 0, s, true, a);
 }
 
 }  // namespace
