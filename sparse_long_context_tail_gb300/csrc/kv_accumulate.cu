@@ -4,8 +4,11 @@
 // exp(scale q.k_e - lse), with lse the row's from the attention.  Rows whose lse is -inf saw nothing.
 //
 // Only the keys' half of the records is read, and each entry's sum is added up in one order, so results repeat.  This file
-// has the kernel for at most eight rows a kv head (decoding), bound by reading the cache and, close behind,
-// by turning codes into f16; more rows take kv_accumulate_tc.cu.
+// has the kernel for at most eight rows a kv head (decoding); more rows take kv_accumulate_tc.cu.
+//
+// What bounds it: 184 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 16
+// products, at 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 1500 to
+// 131072 entries (8 heads, d = 128, 32 q heads): 61.5 us, 4.3 TB/s; one of 131072: 23.4 us; of 4096 (d = 64): 6.2 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -180,7 +183,7 @@ __device__ __forceinline__ Tiles tiles_of(const KvAccumulateArgs& a, const Reque
 }
 
 template <typename T, int kDim>
-__global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccumulateArgs a, const int group) {
+__global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccumulateArgs a) {
   using S = Shape<kDim>;
   using R = Ring<kDim>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -211,8 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
     // those that every row sees whole: [whole, whole + wholes), along the entries one run
     const int last_e = (view.base + 1) / 16 * 16, first_e = a.window ? max(0, view.base + x.q_len - a.window + 15) / 16 * 16 : 0;
     const int whole = first_e / 16 - tiles.lo_t + tiles.sink_t - begin, wholes = max(0, (last_e - first_e) / 16);
-    for (int h0 = 0; h0 < a.H; h0 += group) {
-      const int hn = min(group, a.H - h0), lanes = kWarps / hn;          // heads; warps of a head
+    // as many heads at a time as there are warps (16 at a time: 64 heads 55 us for 51, 32 heads 29.9 for 29.3)
+    for (int h0 = 0; h0 < a.H; h0 += kWarps) {
+      const int hn = min(kWarps, a.H - h0), lanes = kWarps / hn;          // heads; warps of a head
       const int block = min(kBlockTiles, kSumTiles / hn) / lanes * lanes;   // tiles of a block
       const int around = 4 * block;                                      // of the table
       // Those of the block from tile j0 on.  Where there is none (a bad page) the cache's first record is copied,
@@ -317,21 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
   }
 }
 
-// kv heads at a time: as many as keep most of the warps at work, and of those as many as there are.
-int heads_at_once(int H) {
-  int best = 1, busy = 0;
-  for (int g = 1; g <= std::min(H, kWarps); ++g) {
-    const int passes = (H + g - 1) / g, last = H - (passes - 1) * g;
-    // warps at work, over the passes: a pass costs by its heads over its warps
-    const int now = 1000 * H / ((passes - 1) * ((1000 + kWarps / g - 1) / (kWarps / g)) + (1000 + kWarps / last - 1) / (kWarps / last));
-    if (now >= busy) {
-      busy = now;
-      best = g;
-    }
-  }
-  return best;
-}
-
 template <typename T, int kDim>
 cudaError_t launch(const KvAccumulateArgs& a, cudaStream_t s) {
   constexpr int kSmem = Ring<kDim>::kSmem;
@@ -344,8 +333,7 @@ cudaError_t launch(const KvAccumulateArgs& a, cudaStream_t s) {
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   const long long tiles = (long long)a.R * ((((int64_t)a.max_pages << a.page_shift) + 15) / 16);   // at most
-  return launch_kernel(kv_accumulate_kernel<T, kDim>, dim3(unsigned(std::min<long long>(kPlanSMs, tiles))), kThreads, kSmem, s, true, a,
-                       heads_at_once(a.H));
+  return launch_kernel(kv_accumulate_kernel<T, kDim>, dim3(unsigned(std::min<long long>(kPlanSMs, tiles))), kThreads, kSmem, s, true, a);
 }
 
 template <int kDim>
@@ -353,6 +341,8 @@ cudaError_t launch_dim(const KvAccumulateArgs& a, bool f16, cudaStream_t s) {
   return f16 ? launch<__half, kDim>(a, s) : launch<__nv_bfloat16, kDim>(a, s);
 }
 
+// One new token of 131072 entries of 8 heads, 8 rows a head: 23.8 us here, 29.3 there; 12 rows would be two passes here, 29 us there.
+// 16 ragged requests of 4 rows: 61.8 and 80.5 us.
 bool few_rows(int gamma, int max_q) { return gamma * max_q <= 8; }
 
 }  // namespace

@@ -7,13 +7,18 @@
 // operands of an M128 N128 product would take more of its bandwidth than there is.  The rows
 // are made ready once by a launch of their own, in the swizzled layout that the product reads, and copied in bulk.
 //
-// What bounds it: with n rows a kv head every entry and head costs 2 d n flop, n exponentials and one pass over
-// its codes.  At d = 128 and 128 rows the three units need about the same time.
-//
 // A CTA (one an SM) has a run of 128-entry blocks of one request after another.  For each head and chunk of rows it goes
-// through its blocks, so that rows are copied once a run; the entries' sums wait in shared memory.  Warps: eight work
-// out keys (four for every other block), eight add up weights (a half of the columns each), one issues
-// the products, one the copies.
+// through its blocks, so that rows are copied once a run; the entries' sums wait in shared memory.  Warps: two teams of
+// four work out keys, two teams of four add up weights (every other product each), one issues
+// the products, one the copies.  Tensor memory has a slot of keys a team (d = 128) and three of sums.
+//
+// What bounds it: with n rows a kv head every entry and head costs 2 d n flop, n exponentials and one pass over
+// its codes.  A product of 128 rows at d = 128 takes 1090 cycles; its exponentials alone would take 512 (32 a clock and SM),
+// the product about 560, the conversion of its keys 250 to 500.  With any one of these left out in a trial the time
+// fell by 2 to 6 %: what is left is the hand-over between the roles.  32 queries of 4 q heads a kv head over
+// 131072 entries of 8 heads: 42 us (820 TFLOP/s, 3.2 exponentials a ps), 128 queries 128 us.  Measured beside it:
+// both teams at one product, a half of its columns each: 53 and 171 us; three sum teams 46 and 140; two slots of
+// sums and four of keys 48 and 150.
 #include <algorithm>
 #include <atomic>
 #include <climits>

