@@ -7,7 +7,7 @@
 // has the kernel for at most eight rows a kv head (decoding); more rows take kv_accumulate_tc.cu.
 //
 // What bounds it: 184 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 16
-// products, at 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 1500 to
+// products, at 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 4096 to
 // 131072 entries (8 heads, d = 128, 32 q heads): 61.5 us, 4.3 TB/s; one of 131072: 23.4 us; of 4096 (d = 64): 6.2 us.
 #include <algorithm>
 #include <atomic>
