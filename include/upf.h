@@ -480,7 +480,7 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
  * query:   as for upf_kv_attend.
  * q, lse:  what upf_kv_attend was given and gave back.  An error of lse is a relative error of
  *          the weights: in fp32 |lse| * 2^-24 and more.
- * decay:   in [0, 1]; 1 adds.
+ * decay:   in [0, 1]; 1 adds, with 0 weights_in is not read.
  * weights_in (nullable: zeros), weights_out: device float32, request r entry e at
  *    r*weights_stride + e, `weights_cols` entries a row; they may be the same.
  * A row whose lse is -inf adds nothing (it saw nothing); one whose lse is a NaN or +inf, or with

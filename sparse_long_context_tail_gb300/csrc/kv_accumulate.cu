@@ -7,7 +7,7 @@
 // has the kernel for at most eight rows a kv head (decoding); more rows take kv_accumulate_tc.cu.
 //
 // What bounds it: 184 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 16
-// products, at 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 4096 to
+// products, at 2.3 to 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 4096 to
 // 131072 entries (8 heads, d = 128, 32 q heads): 61.5 us, 4.3 TB/s; one of 131072: 23.4 us; of 4096 (d = 64): 6.2 us.
 #include <algorithm>
 #include <atomic>
@@ -219,17 +219,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
       const int hn = min(kWarps, a.H - h0), lanes = kWarps / hn;          // heads; warps of a head
       const int block = min(kBlockTiles, kSumTiles / hn) / lanes * lanes;   // tiles of a block
       const int around = 4 * block;                                      // of the table
-      // Those of the block from tile j0 on.  Where there is none (a bad page) the cache's first record is copied,
+      // Those of tiles [from, to).  Where there is none (a bad page) the cache's first record is copied,
       // and not looked at.
-      auto look_up = [&](int j0) {
-        for (int j = j0 + threadIdx.x; j < min(n, j0 + block); j += kThreads) {
+      auto look_up = [&](int from, int to) {
+        for (int j = from + threadIdx.x; j < min(n, to); j += kThreads) {
           const uint8_t* const rec = record_at<kDim>(a, r, x, view, tiles.entry(begin + j));
           table[j % around] = reinterpret_cast<unsigned long long>((rec ? rec : a.data) + (int64_t)h0 * S::kRecord) | !rec;
         }
       };
-      look_up(0);
-      look_up(block);
-      look_up(2 * block);
+      look_up(0, 3 * block);
       const int mine = warp / hn, h = warp - mine * hn;       // this warp's first tile and its head; warps past the last one of a head: none
       Rows<kDim> y;
       load_rows<T, kDim>(a, y, x, h0 + h);
@@ -294,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
         work(std::true_type(), j1);
         __syncthreads();
         // ---- over the heads, while other warps are in the next block
-        look_up(j0 + 3 * block);
+        look_up(j0 + 3 * block, j0 + 4 * block);
         for (int i = threadIdx.x; i < (j1 - j0) * 16; i += kThreads) {
           const int t = j0 + (i >> 4), e = tiles.entry(begin + t) + (i & 15);
           if (e >= x.n) continue;
