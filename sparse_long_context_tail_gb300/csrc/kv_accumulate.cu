@@ -8,7 +8,7 @@
 //
 // What bounds it: 184 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 16
 // products, at 2.3 to 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 4096 to
-// 131072 entries (8 heads, d = 128, 32 q heads): 61.5 us, 4.3 TB/s; one of 131072: 23.4 us; of 4096 (d = 64): 6.2 us.
+// 131072 entries (8 heads, d = 128, 32 q heads): 60 us, 4.4 TB/s; one of 131072: 23 us; of 4096 (d = 64): 6.1 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -221,16 +221,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
       const int around = 4 * block;                                      // of the table
       // Those of tiles [from, to).  Where there is none (a bad page) the cache's first record is copied,
       // and not looked at.
-      auto look_up = [&](int from, int to) {
-        for (int j = from + threadIdx.x; j < min(n, to); j += kThreads) {
-          const uint8_t* const rec = record_at<kDim>(a, r, x, view, tiles.entry(begin + j));
-          table[j % around] = reinterpret_cast<unsigned long long>((rec ? rec : a.data) + (int64_t)h0 * S::kRecord) | !rec;
-        }
+      auto note = [&](int j, const uint8_t* rec) {
+        table[j % around] = reinterpret_cast<unsigned long long>((rec ? rec : a.data) + (int64_t)h0 * S::kRecord) | !rec;
       };
-      look_up(0, 3 * block);
+      auto look_up = [&](int from, int to) {
+        for (int j = from + threadIdx.x; j < min(n, to); j += kThreads) note(j, record_at<kDim>(a, r, x, view, tiles.entry(begin + j)));
+      };
+      // the first three blocks' pages (a thread has one at most) are on their way while the rows are made ready
+      static_assert(3 * kBlockTiles <= kThreads, "a page a thread");
+      const int e_first = tiles.entry(begin + threadIdx.x);
+      const bool looks = threadIdx.x < min(n, 3 * block) && !unseen(x, view, e_first);
+      const int page = looks ? page_at(a, r, e_first) : -1;
       const int mine = warp / hn, h = warp - mine * hn;       // this warp's first tile and its head; warps past the last one of a head: none
       Rows<kDim> y;
       load_rows<T, kDim>(a, y, x, h0 + h);
+      if (threadIdx.x < min(n, 3 * block)) note(threadIdx.x, looks ? record_in<kDim>(a, page, e_first) : nullptr);
       __syncthreads();
       // ---- the copies, kAhead tiles before the products
       int copy_j = mine < lanes ? mine : n, copy_at = mine, copy_slot = 0;               // tile, its places in the table and in the ring
@@ -290,6 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
         work(std::true_type(), min(j1, whole));
         work(std::false_type(), min(j1, whole + wholes));
         work(std::true_type(), j1);
+        // what the entry had, of the first entry that this thread adds up, while the other warps finish
+        auto had = [&](int i) { return a.w_in[r * a.w_stride + tiles.entry(begin + j0 + (i >> 4)) + (i & 15)]; };
+        float old = 0.f;
+        if (h0 == 0 && a.w_in && threadIdx.x < (j1 - j0) * 16 &&
+            tiles.entry(begin + j0 + (threadIdx.x >> 4)) + (threadIdx.x & 15) < x.n)
+          old = had(threadIdx.x);
         __syncthreads();
         // ---- over the heads, while other warps are in the next block
         look_up(j0 + 3 * block, j0 + 4 * block);
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
           if (!(table[t % around] & 1))      // an entry of a bad page is not seen
             for (int k = 0; k < hn; ++k) v += sums[buffer + ((i >> 4) * hn + k) * 16 + (i & 15)];
           const int64_t to = r * a.w_stride + e;
-          a.w_out[to] = h0 ? a.w_out[to] + v : a.w_in ? __fmaf_rn(a.decay, a.w_in[to], v) : v;
+          a.w_out[to] = h0 ? a.w_out[to] + v : a.w_in ? __fmaf_rn(a.decay, i == threadIdx.x ? old : had(i), v) : v;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");

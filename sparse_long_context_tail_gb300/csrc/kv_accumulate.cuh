@@ -55,14 +55,20 @@ __device__ __forceinline__ View view_of(const KvAccumulateArgs& a, const Request
 }
 
 // Keys of head 0 of the 16 entries from e on, or null if no row sees one of them or their page is bad.
+__device__ __forceinline__ bool unseen(const Request& x, const View& v, int e) { return e >= x.n || (e + 15 < v.w0 && e >= v.sinks); }
+__device__ __forceinline__ int page_at(const KvAccumulateArgs& a, int r, int e) {
+  return a.page_table[(int64_t)r * a.page_stride + (e >> a.page_shift)];
+}
 template <int kDim>
-__device__ __forceinline__ const uint8_t* record_at(const KvAccumulateArgs& a, int r, const Request& x, const View& v, int e) {
-  if (e >= x.n || (e + 15 < v.w0 && e >= v.sinks)) return nullptr;
-  const int page = a.page_table[(int64_t)r * a.page_stride + (e >> a.page_shift)];
+__device__ __forceinline__ const uint8_t* record_in(const KvAccumulateArgs& a, int page, int e) {
   const int64_t b = ((int64_t)page << (a.page_shift - 4)) + ((e & ((1 << a.page_shift) - 1)) >> 4);
   if (page >= 0 && b < (a.num_slots >> 4)) return a.data + b * a.H * Shape<kDim>::kRecord;
   set_status(a.status, UPF_ERR_INVALID_ARG);
   return nullptr;
+}
+template <int kDim>
+__device__ __forceinline__ const uint8_t* record_at(const KvAccumulateArgs& a, int r, const Request& x, const View& v, int e) {
+  return unseen(x, v, e) ? nullptr : record_in<kDim>(a, page_at(a, r, e), e);
 }
 
 // Does query i of the request (-1: none) see entry e?
