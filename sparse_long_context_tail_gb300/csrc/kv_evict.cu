@@ -42,7 +42,7 @@ constexpr int kMaxCluster = 16, kManyCluster = 8;    // of few requests, of many
 constexpr int kUnroll = 2;
 constexpr int kPasses = 3, kBins = 2048, kOwnBins = 4;   // digits; bins of a digit; of a thread
 constexpr int kMaxHeld = 9;           // fours of weights of a thread that stay in shared memory (144 KB a CTA)
-constexpr int kChunk = 64;            // places of a moving CTA
+constexpr int kChunk = 64;            // places of a moving CTA (16 ragged requests of d = 128: 59 us, with 32 places 62)
 // Threads of a moving CTA (evicting of 64 requests of d = 256: 55.6 us with 128, 51.5 with 256; 16 of d = 128: 58.9 and 60.8).
 constexpr int move_threads(int d) { return d == 256 ? 256 : 128; }
 static_assert(move_threads(64) >= kChunk, "a thread for each entry of a chunk");
