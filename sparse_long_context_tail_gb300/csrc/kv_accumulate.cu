@@ -6,9 +6,9 @@
 // Only the keys' half of the records is read, and each entry's sum is added up in one order, so results repeat.  This file
 // has the kernel for at most eight rows a kv head (decoding); more rows take kv_accumulate_tc.cu.
 //
-// What bounds it: 184 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 16
+// What bounds it: about 160 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 8
 // products, at 2.3 to 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 4096 to
-// 131072 entries (8 heads, d = 128, 32 q heads): 60 us, 4.4 TB/s; one of 131072: 23 us; of 4096 (d = 64): 6.1 us.
+// 131072 entries (8 heads, d = 128, 32 q heads): 59.5 us, 4.4 TB/s; one of 131072: 23 us; of 4096 (d = 64): 6.0 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -27,6 +27,7 @@ using namespace acc;
 // as operand A straight from registers.  It leaves the tile's sums in shared memory, and after the
 // block they are added up over the heads.  (With whole tiles to a warp, all heads of them, the last
 // warps of an SM worked alone for a quarter of the time: a tile takes one warp of 24 about 6 us.)
+// (With 32 warps 16 ragged requests take 58.7 us for 59.4, and 4096 entries 7.4 for 6.0.)
 constexpr int kWarps = 24, kThreads = 32 * kWarps;
 constexpr int kSumTiles = 384;          // tiles times heads of a block
 constexpr int kBlockTiles = 192;        // most tiles of a block
@@ -161,7 +162,10 @@ __device__ __forceinline__ void load_rows(const KvAccumulateArgs& a, Rows<kDim>&
 template <int kDim>
 struct Ring {
   static constexpr int kCodes = 8 * kDim, kTile = kCodes + kDim;   // bytes of 16 entries' codes of a head, and with their scales
-  static constexpr int kAhead = kDim == 64 ? 8 : kDim == 128 ? 4 : 3;
+  // Enough for the latency, and no more: 8, 4 and 3 take 28.8, 60.1 and 48.1 us where these take 26.8, 59.4 and 46.9 (32 heads of
+  // d = 64, 16 requests of d = 128, 24 of d = 256).
+  static constexpr int kAhead = kDim == 64 ? 4 : kDim == 128 ? 3 : 2;
+  static_assert(kAhead * kWarps <= kBlockTiles, "tiles are copied a block ahead at most, where their records are known");
   static constexpr int kBytes = kAhead * kTile;
   // Of 128 bytes of scales a lane copies four; of 64 two lanes copy the same ones.
   __device__ static constexpr int kScaleAt(int lane) { return (kDim == 64 ? lane & 15 : lane) * 4; }
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
     // those that every row sees whole: [whole, whole + wholes), along the entries one run
     const int last_e = (view.base + 1) / 16 * 16, first_e = a.window ? max(0, view.base + x.q_len - a.window + 15) / 16 * 16 : 0;
     const int whole = first_e / 16 - tiles.lo_t + tiles.sink_t - begin, wholes = max(0, (last_e - first_e) / 16);
-    // as many heads at a time as there are warps (16 at a time: 64 heads 55 us for 51, 32 heads 29.9 for 29.3)
+    // as many heads at a time as there are warps (16 at a time: 64 heads 55 us for 51)
     for (int h0 = 0; h0 < a.H; h0 += kWarps) {
       const int hn = min(kWarps, a.H - h0), lanes = kWarps / hn;          // heads; warps of a head
       const int block = min(kBlockTiles, kSumTiles / hn) / lanes * lanes;   // tiles of a block
