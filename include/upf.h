@@ -479,12 +479,14 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
  * Added up in fp32, in the same order at every call.
  * query:   as for upf_kv_attend.
  * q, lse:  what upf_kv_attend was given and gave back.  An error of lse is a relative error of
- *          the weights: in fp32 |lse| * 2^-24 and more.
+ *          the weights: in fp32 |lse| * 2^-24 and more.  Where that is no error any longer but a
+ *          factor (|lse| * log2 e from 2^23 on), a row's weight for an entry is held at 1 at most.
  * decay:   in [0, 1]; 1 adds, with 0 weights_in is not read.
  * weights_in (nullable: zeros), weights_out: device float32, request r entry e at
  *    r*weights_stride + e, `weights_cols` entries a row; they may be the same.
- * A row whose lse is -inf adds nothing (it saw nothing); one whose lse is a NaN or +inf, or with
- * a NaN or an infinity in q, adds nothing and sets UPF_ERR_NONFINITE in the status word.
+ * A row whose lse is -inf adds nothing (it saw nothing); one whose lse is a NaN or +inf or has no
+ * lse * log2 e in fp32, or with a NaN or an infinity in q, adds nothing and sets UPF_ERR_NONFINITE
+ * in the status word.
  * An entry whose key holds a NaN gets a NaN.  Errors in device tables as for upf_kv_attend:
  * the request is skipped (also with kv_len[r] > weights_cols); an entry of a bad page is not seen.
  * ws: upf_kv_accumulate_workspace_bytes() bytes.

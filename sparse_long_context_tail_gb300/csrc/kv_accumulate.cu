@@ -112,6 +112,7 @@ struct Rows {
   uint4 q[Shape<kDim>::kWords];      // of two steps each
   float f[2], lse[2], lift[2];       // lse with a minus
   int i[2];                          // queries; -1: no such row
+  bool far;                          // some row's weights are held at 1 (the same in all lanes)
 };
 
 // By a warp; lane (g, t4) has the t4-th quarters of row g's parts.
@@ -148,6 +149,7 @@ __device__ __forceinline__ void load_rows(const KvAccumulateArgs& a, Rows<kDim>&
   for (int w = 0; w < S::kWords; ++w) out.q[w] = make_uint4(half(out.q[w].x), half(out.q[w].y), half(out.q[w].z), half(out.q[w].w));
   // a row that is not there has the weight 0
   const float f = c.on ? c.f : 0.f, minus = c.on ? -c.hi : -INFINITY, lift = c.on ? c.lift : 0.f;
+  out.far = __any_sync(0xFFFFFFFFu, is_far(minus));
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int from = (2 * t4 + b) * 4;
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
     const int begin = int(u - first), n = int(min(end - first, (long long)tiles.count)) - begin;   // the run's tiles of this request
     // those that every row sees whole: [whole, whole + wholes), along the entries one run
     const int last_e = (view.base + 1) / 16 * 16, first_e = a.window ? max(0, view.base + x.q_len - a.window + 15) / 16 * 16 : 0;
-    const int whole = first_e / 16 - tiles.lo_t + tiles.sink_t - begin, wholes = max(0, (last_e - first_e) / 16);
+    const int whole = first_e / 16 - tiles.lo_t + tiles.sink_t - begin, all_wholes = max(0, (last_e - first_e) / 16);
     // as many heads at a time as there are warps (16 at a time: 64 heads 55 us for 51)
     for (int h0 = 0; h0 < a.H; h0 += kWarps) {
       const int hn = min(kWarps, a.H - h0), lanes = kWarps / hn;          // heads; warps of a head
@@ -239,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
       const int mine = warp / hn, h = warp - mine * hn;       // this warp's first tile and its head; warps past the last one of a head: none
       Rows<kDim> y;
       load_rows<T, kDim>(a, y, x, h0 + h);
+      const int wholes = y.far ? 0 : all_wholes;     // the loop that looks at each entry holds weights at 1, too
       if (threadIdx.x < min(n, 3 * block)) note(threadIdx.x, looks ? record_in<kDim>(a, page, e_first) : nullptr);
       __syncthreads();
       // ---- the copies, kAhead tiles before the products
@@ -282,7 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
             __syncwarp();      // these keys are in registers
             copy_tile();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[c] = ptx::ex2_approx(__fmaf_rn(s[c], y.f[c & 1], y.lse[c & 1]));
+            for (int c = 0; c < 4; ++c) {
+              s[c] = __fmaf_rn(s[c], y.f[c & 1], y.lse[c & 1]);
+              if constexpr (decltype(masked)::value) s[c] = held(s[c], y.lse[c & 1]);
+              s[c] = ptx::ex2_approx(s[c]);
+            }
             if constexpr (decltype(masked)::value) {
               const int e = tiles.entry(begin + j);
 #pragma unroll

@@ -179,25 +179,42 @@ __device__ __forceinline__ float factor_of(const KvAccumulateArgs& a, int exp) {
 
 // A weight is 2^(s f - hi) lift, with s the product of the key and of the row divided by a power of two
 // (times `down`).  hi and what its rounding leaves (in `lift`) are lse * log2 e: the rounding of one number would be
-// that of every weight of the row.
+// that of every weight of the row.  (So in the kernel for few rows.  The one for many rows has one number for both, -(hi + low),
+// a word less a row to read for each entry: its weights are off by 2^-24 |lse| more, which an fp32 lse is off by itself.)
+//
+// From |hi| = kFar on the rounding of lse alone is half a power of two and more, so there lift is 1, and
+// a weight, which the row's other weights leave 1 at most, is held at 1: an exponent that is off by
+// thousands would make it infinite.  (At 1e10 `low` is -247, and lift as a factor of its own infinite: 0 times it a NaN.)
+constexpr float kFar = 0x1p23f;
+
 struct RowConstants {
   bool on, bad, zero;      // does it count; is it not finite; is it all zeros
   int e;                   // the power of two
   float down, f, hi, low, lift;
 };
 
+// Is a row with hi (or -hi) one whose weights are held at 1?
+__device__ __forceinline__ bool is_far(float hi) { return fabsf(hi) >= kFar && fabsf(hi) < INFINITY; }
+// The exponent of a weight of such a row (a NaN stays one), or of any other.
+__device__ __forceinline__ float held(float x, float hi) { return fabsf(hi) >= kFar && x > 0.f ? 0.f : x; }
+
 // `amax`: bits of the row's largest magnitude in fp32 (at and above those of infinity if it has a NaN or an infinity).
 __device__ __forceinline__ RowConstants row_constants(const KvAccumulateArgs& a, bool real, uint32_t amax, float lse) {
   constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.9259629911266174e-8f;   // their sum is log2 e to 2^-49
   RowConstants c;
-  c.bad = real && (amax >= 0x7F800000u || !(lse < INFINITY));
+  c.hi = lse * kLog2e;
+  c.bad = real && (amax >= 0x7F800000u || (lse != -INFINITY && !(fabsf(c.hi) < INFINITY)));
   c.on = real && !c.bad && lse > -INFINITY;
   c.zero = amax == 0;
   c.e = !c.on || c.zero ? 0 : max(-126, min(int(amax >> 23) - 127, 126));
   c.down = __uint_as_float(uint32_t(127 - c.e) << 23);
   c.f = factor_of(a, a.scale_exp + c.e);
-  c.hi = lse * kLog2e;
   c.low = __fmaf_rn(lse, kLog2e, -c.hi) + lse * kLog2eLow;
+  if (is_far(c.hi)) {
+    const float both = c.hi + c.low;
+    if (fabsf(both) < INFINITY) c.hi = both;
+    c.low = 0.f;
+  }
   c.lift = ptx::ex2_approx(-c.low);
   return c;
 }

@@ -48,7 +48,7 @@ __device__ __forceinline__ int64_t first_row(const KvAccumulateArgs& a, int q0, 
 }
 struct RowsMem {
   uint8_t* q;        // [rows][d] f16: per request and head [slab][row][64 dims], 16-byte pieces swizzled
-  float* f;          // [rows] logit factors
+  float* f;          // [rows] logit factors; with a minus: the row's weights are held at 1
   float* lse;        // [rows] -lse * log2 e
   int32_t* i;        // [rows] queries; -1: none
   int64_t rows;
@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
         else if constexpr (kEach == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
         else *reinterpret_cast<uint32_t*>(dst) = v[0];
         if (lane == 0) {
-          m.f[region + rho] = factor_of(a, a.scale_exp + e);
+          const float f = factor_of(a, a.scale_exp + e);
+          m.f[region + rho] = c[y].on && is_far(c[y].hi) ? -f : f;
           m.lse[region + rho] = c[y].on ? -(c[y].hi + c[y].low) : -INFINITY;      // a row that does not count has the weight 0
           m.i[region + rho] = c[y].on ? query[y] : -1;
         }
@@ -431,11 +432,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
           const uint32_t rs = rn % kSlots;
           ok = __all_sync(0xFFFFFFFFu, wait(rows_full(rs), rn / kSlots & 1));
           const float* const cf = reinterpret_cast<const float*>(smem + C::kConstAt + rs * C::kConstBytes);
-          // a broadcast from shared memory takes as long as it has words, so the factor is one where the rows allow it
+          // a broadcast from shared memory takes as long as it has words, so the factor is one where the rows allow it:
+          // all have the same, and none's weights are held at 1 (its factor has a minus)
           bool same = true;
           if (ok && lane * 4 < cols) {
             const float4 f = *reinterpret_cast<const float4*>(cf + lane * 4);
-            same = f.x == cf[0] && f.y == f.x && f.z == f.x && f.w == f.x;
+            same = f.x == fabsf(cf[0]) && f.y == f.x && f.z == f.x && f.w == f.x;
           }
           same = __all_sync(0xFFFFFFFFu, same);
           const uint64_t one_f = ok ? ptx::pack2(cf[0], cf[0]) : 0;
@@ -443,28 +445,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const uint32_t n = sn + b, ss = n % C::kSumSlots;
             const int e0 = blocks.entry(run0 + b), e = e0 + quarter * 32 + lane;
             const bool whole = all_seen(a, x, view, e0, e0 + kBlock);
+            // the queries that see this entry: `count` from `from` on
+            const int from = max(0, e - view.base);
+            const uint32_t count = a.window == 0 || e < a.sinks ? INT_MAX : max(0, e - view.base + a.window - from);
             if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), n / C::kSumSlots & 1)))) break;
             ptx::tc_fence_after();
             const uint32_t at = tmem + (uint32_t(quarter * 32) << 16) + C::kSumCol + ss * kRows;
             uint64_t total = 0;      // over the even and over the odd columns
             // four logits as weights, added up
-            auto add = [&](auto plain, const float* v, int j) {      // plain: one factor, all seen
+            auto add = [&](auto plain, const float* v, int j) {      // plain: one factor, none held at 1, all seen
               constexpr bool kPlain = decltype(plain)::value;
               const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(cf + kRows + j);
               ulonglong2 f;
               if constexpr (kPlain) f = make_ulonglong2(one_f, one_f);
-              else f = *reinterpret_cast<const ulonglong2*>(cf + j);
+              else {
+                f = *reinterpret_cast<const ulonglong2*>(cf + j);
+                f.x &= 0x7FFFFFFF7FFFFFFFull, f.y &= 0x7FFFFFFF7FFFFFFFull;     // without the minus
+              }
               float w[4];
               ptx::unpack2(ptx::fma2(ptx::pack2(v[0], v[1]), f.x, l.x), w[0], w[1]);
               ptx::unpack2(ptx::fma2(ptx::pack2(v[2], v[3]), f.y, l.y), w[2], w[3]);
+              if constexpr (!kPlain) {
+                float minus[4];
+                ptx::unpack2(l.x, minus[0], minus[1]);
+                ptx::unpack2(l.y, minus[2], minus[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = held(w[k], minus[k]);
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) w[k] = ptx::ex2_approx(w[k]);
               if constexpr (!kPlain) {
                 const int4 i = *reinterpret_cast<const int4*>(cf + 2 * kRows + j);
-                w[0] = sees(a, view, i.x, e) ? w[0] : 0.f;
-                w[1] = sees(a, view, i.y, e) ? w[1] : 0.f;
-                w[2] = sees(a, view, i.z, e) ? w[2] : 0.f;
-                w[3] = sees(a, view, i.w, e) ? w[3] : 0.f;
+                w[0] = uint32_t(i.x - from) < count ? w[0] : 0.f;
+                w[1] = uint32_t(i.y - from) < count ? w[1] : 0.f;
+                w[2] = uint32_t(i.z - from) < count ? w[2] : 0.f;
+                w[3] = uint32_t(i.w - from) < count ? w[3] : 0.f;
               }
               total = ptx::add2(total, ptx::add2(ptx::pack2(w[0], w[1]), ptx::pack2(w[2], w[3])));
             };

@@ -1,0 +1,121 @@
+"""Accumulated weights and eviction where numbers are at the ends of their range, against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_oracle as K
+from test_gpu_evict import BF16, DEV, F16, Batch, f64, queries
+from test_gpu_kv import peaked
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+# ------------------------------------------------------- logits of any size --
+
+FAR = 2.0 ** 23     # of |lse| log2 e: from there on a weight is held at 1
+
+
+def accumulated(b, q, lse, old, **kw):
+    return b.cache.accumulate(q, lse, b.table, b.kv_len, b.page, old, out=torch.full_like(old, 7.0), **kw)
+
+
+def most_drawn(q, lse, k, window=0, sinks=0):
+    """What the entries of one request draw at most, from q [rows, H_q, d] and lse [rows, H_q]; 0 where nothing is for certain.
+
+    The exponent x - lse is off by the product's error (d + 8 terms of 2^-23 of sum |q_j k_j|), 2^-22 of x and of lse, and
+    2^-20; from FAR on a weight is 1 at most; 2^-150 is below fp32's least number."""
+    news, Hq, d = q.shape
+    total = np.zeros(len(k))
+    for i in range(news):
+        seen = np.zeros(len(k), bool)
+        seen[K.visible(len(k), news, i, window, sinks)] = True
+        for h in range(Hq):
+            if not np.isfinite(lse[i, h]):
+                continue
+            key = k[:, h // (Hq // k.shape[1])]
+            x, reach = key @ q[i, h] * d ** -0.5, np.abs(key) @ np.abs(q[i, h]) * d ** -0.5
+            u = x - lse[i, h] + reach * (d + 8) * 2.0 ** -23 + (np.abs(x) + abs(lse[i, h])) * 2.0 ** -22 + 2.0 ** -20
+            if abs(lse[i, h]) * np.log2(np.e) >= FAR:
+                u = np.minimum(u, 0)
+            total += np.where(seen & (u > -104), np.exp(np.clip(u, -104, 700)), 0)
+    return total
+
+
+@pytest.mark.parametrize("Hq,d", [(4, 64), (12, 64), (4, 128), (12, 128), (4, 256), (12, 256)])
+@pytest.mark.parametrize("logit", [1e5, 1e7, 1e9, 1e10, 2.0 ** 34, 1e12, 1e30, 1.2 * 2.0 ** 126])
+def test_weights_of_peaked_rows(logit, Hq, d):
+    """One entry (or two) far above all others, four rows a kv head and twelve: no NaN, no infinity, and what is far below or
+    not seen keeps exactly what it had."""
+    for twice in (False, True):
+        for window, sinks in ((0, 0), (37, 5)):
+            b, q, cu_q, top = peaked([1, 40, 700], Hq, 1, d, logit, twice=twice)
+            b.page = 16
+            lse = b.cache.attend(q, b.table, b.kv_len, 16, window=window, sinks=sinks).lse
+            assert b.cache.status() == 0 and torch.isfinite(lse).all()
+            old = torch.rand(3, 704, generator=torch.Generator().manual_seed(1)).to(DEV)
+            got = accumulated(b, q, lse, old, window=window, sinks=sinks)
+            assert b.cache.status() == 0
+            for r, n in enumerate(b.lens):
+                most = most_drawn(f64(q[r:r + 1]), f64(lse[r:r + 1]), b.k[r], window, sinks)
+                none = torch.from_numpy(most == 0).to(DEV)
+                assert torch.equal(got[r, :n][none], old[r, :n][none]) and (got[r, n:] == 7).all()
+                drew = f64(got[r, :n]) - f64(old[r, :n])
+                # the sum of the rows and of the old weight: its roundings
+                assert (drew >= -2.0 ** -22).all() and (drew <= most * (1 + 2.0 ** -20) + 2.0 ** -22).all()
+            kept = b.cache.evict(got, b.table, b.kv_len, 16, 20)
+            assert b.cache.status() == 0 and (kept[2] >= 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,news", [(2, [1, 3]), (4, [1, 2]), (24, [1, 1]), (8, [7, 40])])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e9])
+def test_rows_of_large_logits_beside_ordinary_ones(size, Hq, news, dtype):
+    """Every third row is multiplied by `size`; the others' weights are right within their arithmetic, and the large rows add
+    what they may, nothing where their weight is 0 for certain."""
+    if dtype == F16:
+        size = min(size, 1e3)
+    b = Batch([150, 333], 2, 128, seed=70)
+    q, cu = queries(news, Hq, 128, dtype, 71)
+    big = torch.zeros(q.shape[:2], dtype=torch.bool)
+    big.view(-1)[::3] = True
+    q = torch.where(big[:, :, None].to(DEV), (q.float() * size).to(dtype), q)
+    assert torch.isfinite(q).all()
+    kw = dict(cu_q=cu, max_q_len=max(news))
+    lse = b.cache.attend(q, b.table, b.kv_len, 16, **kw).lse
+    old = torch.zeros(2, 352, device=DEV)
+    got = accumulated(b, q, lse, old, **kw)
+    assert b.cache.status() == 0
+    q64, l64, at = f64(q), f64(lse), cu.tolist()
+    plain, slack = K.accumulate(q64, np.where(big.numpy(), -np.inf, l64), b.keys(), at)
+    for r, n in enumerate(b.lens):
+        mine = slice(at[r], at[r + 1])
+        rows = news[r] * Hq
+        large = most_drawn(q64[mine], np.where(big.numpy(), l64, -np.inf)[mine], b.keys()[r])
+        s = slack[r]
+        # as for all weights: products, the rounding of the row, logit factor and lse, the sum of all rows
+        bound = (s["reach"] * 136 * 2.0 ** -23 + s["flat"] * 2.0 ** -25 + s["far"] * 2.0 ** -22 + s["one"] * 2.0 ** -21
+                 + (rows + 2) * 2.0 ** -24 * (plain[r] + large) + 2.0 ** -125 * rows)
+        over = f64(got[r, :n]) - plain[r]
+        assert (over >= -bound).all() and (over <= bound + large).all()
+
+
+def test_lse_whose_binary_logarithm_is_past_fp32_adds_nothing():
+    """No attention gives such an lse back: it is reported as an infinite one is."""
+    b = Batch([40, 50, 60], 2, 64, seed=12)
+    for Hq in (4, 32):
+        q, _ = queries([1, 1, 1], Hq, 64, BF16, 13)
+        lse = b.cache.attend(q, b.table, b.kv_len, 16).lse
+        old = torch.zeros(3, 64, device=DEV)
+        base = accumulated(b, q, lse, old)
+        for far, status in ((2.4e38, 5), (3.4e38, 5), (-2.4e38, 5), (2.3e38, 0)):
+            l2 = lse.clone()
+            l2[1] = far
+            got = accumulated(b, q, l2, old)
+            assert b.cache.status() == status
+            assert not got[1, :50].any() and torch.equal(got[0], base[0]) and torch.equal(got[2], base[2])
