@@ -487,7 +487,8 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
  * A row whose lse is -inf adds nothing (it saw nothing); one whose lse is a NaN or +inf or has no
  * lse * log2 e in fp32, or with a NaN or an infinity in q, adds nothing and sets UPF_ERR_NONFINITE
  * in the status word.
- * An entry whose key holds a NaN gets a NaN.  Errors in device tables as for upf_kv_attend:
+ * An entry whose key holds a NaN gets a NaN from every row that sees it, those that add nothing else
+ * among them.  Errors in device tables as for upf_kv_attend:
  * the request is skipped (also with kv_len[r] > weights_cols); an entry of a bad page is not seen.
  * ws: upf_kv_accumulate_workspace_bytes() bytes.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

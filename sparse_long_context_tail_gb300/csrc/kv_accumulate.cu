@@ -156,7 +156,7 @@ __device__ __forceinline__ void load_rows(const KvAccumulateArgs& a, Rows<kDim>&
     out.f[b] = __shfl_sync(0xFFFFFFFFu, f, from);
     out.lse[b] = __shfl_sync(0xFFFFFFFFu, minus, from);
     out.lift[b] = __shfl_sync(0xFFFFFFFFu, lift, from);
-    out.i[b] = __shfl_sync(0xFFFFFFFFu, c.on ? i : -1, from);
+    out.i[b] = __shfl_sync(0xFFFFFFFFu, real ? i : -1, from);    // one that does not count sees NaNs, too
   }
 }
 

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
           const float f = factor_of(a, a.scale_exp + e);
           m.f[region + rho] = c[y].on && is_far(c[y].hi) ? -f : f;
           m.lse[region + rho] = c[y].on ? -(c[y].hi + c[y].low) : -INFINITY;      // a row that does not count has the weight 0
-          m.i[region + rho] = c[y].on ? query[y] : -1;
+          m.i[region + rho] = query[y];      // one that does not count sees NaNs, too
         }
       }
     }

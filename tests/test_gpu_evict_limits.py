@@ -119,3 +119,37 @@ def test_lse_whose_binary_logarithm_is_past_fp32_adds_nothing():
             got = accumulated(b, q, l2, old)
             assert b.cache.status() == status
             assert not got[1, :50].any() and torch.equal(got[0], base[0]) and torch.equal(got[2], base[2])
+
+
+# ----------------------------------------------------- keys that hold a NaN --
+
+@pytest.mark.parametrize("Hq,news", [(2, 5), (8, 5), (8, 1), (32, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 20)])
+def test_a_key_with_a_nan_marks_its_entry_wherever_it_is_seen(Hq, news, window, sinks):
+    """Rows that count and rows that do not, tiles that are seen whole and in part: NaN where a row sees the entry, and
+    nowhere else."""
+    n, H = 300, 2
+    b = Batch([n], H, 64, seed=72)
+    odd = [3, 17, 130, 200, 257, 262, 297, 299]
+    k = b.k.clone()
+    k[odd, 1, 5] = float("nan")
+    b.cache.write(k, b.v, b.slots[0])
+    q, cu = queries([news], Hq, 64, BF16, 73)
+    kw = dict(cu_q=cu, max_q_len=news, window=window, sinks=sinks)
+    lse = b.cache.attend(q, b.table, b.kv_len, 16, **kw).lse
+    assert lse[:, Hq // 2:].isnan().all() and lse[:, :Hq // 2].isfinite().all()
+    seen = np.zeros(n, bool)
+    for i in range(news):
+        seen[K.visible(n, news, i, window, sinks)] = True
+    want = np.zeros(n, bool)
+    want[odd] = True
+    want &= seen
+    assert 0 < want.sum() < len(odd) or not window
+    other = lse.clone()
+    other[:, Hq // 2:] = -float("inf")
+    drawn = K.accumulate(f64(q), f64(other), [K.cache_values(f64(k), 0)], cu.tolist(), window, sinks)[0][0]
+    for x, status in ((lse, 5), (other, 0)):
+        got = f64(accumulated(b, q, x, torch.zeros(1, n, device=DEV), **kw)[0])
+        assert b.cache.status() == status
+        np.testing.assert_array_equal(np.isnan(got), want)
+        assert np.allclose(got[~want], drawn[~want], rtol=1e-4)
