@@ -489,7 +489,9 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
  * in the status word.
  * An entry whose key holds a NaN gets a NaN from every row that sees it, those that add nothing else
  * among them.  Errors in device tables as for upf_kv_attend:
- * the request is skipped (also with kv_len[r] > weights_cols); an entry of a bad page is not seen.
+ * the request is skipped (also with kv_len[r] > weights_cols; and where cu_q is not ascending, with more
+ * than eight rows a kv head, max_q_len * H_q / H_kv, one whose rows begin before those of an earlier good
+ * request end); an entry of a bad page is not seen.
  * ws: upf_kv_accumulate_workspace_bytes() bytes.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,

@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
   __shared__ unsigned long long table[4 * kBlockTiles];      // records of the tiles of four blocks; bit 0: its page is bad
   pdl_wait();
   auto count = [&](const Request& x) { return tiles_of(a, x).count; };
-  const Deal deal = deal_out<kThreads>(a, starts, count);
-  fade_unseen<kThreads>(a, [&](const Request& x, int& from, int& to) {
+  const Deal deal = deal_out<kThreads, false>(a, starts, nullptr, count);
+  fade_unseen<kThreads, false>(a, [&](const Request& x, int& from, int& to) {
     const Tiles t = tiles_of(a, x);
     from = t.sink_t * 16;
     to = t.lo_t * 16;
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
   const long long share = (deal.total + gridDim.x - 1) / gridDim.x;
   long long u = blockIdx.x * share, first;
   const long long end = min(u + share, deal.total);
-  int r;
+  int r, top;
   Request x;
-  if (u >= end || !find_request<kThreads>(a, starts, deal, u, r, x, first, count)) return;
+  if (u >= end || !find_request<kThreads, false>(a, starts, nullptr, deal, u, r, x, first, top, count)) return;
   for (;;) {
     const Tiles tiles = tiles_of(a, x);
     const View view = view_of(a, x);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_accumulate_kernel(const KvAccu
     if (u >= end) break;
     first += tiles.count;
     for (++r; r < a.R; ++r) {
-      x = load_request(a, r);
+      x = load_request<false>(a, r, top);
       const int mine = count(x);
       if (u < first + mine) break;
       first += mine;

@@ -15,8 +15,9 @@ struct Request {
   int q0, q_len, n;     // first row, rows, entries; no rows: nothing to do
 };
 
-__device__ __forceinline__ Request load_request(const KvAccumulateArgs& a, int r) {
-  Request x{r, 1, a.kv_len[r]};
+// Request r, and whether it makes sense by itself.
+__device__ __forceinline__ bool look_at(const KvAccumulateArgs& a, int r, Request& x) {
+  x = Request{r, 1, a.kv_len[r]};
   bool ok = x.n >= 0 && x.n <= ((int64_t)a.max_pages << a.page_shift) && x.n <= a.w_cols;
   if (a.cu_q) {
     x.q0 = a.cu_q[r];
@@ -24,10 +25,31 @@ __device__ __forceinline__ Request load_request(const KvAccumulateArgs& a, int r
     ok = ok && x.q0 >= 0 && q1 >= x.q0 && q1 <= a.num_q && q1 - x.q0 <= a.max_q;
     x.q_len = q1 - x.q0;
   }
+  return ok;
+}
+// Where the rows end of requests up to this one, of which `top` were those of the ones before it.
+__device__ __forceinline__ int end_of(const Request& x, bool ok, int top) { return ok && x.q_len > 0 ? max(top, x.q0 + x.q_len) : top; }
+
+// Request x after look_at(): with no rows if it is to be skipped.  kRowsOnce: also a request whose rows begin before `top`, which
+// is moved on (cu_q is not ascending then): the many-row kernel's rows have places in the workspace by their numbers, and
+// those of requests that go back may be others' places.
+template <bool kRowsOnce>
+__device__ __forceinline__ void admit(const KvAccumulateArgs& a, Request& x, bool ok, int& top) {
+  if (kRowsOnce && a.cu_q) {
+    const int before = top;
+    top = end_of(x, ok, top);
+    ok = ok && (x.q_len == 0 || x.q0 >= before);
+  }
   if (!ok) {
     set_status(a.status, UPF_ERR_INVALID_ARG);
     x.q0 = x.q_len = x.n = 0;
   }
+}
+template <bool kRowsOnce>
+__device__ __forceinline__ Request load_request(const KvAccumulateArgs& a, int r, int& top) {
+  Request x;
+  const bool ok = look_at(a, r, x);
+  admit<kRowsOnce>(a, x, ok, top);
   return x;
 }
 
@@ -93,17 +115,47 @@ template <int kThreads>
 struct Starts {
   long long starts[kThreads + 1];        // units before each thread's requests
   long long warp_sums[kThreads / 32];
+  int warp_tops[kThreads / 32];
 };
 
-template <int kThreads, typename Count>
-__device__ __forceinline__ Deal deal_out(const KvAccumulateArgs& a, Starts<kThreads>& s, Count&& count) {
+// `tops` [kThreads], in shared memory: where the rows of the requests before each thread's end (kRowsOnce).
+template <int kThreads, bool kRowsOnce, typename Count>
+__device__ __forceinline__ Deal deal_out(const KvAccumulateArgs& a, Starts<kThreads>& s, int* tops, Count&& count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Deal d;
   d.per = (a.R + kThreads - 1) / kThreads;
+  int top = 0;
+  Request x{};
+  bool ok = false;
+  const bool kept = kRowsOnce && a.cu_q && a.R > 1 && d.per == 1;      // this thread's request is looked at once
+  if (kRowsOnce && a.cu_q && a.R > 1) {
+    for (int j = 0; j < d.per; ++j) {
+      const int r = threadIdx.x * d.per + j;
+      if (r < a.R) {
+        ok = look_at(a, r, x);
+        top = end_of(x, ok, top);
+      }
+    }
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, top, k);
+      if (lane >= k) top = max(top, y);
+    }
+    if (lane == 31) s.warp_tops[warp] = top;
+    top = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+    if (lane == 0) top = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) top = max(top, s.warp_tops[w]);
+  }
+  if (kRowsOnce) tops[threadIdx.x] = top;
   long long sum = 0;
   for (int j = 0; j < d.per; ++j) {
     const int r = threadIdx.x * d.per + j;
-    if (r < a.R) sum += count(load_request(a, r));
+    if (r < a.R) {
+      if (!kept) ok = look_at(a, r, x);
+      admit<kRowsOnce>(a, x, ok, top);
+      sum += count(x);
+    }
   }
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
@@ -120,10 +172,11 @@ __device__ __forceinline__ Deal deal_out(const KvAccumulateArgs& a, Starts<kThre
   return d;
 }
 
-// The request that unit u belongs to, and the units before it; false if the lengths have changed under the call.
-template <int kThreads, typename Count>
-__device__ __forceinline__ bool find_request(const KvAccumulateArgs& a, const Starts<kThreads>& s, const Deal& d, long long u, int& r,
-                                             Request& x, long long& first, Count&& count) {
+// The request that unit u belongs to, the units before it, and where the rows up to it end; false if the lengths have changed under
+// the call.
+template <int kThreads, bool kRowsOnce, typename Count>
+__device__ __forceinline__ bool find_request(const KvAccumulateArgs& a, const Starts<kThreads>& s, const int* tops, const Deal& d,
+                                             long long u, int& r, Request& x, long long& first, int& top, Count&& count) {
   // the thread whose run of requests holds it, then along that run
   int lo = 0, hi = kThreads;      // starts[lo] <= u < starts[hi]
   while (hi - lo > 1) {
@@ -132,8 +185,9 @@ __device__ __forceinline__ bool find_request(const KvAccumulateArgs& a, const St
     else hi = mid;
   }
   first = s.starts[lo];
+  top = kRowsOnce ? tops[lo] : 0;
   for (r = lo * d.per; r < a.R; ++r) {
-    x = load_request(a, r);
+    x = load_request<kRowsOnce>(a, r, top);
     const int mine = count(x);
     if (u < first + mine) return true;
     first += mine;
@@ -142,11 +196,11 @@ __device__ __forceinline__ bool find_request(const KvAccumulateArgs& a, const St
 }
 
 // Entries behind the window, where no unit is, fade too: [from, to) of each request, which range() gives.
-template <int kThreads, typename Range>
+template <int kThreads, bool kRowsOnce, typename Range>
 __device__ __forceinline__ void fade_unseen(const KvAccumulateArgs& a, Range&& range) {
   if (!a.window || (a.w_in == a.w_out && a.decay == 1.f)) return;
-  for (int r = 0; r < a.R; ++r) {
-    const Request x = load_request(a, r);
+  for (int r = 0, top = 0; r < a.R; ++r) {
+    const Request x = load_request<kRowsOnce>(a, r, top);
     if (!x.q_len) continue;
     int from, to;
     range(x, from, to);

@@ -77,11 +77,18 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
   constexpr int kTop = 14;                     // exponent of the largest element
   constexpr int kOwn = kRows / kRowWarps;      // rows of a warp
   __shared__ int most, least;                  // of the exponents of the rows that count
+  __shared__ int back;                         // do they begin before those of an earlier request end
   pdl_wait();
   pdl_trigger();         // only now: the second launch reads and writes what launches before this one do
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int looked = 0, top = 0;     // requests looked at, and where the rows of this thread's among them end
   for (int r = blockIdx.y; r < a.R; r += gridDim.y) {
-    const Request x = load_request(a, r);
+    for (int j = looked + threadIdx.x; a.cu_q && j < r; j += 32 * kRowWarps) {
+      Request y;
+      top = end_of(y, look_at(a, j, y), top);
+    }
+    looked = r;
+    const Request x = load_request<false>(a, r, top);
     const int rows = x.q_len * a.gamma, padded = pad16(rows), chunks = (padded + kRows - 1) / kRows;
     for (int hc = blockIdx.x; hc < a.H * chunks; hc += gridDim.x) {
       const int h = hc / chunks, row0 = (hc - h * chunks) * kRows, row1 = min(padded, row0 + kRows);
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
       if (threadIdx.x == 0) {
         most = INT_MIN;
         least = INT_MAX;
+        back = 0;
       }
       __syncthreads();
       RowConstants c[kOwn];
@@ -123,11 +131,13 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv_accumulate_rows_kernel(cons
         hi = max(hi, c[y].e);
         lo = min(lo, c[y].e);
       }
+      if (top > x.q0) back = 1;
       if (lane == 0 && hi >= lo) {
         atomicMax(&most, hi);
         atomicMin(&least, lo);
       }
       __syncthreads();
+      if (back) continue;      // their places are another's
       const bool same = most < least || most - least <= kTop;     // none, or near one another
 #pragma unroll
       for (int y = 0; y < kOwn; ++y) {
@@ -280,10 +290,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
     ptx::tmem_relinquish();
   }
   ptx::fence_barrier_init();
-  const Deal deal = deal_out<kTcThreads>(a, starts, [&](const Request& x) { return blocks_of(a, x).count; });   // barriers inside
+  int* const tops = reinterpret_cast<int*>(smem + C::kRingAt);      // the rings come later
+  const Deal deal = deal_out<kTcThreads, true>(a, starts, tops, [&](const Request& x) { return blocks_of(a, x).count; });   // barriers inside
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_word;
-  fade_unseen<kTcThreads>(a, [&](const Request& x, int& from, int& to) {
+  fade_unseen<kTcThreads, true>(a, [&](const Request& x, int& from, int& to) {
     const Blocks b = blocks_of(a, x);
     from = b.sink_b * kBlock;
     to = b.lo_b * kBlock;
@@ -310,7 +321,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
   int r = 0;
   Request x{};
   long long first = 0;
-  if (u < end && !find_request<kTcThreads>(a, starts, deal, u, r, x, first, [&](const Request& y) { return blocks_of(a, y).count; })) u = end;
+  int top = 0;
+  if (u < end && !find_request<kTcThreads, true>(a, starts, tops, deal, u, r, x, first, top, [&](const Request& y) { return blocks_of(a, y).count; })) u = end;
   while (u < end) {
     const Blocks blocks = blocks_of(a, x);
     const View view = view_of(a, x);
@@ -599,7 +611,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
     u = first + stop;
     first += blocks.count;
     for (++r; u < end && r < a.R; ++r) {
-      x = load_request(a, r);
+      x = load_request<true>(a, r, top);
       const int count = blocks_of(a, x).count;
       if (u < first + count) break;
       first += count;

@@ -153,3 +153,52 @@ def test_a_key_with_a_nan_marks_its_entry_wherever_it_is_seen(Hq, news, window, 
         assert b.cache.status() == status
         np.testing.assert_array_equal(np.isnan(got), want)
         assert np.allclose(got[~want], drawn[~want], rtol=1e-4)
+
+
+# ------------------------------------------- rows that two requests begin with --
+
+@pytest.mark.parametrize("Hq", [2, 9, 128])
+def test_requests_whose_rows_begin_before_an_earlier_one_ends_are_skipped(Hq):
+    """cu_q that goes back: each request by itself may make sense, but a row has one place in the call."""
+    b = Batch([40, 50, 60, 200], 1, 64, seed=77)
+    q, _ = queries([12], Hq, 64, BF16, 78)
+    lse = torch.full((12, Hq), 2.0, device=DEV)
+    old = torch.rand(4, 208, generator=torch.Generator().manual_seed(79)).to(DEV)
+    keys = b.keys()
+    for cu, first_len, good in (([0, 8, 0, 8, 12], 40, [0, 3]), ([0, 5, 2, 9, 12], 40, [0, 3]), ([4, 9, 0, 4, 8], 40, [0]),
+                                ([0, 8, 2, 6, 12], -1, [2, 3]), ([7, 7, 2, 5, 6], 40, [2, 3]), ([0, 3, 3, 2, 4], 40, [0]),
+                                ([0, 4, 8, 8, 12], 40, [0, 1, 3])):
+        kv_len = b.kv_len.clone()
+        kv_len[0] = first_len
+        c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        got = b.cache.accumulate(q, lse, b.table, kv_len, 16, old, cu_q=c, max_q_len=8, out=old.clone())
+        fine = all(x <= y for x, y in zip(cu, cu[1:])) and first_len >= 0
+        assert b.cache.status() == (0 if fine else 1), cu
+        for r, n in enumerate(b.lens):
+            if r not in good:
+                assert torch.equal(got[r], old[r]), (cu, r)
+                continue
+            mine = slice(cu[r], cu[r + 1])
+            drawn = K.accumulate(f64(q[mine]), f64(lse[mine]), [keys[r]], [0, cu[r + 1] - cu[r]])[0][0]
+            assert np.allclose(f64(got[r, :n]), f64(old[r, :n]) + drawn, rtol=1e-4), (cu, r)
+            assert torch.equal(got[r, n:], old[r, n:])
+
+
+@pytest.mark.parametrize("Hq", [5, 18])
+def test_many_requests_whose_rows_go_back(Hq):
+    """2500 requests of a row: from the thousandth on they begin again at row 500, and count again from row 1000 on."""
+    R = 2500
+    b = Batch([(5 * i) % 23 for i in range(R)], 1, 64, seed=80)
+    N = 2000
+    q, _ = queries([N], Hq, 64, BF16, 81)
+    lse = torch.full((N, Hq), 3.0, device=DEV)
+    old = torch.rand(R, 32, generator=torch.Generator().manual_seed(82)).to(DEV)
+    back = torch.cat([torch.arange(1001), torch.arange(500, 2000)]).int()         # [1000, 500) is no request's range
+    assert back.numel() == R + 1
+    got = b.cache.accumulate(q, lse, b.table, b.kv_len, 16, old, cu_q=back.to(DEV), max_q_len=2, out=old.clone())
+    assert b.cache.status() == 1
+    level = torch.cummax(back, 0).values          # the same without those that are skipped: they are empty
+    want = b.cache.accumulate(q, lse, b.table, b.kv_len, 16, old, cu_q=level.to(DEV), max_q_len=2, out=old.clone())
+    assert b.cache.status() == 0
+    assert torch.equal(got[1000:1501], old[1000:1501])
+    assert torch.allclose(got, want, rtol=1e-5) and not torch.equal(got[1501:], old[1501:])
