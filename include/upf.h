@@ -256,6 +256,13 @@ upf_status upf_select_tokens(upf_ctx* ctx, const upf_batch* batch, const upf_par
                              float* scores, float* block_scores, uint32_t* keep_bits, int32_t* kept_count,
                              const upf_compact_io* io, void* ws, size_t ws_bytes, void* stream);
 
+/* What upf_select_tokens would return for these arguments before it launches anything (host only).  For
+ * callers that change q or k in place first (upf_rope_apply) and could not make a refused call again. */
+upf_status upf_select_tokens_check(upf_ctx* ctx, const upf_batch* batch, const upf_params* params,
+                                   const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                   const uint32_t* keep_bits, const int32_t* kept_count, const upf_compact_io* io,
+                                   void* ws, size_t ws_bytes);
+
 /* Revival of frozen tokens (section 二, third step: the hidden states of
  * dropped tokens are frozen and carried forward so they can be revived).
  * Writes the rows a compacted batch produced back to their token positions

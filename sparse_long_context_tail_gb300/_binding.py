@@ -127,6 +127,8 @@ _SIGNATURES = {
     "upf_select_tokens": ([c_void_p, POINTER(UpfBatch), POINTER(UpfParams), c_void_p, c_int64, c_void_p, c_int64,
                            c_void_p, c_void_p, c_void_p, c_void_p, POINTER(UpfCompactIO), c_void_p, c_size_t,
                            c_void_p], c_int),
+    "upf_select_tokens_check": ([c_void_p, POINTER(UpfBatch), POINTER(UpfParams), c_void_p, c_int64, c_void_p, c_int64,
+                                 c_void_p, c_void_p, POINTER(UpfCompactIO), c_void_p, c_size_t], c_int),
 }
 
 _lib = None
@@ -447,3 +449,9 @@ def upf_select_tokens(ctx, batch, params, q, q_row_stride, k, k_row_stride, scor
     _check(load().upf_select_tokens(ctx, ctypes.byref(batch), ctypes.byref(params), q, q_row_stride, k,
                                     k_row_stride, scores or None, block_scores or None, keep_bits, kept_count,
                                     ctypes.byref(io), ws, ws_bytes, stream or None))
+
+
+def upf_select_tokens_check(ctx, batch, params, q, q_row_stride, k, k_row_stride, keep_bits, kept_count, io: UpfCompactIO,
+                            ws, ws_bytes):
+    _check(load().upf_select_tokens_check(ctx, ctypes.byref(batch), ctypes.byref(params), q, q_row_stride, k,
+                                          k_row_stride, keep_bits, kept_count, ctypes.byref(io), ws, ws_bytes))

@@ -505,6 +505,19 @@ upf_status check_compact_io(const Plan& pl, const uint32_t* keep_bits, const upf
   return UPF_OK;
 }
 
+// Everything that a selection is refused for.
+upf_status check_selection(const upf_ctx* ctx, const upf_batch* batch, const upf_params* params, const void* q, int64_t qs,
+                           const void* k, int64_t ks, const uint32_t* keep_bits, const int32_t* kept_count,
+                           const upf_compact_io* io, void* ws, size_t ws_bytes, Plan* pl) {
+  upf_status st;
+  if ((st = check_ctx(ctx)) != UPF_OK) return st;
+  if ((st = make_plan(ctx, batch, params, true, pl)) != UPF_OK) return st;
+  if ((st = check_ws(*pl, ws, ws_bytes)) != UPF_OK) return st;
+  if ((st = check_score_io(*pl, q, qs, k, ks)) != UPF_OK) return st;
+  if (!keep_bits || !kept_count) return fail(UPF_ERR_INVALID_ARG, "keep_bits and kept_count are required");
+  return check_compact_io(*pl, keep_bits, io, ctx->device);
+}
+
 upf::ScoreArgs score_args(const upf_ctx* ctx, const upf_batch* b, const Plan& pl, const void* q, int64_t qs,
                           const void* k, int64_t ks, void* ws) {
   upf::ScoreArgs a;
@@ -1236,18 +1249,21 @@ upf_status upf_history_kv_len(upf_ctx* ctx, const upf_batch* batch, const int32_
   return UPF_OK;
 }
 
+upf_status upf_select_tokens_check(upf_ctx* ctx, const upf_batch* batch, const upf_params* params, const void* q,
+                                   int64_t q_row_stride, const void* k, int64_t k_row_stride, const uint32_t* keep_bits,
+                                   const int32_t* kept_count, const upf_compact_io* io, void* ws, size_t ws_bytes) {
+  Plan pl;
+  return check_selection(ctx, batch, params, q, q_row_stride, k, k_row_stride, keep_bits, kept_count, io, ws, ws_bytes, &pl);
+}
+
 upf_status upf_select_tokens(upf_ctx* ctx, const upf_batch* batch, const upf_params* params, const void* q,
                              int64_t q_row_stride, const void* k, int64_t k_row_stride, float* scores,
                              float* block_scores, uint32_t* keep_bits, int32_t* kept_count,
                              const upf_compact_io* io, void* ws, size_t ws_bytes, void* stream) {
-  upf_status st;
-  if ((st = check_ctx(ctx)) != UPF_OK) return st;
   Plan pl;
-  if ((st = make_plan(ctx, batch, params, true, &pl)) != UPF_OK) return st;
-  if ((st = check_ws(pl, ws, ws_bytes)) != UPF_OK) return st;
-  if ((st = check_score_io(pl, q, q_row_stride, k, k_row_stride)) != UPF_OK) return st;
-  if (!keep_bits || !kept_count) return fail(UPF_ERR_INVALID_ARG, "keep_bits and kept_count are required");
-  if ((st = check_compact_io(pl, keep_bits, io, ctx->device)) != UPF_OK) return st;
+  const upf_status st = check_selection(ctx, batch, params, q, q_row_stride, k, k_row_stride, keep_bits, kept_count, io, ws,
+                                        ws_bytes, &pl);
+  if (st != UPF_OK) return st;
   DeviceGuard guard(ctx->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   upf::ScoreArgs sa = score_args(ctx, batch, pl, q, q_row_stride, k, k_row_stride, ws);

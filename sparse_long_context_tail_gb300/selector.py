@@ -103,13 +103,11 @@ class TokenSelector:
         """q: bf16 [T, H_q, d] (rows may be strided), k: bf16 [T, H_kv, d]; hidden: [T, hidden].
 
         ``rope``: q and k come before their rotary positions; they are turned by ``positions`` first (into
-        ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored."""
+        ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored.  A call
+        that is refused has turned nothing."""
         params = params or B.make_params()
-        if rope is not None:
-            if positions is None:
-                raise ValueError("rope needs positions")
-            turned = None if out is None else (out.q_out, out.k_out)
-            q, k = rope.apply(q, k, positions, out=turned)
+        if rope is not None and positions is None:
+            raise ValueError("rope needs positions")
         batch, keep = B.make_batch(cu_seqlens_dev.data_ptr(), cu_seqlens_host, num_q_heads, num_kv_heads,
                                    head_dim, kv_of_q)
         nbytes = B.upf_workspace_bytes(batch, params)
@@ -125,6 +123,16 @@ class TokenSelector:
             history_cap=0 if history is None else history.shape[1], history=_ptr(history),
             history_len=_ptr(history_len))
         if rope is not None:
+            # in place, rows are turned once: nothing may be refused behind this
+            raw = (("q", q, num_q_heads), ("k", k, num_kv_heads))
+            for name, t, heads in raw:
+                if t.dim() != 3 or t.shape[0] < cu_seqlens_host[-1] or t.shape[1:] != (heads, head_dim):
+                    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{cu_seqlens_host[-1]}, {heads}, {head_dim}]")
+            q, k = (torch.empty(t.shape, dtype=t.dtype, device=self.device) if x is None else x
+                    for (_, t, _), x in zip(raw, (out.q_out, out.k_out)))
+            B.upf_select_tokens_check(self.ctx, batch, params, q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
+                                      _ptr(out.keep_bits), _ptr(out.kept_count), io, ws.data_ptr(), ws.numel())
+            rope.apply(raw[0][1], raw[1][1], positions, out=(q, k))
             out.q_out, out.k_out = q, k
         stream = torch.cuda.current_stream(self.device).cuda_stream
         B.upf_select_tokens(self.ctx, batch, params, q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
