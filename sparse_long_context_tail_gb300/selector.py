@@ -126,6 +126,8 @@ class TokenSelector:
             # in place, rows are turned once: nothing may be refused behind this
             raw = (("q", q, num_q_heads), ("k", k, num_kv_heads))
             for name, t, heads in raw:
+                if t.dtype != torch.bfloat16:
+                    raise ValueError(f"{name} must be bfloat16, which the selection scores, not {t.dtype}")
                 if t.dim() != 3 or t.shape[0] < cu_seqlens_host[-1] or t.shape[1:] != (heads, head_dim):
                     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{cu_seqlens_host[-1]}, {heads}, {head_dim}]")
             q, k = (torch.empty(t.shape, dtype=t.dtype, device=self.device) if x is None else x

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from sparse_long_context_tail_gb300 import _binding as B
-from test_gpu_rope import BF16, DEV, places, rand, rotation
+from test_gpu_rope import BF16, DEV, F16, places, rand, rotation
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,11 @@ def test_a_refused_selection_leaves_queries_and_keys_as_they_were():
     assert got.q_out is q and torch.equal(q, q2) and torch.equal(k, k2) and torch.equal(got.scores, want.scores)
     # hidden_in are the projection's rows themselves, turned by then
     assert int(got.total_kept) == n and torch.equal(got.hidden_out[:n, 10 * 128:], keep[:, 10 * 128:]) and sel.status() == 0
+
+
+def test_queries_of_another_type_are_refused_with_a_rotary_embedding():
+    """The selection scores bf16; the rotation alone takes fp16 too."""
+    sel, rope, rows, q, k, pos, cu, cu_dev = inputs(dtype=F16)
+    with pytest.raises(ValueError, match="bfloat16"):
+        sel.select_tokens(q, k, cu, cu_dev, 8, 2, 128, positions=pos, rope=rope)
+    assert torch.isfinite(rope.apply(q, k, pos)[0]).all()
