@@ -103,7 +103,7 @@ class TokenSelector:
         """q: bf16 [T, H_q, d] (rows may be strided), k: bf16 [T, H_kv, d]; hidden: [T, hidden].
 
         ``rope``: q and k come before their rotary positions; they are turned by ``positions`` first (into
-        ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored.  A call
+        the first rows of ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored.  A call
         that is refused has turned nothing."""
         params = params or B.make_params()
         if rope is not None and positions is None:
@@ -130,12 +130,15 @@ class TokenSelector:
                     raise ValueError(f"{name} must be bfloat16, which the selection scores, not {t.dtype}")
                 if t.dim() != 3 or t.shape[0] < cu_seqlens_host[-1] or t.shape[1:] != (heads, head_dim):
                     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{cu_seqlens_host[-1]}, {heads}, {head_dim}]")
-            q, k = (torch.empty(t.shape, dtype=t.dtype, device=self.device) if x is None else x
-                    for (_, t, _), x in zip(raw, (out.q_out, out.k_out)))
+            if out.q_out is None:
+                out.q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            if out.k_out is None:
+                out.k_out = torch.empty(k.shape, dtype=k.dtype, device=self.device)
+            # outputs of an earlier, longer call serve this one, as the others do
+            q, k = out.q_out[:q.shape[0]], out.k_out[:k.shape[0]]
             B.upf_select_tokens_check(self.ctx, batch, params, q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
                                       _ptr(out.keep_bits), _ptr(out.kept_count), io, ws.data_ptr(), ws.numel())
             rope.apply(raw[0][1], raw[1][1], positions, out=(q, k))
-            out.q_out, out.k_out = q, k
         stream = torch.cuda.current_stream(self.device).cuda_stream
         B.upf_select_tokens(self.ctx, batch, params, q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
                             _ptr(out.scores), _ptr(out.block_scores), _ptr(out.keep_bits), _ptr(out.kept_count),

@@ -64,3 +64,30 @@ def test_queries_of_another_type_are_refused_with_a_rotary_embedding():
     with pytest.raises(ValueError, match="bfloat16"):
         sel.select_tokens(q, k, cu, cu_dev, 8, 2, 128, positions=pos, rope=rope)
     assert torch.isfinite(rope.apply(q, k, pos)[0]).all()
+
+
+def test_outputs_that_serve_calls_of_several_lengths():
+    """Outputs that were made for 700 tokens, given to a call of 450 and again to one of 700."""
+    sel, rope, rows, q, k, pos, cu, cu_dev = inputs()
+    params = B.make_params(32, 16, 32, 32, 0.6)
+    out = None
+    for T in (700, 450, 700, 1):
+        host = np.array([0, min(300, T), T], np.int32)
+        dev = torch.from_numpy(host).to(DEV)
+        a = (q[:T], k[:T], host, dev, 8, 2, 128)
+        got = sel.select_tokens(*a, positions=pos[:T], params=params, rope=rope, out=out)
+        assert out is None or got is out
+        out = got
+        want = rope.apply(q[:T], k[:T], pos[:T])
+        assert torch.equal(out.q_out[:T], want[0]) and torch.equal(out.k_out[:T], want[1])
+        plain = sel.select_tokens(want[0], want[1], host, dev, 8, 2, 128, positions=pos[:T], params=params)
+        n = int(plain.total_kept)
+        assert int(out.total_kept) == n and torch.equal(out.scores[:T], plain.scores)
+        assert torch.equal(out.pos_out[:n], plain.pos_out[:n])
+    assert out.q_out.shape[0] == 700
+    # too few rows
+    small = sel.alloc_outputs(cu, params.block, None, pos)
+    small.q_out, small.k_out = torch.empty_like(q[:600]), torch.empty_like(k)
+    with pytest.raises(ValueError, match="q"):
+        sel.select_tokens(q, k, cu, cu_dev, 8, 2, 128, positions=pos, params=params, rope=rope, out=small)
+    assert sel.status() == 0
