@@ -531,7 +531,9 @@ size_t upf_kv_accumulate_workspace_bytes(const upf_kv_cache* cache, const upf_kv
  * A negative, infinite or NaN weight in a request to be cut sets UPF_ERR_NONFINITE; a bad kv_len
  * (also one above weights_cols), a bad page among the request's entries or new places, or more
  * entries to keep than places (of max_pages_out or weights_out_cols) set UPF_ERR_INVALID_ARG.  Such a
- * request is skipped: nothing of it is moved, kv_len_out[r] is kv_len[r], or 0 where page_table_out is given. */
+ * request is skipped: nothing of it is moved, and kv_len_out[r] is kv_len[r].  Where page_table_out is given, which has none of
+ * its entries then, it is 0; or, if kv_len_out is kv_len, -1 - kv_len[r] (a negative one stays): no length to any
+ * call, and the caller has it back from it. */
 typedef struct upf_kv_eviction {
   int32_t num_reqs;
   const int32_t* kv_len;

@@ -243,7 +243,10 @@ __global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEv
   int32_t* const kept = a.kept ? a.kept + r * a.kept_stride : nullptr;
   int32_t* const bounds = a.bounds + r * (chunks_of(a.cap) + 1);
   if (!fine || !cut) {
-    const int now = fine ? left : a.table_out ? 0 : n;
+    // a request that is skipped: its length, which of other pages' entries is 0, and where that would be the last
+    // to be known of it, its length marked as a bad one
+    const int gone = a.len_out != a.kv_len ? 0 : n < 0 ? n : -1 - n;
+    const int now = fine ? left : a.table_out ? gone : n;
     if (first == 0) {
       a.plan[r] = KvEvictPlan{n, now, fine && move ? 1 : 0, 0};
       a.len_out[r] = now;

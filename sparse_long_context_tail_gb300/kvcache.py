@@ -278,7 +278,10 @@ class QuantKVCache:
         copied too).  ``kv_len`` and ``weights`` follow, in place or into ``kv_len_out`` and ``weights_out``; weights
         from the new length up to the old one become zero.  Returns ``kept``, int32 [R, budget]: what number the entry
         had that is number j now; -1 past the new length.  Pages that several requests share have to be
-        evicted into others."""
+        evicted into others.
+
+        A request that is skipped (``include/upf.h`` says when; ``status()`` reports it) keeps its entries, and its length n
+        if they stay in its pages; of others' its new length is 0, or -1 - n where ``kv_len`` itself is rewritten."""
         R, pages, table_row = self._table("page_table", page_table)
         op = ostride = opages = 0
         if page_table_out is not None:

@@ -202,3 +202,32 @@ def test_many_requests_whose_rows_go_back(Hq):
     assert b.cache.status() == 0
     assert torch.equal(got[1000:1501], old[1000:1501])
     assert torch.allclose(got, want, rtol=1e-5) and not torch.equal(got[1501:], old[1501:])
+
+
+# ------------------------------------------- requests that cannot be evicted --
+
+def test_a_refused_request_keeps_its_length_when_lengths_are_rewritten_in_place():
+    """Into other pages with kv_len itself as the new lengths: a request that is skipped is marked as not there, and its
+    length can be had back."""
+    b = Batch([100, 90, 80, 0], 2, 64, seed=74, spare=40)
+    was = [b.contents(s) for s in b.slots]
+    w = torch.rand(4, 120, generator=torch.Generator().manual_seed(75)).to(DEV)
+    fine, want = w.clone(), K.evict(w[1, :90].tolist(), 50, 50, 0, 5)
+    w[1, 40] = float("nan")
+    out = b.free[:16].view(4, 4).to(DEV)
+    kept = b.cache.evict(w, b.table, b.kv_len, 16, 50, recent=5, page_table_out=out)
+    assert b.cache.status() == 5 and (kept[1] == -1).all()
+    assert b.kv_len.tolist() == [50, -1 - 90, 50, 0]
+    # the new table says so to whoever reads it, and a second call leaves it
+    q, cu = queries([1] * 4, 4, 64, BF16, 76)
+    got = b.cache.attend(q, out, b.kv_len, 16)
+    assert b.cache.status() == 1 and not got.out[1].any() and torch.isneginf(got.lse[1]).all()
+    again = torch.tensor([-1 - 90, -2 ** 31, 2 ** 31 - 1, -1], dtype=torch.int32, device=DEV)
+    b.cache.evict(fine, b.table, again, 16, 50, recent=5, page_table_out=out)
+    assert b.cache.status() == 1 and again.tolist() == [-1 - 90, -2 ** 31, -2 ** 31, -1]
+    # the old pages hold its entries as before
+    n = -1 - int(b.kv_len[1])
+    assert n == 90 and all(torch.equal(x, y) for x, y in zip(b.contents(b.slots[1]), was[1]))
+    lens = torch.tensor([0, n, 0, 0], dtype=torch.int32, device=DEV)
+    kept = b.cache.evict(fine, b.table, lens, 16, 50, recent=5, page_table_out=out)
+    assert b.cache.status() == 0 and lens.tolist() == [0, 50, 0, 0] and kept[1].tolist() == want
