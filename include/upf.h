@@ -326,8 +326,8 @@ upf_status upf_select_noalloc(const upf_batch* batch, const upf_params* params, 
  * inside the tensor-core scoring kernels is bounded; when one expires the
  * kernel records UPF_ERR_TIMEOUT in the status word, stops issuing work,
  * waits for its outstanding copies and MMAs, frees its tensor memory and
- * returns, so the context stays usable.  The cache attention's waits for its
- * copies are bounded in the same way.  This sets the limit of the pipeline
+ * returns, so the context stays usable.  The waits of the cache attention, of
+ * accumulating over many rows and of evicting are bounded in the same way.  This sets the limit of the pipeline
  * waits (a role waiting for another role's data), in SM clock cycles, for
  * later calls on `ctx`; 0 restores the default (4e9 cycles, about 2 s).  The
  * waits that wind a kernel down always keep the default.  A very small limit
@@ -499,6 +499,8 @@ upf_status upf_kv_attend(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_q
  * the request is skipped (also with kv_len[r] > weights_cols; and where cu_q is not ascending, with more
  * than eight rows a kv head, max_q_len * H_q / H_kv, one whose rows begin before those of an earlier good
  * request end); an entry of a bad page is not seen.
+ * UPF_ERR_TIMEOUT in the status word (upf_set_wait_limit): some entries of weights_out have their new weights, the
+ * others what was there.
  * ws: upf_kv_accumulate_workspace_bytes() bytes.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 upf_status upf_kv_accumulate(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_query* query, int32_t dtype,
@@ -564,7 +566,11 @@ typedef struct upf_kv_eviction {
 size_t upf_kv_evict_workspace_bytes(const upf_kv_cache* cache, const upf_kv_eviction* eviction);
 
 /* Run an eviction.  kv_len, the page tables and weights must not change while the call runs; a captured call
- * may be replayed with other contents.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * may be replayed with other contents.
+ * UPF_ERR_TIMEOUT in the status word (upf_set_wait_limit): kv_len_out, kept and weights_out are what they would be, but of
+ * requests that were cut or copied some entries have been moved and others not, so that these requests' entries
+ * have to be written again.  Those of all other requests, and other slots, are as they were.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 upf_status upf_kv_evict(upf_ctx* ctx, const upf_kv_cache* cache, const upf_kv_eviction* eviction, void* ws,
                         size_t ws_bytes, void* stream);
 

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from oracle import kv_oracle as K
+from sparse_long_context_tail_gb300 import _binding as B
 from test_gpu_evict import BF16, DEV, F16, Batch, f64, queries
 from test_gpu_kv import peaked
 
@@ -231,3 +232,54 @@ def test_a_refused_request_keeps_its_length_when_lengths_are_rewritten_in_place(
     lens = torch.tensor([0, n, 0, 0], dtype=torch.int32, device=DEV)
     kept = b.cache.evict(fine, b.table, lens, 16, 50, recent=5, page_table_out=out)
     assert b.cache.status() == 0 and lens.tolist() == [0, 50, 0, 0] and kept[1].tolist() == want
+
+
+# --------------------------------------------------------- waits that run out --
+
+@pytest.mark.parametrize("elsewhere", [False, True])
+def test_a_wait_of_an_eviction_that_runs_out(elsewhere):
+    """With a limit of one cycle, as often as it takes until some chunk looks for another one before that has been read: it
+    is reported, lists, lengths and weights are those of a whole eviction, and what was not to be moved is as it was."""
+    lens, budget, trigger = [20000, 500, 20000, 900, 20000, 0, 20000], 19000, 19500
+    b = Batch(lens, 2, 64, seed=83, spare=len(lens) * 1250 if elsewhere else 20)
+    w0 = torch.rand(7, 20000, generator=torch.Generator().manual_seed(84)).to(DEV)
+    storage, want = b.cache.storage.clone(), [K.evict(w0[r, :n].tolist(), budget, trigger, 3, 40) for r, n in enumerate(lens)]
+    kw, slots = {}, b.slots
+    if elsewhere:          # the first pages are the request's own
+        out = b.free[:7 * 1250].view(7, 1250).to(DEV).clone()
+        own = min(600, b.table.shape[1])
+        long = [0, 2, 4, 6]
+        out[long, :own] = b.table[long, :own]
+        kw["page_table_out"] = out
+        slots = [b.slot_list(out[r], len(want[r])) for r in range(7)]
+    mine = torch.zeros(b.cache.num_slots, dtype=torch.bool, device=DEV)
+    for r, n in enumerate(lens):
+        if elsewhere or n > trigger:
+            mine[slots[r]] = True
+        if not elsewhere and n > trigger:
+            mine[b.slots[r]] = True
+    others = (~mine).nonzero().flatten()
+    before = b.contents(others)
+    B.upf_set_wait_limit(b.cache.ctx, 1)
+    for _ in range(100):
+        b.cache.storage.copy_(storage)
+        w, n2 = w0.clone(), b.kv_len.clone()
+        kept = b.cache.evict(w, b.table, n2, b.page, budget, trigger=trigger, sinks=3, recent=40, **kw)
+        status = b.cache.status()
+        assert n2.tolist() == [len(x) for x in want]
+        if status:
+            break
+    assert status == 6
+    for r, n in enumerate(lens):
+        assert kept[r].tolist() == (want[r] + [-1] * budget)[:budget]
+        at = torch.tensor(want[r], dtype=torch.long, device=DEV)
+        assert torch.equal(w[r, :len(at)], w0[r, at]) and not w[r, len(at):n].any() and torch.equal(w[r, n:], w0[r, n:])
+    assert all(torch.equal(x, y) for x, y in zip(b.contents(others), before))
+    B.upf_set_wait_limit(b.cache.ctx, 0)
+    b.cache.storage.copy_(storage)
+    was = [b.contents(s) for s in b.slots]
+    kept = b.cache.evict(w0.clone(), b.table, b.kv_len, b.page, budget, trigger=trigger, sinks=3, recent=40, **kw)
+    assert b.cache.status() == 0
+    for r in range(7):
+        at = torch.tensor(want[r], dtype=torch.long, device=DEV)
+        assert all(torch.equal(x, y[at]) for x, y in zip(b.contents(b.slot_list(kw["page_table_out"][r] if elsewhere else b.table[r], len(at))), was[r]))
