@@ -5,7 +5,7 @@ import torch
 
 from oracle import kv_oracle as K
 from sparse_long_context_tail_gb300 import _binding as B
-from test_gpu_evict import BF16, DEV, F16, Batch, f64, queries
+from test_gpu_evict import BF16, DEV, F16, Batch, check_evict, f64, queries
 from test_gpu_kv import peaked
 
 pytestmark = pytest.mark.gpu
@@ -283,3 +283,32 @@ def test_a_wait_of_an_eviction_that_runs_out(elsewhere):
     for r in range(7):
         at = torch.tensor(want[r], dtype=torch.long, device=DEV)
         assert all(torch.equal(x, y[at]) for x, y in zip(b.contents(b.slot_list(kw["page_table_out"][r] if elsewhere else b.table[r], len(at))), was[r]))
+
+
+# ----------------------------------------- clusters and shared memory in full --
+
+@pytest.mark.parametrize("kind", ["mixed", "equal", "near"])
+@pytest.mark.parametrize("lens,budget", [([50000], 11111),                       # a cluster of eight
+                                         ([40000, 900, 33000, 0, 17], 800),      # of eight, for more than four requests
+                                         ([700000], 200000),                     # of sixteen, weights past shared memory
+                                         ([350000, 10, 5000, 20, 30], 4000)])    # of eight, weights past shared memory
+def test_requests_whose_weights_do_not_fit_a_cluster(lens, budget, kind):
+    check_evict(Batch(lens, 1, 64, page=256, seed=85), budget, sinks=3, recent=50, kind=kind)
+
+
+def test_bad_weights_past_shared_memory_are_found():
+    """The last weights of a warp, and of the last one; a tie across the whole request."""
+    n = 700000
+    b = Batch([n], 1, 64, page=256, seed=86)
+    storage = b.cache.storage.clone()
+    w = torch.full((1, n), 0.25, device=DEV)
+    w[0, 1000::7] = 0.5
+    for at in (1300, 1405, n - 60, n - 55, n - 1, 0):
+        for bad in (float("nan"), -1.0):
+            x = w.clone()
+            x[0, at] = bad
+            kept = b.cache.evict(x, b.table, b.kv_len, 256, 150000, sinks=3, recent=50)
+            assert b.cache.status() == 5 and (kept == -1).all() and b.kv_len.tolist() == [n]
+            assert torch.equal(b.cache.storage, storage)
+    kept = b.cache.evict(w.clone(), b.table, b.kv_len.clone(), 256, 150000, sinks=3, recent=50)
+    assert b.cache.status() == 0 and kept[0].tolist() == K.evict(w[0].tolist(), 150000, 150000, 3, 50)
