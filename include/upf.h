@@ -624,9 +624,10 @@ typedef struct upf_rope {
 } upf_rope;
 
 /* The rotation's table (host only, no GPU): turns[i] (host, rotary_dim / 2) is
- * f_i / (2 pi) as a fraction of a turn in units of 2^-64, modulo one turn, so that
- * position * turns[i] modulo 2^64 is the angle, at any position to 2^-53 of
- * position * f_i.  The caller copies it to the device.  magnitude: receives m
+ * f_i / (2 pi) as a fraction of a turn in units of 2^-64, cut off there, modulo one turn, so that
+ * position * turns[i] modulo 2^64 is the angle, at any position to |position| * (2^-64 + e f_i / (2 pi))
+ * of a turn; e, of the frequency in double precision, is about 2^-50.  (Of f_i a pair of few turns thus has fewer
+ * bits: of one in 2^30 positions 34.)  The caller copies it to the device.  magnitude: receives m
  * (nullable).  Errors: INVALID_ARG, UNSUPPORTED. */
 upf_status upf_rope_turns(const upf_rope* rope, uint64_t* turns, double* magnitude);
 

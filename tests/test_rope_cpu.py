@@ -160,3 +160,18 @@ def test_calls_that_are_not_refused(good):
     with pytest.raises(B.UpfError) as e:
         _apply(**good)
     assert "context" in e.value.message, e.value.message
+
+
+@pytest.mark.parametrize("n,base,kind", [(256, 1e7, dict(scaling="linear", factor=32.0)), (128, 5e5, dict(scaling="linear", factor=8.0)),
+                                         (128, 5e5, dict(scaling="base", factor=8.0)), (128, 1e4, dict()),
+                                         (128, 5e5, dict(scaling="bands", factor=32.0, original_len=8192, low=1, high=4)),
+                                         (64, 1e6, dict(scaling="yarn", factor=40.0, original_len=32768, low=1, high=32))])
+def test_angles_at_any_position_are_as_near_as_the_header_says(n, base, kind):
+    """Positions times the table modulo a turn, against 60-digit decimals: |position| (2^-64 + 2^-50 f / 2 pi) of a turn."""
+    rope, keep = B.make_rope(256, n, base, **kind)
+    turns, _ = B.upf_rope_turns(rope)
+    for t, f in zip(turns, O.frequencies(n, base, **kind)):
+        for p in (1, 131071, 2 ** 31 - 1, 2 ** 40 + 7):
+            off = (Decimal(p * int(t) % 2 ** 64) / 2 ** 64 - p * f / O.TWO_PI) % 1
+            off = min(abs(off), abs(1 - abs(off)))
+            assert off <= p * (Decimal(2) ** -64 + Decimal(2) ** -50 * f / O.TWO_PI), (p, f)
