@@ -754,6 +754,12 @@ upf_status check_rows(const char* name, const void* p, int64_t stride, int heads
   return UPF_OK;
 }
 
+// Arrays of whole numbers, which the kernels read element by element.
+upf_status check_ints(const char* name, const void* p, size_t bytes) {
+  if (reinterpret_cast<uintptr_t>(p) % bytes) return fail(UPF_ERR_INVALID_ARG, "%s must be %zu-byte aligned", name, bytes);
+  return UPF_OK;
+}
+
 upf_status check_ws_bytes(const void* ws, size_t have, size_t need) {
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return fail(UPF_ERR_INVALID_ARG, "workspace must be set and 256-byte aligned");
   if (have < need) return fail(UPF_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", have, need);
@@ -799,6 +805,10 @@ upf_status check_query(const upf_kv_cache* c, const upf_kv_query* x, bool need_d
   if (!std::isfinite(x->softmax_scale)) return fail(UPF_ERR_INVALID_ARG, "softmax_scale must be finite");
   if (!need_data) return UPF_OK;
   if (!x->kv_len || !x->page_table) return fail(UPF_ERR_INVALID_ARG, "kv_len and page_table are required");
+  upf_status st;
+  if ((st = check_ints("kv_len", x->kv_len, 4)) != UPF_OK || (st = check_ints("page_table", x->page_table, 4)) != UPF_OK ||
+      (st = check_ints("cu_q", x->cu_q, 4)) != UPF_OK)
+    return st;
   if (x->page_stride < x->max_pages) return fail(UPF_ERR_INVALID_ARG, "page_stride must be >= max_pages");
   if (!x->cu_q && x->num_q_tokens != x->num_reqs)
     return fail(UPF_ERR_INVALID_ARG, "without cu_q there is one new token per request (num_q_tokens %d, num_reqs %d)",
@@ -863,13 +873,17 @@ upf_status check_eviction(const upf_kv_cache* c, const upf_kv_eviction* x, bool 
   if (!need_data) return UPF_OK;
   if (!x->kv_len || !x->kv_len_out || !x->page_table)
     return fail(UPF_ERR_INVALID_ARG, "kv_len, kv_len_out and page_table are required");
+  upf_status st;
+  if ((st = check_ints("kv_len", x->kv_len, 4)) != UPF_OK || (st = check_ints("kv_len_out", x->kv_len_out, 4)) != UPF_OK ||
+      (st = check_ints("page_table", x->page_table, 4)) != UPF_OK ||
+      (st = check_ints("page_table_out", x->page_table_out, 4)) != UPF_OK || (st = check_ints("kept", x->kept, 4)) != UPF_OK)
+    return st;
   if (x->page_stride < x->max_pages) return fail(UPF_ERR_INVALID_ARG, "page_stride must be >= max_pages");
   if (x->page_table_out) {
     if (x->max_pages_out < 1 || (int64_t)x->max_pages_out * x->page_size > (1LL << 30))
       return fail(UPF_ERR_INVALID_ARG, "max_pages_out must be >= 1 and max_pages_out * page_size at most 2^30");
     if (x->page_stride_out < x->max_pages_out) return fail(UPF_ERR_INVALID_ARG, "page_stride_out must be >= max_pages_out");
   }
-  upf_status st;
   if ((st = check_weights("weights", x->weights, x->weights_stride, x->weights_cols)) != UPF_OK) return st;
   if ((st = check_weights("weights_out", x->weights_out, x->weights_out_stride, x->weights_out_cols)) != UPF_OK) return st;
   if (!(x->weights == x->weights_out && (x->num_reqs == 1 || x->weights_stride == x->weights_out_stride)) &&
@@ -1605,6 +1619,8 @@ upf_status upf_rope_apply(upf_ctx* ctx, const upf_rope* rope, const uint64_t* tu
         return fail(UPF_ERR_INVALID_ARG, "q_out and k_out overlap");
     }
   if (!positions) return fail(UPF_ERR_INVALID_ARG, "positions is NULL");
+  if ((st = check_ints("positions", positions, 8)) != UPF_OK || (st = check_ints("num_tokens_dev", num_tokens_dev, 4)) != UPF_OK)
+    return st;
   if (!turns_dev || !aligned16(turns_dev)) return fail(UPF_ERR_INVALID_ARG, "turns_dev must be set and 16-byte aligned");
   if ((st = check_ctx(ctx)) != UPF_OK) return st;
   DeviceGuard guard(ctx->device);

@@ -167,3 +167,26 @@ def test_accumulations_with_bad_queries_are_refused(bad, word):
     with pytest.raises(B.UpfError) as e:
         _accumulate(query=_query(**bad))
     assert word in e.value.message, e.value.message
+
+
+@pytest.mark.parametrize("name", ["kv_len", "kv_len_out", "page_table", "page_table_out", "kept"])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_evictions_with_misaligned_arrays_are_refused(name, off):
+    a = dict(kv_len=0x100, kv_len_out=0x200, page_table=0x300, page_table_out=0x400, page_stride_out=4, max_pages_out=4, kept=0x500,
+             kept_stride=32)
+    with pytest.raises(B.UpfError, match="context"):
+        B.upf_kv_evict(None, _cache(), _eviction(**a), 256, 1 << 20)
+    a[name] += off
+    with pytest.raises(B.UpfError, match=f"{name} must be 4-byte aligned"):
+        B.upf_kv_evict(None, _cache(), _eviction(**a), 256, 1 << 20)
+
+
+@pytest.mark.parametrize("name", ["kv_len", "page_table", "cu_q"])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_accumulations_with_misaligned_arrays_are_refused(name, off):
+    a = dict(kv_len=0x100, page_table=0x300, cu_q=0x400)
+    with pytest.raises(B.UpfError, match="context"):
+        _accumulate(query=_query(**a))
+    a[name] += off
+    with pytest.raises(B.UpfError, match=f"{name} must be 4-byte aligned"):
+        _accumulate(query=_query(**a))

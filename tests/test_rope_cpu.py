@@ -175,3 +175,10 @@ def test_angles_at_any_position_are_as_near_as_the_header_says(n, base, kind):
             off = (Decimal(p * int(t) % 2 ** 64) / 2 ** 64 - p * f / O.TWO_PI) % 1
             off = min(abs(off), abs(1 - abs(off)))
             assert off <= p * (Decimal(2) ** -64 + Decimal(2) ** -50 * f / O.TWO_PI), (p, f)
+
+
+@pytest.mark.parametrize("bad,word", [(dict(positions=12), "positions"), (dict(positions=9), "positions"), (dict(count=6), "num_tokens_dev"),
+                                      (dict(count=1), "num_tokens_dev")])
+def test_misaligned_positions_and_counts_are_refused(bad, word):
+    with pytest.raises(B.UpfError, match=f"{word} must be"):
+        _apply(**bad)
