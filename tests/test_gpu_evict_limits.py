@@ -122,6 +122,25 @@ def test_lse_whose_binary_logarithm_is_past_fp32_adds_nothing():
             assert not got[1, :50].any() and torch.equal(got[0], base[0]) and torch.equal(got[2], base[2])
 
 
+@pytest.mark.parametrize("Hq", [1, 12])
+def test_how_exactly_lse_is_taken(Hq):
+    """Zero queries, so that a weight is exp(-lse) by itself.  Few rows: lse log2 e in two parts, so that two powers of two (2^-22
+    each), their product and the sum are all; its rounding as one number would be 2^-18 at |lse| = 80.  Many rows have it as
+    one: 2^-24 |lse|, one power and the sum."""
+    R = 64
+    b = Batch([5] * R, 1, 64, seed=87)
+    q = torch.zeros(R, Hq, 64, dtype=BF16, device=DEV)
+    at = np.linspace(-80, 80, R) + 0.1 * np.sin(np.arange(R))
+    lse = torch.full((R, Hq), -float("inf"), device=DEV)
+    lse[:, Hq // 2] = torch.from_numpy(at).float().to(DEV)
+    got = f64(accumulated(b, q, lse, torch.zeros(R, 8, device=DEV))[:, :5])
+    assert b.cache.status() == 0
+    l64 = f64(lse[:, Hq // 2])[:, None]
+    want = np.exp(-l64)
+    error = 2.0 ** -21 + 2.0 ** -23 if Hq == 1 else np.abs(l64) * 2.0 ** -24 + 2.0 ** -21
+    assert (np.abs(got / want - 1) <= error).all(), np.abs(got / want - 1).max()
+
+
 # ----------------------------------------------------- keys that hold a NaN --
 
 @pytest.mark.parametrize("Hq,news", [(2, 5), (8, 5), (8, 1), (32, 1)])
