@@ -6,9 +6,10 @@
 // Only the keys' half of the records is read, and each entry's sum is added up in one order, so results repeat.  This file
 // has the kernel for at most eight rows a kv head (decoding); more rows take kv_accumulate_tc.cu.
 //
-// What bounds it: about 160 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 8
-// products, at 2.3 to 2.7 a clock and SM; HBM would allow 40 % more.  One new token of 16 requests of 4096 to
-// 131072 entries (8 heads, d = 128, 32 q heads): 59.5 us, 4.4 TB/s; one of 131072: 23 us; of 4096 (d = 64): 6.0 us.
+// What it takes: about 160 instructions per 16 entries and head of d = 128, 32 of them conversions, 32 scalings and 8
+// products, at 2.3 to 2.7 a clock and SM.  Neither the issue slots, a third of which are idle, nor HBM, which would allow 40 % more,
+// are at their limit: a tile's wait, products, exponentials and sums are one chain.  One new token of 16 requests of 4096 to
+// 131072 entries (8 heads, d = 128, 32 q heads): 60 us, 4.4 TB/s; one of 131072: 22.7 us; of 4096 (d = 64): 6.0 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -27,7 +28,7 @@ using namespace acc;
 // as operand A straight from registers.  It leaves the tile's sums in shared memory, and after the
 // block they are added up over the heads.  (With whole tiles to a warp, all heads of them, the last
 // warps of an SM worked alone for a quarter of the time: a tile takes one warp of 24 about 6 us.)
-// (With 32 warps 16 ragged requests take 58.7 us for 59.4, and 4096 entries 7.4 for 6.0.)
+// (With 32 warps 16 ragged requests took 58.7 us for 59.4, and 4096 entries 7.4 for 6.0.)
 constexpr int kWarps = 24, kThreads = 32 * kWarps;
 constexpr int kSumTiles = 384;          // tiles times heads of a block
 constexpr int kBlockTiles = 192;        // most tiles of a block
@@ -361,8 +362,8 @@ cudaError_t launch_dim(const KvAccumulateArgs& a, bool f16, cudaStream_t s) {
   return f16 ? launch<__half, kDim>(a, s) : launch<__nv_bfloat16, kDim>(a, s);
 }
 
-// One new token of 131072 entries of 8 heads, 8 rows a head: 23.8 us here, 29.3 there; 12 rows would be two passes here, 29 us there.
-// 16 ragged requests of 4 rows: 61.8 and 80.5 us.
+// One new token of 131072 entries of 8 heads, 8 rows a head: 23.0 us here, 28.7 there; 12 rows would be two passes here, 29 us there.
+// 16 ragged requests of 4 rows: 60 and 81 us.
 bool few_rows(int gamma, int max_q) { return gamma * max_q <= 8; }
 
 }  // namespace

@@ -16,7 +16,7 @@
 // its codes.  A product of 128 rows at d = 128 takes 1090 cycles; its exponentials alone would take 512 (32 a clock and SM),
 // the product about 560, the conversion of its keys 250 to 500.  With any one of these left out in a trial the time
 // fell by 2 to 6 %: what is left is the hand-over between the roles.  32 queries of 4 q heads a kv head over
-// 131072 entries of 8 heads: 42 us (820 TFLOP/s, 3.2 exponentials a ps), 128 queries 128 us.  Measured beside it:
+// 131072 entries of 8 heads: 43 us (800 TFLOP/s, 3.1 exponentials a ps), 128 queries 131 us.  Measured beside 42 and 128:
 // both teams at one product, a half of its columns each: 53 and 171 us; three sum teams 46 and 140; two slots of
 // sums and four of keys 48 and 150.
 #include <algorithm>
@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_accumulate_tc_kernel(const K
             const uint32_t n = sn + b, ss = n % C::kSumSlots;
             const int e0 = blocks.entry(run0 + b), e = e0 + quarter * 32 + lane;
             const bool whole = all_seen(a, x, view, e0, e0 + kBlock);
-            // the queries that see this entry: `count` from `from` on
+            // The queries that see this entry: `count` from `from` on.  (With each row's four comparisons instead 53 us for 43: the CTA
+            // with the blocks that rows see in part is the last one.)
             const int from = max(0, e - view.base);
             const uint32_t count = a.window == 0 || e < a.sinks ? INT_MAX : max(0, e - view.base + a.window - from);
             if (!(ok = __all_sync(0xFFFFFFFFu, wait(sums_full(ss), n / C::kSumSlots & 1)))) break;

@@ -7,7 +7,7 @@
 // Of entries as heavy as it the first ones are kept.  Each CTA then lists the kept ones of its
 // run of entries, in order.
 //
-// Bound by latency: about ten steps over the whole cluster, a load, a barrier or a scan each (131072 entries 15 us, 1088 9 us).
+// Bound by latency: about ten steps over the whole cluster, a load, a barrier or a scan each (131072 entries 15 us, 1088 8 us).
 //
 // The second moves them together.  Entry j of the result was entry s_j >= j, so chunks of
 // places written in ascending order never overwrite what a later chunk has yet to read.  To run

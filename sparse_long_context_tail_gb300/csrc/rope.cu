@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   }
 }
 
-// Any even rotary_dim: a thread per token and two dims, all heads.
+// Any even rotary_dim: a thread per token and two dims, all heads.  Element by element, a table load and a sine a pair:
+// 131072 tokens of 32 + 8 heads of d = 128, 24 dims of them turned, 717 us; 48 dims by the kernel above 396.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_any_kernel(const RopeArgs a) {
   constexpr const T* kT = nullptr;

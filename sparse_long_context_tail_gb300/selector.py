@@ -102,9 +102,9 @@ class TokenSelector:
                       rope: Optional[RotaryEmbedding] = None) -> SelectOutputs:
         """q: bf16 [T, H_q, d] (rows may be strided), k: bf16 [T, H_kv, d]; hidden: [T, hidden].
 
-        ``rope``: q and k come before their rotary positions; they are turned by ``positions`` first (into
-        the first rows of ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored.  A call
-        that is refused has turned nothing."""
+        ``rope``: q and k come before their rotary positions; they are turned by ``positions`` first (into the first
+        rows of ``out.q_out`` and ``out.k_out``, which may be q and k themselves), and the turned ones are scored.
+        A call that is refused has turned nothing."""
         params = params or B.make_params()
         if rope is not None and positions is None:
             raise ValueError("rope needs positions")
