@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(move_threads(kDim)) kv_evict_move_kernel(const
     place[k] = record_of(slot_of(a.table_out ? a.table_out + r * a.table_out_stride : a.table + r * a.table_stride, j0 + k * 16,
                                  a.page_shift, a.num_slots));
   // ---- nothing to move where all entries stay where they are: list[j] >= j, so that the last one tells
-  const bool in_place = !a.table_out || a.table_out == a.table;
+  const bool in_place = !a.table_out || (a.table_out == a.table && (r == 0 || a.table_out_stride == a.table_stride));
   if (__syncthreads_or(in_place && tid == places - 1 && mine == j0 + tid)) {
     if (tid == 0) store_release(mark + c, 1);
     return;

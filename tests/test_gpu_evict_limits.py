@@ -331,3 +331,27 @@ def test_bad_weights_past_shared_memory_are_found():
             assert torch.equal(b.cache.storage, storage)
     kept = b.cache.evict(w.clone(), b.table, b.kv_len.clone(), 256, 150000, sinks=3, recent=50)
     assert b.cache.status() == 0 and kept[0].tolist() == K.evict(w[0].tolist(), 150000, 150000, 3, 50)
+
+
+# ------------------------------------------------- one table with two strides --
+
+def test_places_in_the_same_table_with_another_stride():
+    """page_table_out begins where page_table does, but its second row is another one: entries of requests that are not cut
+    are copied there all the same."""
+    b = Batch([60, 50], 2, 64, seed=88, spare=12)
+    was = [b.contents(s) for s in b.slots]
+    P = b.table.shape[1]
+    room = torch.full((4 * P,), -7, dtype=torch.int32, device=DEV)
+    room[:2 * P] = b.table.flatten()
+    room[3 * P:] = b.free[:P].to(DEV)
+    table, out = room.as_strided((2, P), (P, 1)), room.as_strided((2, P), (3 * P, 1))
+    w = torch.rand(2, 64, device=DEV)
+    old = w.clone()
+    for budget in (64, 55):        # none cut, the first one cut
+        kept = b.cache.evict(w, table, b.kv_len, 16, budget, page_table_out=out)
+        assert b.cache.status() == 0
+        for r, n in enumerate(b.lens):
+            want = K.evict(old[r, :n].tolist(), budget, budget, 0, 0)
+            assert kept[r].tolist() == want + [-1] * (budget - len(want)) and int(b.kv_len[r]) == len(want)
+            at = torch.tensor(want, device=DEV)
+            assert all(torch.equal(x, y[at]) for x, y in zip(b.contents(b.slot_list(out[r], len(want))), was[r]))
